@@ -372,6 +372,195 @@ int mt_scan_debug_lookback(int64_t skip_publish_tile, uint32_t spin_limit);
 int mt_scan_rows_noalloc(const void *inp, void *out, int64_t rows, int64_t n, int dtype,
                          int inclusive, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Operators of sequence models: the embedding lookup, the short causal
+ * convolution and the selective state space scan, forward, backward and for
+ * single tokens. They follow the rules above: caller-owned device memory,
+ * work enqueued on `stream` only, host-checkable mistakes refused before any
+ * launch, f32 arithmetic with one rounding at each store. Every sum has a
+ * fixed order, so a call gives the same bits each time. No call waits
+ * between CTAs.
+ *
+ * Activations are [batch, len, dim] with the channels contiguous and any
+ * strides (in elements) of the other two axes, so they may be parts of wider
+ * rows. `lens` (optional, device int32 [batch]) gives each sequence's live
+ * length (clamped to 0..len): what is stored past it is not read, outputs and
+ * gradients there are written as zeros, and states are those after the last
+ * live token. `slots` (optional, device int32 [batch]) names each sequence's
+ * row in a pool of `nslots` states; a sequence whose slot lies outside the pool is
+ * inactive: its output is zeros and no state is read or written. Without slots,
+ * sequence b has row b. No two active sequences of a call may share a slot.
+ * No output may overlap an input or another output, except a state, which
+ * is updated in place.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * mt_embed -- embedding lookup with scaling: out[i, :] = scale * table[tokens[i], :].
+ *
+ * tokens : device array of ntokens int32 or int64 (token_dtype MT_I32 or
+ *          MT_I64). A token outside 0..vocab-1 (padding) gives a row of zeros.
+ * table  : [vocab, dim], out: [ntokens, dim], both contiguous and of `dtype`
+ *          (MT_F32, MT_BF16 or MT_F16); the product is made in f32 and rounded once.
+ * Errors: MT_ERR_ARG, MT_ERR_DTYPE, MT_ERR_ALIAS, MT_ERR_ALIGN, MT_ERR_MEMORY, MT_ERR_CUDA.
+ */
+int mt_embed(const void *tokens, int64_t ntokens, int token_dtype, const void *table, int64_t vocab, int64_t dim,
+             int dtype, float scale, void *out, void *stream);
+
+/*
+ * mt_embed_grad -- the gradient of mt_embed's table, by sorted tokens:
+ *   dtable[v, :] = scale * sum over i with tokens[i] == v of dout[i, :]
+ * summed in f32 in the order of i (in a fixed grouping). With accumulate the
+ * sums are added to what dtable holds and rows that no token names are left
+ * as they are; otherwise those rows are written as zeros.
+ *
+ * dout       : [ntokens, dim] contiguous, `dtype`.
+ * dtable     : [vocab, dim] contiguous, grad_dtype: MT_F32 or `dtype`.
+ * scratch    : mt_embed_grad_scratch_slots(ntokens, vocab, dim) 8-byte slots,
+ *              16-byte aligned, no initialisation needed.
+ * ntokens and vocab are below 2^31. Errors: as mt_embed.
+ */
+int mt_embed_grad(const void *tokens, int64_t ntokens, int token_dtype, const void *dout, int dtype, int64_t vocab,
+                  int64_t dim, float scale, void *dtable, int grad_dtype, int accumulate, void *scratch, void *stream);
+
+/* 8-byte scratch slots of mt_embed_grad; -1 for a negative or too large size.
+ * Plain host arithmetic, as the other two scratch sizes below. */
+int64_t mt_embed_grad_scratch_slots(int64_t ntokens, int64_t vocab, int64_t dim);
+
+/*
+ * mt_conv_args -- arguments of the causal convolution calls. Every field is
+ * eight bytes wide; strides count elements; optional pointers may be NULL.
+ *   p_t[d] = bias[d] + sum_{k < width} weight[d, k] * x_{t-width+1+k}[d]
+ *   out_t  = p_t, or p_t * sigmoid(p_t) with silu
+ */
+typedef struct {
+    int64_t dtype;                 /* x, out, state, dout, dx, dstate: MT_F32, MT_BF16 or MT_F16 */
+    int64_t wdtype;                /* weight and bias: MT_F32 or dtype */
+    int64_t batch, len, dim;       /* mt_causal_conv_step: len is ignored (one token) */
+    int64_t width;                 /* 1..4 */
+    int64_t silu;                  /* nonzero: out = p * sigmoid(p) */
+    int64_t carry_in;              /* nonzero: the inputs before token 0 are the state's; zero: they are 0 */
+    int64_t nslots;                /* rows of the state pool (batch without slots) */
+    const void *x;                 /* [batch, len, dim] */
+    int64_t x_batch, x_token;
+    const void *weight;            /* [dim, width] contiguous */
+    const void *bias;              /* [dim], optional */
+    void *state;                   /* [nslots, width - 1, dim] contiguous: the last width - 1 inputs, oldest first */
+    const int32_t *slots, *lens;   /* optional */
+    void *out;                     /* [batch, len, dim] */
+    int64_t out_batch, out_token;
+    /* mt_causal_conv_grad only */
+    const void *dout;              /* [batch, len, dim] */
+    int64_t dout_batch, dout_token;
+    void *dx;                      /* [batch, len, dim] */
+    int64_t dx_batch, dx_token;
+    float *dweight;                /* [dim, width] contiguous f32 */
+    float *dbias;                  /* [dim] f32, optional */
+    void *dstate;                  /* [batch, width - 1, dim], optional: the gradient of the state before token 0 */
+    void *scratch;                 /* mt_causal_conv_grad_scratch_slots(...) slots, 16-byte aligned */
+} mt_conv_args;
+
+/*
+ * mt_causal_conv -- the convolution of whole prompts. `state` is optional; if
+ * given it is read (with carry_in) and left holding the last width - 1 inputs
+ * of each sequence. dout .. scratch are ignored.
+ * Errors of the three calls: MT_ERR_ARG, MT_ERR_DTYPE, MT_ERR_ALIAS,
+ * MT_ERR_ALIGN, MT_ERR_MEMORY, MT_ERR_CUDA.
+ */
+int mt_causal_conv(const mt_conv_args *args, void *stream);
+
+/* mt_causal_conv_step -- one token of each sequence: x and out are [batch, dim]
+ * (x_batch and out_batch their strides); state is required, read and shifted
+ * by the token (carry_in and lens are ignored). */
+int mt_causal_conv_step(const mt_conv_args *args, void *stream);
+
+/* mt_causal_conv_grad -- gradients of mt_causal_conv by x, weight, bias and
+ * (dstate) the first state, from dout. The state is only read here, row b for
+ * sequence b (slots must be NULL): it holds what it held before the forward call. out is ignored. */
+int mt_causal_conv_grad(const mt_conv_args *args, void *stream);
+int64_t mt_causal_conv_grad_scratch_slots(int64_t batch, int64_t len, int64_t dim, int64_t width);
+
+/*
+ * mt_ssm_args -- arguments of the selective scan calls. Every field is
+ * eight bytes wide; strides count elements; optional pointers may be NULL.
+ *   Delta  = softplus(delta + delta_bias)            (delta + delta_bias without softplus)
+ *   h_t[d, n] = exp(Delta_t[d] * A[d, n]) * h_{t-1}[d, n] + Delta_t[d] * u_t[d] * B_t[n]
+ *   y_t[d] = sum_n C_t[n] * h_t[d, n] + D[d] * u_t[d],   out = y, or y * z * sigmoid(z)
+ * with channel d using row d / (dim / groups) of B and C.
+ */
+typedef struct {
+    int64_t dtype;                 /* all activations and their gradients: MT_F32, MT_BF16 or MT_F16 */
+    int64_t batch, len, dim;       /* mt_selective_scan_step: len is ignored (one token) */
+    int64_t nstate;                /* 1..128 */
+    int64_t groups;                /* divides dim */
+    int64_t softplus;              /* nonzero: softplus of delta + delta_bias */
+    int64_t carry_in;              /* nonzero: the state before token 0 is the pool's; zero: it is 0 */
+    int64_t nslots;                /* rows of the state pool (batch without slots) */
+    const void *u;                 /* [batch, len, dim] */
+    int64_t u_batch, u_token;
+    const void *delta;             /* [batch, len, dim] */
+    int64_t delta_batch, delta_token;
+    const void *z;                 /* [batch, len, dim], optional gate */
+    int64_t z_batch, z_token;
+    const void *B;                 /* [batch, len, groups, nstate], the last two contiguous */
+    int64_t B_batch, B_token;
+    const void *C;
+    int64_t C_batch, C_token;
+    const float *A;                /* [dim, nstate] contiguous */
+    const float *D;                /* [dim], optional */
+    const float *delta_bias;       /* [dim], optional */
+    float *state;                  /* [nslots, dim, nstate] contiguous */
+    const int32_t *slots, *lens;   /* optional */
+    void *out;                     /* [batch, len, dim] */
+    int64_t out_batch, out_token;
+    float *checkpoints;            /* mt_selective_scan_checkpoint_slots(...) slots: written by the scan where given
+                                      (slots must then be NULL), read by the gradient */
+    void *scratch;                 /* mt_selective_scan_scratch_slots(...) slots, 16-byte aligned; may be NULL when 0 */
+    /* mt_selective_scan_grad only */
+    const void *dout;              /* [batch, len, dim] */
+    int64_t dout_batch, dout_token;
+    void *du;
+    int64_t du_batch, du_token;
+    void *ddelta;
+    int64_t ddelta_batch, ddelta_token;
+    void *dz;                      /* required with z */
+    int64_t dz_batch, dz_token;
+    void *dB;                      /* [batch, len, groups, nstate] */
+    int64_t dB_batch, dB_token;
+    void *dC;
+    int64_t dC_batch, dC_token;
+    float *dA;                     /* [dim, nstate] */
+    float *dD;                     /* [dim], optional */
+    float *ddelta_bias;            /* [dim], optional */
+    const float *dfinal;           /* [batch, dim, nstate], optional: gradient of the last states */
+    float *dinit;                  /* [batch, dim, nstate], optional: gradient of the first states */
+} mt_ssm_args;
+
+/*
+ * mt_selective_scan -- the scan of whole prompts. `state` is optional; if
+ * given it is read (with carry_in) and left holding the state after each
+ * sequence's last live token. With few sequences and channels the tokens are
+ * cut into segments that run side by side (scratch). dout .. dinit are ignored.
+ * Errors of the three calls: MT_ERR_ARG, MT_ERR_DTYPE, MT_ERR_ALIAS,
+ * MT_ERR_ALIGN, MT_ERR_MEMORY, MT_ERR_CUDA.
+ */
+int mt_selective_scan(const mt_ssm_args *args, void *stream);
+
+/* mt_selective_scan_step -- one token of each sequence: u, delta, z and out are
+ * [batch, dim] and B and C [batch, groups, nstate] (the _batch strides count);
+ * state is required and updated in place (carry_in, lens and scratch are ignored). */
+int mt_selective_scan_step(const mt_ssm_args *args, void *stream);
+
+/* mt_selective_scan_grad -- every gradient of mt_selective_scan from dout (and
+ * dfinal), with the checkpoints that the forward call of the same arguments
+ * wrote. state, slots, carry_in and out are ignored (the first states are in the
+ * checkpoints; slots must be NULL). */
+int mt_selective_scan_grad(const mt_ssm_args *args, void *stream);
+
+/* 8-byte scratch slots of mt_selective_scan (grad 0) or mt_selective_scan_grad
+ * (grad nonzero), and of the checkpoints; -1 for a size out of range. */
+int64_t mt_selective_scan_scratch_slots(int64_t batch, int64_t len, int64_t dim, int64_t nstate, int64_t groups, int grad);
+int64_t mt_selective_scan_checkpoint_slots(int64_t batch, int64_t len, int64_t dim, int64_t nstate);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,135 @@
+// mt_seq.cuh -- what the sequence-model kernels (embedding lookup, short
+// causal convolution, selective state space scan) share: widening loads and
+// rounding stores of a few neighbouring channels, and the scalar functions.
+//
+// Activations are f32, bf16 or f16 and are widened to f32 at the load; every
+// product, sum and state is f32; a result is rounded once, to nearest even,
+// at its store.
+#pragma once
+
+#include "mt_tile.cuh"
+
+namespace mt {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// ---- V neighbouring values --------------------------------------------------
+// load_n / store_n move V values as one vector access when `vec` (then p is
+// aligned to V values) and otherwise value by value; `live` values exist, the
+// others load as 0 and are not stored.
+template <class S, int V> struct VecOf;
+template <> struct VecOf<float, 4> { using T = uint4; };
+template <> struct VecOf<__nv_bfloat16, 4> { using T = uint2; };
+template <> struct VecOf<__half, 4> { using T = uint2; };
+template <> struct VecOf<__nv_bfloat16, 8> { using T = uint4; };
+template <> struct VecOf<__half, 8> { using T = uint4; };
+
+template <class S> __device__ __forceinline__ void widen4(const typename VecOf<S, 4>::T &w, float (&x)[4]);
+template <> __device__ __forceinline__ void widen4<float>(const uint4 &w, float (&x)[4]) { Codec<float>::unpack(w, x); }
+template <> __device__ __forceinline__ void widen4<__nv_bfloat16>(const uint2 &w, float (&x)[4]) {
+    Codec<__nv_bfloat16>::two(w.x, x[0], x[1]);
+    Codec<__nv_bfloat16>::two(w.y, x[2], x[3]);
+}
+template <> __device__ __forceinline__ void widen4<__half>(const uint2 &w, float (&x)[4]) {
+    Codec<__half>::two(w.x, x[0], x[1]);
+    Codec<__half>::two(w.y, x[2], x[3]);
+}
+template <class S> __device__ __forceinline__ typename VecOf<S, 4>::T narrow4(const float (&x)[4]);
+template <> __device__ __forceinline__ uint4 narrow4<float>(const float (&x)[4]) { return Codec<float>::pack(x); }
+template <> __device__ __forceinline__ uint2 narrow4<__nv_bfloat16>(const float (&x)[4]) {
+    return make_uint2(Codec<__nv_bfloat16>::pack2(x[0], x[1]), Codec<__nv_bfloat16>::pack2(x[2], x[3]));
+}
+template <> __device__ __forceinline__ uint2 narrow4<__half>(const float (&x)[4]) {
+    return make_uint2(Codec<__half>::pack2(x[0], x[1]), Codec<__half>::pack2(x[2], x[3]));
+}
+
+// Four values kept in their storage form, so that a load can be in flight
+// while earlier ones are worked on.
+template <class S> struct Raw4 {
+    typename VecOf<S, 4>::T w;
+    __device__ __forceinline__ void load(const S *p, bool vec, int live) {
+        if (vec && live == 4) {
+            w = *reinterpret_cast<const typename VecOf<S, 4>::T *>(p);
+        } else {
+            S v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                v[k] = k < live ? p[k] : S(0.0f);
+            w = *reinterpret_cast<typename VecOf<S, 4>::T *>(v);
+        }
+    }
+    __device__ __forceinline__ void widen(float (&x)[4]) const { widen4<S>(w, x); }
+};
+template <class S> __device__ __forceinline__ void store4(S *p, const float (&x)[4], bool vec, int live) {
+    if (vec && live == 4) {
+        *reinterpret_cast<typename VecOf<S, 4>::T *>(p) = narrow4<S>(x);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (k < live)
+                Codec<S>::store1(p + k, x[k]);
+    }
+}
+
+// ---- scalar functions ---------------------------------------------------------
+__device__ __forceinline__ float ex2f(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcpf(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float sigmoidf(float x) { return rcpf(1.0f + ex2f(-kLog2e * x)); }
+
+// log(1 + exp(x)) = max(x, 0) + log(1 + e), e = exp(-|x|) in (0, 1], and
+// log(1 + e) = 2 atanh(s), s = e / (2 + e) <= 1/3, by the odd series of atanh
+// (the classical series for a logarithm): the first term left out is below
+// 1.5e-9 of the sum. No cancellation, so the small steps that a scan lives on
+// (exp(x) far below 1) keep f32's relative precision, which log(1 + exp(x))
+// evaluated as written does not.
+__device__ __forceinline__ float softplusf(float x) {
+    const float e = ex2f(-kLog2e * fabsf(x));
+    const float s = e * rcpf(2.0f + e);
+    const float q = s * s;
+    float p = 1.0f / 15.0f;
+    p = fmaf(p, q, 1.0f / 13.0f);
+    p = fmaf(p, q, 1.0f / 11.0f);
+    p = fmaf(p, q, 1.0f / 9.0f);
+    p = fmaf(p, q, 1.0f / 7.0f);
+    p = fmaf(p, q, 1.0f / 5.0f);
+    p = fmaf(p, q, 1.0f / 3.0f);
+    p = fmaf(p, q, 1.0f);
+    return fmaf(2.0f * s, p, fmaxf(x, 0.0f));
+}
+
+// ---- two f32 lanes in a register pair -------------------------------------------
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pack2f(float lo, float hi) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpack2f(f32x2 v, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ f32x2 fma2f(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f32x2 mul2f(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 ex2_2f(f32x2 v) {
+    float a, b;
+    unpack2f(v, a, b);
+    return pack2f(ex2f(a), ex2f(b));
+}
+
+}  // namespace mt

@@ -1,0 +1,96 @@
+// mt_ssm.cu -- plans of the selective state space scan: how many lanes share a
+// channel, into how many segments the tokens are cut, and the scratch's parts.
+#include "mt_ssm.cuh"
+
+namespace mt {
+
+// Warps that keep an SM's arithmetic busy: a lane has 16 independent
+// recurrences, so a few warps a scheduler suffice. The plan must not ask the
+// device (scratch is sized on the host), so it counts GB300's 152 SMs.
+constexpr int64_t kSsmSms = 152;
+constexpr int64_t kEnoughWarps = kSsmSms * 6;   // from here on the tokens are not cut
+constexpr int64_t kTargetWarps = kSsmSms * 16;  // what a cut aims at
+constexpr int64_t kTargetCtas = kSsmSms * 2;    // the same for the gradient's CTAs
+constexpr int64_t kLeastSegment = 64;           // tokens: below, a carry costs more than it frees
+
+SsmPlan ssm_plan(int64_t batch, int64_t len, int64_t dim, int64_t nstate, int64_t groups, bool grad) {
+    SsmPlan p;
+    p.lanes = 2;
+    while (p.lanes < 32 && 4 * p.lanes < nstate)
+        p.lanes *= 2;
+    const int64_t gdim = dim / groups;
+    const int64_t channels = 128 / p.lanes * (grad ? kSsmWarps : 1);
+    p.ctiles = (gdim + channels - 1) / channels;
+    const int64_t units = batch * groups * p.ctiles;  // warps or CTAs of one segment
+    const int64_t enough = grad ? kTargetCtas / 2 : kEnoughWarps, target = grad ? kTargetCtas : kTargetWarps;
+    p.segments = 1;
+    p.seg_len = len > 0 ? (len + T16 - 1) / T16 * T16 : T16;
+    if (units > 0 && units < enough && len > kLeastSegment) {
+        int64_t s = target / units;
+        const int64_t most = len / kLeastSegment;
+        if (s > most)
+            s = most;
+        if (s > 1) {
+            p.seg_len = ((len + s - 1) / s + T16 - 1) / T16 * T16;
+            p.segments = (len + p.seg_len - 1) / p.seg_len;
+        }
+    }
+    const int64_t cut = p.segments > 1 ? batch * p.segments * dim : 0;
+    p.carry_slots = (cut * nstate + 3) / 4 * 2;
+    p.decay_slots = (cut + 3) / 4 * 2;
+    p.shared_slots = p.param_slots = 0;
+    if (grad) {
+        p.shared_slots = groups * p.ctiles * batch * len * (4 * p.lanes);  // 2 x 4 lanes values of f32
+        p.param_slots = (batch * p.segments * dim * (nstate + 2) + 3) / 4 * 2;
+    }
+    return p;
+}
+
+static bool fits(const void *p, int64_t a, int64_t b, int64_t bytes) {
+    return (uintptr_t)p % bytes == 0 && a % 4 == 0 && b % 4 == 0;
+}
+
+static cudaError_t ssm_any(const mt_ssm_args &p, SsmWhat what, const Launch &L) {
+    SsmArgs a;
+    a.p = p;
+    a.plan = ssm_plan(p.batch, p.len, p.dim, p.nstate, p.groups, what == kSsmGrad);
+    a.ntiles = (p.len + T16 - 1) / T16;
+    a.gdim = p.dim / p.groups;
+    const int64_t v = p.dtype == MT_F32 ? 16 : 8;  // bytes of four values
+    a.cvec = a.gdim % 4 == 0 && fits(p.u, p.u_batch, p.u_token, v) && fits(p.delta, p.delta_batch, p.delta_token, v) &&
+             fits(p.z, p.z_batch, p.z_token, v);
+    if (what == kSsmGrad)
+        a.cvec = a.cvec && fits(p.dout, p.dout_batch, p.dout_token, v) && fits(p.du, p.du_batch, p.du_token, v) &&
+                 fits(p.ddelta, p.ddelta_batch, p.ddelta_token, v) && fits(p.dz, p.dz_batch, p.dz_token, v);
+    else
+        a.cvec = a.cvec && fits(p.out, p.out_batch, p.out_token, v);
+    a.nvec = p.nstate % 4 == 0 && fits(p.A, 0, 0, 16) && fits(p.state, 0, 0, 16) && fits(p.checkpoints, 0, 0, 16) &&
+             fits(p.dfinal, 0, 0, 16) && fits(p.dinit, 0, 0, 16);
+    a.bvec = p.nstate % 4 == 0 && fits(p.B, p.B_batch, p.B_token, v) && fits(p.C, p.C_batch, p.C_token, v);
+    uint64_t *s = static_cast<uint64_t *>(p.scratch);
+    if (s != nullptr) {
+        a.carry = reinterpret_cast<float *>(s);
+        s += a.plan.carry_slots;
+        a.decay = reinterpret_cast<float *>(s);
+        s += a.plan.decay_slots;
+        a.shared = reinterpret_cast<float *>(s);
+        s += a.plan.shared_slots;
+        a.dA_part = reinterpret_cast<float *>(s);
+        a.dD_part = a.dA_part + p.batch * a.plan.segments * p.dim * p.nstate;
+        a.dbias_part = a.dD_part + p.batch * a.plan.segments * p.dim;
+    } else {
+        a.carry = a.decay = a.shared = a.dA_part = a.dD_part = a.dbias_part = nullptr;
+    }
+    switch (p.dtype) {
+    case MT_F32: return ssm_f32(a, what, L);
+    case MT_BF16: return ssm_bf16(a, what, L);
+    case MT_F16: return ssm_f16(a, what, L);
+    default: return cudaErrorInvalidValue;
+    }
+}
+
+cudaError_t ssm_launch(const mt_ssm_args &a, const Launch &L) { return ssm_any(a, kSsmForward, L); }
+cudaError_t ssm_grad_launch(const mt_ssm_args &a, const Launch &L) { return ssm_any(a, kSsmGrad, L); }
+cudaError_t ssm_step_launch(const mt_ssm_args &a, const Launch &L) { return ssm_any(a, kSsmStep, L); }
+
+}  // namespace mt
