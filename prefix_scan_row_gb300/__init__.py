@@ -144,6 +144,8 @@ def _check(code: int, where: str) -> None:
 
 def _stream(stream) -> int:
     if stream is None:
+        if torch.cuda.is_initialized():  # the handle alone: a Stream object costs 3 us of host time a call
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -170,7 +172,7 @@ _NO_ACT = (0, 0, 0)  # an activation that is absent: pointer, batch and token st
 def _act(name, t, shape, dtype):
     """An activation's pointer and its batch and token strides; its innermost
     axis (two for B and C of a scan) must be contiguous."""
-    if t.dtype != dtype or tuple(t.shape) != shape:
+    if t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)} of {dtype}, not {list(t.shape)} of {t.dtype}")
     s = t.stride()
     if s[-1] != 1 and shape[-1] > 1:
@@ -182,7 +184,7 @@ def _act(name, t, shape, dtype):
 
 def _act_step(name, t, shape, dtype):
     """The same of one token a sequence: the token stride does not count."""
-    if t.dtype != dtype or tuple(t.shape) != shape:
+    if t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)} of {dtype}, not {list(t.shape)} of {t.dtype}")
     s = t.stride()
     if s[-1] != 1 and shape[-1] > 1:
@@ -196,7 +198,7 @@ def _flat(name, t, shape, dtype):
     """The pointer of a contiguous tensor; 0 for None."""
     if t is None:
         return 0
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous {list(shape)} of {dtype}, not {list(t.shape)} of {t.dtype}")
     return t.data_ptr()
 

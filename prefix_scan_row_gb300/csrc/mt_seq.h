@@ -29,11 +29,11 @@ cudaError_t conv_step_launch(const mt_conv_args &a, const Launch &L);
 cudaError_t conv_grad_launch(const mt_conv_args &a, const Launch &L);
 
 // ---- selective state space scan (mt_ssm*.cu) -----------------------------------
-constexpr int kSsmTile = 16;  // tokens per tile, and per checkpoint
+constexpr int kSsmTile = 8;  // tokens per checkpoint
 struct SsmPlan {
     int lanes;         // lanes that share a channel's states, four states each
     int64_t segments;  // pieces of the token axis that run side by side
-    int64_t seg_len;   // tokens per segment, a multiple of kSsmTile
+    int64_t seg_len;   // tokens per segment, a multiple of 16
     int64_t ctiles;    // channel tiles per group (forward: of a warp; gradient: of a CTA)
     int64_t carry_slots, decay_slots, shared_slots, param_slots;  // 8-byte slots of the scratch's parts
 };

@@ -8,9 +8,15 @@ namespace mt {
 // recurrences, so a few warps a scheduler suffice. The plan must not ask the
 // device (scratch is sized on the host), so it counts GB300's 152 SMs.
 constexpr int64_t kSsmSms = 152;
-constexpr int64_t kEnoughWarps = kSsmSms * 6;   // from here on the tokens are not cut
-constexpr int64_t kTargetWarps = kSsmSms * 16;  // what a cut aims at
-constexpr int64_t kTargetCtas = kSsmSms * 2;    // the same for the gradient's CTAs
+constexpr int64_t kEnoughWarps = kSsmSms * 5;   // from here on the tokens are not cut
+#ifndef MT_XT
+#define MT_XT 24
+#endif
+constexpr int64_t kTargetWarps = kSsmSms * MT_XT;  // what a cut aims at
+#ifndef MT_XGT
+#define MT_XGT 6
+#endif
+constexpr int64_t kTargetCtas = kSsmSms * MT_XGT;    // the same for the gradient's CTAs
 constexpr int64_t kLeastSegment = 64;           // tokens: below, a carry costs more than it frees
 
 SsmPlan ssm_plan(int64_t batch, int64_t len, int64_t dim, int64_t nstate, int64_t groups, bool grad) {
@@ -19,19 +25,20 @@ SsmPlan ssm_plan(int64_t batch, int64_t len, int64_t dim, int64_t nstate, int64_
     while (p.lanes < 32 && 4 * p.lanes < nstate)
         p.lanes *= 2;
     const int64_t gdim = dim / groups;
-    const int64_t channels = 128 / p.lanes * (grad ? kSsmWarps : 1);
+    // gradient: a CTA's channels; forward: a warp's, 64 until more than 16 states share them out
+    const int64_t channels = grad ? 128 / p.lanes * kSsmWarps : nstate <= 16 ? 64 : nstate <= 32 ? 32 : nstate <= 64 ? 16 : 8;
     p.ctiles = (gdim + channels - 1) / channels;
     const int64_t units = batch * groups * p.ctiles;  // warps or CTAs of one segment
-    const int64_t enough = grad ? kTargetCtas / 2 : kEnoughWarps, target = grad ? kTargetCtas : kTargetWarps;
+    const int64_t enough = grad ? kSsmSms * 3 : kEnoughWarps, target = grad ? kTargetCtas : kTargetWarps;
     p.segments = 1;
-    p.seg_len = len > 0 ? (len + T16 - 1) / T16 * T16 : T16;
+    p.seg_len = len > 0 ? (len + 15) / 16 * 16 : 16;
     if (units > 0 && units < enough && len > kLeastSegment) {
         int64_t s = target / units;
         const int64_t most = len / kLeastSegment;
         if (s > most)
             s = most;
         if (s > 1) {
-            p.seg_len = ((len + s - 1) / s + T16 - 1) / T16 * T16;
+            p.seg_len = ((len + s - 1) / s + 15) / 16 * 16;
             p.segments = (len + p.seg_len - 1) / p.seg_len;
         }
     }
@@ -46,24 +53,29 @@ SsmPlan ssm_plan(int64_t batch, int64_t len, int64_t dim, int64_t nstate, int64_
     return p;
 }
 
-static bool fits(const void *p, int64_t a, int64_t b, int64_t bytes) {
-    return (uintptr_t)p % bytes == 0 && a % 4 == 0 && b % 4 == 0;
+static bool fits(const void *p, int64_t a, int64_t b, int64_t bytes, int64_t values = 4) {
+    return (uintptr_t)p % bytes == 0 && a % values == 0 && b % values == 0;
+}
+// whether `values` neighbouring channels of every tensor of the call can be moved as one
+static bool channels_fit(const mt_ssm_args &p, bool grad, int64_t gdim, int64_t values) {
+    const int64_t v = values * (p.dtype == MT_F32 ? 4 : 2);
+    const bool in = gdim % values == 0 && fits(p.u, p.u_batch, p.u_token, v, values) &&
+                    fits(p.delta, p.delta_batch, p.delta_token, v, values) && fits(p.z, p.z_batch, p.z_token, v, values);
+    if (!grad)
+        return in && fits(p.out, p.out_batch, p.out_token, v, values);
+    return in && fits(p.dout, p.dout_batch, p.dout_token, v, values) && fits(p.du, p.du_batch, p.du_token, v, values) &&
+           fits(p.ddelta, p.ddelta_batch, p.ddelta_token, v, values) && fits(p.dz, p.dz_batch, p.dz_token, v, values);
 }
 
 static cudaError_t ssm_any(const mt_ssm_args &p, SsmWhat what, const Launch &L) {
     SsmArgs a;
     a.p = p;
     a.plan = ssm_plan(p.batch, p.len, p.dim, p.nstate, p.groups, what == kSsmGrad);
-    a.ntiles = (p.len + T16 - 1) / T16;
+    a.ntiles = (p.len + kSsmTile - 1) / kSsmTile;
     a.gdim = p.dim / p.groups;
     const int64_t v = p.dtype == MT_F32 ? 16 : 8;  // bytes of four values
-    a.cvec = a.gdim % 4 == 0 && fits(p.u, p.u_batch, p.u_token, v) && fits(p.delta, p.delta_batch, p.delta_token, v) &&
-             fits(p.z, p.z_batch, p.z_token, v);
-    if (what == kSsmGrad)
-        a.cvec = a.cvec && fits(p.dout, p.dout_batch, p.dout_token, v) && fits(p.du, p.du_batch, p.du_token, v) &&
-                 fits(p.ddelta, p.ddelta_batch, p.ddelta_token, v) && fits(p.dz, p.dz_batch, p.dz_token, v);
-    else
-        a.cvec = a.cvec && fits(p.out, p.out_batch, p.out_token, v);
+    a.cvec = channels_fit(p, what == kSsmGrad, a.gdim, 4);
+    a.v16 = channels_fit(p, what == kSsmGrad, a.gdim, p.dtype == MT_F32 ? 4 : 8);
     a.nvec = p.nstate % 4 == 0 && fits(p.A, 0, 0, 16) && fits(p.state, 0, 0, 16) && fits(p.checkpoints, 0, 0, 16) &&
              fits(p.dfinal, 0, 0, 16) && fits(p.dinit, 0, 0, 16);
     a.bvec = p.nstate % 4 == 0 && fits(p.B, p.B_batch, p.B_token, v) && fits(p.C, p.C_batch, p.C_token, v);

@@ -1,5 +1,5 @@
 // mt_ssm_f32.cu -- the selective state space scan's kernels for f32 activations.
-#include "mt_ssm.cuh"
+#include "mt_ssm_launch.cuh"
 
 namespace mt {
 
