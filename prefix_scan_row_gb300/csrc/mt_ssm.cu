@@ -14,7 +14,7 @@ constexpr int64_t kEnoughWarps = kSsmSms * 5;   // from here on the tokens are n
 #endif
 constexpr int64_t kTargetWarps = kSsmSms * MT_XT;  // what a cut aims at
 #ifndef MT_XGT
-#define MT_XGT 6
+#define MT_XGT 9
 #endif
 constexpr int64_t kTargetCtas = kSsmSms * MT_XGT;    // the same for the gradient's CTAs
 constexpr int64_t kLeastSegment = 64;           // tokens: below, a carry costs more than it frees
@@ -67,19 +67,19 @@ static bool channels_fit(const mt_ssm_args &p, bool grad, int64_t gdim, int64_t 
            fits(p.ddelta, p.ddelta_batch, p.ddelta_token, v, values) && fits(p.dz, p.dz_batch, p.dz_token, v, values);
 }
 
-static cudaError_t ssm_any(const mt_ssm_args &p, SsmWhat what, const Launch &L) {
+// The kernels' arguments of a call: what its plan and its addresses allow.
+static SsmArgs ssm_args(const mt_ssm_args &p, bool grad) {
     SsmArgs a;
     a.p = p;
-    a.plan = ssm_plan(p.batch, p.len, p.dim, p.nstate, p.groups, what == kSsmGrad);
+    a.plan = ssm_plan(p.batch, p.len, p.dim, p.nstate, p.groups, grad);
     a.ntiles = (p.len + kSsmTile - 1) / kSsmTile;
     a.gdim = p.dim / p.groups;
     const int64_t v = p.dtype == MT_F32 ? 16 : 8;  // bytes of four values
-    a.cvec = channels_fit(p, what == kSsmGrad, a.gdim, 4);
-    a.v16 = channels_fit(p, what == kSsmGrad, a.gdim, p.dtype == MT_F32 ? 4 : 8);
-    a.nvec = p.nstate % 4 == 0 && fits(p.A, 0, 0, 16) && fits(p.state, 0, 0, 16) && fits(p.checkpoints, 0, 0, 16) &&
-             fits(p.dfinal, 0, 0, 16) && fits(p.dinit, 0, 0, 16);
-    a.bvec = p.nstate % 4 == 0 && fits(p.B, p.B_batch, p.B_token, v) && fits(p.C, p.C_batch, p.C_token, v);
+    a.aligned = channels_fit(p, grad, a.gdim, p.dtype == MT_F32 ? 4 : 8) && p.nstate % 4 == 0 && fits(p.A, 0, 0, 16) &&
+                fits(p.state, 0, 0, 16) && fits(p.checkpoints, 0, 0, 16) && fits(p.dfinal, 0, 0, 16) && fits(p.dinit, 0, 0, 16) &&
+                fits(p.B, p.B_batch, p.B_token, v) && fits(p.C, p.C_batch, p.C_token, v);
     uint64_t *s = static_cast<uint64_t *>(p.scratch);
+    a.carry = a.decay = a.shared = a.dA_part = a.dD_part = a.dbias_part = nullptr;
     if (s != nullptr) {
         a.carry = reinterpret_cast<float *>(s);
         s += a.plan.carry_slots;
@@ -90,19 +90,35 @@ static cudaError_t ssm_any(const mt_ssm_args &p, SsmWhat what, const Launch &L) 
         a.dA_part = reinterpret_cast<float *>(s);
         a.dD_part = a.dA_part + p.batch * a.plan.segments * p.dim * p.nstate;
         a.dbias_part = a.dD_part + p.batch * a.plan.segments * p.dim;
-    } else {
-        a.carry = a.decay = a.shared = a.dA_part = a.dD_part = a.dbias_part = nullptr;
     }
-    switch (p.dtype) {
-    case MT_F32: return ssm_f32(a, what, L);
-    case MT_BF16: return ssm_bf16(a, what, L);
-    case MT_F16: return ssm_f16(a, what, L);
-    default: return cudaErrorInvalidValue;
-    }
+    return a;
 }
 
-cudaError_t ssm_launch(const mt_ssm_args &a, const Launch &L) { return ssm_any(a, kSsmForward, L); }
-cudaError_t ssm_grad_launch(const mt_ssm_args &a, const Launch &L) { return ssm_any(a, kSsmGrad, L); }
-cudaError_t ssm_step_launch(const mt_ssm_args &a, const Launch &L) { return ssm_any(a, kSsmStep, L); }
+#define MT_BY_TYPE(f)                          \
+    switch (p.dtype) {                         \
+    case MT_F32: return f##_f32(a, L);         \
+    case MT_BF16: return f##_bf16(a, L);       \
+    case MT_F16: return f##_f16(a, L);         \
+    default: return cudaErrorInvalidValue;     \
+    }
+cudaError_t ssm_launch(const mt_ssm_args &p, const Launch &L) {
+    const SsmArgs a = ssm_args(p, false);
+    MT_BY_TYPE(ssm_prompt)
+}
+cudaError_t ssm_step_launch(const mt_ssm_args &p, const Launch &L) {
+    const SsmArgs a = ssm_args(p, false);
+    MT_BY_TYPE(ssm_step)
+}
+static cudaError_t carries(const mt_ssm_args &p, const SsmArgs &a, const Launch &L) { MT_BY_TYPE(ssm_adjoint_carries) }
+cudaError_t ssm_grad_launch(const mt_ssm_args &p, const Launch &L) {
+    const SsmArgs a = ssm_args(p, true);
+    if (a.plan.segments > 1) {
+        const cudaError_t e = carries(p, a, L);
+        if (e != cudaSuccess)
+            return e;
+    }
+    MT_BY_TYPE(ssm_grad)
+}
+#undef MT_BY_TYPE
 
 }  // namespace mt

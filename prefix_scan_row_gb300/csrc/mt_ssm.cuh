@@ -46,7 +46,7 @@ struct SsmArgs {
     SsmPlan plan;
     int64_t ntiles;  // of the whole token axis
     int64_t gdim;    // channels per group
-    int cvec, v16, nvec, bvec;  // 4 channels, 16 bytes of them, 4 states, 4 values of B and C may be moved as a vector
+    int aligned;  // 16 bytes of channels, 4 states, and 4 values of B and C, may be moved as one
     float *carry, *decay, *shared, *dA_part, *dD_part, *dbias_part;
 };
 
@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(256) k_ssm_step(const __grid_constant__ SsmArg
         float *sp = a.p.state + (slot * a.p.dim + ch) * N + n0;
         const float *ap = a.p.A + ch * N + n0;
         float h[4] = {0.0f, 0.0f, 0.0f, 0.0f}, A[4] = {0.0f, 0.0f, 0.0f, 0.0f}, bb[4], cc[4];
-        if (a.nvec && live == 4) {
+        if (a.aligned && live == 4) {
             lds4(sp, h);
             lds4(ap, A);
         } else {
@@ -229,8 +229,8 @@ __global__ void __launch_bounds__(256) k_ssm_step(const __grid_constant__ SsmArg
                 }
         }
         Raw4<S> rb, rc;
-        rb.load(static_cast<const S *>(a.p.B) + b * a.p.B_batch + g * N + n0, a.bvec, live);
-        rc.load(static_cast<const S *>(a.p.C) + b * a.p.C_batch + g * N + n0, a.bvec, live);
+        rb.load(static_cast<const S *>(a.p.B) + b * a.p.B_batch + g * N + n0, a.aligned, live);
+        rc.load(static_cast<const S *>(a.p.C) + b * a.p.C_batch + g * N + n0, a.aligned, live);
         rb.widen(bb);
         rc.widen(cc);
         if (a.p.delta_bias != nullptr)
@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(256) k_ssm_step(const __grid_constant__ SsmArg
             h[k] = fmaf(ex2f(d * (A[k] * kLog2e)), h[k], d * u * bb[k]);
             y = fmaf(cc[k], h[k], y);
         }
-        if (a.nvec && live == 4)
+        if (a.aligned && live == 4)
             *reinterpret_cast<float4 *>(sp) = make_float4(h[0], h[1], h[2], h[3]);
         else
 #pragma unroll
@@ -266,9 +266,33 @@ __global__ void __launch_bounds__(256) k_ssm_step(const __grid_constant__ SsmArg
     }
 }
 
-enum SsmWhat { kSsmForward, kSsmGrad, kSsmStep };
-cudaError_t ssm_f32(const SsmArgs &a, SsmWhat what, const Launch &L);   // mt_ssm_f32.cu
-cudaError_t ssm_bf16(const SsmArgs &a, SsmWhat what, const Launch &L);  // mt_ssm_bf16.cu
-cudaError_t ssm_f16(const SsmArgs &a, SsmWhat what, const Launch &L);   // mt_ssm_f16.cu
+template <class S, int P> static cudaError_t step_go(const SsmArgs &a, const Launch &L) {
+    const int64_t grid = (a.p.batch * a.p.dim * P + 255) / 256;
+    if (grid > INT32_MAX)
+        return cudaErrorInvalidValue;
+    note_launch();
+    return launch_pdl(k_ssm_step<S, P>, (unsigned)grid, 256, 0, L.stream, a);
+}
+template <class S> static cudaError_t step_states(const SsmArgs &a, const Launch &L) {
+    switch (a.plan.lanes) {
+    case 2: return step_go<S, 2>(a, L);
+    case 4: return step_go<S, 4>(a, L);
+    case 8: return step_go<S, 8>(a, L);
+    case 16: return step_go<S, 16>(a, L);
+    case 32: return step_go<S, 32>(a, L);
+    default: return cudaErrorInvalidValue;
+    }
+}
+
+// One translation unit per kernel family and activation type (mt_ssm_*.cu).
+#define MT_SSM_LAUNCHES(t)                                                                                    \
+    cudaError_t ssm_prompt_##t(const SsmArgs &a, const Launch &L);                                            \
+    cudaError_t ssm_adjoint_carries_##t(const SsmArgs &a, const Launch &L);                                   \
+    cudaError_t ssm_grad_##t(const SsmArgs &a, const Launch &L);                                              \
+    cudaError_t ssm_step_##t(const SsmArgs &a, const Launch &L);
+MT_SSM_LAUNCHES(f32)
+MT_SSM_LAUNCHES(bf16)
+MT_SSM_LAUNCHES(f16)
+#undef MT_SSM_LAUNCHES
 
 }  // namespace mt

@@ -108,7 +108,7 @@ template <class S, int P> struct GradSmem {
     static constexpr int kBytes = kSsmWarps * kWarp + kShared;
 };
 
-template <class S, int P>
+template <class S, int P, bool ALN>
 __global__ void __launch_bounds__(kSsmThreads, sizeof(S) == 2 && P <= 8 ? MT_XG : 2) k_ssm_grad(const __grid_constant__ SsmArgs a) {
     extern __shared__ float4 smem4[];
     using M = GradSmem<S, P>;
@@ -145,13 +145,13 @@ __global__ void __launch_bounds__(kSsmThreads, sizeof(S) == 2 && P <= 8 ? MT_XG 
     const int64_t stop = begin + a.plan.seg_len < a.p.len ? begin + a.plan.seg_len : a.p.len;
     const int64_t end = n < stop ? n : stop;
     Pairs A, r, dA;
-    A.load(a.p.A + at.ch * N, N, at.n0, at.cl, a.nvec, kLog2e);
+    A.load(a.p.A + at.ch * N, N, at.n0, at.cl, ALN, kLog2e);
     dA.zero();
     r.zero();
     if (SEG > 1)
-        r.load(a.carry + ((at.b * SEG + at.s) * a.p.dim + at.ch) * N, N, at.n0, at.cl, a.nvec);
+        r.load(a.carry + ((at.b * SEG + at.s) * a.p.dim + at.ch) * N, N, at.n0, at.cl, ALN);
     else if (a.p.dfinal != nullptr)
-        r.load(a.p.dfinal + (at.b * a.p.dim + at.ch) * N, N, at.n0, at.cl, a.nvec);
+        r.load(a.p.dfinal + (at.b * a.p.dim + at.ch) * N, N, at.n0, at.cl, ALN);
     // the elementwise parts: a lane has a channel pair, and every kTok-th token
     constexpr int kPairs = CW / 2 < 32 ? CW / 2 : 32, kTok = 32 / kPairs;
     const int ec = lane % kPairs * 2, et = lane / kPairs;
@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kSsmThreads, sizeof(S) == 2 && P <= 8 ? MT_XG 
         const uint32_t to = smem_addr(stages) + (k & 1) * M::kStage;
         const S *dp = static_cast<const S *>(a.p.delta) + at.b * a.p.delta_batch, *up = static_cast<const S *>(a.p.u) + at.b * a.p.u_batch;
         const S *gp = static_cast<const S *>(a.p.dout) + at.b * a.p.dout_batch, *zp = static_cast<const S *>(a.p.z) + at.b * a.p.z_batch;
-        if (a.v16) {
+        if (ALN) {
             R::fetch16(to, dp + tl * a.p.delta_token + cs, a.p.delta_token, left, in, lane);
             R::fetch16(to + R::kBytes, up + tl * a.p.u_token + cs, a.p.u_token, left, in, lane);
             R::fetch16(to + 2 * R::kBytes, gp + tl * a.p.dout_token + cs, a.p.dout_token, left, in, lane);
@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kSsmThreads, sizeof(S) == 2 && P <= 8 ? MT_XG 
         }
         if (warp < 2) {  // warp 0 brings B, warp 1 C
             const uint32_t ks = smem_addr(kept) + ((k & 1) * 2 + warp) * St::kBytes;
-            St::fetch(ks, warp == 0 ? bp : cp, warp == 0 ? a.p.B_token : a.p.C_token, t0, left, (int)N, lane, a.bvec);
+            St::fetch(ks, warp == 0 ? bp : cp, warp == 0 ? a.p.B_token : a.p.C_token, t0, left, (int)N, lane, ALN);
         }
         cp_async_commit();
     };
@@ -198,12 +198,13 @@ __global__ void __launch_bounds__(kSsmThreads, sizeof(S) == 2 && P <= 8 ? MT_XG 
         const int left = end - t0 < kStep ? (int)(end - t0) : kStep;
         if (warp < 2)
             St::widen(wide + ((k & 1) * 2 + warp) * (kStep * NP), kept + ((k & 1) * 2 + warp) * St::kBytes, warp == 0 ? bp : cp,
-                      warp == 0 ? a.p.B_token : a.p.C_token, t0, left, (int)N, lane, a.bvec);
+                      warp == 0 ? a.p.B_token : a.p.C_token, t0, left, (int)N, lane, ALN);
     };
     if (tiles > 0) {
         fetch(tiles - 1);
         cp_async_wait_all();
-        widen(tiles - 1);  // each lane widens what it copied
+        __syncwarp();
+        widen(tiles - 1);  // a warp widens what it copied
         __syncthreads();
     }
     for (int k = tiles - 1; k >= 0; --k) {
@@ -213,7 +214,7 @@ __global__ void __launch_bounds__(kSsmThreads, sizeof(S) == 2 && P <= 8 ? MT_XG 
         const float *sb = wide + (k & 1) * (2 * kStep * NP), *sc = sb + kStep * NP;
         if (k > 0)
             fetch(k - 1);
-        if (!a.v16) {
+        if (!ALN) {
             const S *dp = static_cast<const S *>(a.p.delta) + at.b * a.p.delta_batch, *up = static_cast<const S *>(a.p.u) + at.b * a.p.u_batch;
             const S *gp = static_cast<const S *>(a.p.dout) + at.b * a.p.dout_batch, *zp = static_cast<const S *>(a.p.z) + at.b * a.p.z_batch;
             R::settle(raw, dp + cb, a.p.delta_token, t0, left, channels, lane);
@@ -226,7 +227,7 @@ __global__ void __launch_bounds__(kSsmThreads, sizeof(S) == 2 && P <= 8 ? MT_XG 
         if (left < kStep)
             R::no_steps(raw, left, lane, softplus);
         Pairs h;
-        h.load(a.p.checkpoints + ((at.b * a.ntiles + t0 / kStep) * a.p.dim + at.ch) * N, N, at.n0, at.cl, a.nvec);
+        h.load(a.p.checkpoints + ((at.b * a.ntiles + t0 / kStep) * a.p.dim + at.ch) * N, N, at.n0, at.cl, ALN);
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < (kStep + kTok - 1) / kTok; ++i) {
@@ -379,7 +380,7 @@ __global__ void __launch_bounds__(kSsmThreads, sizeof(S) == 2 && P <= 8 ? MT_XG 
             const int64_t tl = t0 + R::token(lane);
             S *odu = static_cast<S *>(a.p.du) + at.b * a.p.du_batch, *odd = static_cast<S *>(a.p.ddelta) + at.b * a.p.ddelta_batch;
             S *odz = static_cast<S *>(a.p.dz) + at.b * a.p.dz_batch;
-            if (a.v16) {
+            if (ALN) {
                 R::put16(raw, odd + tl * a.p.ddelta_token + cs, a.p.ddelta_token, left, in, lane);
                 R::put16(raw + R::kBytes, odu + tl * a.p.du_token + cs, a.p.du_token, left, in, lane);
                 if (gated)
@@ -401,9 +402,9 @@ __global__ void __launch_bounds__(kSsmThreads, sizeof(S) == 2 && P <= 8 ? MT_XG 
                 Codec<S>::store1(static_cast<S *>(a.p.dz) + at.b * a.p.dz_batch + t * a.p.dz_token + cb + c, 0.0f);
         }
     if (at.s == 0 && a.p.dinit != nullptr)
-        r.store(a.p.dinit + (at.b * a.p.dim + at.ch) * N, N, at.n0, at.cl, a.nvec);
+        r.store(a.p.dinit + (at.b * a.p.dim + at.ch) * N, N, at.n0, at.cl, ALN);
     const int64_t part = at.b * SEG + at.s;
-    dA.store(a.dA_part + (part * a.p.dim + at.ch) * N, N, at.n0, at.cl, a.nvec);
+    dA.store(a.dA_part + (part * a.p.dim + at.ch) * N, N, at.n0, at.cl, ALN);
     float v[4];
     unpack2f(dskip, v[0], v[1]);
     unpack2f(dbias, v[2], v[3]);
@@ -466,6 +467,41 @@ __global__ void __launch_bounds__(256) k_ssm_grad_join(const __grid_constant__ S
                 a.p.ddelta_bias[j] = w;
         }
     }
+}
+
+// ---- launches ------------------------------------------------------------------------------
+template <class S, int P, bool ALN> static cudaError_t grad_go(const SsmArgs &a, const Launch &L) {
+    const int64_t grid = a.p.batch * a.p.groups * a.plan.ctiles * a.plan.segments;
+    if (grid > INT32_MAX)
+        return cudaErrorInvalidValue;
+    if (grid > 0) {
+        const size_t smem = GradSmem<S, P>::kBytes;
+        cudaError_t e = ssm_smem(k_ssm_grad<S, P, ALN>, smem);
+        if (e != cudaSuccess)
+            return e;
+        note_launch();
+        if ((e = launch_pdl(k_ssm_grad<S, P, ALN>, (unsigned)grid, kSsmThreads, smem, L.stream, a)) != cudaSuccess)
+            return e;
+    }
+    const int64_t items = a.p.batch * a.p.len * a.p.groups * 2 * a.p.nstate + a.p.dim * a.p.nstate + a.p.dim;
+    int64_t jgrid = (items + 255) / 256;
+    if (jgrid > 16 * (int64_t)L.sm_count)
+        jgrid = 16 * (int64_t)L.sm_count;
+    note_launch();
+    return launch_pdl(k_ssm_grad_join<S>, (unsigned)jgrid, 256, 0, L.stream, a, 4 * P);
+}
+template <class S> static cudaError_t grad_states(const SsmArgs &a, const Launch &L) {
+#define MT_LANES(P) \
+    case P: return a.aligned ? grad_go<S, P, true>(a, L) : grad_go<S, P, false>(a, L)
+    switch (a.plan.lanes) {
+        MT_LANES(2);
+        MT_LANES(4);
+        MT_LANES(8);
+        MT_LANES(16);
+        MT_LANES(32);
+    default: return cudaErrorInvalidValue;
+    }
+#undef MT_LANES
 }
 
 }  // namespace mt

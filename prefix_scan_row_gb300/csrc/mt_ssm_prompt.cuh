@@ -43,6 +43,29 @@ template <int BYTES> __device__ __forceinline__ void cp_async_zfill(uint32_t dst
         asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" :: "r"(dst), "l"(src), "r"(in ? BYTES : 0), "n"(BYTES) : "memory");
 }
 
+// ROWS rows of up to `values` <= MOST values each, by 32-bit words: the words that a row's
+// live values touch, to dst + row * pitch (16-bit values that start in the middle of a word stay
+// there, half a word in). f32 rows are whole words, with zeros where there is nothing.
+template <class S, int ROWS, int MOST>
+__device__ __forceinline__ void copy_words(uint32_t dst, int pitch, const S *base, int64_t stride, int64_t t0, int left, int values,
+                                           int lane) {
+    constexpr int kWords = sizeof(S) == 4 ? MOST : MOST / 2 + 1;
+#pragma unroll
+    for (int i = 0; i < (ROWS * kWords + 31) / 32; ++i) {
+        const int t = (32 * i + lane) / kWords, w = (32 * i + lane) % kWords;
+        const S *row = base + (t0 + t) * stride;
+        if constexpr (sizeof(S) == 4) {
+            const bool in = t < left && w < values;
+            if (t < ROWS)
+                cp_async_zfill<4>(dst + t * pitch + 4 * w, in ? row + w : base, in);
+        } else {
+            const uintptr_t at = (uintptr_t)row, from = at & ~(uintptr_t)3;
+            if (t < left && values > 0 && from + 4 * w < at + 2 * values)
+                cp_async_zfill<4>(dst + t * pitch + 4 * w, (const void *)(from + 4 * w), true);
+        }
+    }
+}
+
 // A warp's CW channels of kStep tokens in shared memory, in storage form and
 // aligned, zeros where there is nothing. Rows whose channels start on a 16-byte
 // boundary are copied in 16-byte pieces. Any other row (odd sizes and offsets) is copied as
@@ -70,32 +93,32 @@ template <class S, int CW> struct Rows8 {
     }
     static __device__ __forceinline__ void fetch_words(uint32_t dst, const S *base, int64_t stride, int64_t t0, int left, int channels,
                                                        int lane) {
-#pragma unroll 1
-        for (int t = 0; t < kStep && t < left && channels > 0; ++t) {
-            const uintptr_t at = (uintptr_t)(base + (t0 + t) * stride), from = at & ~(uintptr_t)3;
-            const int words = (int)((at + channels * sizeof(S) - from + 3) / 4);
-            for (int w = lane; w < words; w += 32)
-                cp_async_zfill<4>(dst + t * kPitch + 4 * w, (const void *)(from + 4 * w), true);
-        }
+        copy_words<S, kStep, CW>(dst, kPitch, base, stride, t0, left, channels, lane);
     }
-    // rows that fetch copied by words; the caller syncs the warp before and after
+    // rows that fetch_words copied; the caller syncs the warp before and after
     static __device__ __forceinline__ void settle(char *rows, const S *base, int64_t stride, int64_t t0, int left, int channels,
                                                   int lane) {
+        if constexpr (sizeof(S) == 4)
+            return;  // whole words, and zeros where there is nothing
         constexpr int kLanes = CW / 2 < 32 ? CW / 2 : 32, kTok = 32 / kLanes;  // a lane a channel pair, kTok tokens together
+        constexpr int kEach = (kStep + kTok - 1) / kTok;
         const int c = lane % kLanes * 2;
-#pragma unroll 1
-        for (int first = 0; first < kStep; first += kTok) {  // the same for all lanes, so that they sync together
-            const int t = first + lane / kLanes;
-            const bool in = t < left;
-            char *row = rows + (t < kStep ? t : 0) * kPitch;
-            const S *p = reinterpret_cast<const S *>(row + ((uintptr_t)(base + (t0 + t) * stride) & 3u)) + c;
-            S v[2];
-            v[0] = in && c < channels ? p[0] : S(0.0f);
-            v[1] = in && c + 1 < channels ? p[1] : S(0.0f);
-            __syncwarp();
+        S v[kEach][2];
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int t = lane / kLanes + i * kTok;
+            const S *p = reinterpret_cast<const S *>(rows + (t < kStep ? t : 0) * kPitch + ((uintptr_t)(base + (t0 + t) * stride) & 3u)) + c;
+            v[i][0] = t < left && c < channels ? p[0] : S(0.0f);
+            v[i][1] = t < left && c + 1 < channels ? p[1] : S(0.0f);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int t = lane / kLanes + i * kTok;
             if (t < kStep) {
-                reinterpret_cast<S *>(row)[c] = v[0];
-                reinterpret_cast<S *>(row)[c + 1] = v[1];
+                S *to = reinterpret_cast<S *>(rows + t * kPitch) + c;
+                to[0] = v[i][0];
+                to[1] = v[i][1];
             }
         }
     }
@@ -138,10 +161,12 @@ template <class S, int CW> struct Rows8 {
     }
     static __device__ __forceinline__ void put_each(const char *rows, S *base, int64_t stride, int64_t t0, int left, int channels,
                                                     int lane) {
-#pragma unroll 1
-        for (int t = 0; t < left; ++t)
-            for (int c = lane; c < channels; c += 32)
+#pragma unroll
+        for (int i = 0; i < (kStep * CW + 31) / 32; ++i) {
+            const int t = (32 * i + lane) / CW, c = (32 * i + lane) % CW;
+            if (t < left && c < channels)
                 base[(t0 + t) * stride + c] = reinterpret_cast<const S *>(rows + t * kPitch)[c];
+        }
     }
 };
 
@@ -226,19 +251,22 @@ template <int K, int P> struct PromptPlace {
     }
 };
 
-// B or C of kStep tokens: copied in storage form where four states fit a vector
-// (each lane widens what it copied itself), else loaded when they are widened.
+// B or C of kStep tokens: copied in storage form (in vectors of four states,
+// which each lane widens itself, or by words), then widened to f32.
 template <class S, int NP> struct States8 {
     static constexpr int kVecs = kStep * NP / 4, kPer = (kVecs + 31) / 32;
-    static constexpr int kBytes = kStep * NP * (int)sizeof(S);
+    static constexpr int kPitch = NP * (int)sizeof(S) + 8;  // of a token copied by words
+    static constexpr int kBytes = (kStep * kPitch + 15) / 16 * 16;
     static __device__ __forceinline__ int live(int left, int t, int s, int nstate) {
         const int n = t < left ? nstate - s : 0;
         return n <= 0 ? 0 : n > 4 ? 4 : n;
     }
     static __device__ __forceinline__ void fetch(uint32_t dst, const S *base, int64_t stride, int64_t t0, int left, int nstate,
                                                  int lane, bool vec) {
-        if (!vec)
+        if (!vec) {
+            copy_words<S, kStep, NP>(dst, kPitch, base, stride, t0, left, nstate, lane);
             return;
+        }
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int v = 32 * i + lane, t = v / (NP / 4), s = v % (NP / 4) * 4;
@@ -247,6 +275,7 @@ template <class S, int NP> struct States8 {
                 cp_async_zfill<4 * sizeof(S)>(dst + v * 4 * (int)sizeof(S), in ? base + (t0 + t) * stride + s : base, in);
         }
     }
+    // after the copies have arrived: a warp's, and its lanes are in step, unless vec
     static __device__ __forceinline__ void widen(float *to, const char *raw, const S *base, int64_t stride, int64_t t0, int left,
                                                  int nstate, int lane, bool vec) {
 #pragma unroll
@@ -254,10 +283,12 @@ template <class S, int NP> struct States8 {
             const int v = 32 * i + lane, t = v / (NP / 4), s = v % (NP / 4) * 4;
             if (v < kVecs) {
                 Raw4<S> w;
-                if (vec)
+                if (vec) {
                     w.load(reinterpret_cast<const S *>(raw) + 4 * v, true, 4);
-                else
-                    w.load(base + (t0 + t) * stride + s, false, live(left, t, s, nstate));
+                } else {
+                    const int skip = sizeof(S) == 4 ? 0 : (int)((uintptr_t)(base + (t0 + t) * stride) & 3u);
+                    w.load(reinterpret_cast<const S *>(raw + t * kPitch + skip) + s, false, live(left, t, s, nstate));
+                }
                 float x[4];
                 w.widen(x);
                 *reinterpret_cast<float4 *>(to + 4 * v) = make_float4(x[0], x[1], x[2], x[3]);
@@ -286,7 +317,7 @@ __device__ __forceinline__ f32x2 pair_of(const float *p, int64_t ch, int cl) {
 // Forward: the state that a segment leaves from zero (segment 0: from the
 // first state). REV: the same of the adjoint, r = a (r + C g) from the last token
 // down. One exponential and three multiply-adds a pair; no output.
-template <class S, int K, int P, bool REV>
+template <class S, int K, int P, bool REV, bool ALN>
 __global__ void __launch_bounds__(kSsmThreads, MT_XC) k_ssm_carry(const __grid_constant__ SsmArgs a, int64_t warps) {
     using Q = PromptPlace<K, P>;
     using M = PromptSmem<S, K, P, 1>;
@@ -307,16 +338,16 @@ __global__ void __launch_bounds__(kSsmThreads, MT_XC) k_ssm_carry(const __grid_c
     const int64_t begin = at.s * a.plan.seg_len;
     const int64_t end = begin + a.plan.seg_len < n ? begin + a.plan.seg_len : n;
     Rows<K> A, h;
-    A.load(a.p.A + at.ch * N, N, at.n0, at.cl, a.nvec, kLog2e);
+    A.load(a.p.A + at.ch * N, N, at.n0, at.cl, ALN, kLog2e);
     h.zero();
     if (!REV && at.s == 0) {
         const int64_t slot = ssm_slot(a, at.b);
         if (a.p.carry_in && a.p.state != nullptr && slot >= 0)
-            h.load(a.p.state + (slot * a.p.dim + at.ch) * N, N, at.n0, at.cl, a.nvec);
+            h.load(a.p.state + (slot * a.p.dim + at.ch) * N, N, at.n0, at.cl, ALN);
         // the state is written by the next launch's last segment while its first
         // one starts: that one reads this copy, in the place of the last carry
         const int64_t spare = (at.b * a.plan.segments + a.plan.segments - 1) * a.p.dim + at.ch;
-        h.store(a.carry + spare * N, N, at.n0, at.cl, a.nvec);
+        h.store(a.carry + spare * N, N, at.n0, at.cl, ALN);
     }
     f32x2 sum = 0ull;
     const f32x2 bias = pair_of(a.p.delta_bias, at.ch, at.cl);
@@ -334,7 +365,7 @@ __global__ void __launch_bounds__(kSsmThreads, MT_XC) k_ssm_carry(const __grid_c
     const auto fetch = [&](int k, int64_t t0) {
         const int left = end - t0 < kStep ? (int)(end - t0) : kStep;
         const uint32_t to = smem_addr(stage) + (k & 1) * M::kStage;
-        if (a.v16) {
+        if (ALN) {
             R::fetch16(to, d16, dt_, left, in, lane);
             R::fetch16(to + R::kBytes, x16, xt, left, in, lane);
             if (gated)
@@ -349,7 +380,7 @@ __global__ void __launch_bounds__(kSsmThreads, MT_XC) k_ssm_carry(const __grid_c
             if (gated)
                 R::fetch_words(to + 2 * R::kBytes, zp, zt, t0, left, at.channels, lane);
         }
-        St::fetch(to + 3 * R::kBytes, bp, bt, t0, left, (int)N, lane, a.bvec);
+        St::fetch(to + 3 * R::kBytes, bp, bt, t0, left, (int)N, lane, ALN);
         cp_async_commit();
     };
     if (steps > 0)
@@ -363,7 +394,7 @@ __global__ void __launch_bounds__(kSsmThreads, MT_XC) k_ssm_carry(const __grid_c
         if (k + 1 < steps)
             fetch(k + 1, REV ? t0 - kStep : t0 + kStep);
         const int left = end - t0 < kStep ? (int)(end - t0) : kStep;
-        if (!a.v16) {
+        if (!ALN) {
             R::settle(raw, dp, dt_, t0, left, at.channels, lane);
             R::settle(raw + R::kBytes, xp, xt, t0, left, at.channels, lane);
             if (gated)
@@ -372,7 +403,7 @@ __global__ void __launch_bounds__(kSsmThreads, MT_XC) k_ssm_carry(const __grid_c
         }
         if (left < kStep)
             R::no_steps(raw, left, lane, softplus);
-        St::widen(sb, raw + 3 * R::kBytes, bp, bt, t0, left, (int)N, lane, a.bvec);
+        St::widen(sb, raw + 3 * R::kBytes, bp, bt, t0, left, (int)N, lane, ALN);
         __syncwarp();
 #pragma unroll 1
         for (int ii = 0; ii < kStep; ii += kAhead) {
@@ -422,7 +453,7 @@ __global__ void __launch_bounds__(kSsmThreads, MT_XC) k_ssm_carry(const __grid_c
         }
     }
     const int64_t row = (at.b * a.plan.segments + at.s) * a.p.dim + at.ch;
-    h.store(a.carry + row * N, N, at.n0, at.cl, a.nvec);
+    h.store(a.carry + row * N, N, at.n0, at.cl, ALN);
     float s[2];
     unpack2f(sum, s[0], s[1]);
     if (lane % P == 0)
@@ -471,7 +502,7 @@ __global__ void __launch_bounds__(256) k_ssm_chain(const __grid_constant__ SsmAr
 }
 
 // ---- forward -----------------------------------------------------------------------------
-template <class S, int K, int P>
+template <class S, int K, int P, bool ALN>
 __global__ void __launch_bounds__(kSsmThreads, MT_XF) k_ssm(const __grid_constant__ SsmArgs a, int64_t warps) {
     using Q = PromptPlace<K, P>;
     constexpr int NP = Q::NP;
@@ -497,12 +528,12 @@ __global__ void __launch_bounds__(kSsmThreads, MT_XF) k_ssm(const __grid_constan
     const int64_t end = n < stop ? n : stop;
     float *state = a.p.state != nullptr && active ? a.p.state + (slot * a.p.dim + at.ch) * N : nullptr;
     Rows<K> A, h;
-    A.load(a.p.A + at.ch * N, N, at.n0, at.cl, a.nvec, kLog2e);
+    A.load(a.p.A + at.ch * N, N, at.n0, at.cl, ALN, kLog2e);
     h.zero();
     if (a.plan.segments > 1)
-        h.load(a.carry + ((at.b * a.plan.segments + at.s) * a.p.dim + at.ch) * N, N, at.n0, at.cl, a.nvec);
+        h.load(a.carry + ((at.b * a.plan.segments + at.s) * a.p.dim + at.ch) * N, N, at.n0, at.cl, ALN);
     else if (a.p.carry_in && state != nullptr)
-        h.load(state, N, at.n0, at.cl, a.nvec);
+        h.load(state, N, at.n0, at.cl, ALN);
     const f32x2 bias = pair_of(a.p.delta_bias, at.ch, at.cl), skip = pair_of(a.p.D, at.ch, at.cl);
     const S *dp = static_cast<const S *>(a.p.delta) + at.b * a.p.delta_batch + at.cw;
     const S *up = static_cast<const S *>(a.p.u) + at.b * a.p.u_batch + at.cw;
@@ -521,7 +552,7 @@ __global__ void __launch_bounds__(kSsmThreads, MT_XF) k_ssm(const __grid_constan
     const auto fetch = [&](int k, int64_t t0) {
         const int left = end - t0 < kStep ? (int)(end - t0) : kStep;
         const uint32_t to = smem_addr(stage) + (k & 1) * M::kStage;
-        if (a.v16) {
+        if (ALN) {
             R::fetch16(to, d16, a.p.delta_token, left, in, lane);
             R::fetch16(to + R::kBytes, u16, a.p.u_token, left, in, lane);
             if (gated)
@@ -535,8 +566,8 @@ __global__ void __launch_bounds__(kSsmThreads, MT_XF) k_ssm(const __grid_constan
             if (gated)
                 R::fetch_words(to + 2 * R::kBytes, zp, a.p.z_token, t0, left, at.channels, lane);
         }
-        St::fetch(to + 3 * R::kBytes, bp, a.p.B_token, t0, left, (int)N, lane, a.bvec);
-        St::fetch(to + 3 * R::kBytes + St::kBytes, cp, a.p.C_token, t0, left, (int)N, lane, a.bvec);
+        St::fetch(to + 3 * R::kBytes, bp, a.p.B_token, t0, left, (int)N, lane, ALN);
+        St::fetch(to + 3 * R::kBytes + St::kBytes, cp, a.p.C_token, t0, left, (int)N, lane, ALN);
         cp_async_commit();
     };
     if (steps > 0)
@@ -546,13 +577,13 @@ __global__ void __launch_bounds__(kSsmThreads, MT_XF) k_ssm(const __grid_constan
     for (int k = 0; k < steps; ++k, t0 += kStep) {
         char *raw = stage + (k & 1) * M::kStage;
         if (a.p.checkpoints != nullptr)
-            h.store(a.p.checkpoints + ((at.b * a.ntiles + t0 / kStep) * a.p.dim + at.ch) * N, N, at.n0, at.cl, a.nvec);
+            h.store(a.p.checkpoints + ((at.b * a.ntiles + t0 / kStep) * a.p.dim + at.ch) * N, N, at.n0, at.cl, ALN);
         cp_async_wait_all();
         __syncwarp();  // everyone's copies are here, and nobody reads the other stage any more
         if (k + 1 < steps)
             fetch(k + 1, t0 + kStep);
         const int left = end - t0 < kStep ? (int)(end - t0) : kStep;
-        if (!a.v16) {
+        if (!ALN) {
             R::settle(raw, dp, a.p.delta_token, t0, left, at.channels, lane);
             R::settle(raw + R::kBytes, up, a.p.u_token, t0, left, at.channels, lane);
             if (gated)
@@ -561,8 +592,8 @@ __global__ void __launch_bounds__(kSsmThreads, MT_XF) k_ssm(const __grid_constan
         }
         if (left < kStep)
             R::no_steps(raw, left, lane, softplus);
-        St::widen(sb, raw + 3 * R::kBytes, bp, a.p.B_token, t0, left, (int)N, lane, a.bvec);
-        St::widen(sc, raw + 3 * R::kBytes + St::kBytes, cp, a.p.C_token, t0, left, (int)N, lane, a.bvec);
+        St::widen(sb, raw + 3 * R::kBytes, bp, a.p.B_token, t0, left, (int)N, lane, ALN);
+        St::widen(sc, raw + 3 * R::kBytes + St::kBytes, cp, a.p.C_token, t0, left, (int)N, lane, ALN);
         __syncwarp();
 #pragma unroll 1
         for (int i = 0; i < kStep; i += kAhead) {
@@ -627,7 +658,7 @@ __global__ void __launch_bounds__(kSsmThreads, MT_XF) k_ssm(const __grid_constan
             }
         }
         __syncwarp();
-        if (a.v16) {
+        if (ALN) {
             R::put16(raw, o16, a.p.out_token, left, in, lane);
             o16 += kStep * a.p.out_token;
         } else {
@@ -638,7 +669,65 @@ __global__ void __launch_bounds__(kSsmThreads, MT_XF) k_ssm(const __grid_constan
         for (int c = lane; c < at.channels; c += 32)
             Codec<S>::store1(op + t * a.p.out_token + c, 0.0f);
     if (state != nullptr && at.s == a.plan.segments - 1)
-        h.store(state, N, at.n0, at.cl, a.nvec);
+        h.store(state, N, at.n0, at.cl, ALN);
 }
+
+// ---- launches ------------------------------------------------------------------------------
+template <class K> static cudaError_t ssm_smem(K kernel, size_t bytes) {
+    return bytes > 48 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) : cudaSuccess;
+}
+
+template <class S, int K, int P, bool REV, bool ALN> static cudaError_t carry_go(const SsmArgs &a, const Launch &L) {
+    SsmArgs c = a;
+    c.plan.ctiles = (a.gdim + 64 / P - 1) / (64 / P);
+    const int64_t warps = a.p.batch * a.p.groups * c.plan.ctiles * (a.plan.segments - 1);
+    const int64_t grid = (warps + kSsmWarps - 1) / kSsmWarps, chain = (a.p.batch * a.p.dim * a.p.nstate + 255) / 256;
+    if (grid > INT32_MAX || chain > INT32_MAX)
+        return cudaErrorInvalidValue;
+    const size_t smem = kSsmWarps * PromptSmem<S, K, P, 1>::kBytes;
+    cudaError_t e = ssm_smem(k_ssm_carry<S, K, P, REV, ALN>, smem);
+    if (e != cudaSuccess)
+        return e;
+    note_launch();
+    e = launch_pdl(k_ssm_carry<S, K, P, REV, ALN>, (unsigned)grid, kSsmThreads, smem, L.stream, c, warps);
+    if (e != cudaSuccess)
+        return e;
+    note_launch();
+    return launch_pdl(k_ssm_chain<REV>, (unsigned)chain, 256, 0, L.stream, a);
+}
+template <class S, int K, int P, bool ALN> static cudaError_t prompt_go(const SsmArgs &a, const Launch &L) {
+    cudaError_t e;
+    if (a.plan.segments > 1 && (e = carry_go<S, K, P, false, ALN>(a, L)) != cudaSuccess)
+        return e;
+    const int64_t warps = a.p.batch * a.p.groups * a.plan.ctiles * a.plan.segments;
+    const int64_t grid = (warps + kSsmWarps - 1) / kSsmWarps;
+    if (grid > INT32_MAX)
+        return cudaErrorInvalidValue;
+    const size_t smem = kSsmWarps * PromptSmem<S, K, P, 2>::kBytes;
+    if ((e = ssm_smem(k_ssm<S, K, P, ALN>, smem)) != cudaSuccess)
+        return e;
+    note_launch();
+    return launch_pdl(k_ssm<S, K, P, ALN>, (unsigned)grid, kSsmThreads, smem, L.stream, a, warps);
+}
+
+// by the number of states, rounded up to what a lane (and P lanes) hold
+#define MT_BY_STATES(n, f)              \
+    if ((n) <= 4) return f(4, 1);       \
+    if ((n) <= 8) return f(8, 1);       \
+    if ((n) <= 16) return f(16, 1);     \
+    if ((n) <= 32) return f(16, 2);     \
+    if ((n) <= 64) return f(16, 4);     \
+    return f(16, 8)
+template <class S> static cudaError_t prompt_states(const SsmArgs &a, const Launch &L) {
+#define MT_GO(K, P) (a.aligned ? prompt_go<S, K, P, true>(a, L) : prompt_go<S, K, P, false>(a, L))
+    MT_BY_STATES(a.p.nstate, MT_GO);
+#undef MT_GO
+}
+template <class S> static cudaError_t adjoint_carries(const SsmArgs &a, const Launch &L) {
+#define MT_GO(K, P) (a.aligned ? carry_go<S, K, P, true, true>(a, L) : carry_go<S, K, P, true, false>(a, L))
+    MT_BY_STATES(a.p.nstate, MT_GO);
+#undef MT_GO
+}
+#undef MT_BY_STATES
 
 }  // namespace mt
