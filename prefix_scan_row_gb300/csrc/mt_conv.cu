@@ -5,37 +5,82 @@
 //
 // where the W-1 inputs before token 0 come from a state (or are 0) and the
 // last W-1 inputs are left in it. 2W + 5 operations per value of 2 or 4 bytes
-// read and written: bound by bytes. A lane owns V neighbouring channels (16
-// bytes, or one value where the rows fit no vector) and walks down a span of
+// read and written: bound by bytes. A lane owns four channels (neighbours,
+// moved as one, or 32 apart where the rows fit no vector) and walks down a span of
 // tokens with the W-1 inputs before the present one in registers, so an input is
-// read once, plus W-1 per span; a warp's lanes are neighbouring channels.
+// read once, plus W-1 per span; products are made for two channels at a time.
+#include <type_traits>
+
 #include "mt_seq.cuh"
 #include "mt_seq.h"
 
 namespace mt {
 
 constexpr int kConvThreads = 128;
+#ifndef MT_XCC
+#define MT_XCC 6
+#endif
+#ifndef MT_XCN
+#define MT_XCN 32
+#endif
 
-// V values of one lane.
-template <class S, int V> struct Lane {
-    float x[V];
-    __device__ __forceinline__ void load(const S *p) {
-        if constexpr (V == 1)
-            x[0] = Codec<S>::load1(p);
-        else
-            Codec<S>::unpack(*reinterpret_cast<const uint4 *>(p), x);
-    }
-    __device__ __forceinline__ void store(S *p) const {
-        if constexpr (V == 1)
-            Codec<S>::store1(p, x[0]);
-        else
-            *reinterpret_cast<uint4 *>(p) = Codec<S>::pack(x);
-    }
-    __device__ __forceinline__ void fill(float v) {
+// Four values of one lane in storage form: neighbouring channels moved as one
+// (ALN), or channels 32 apart (rows that no vector fits), of which `live` exist.
+template <class S, bool ALN> struct Quad {
+    Raw4<S> w;
+    __device__ __forceinline__ void load(const S *p, int live) {
+        if constexpr (ALN) {
+            w.load(p, true, 4);
+        } else {
+            S v[4];
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            x[i] = v;
+            for (int e = 0; e < 4; ++e)
+                v[e] = e < live ? p[32 * e] : S(0.0f);
+            w.w = *reinterpret_cast<typename VecOf<S, 4>::T *>(v);
+        }
     }
+    __device__ __forceinline__ void zero() {
+        if constexpr (sizeof(S) == 4)
+            w.w = make_uint4(0u, 0u, 0u, 0u);
+        else
+            w.w = make_uint2(0u, 0u);
+    }
+    __device__ __forceinline__ void store(S *p, int live) const {
+        if constexpr (ALN) {
+            *reinterpret_cast<typename VecOf<S, 4>::T *>(p) = w.w;
+        } else {
+            const S *v = reinterpret_cast<const S *>(&w.w);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (e < live)
+                    p[32 * e] = v[e];
+        }
+    }
+    __device__ __forceinline__ void widen(f32x2 (&x)[2]) const {
+        float v[4];
+        w.widen(v);
+        x[0] = pack2f(v[0], v[1]);
+        x[1] = pack2f(v[2], v[3]);
+    }
+    __device__ __forceinline__ void narrow(const f32x2 (&x)[2]) {
+        float v[4];
+        unpack2f(x[0], v[0], v[1]);
+        unpack2f(x[1], v[2], v[3]);
+        w.w = narrow4<S>(v);
+    }
+};
+// A lane's first channel, how many it has, and the distance between them.
+template <bool ALN> struct ConvLane {
+    int64_t c;
+    int live;
+    __device__ __forceinline__ void set(int64_t group, int lane, int64_t dim) {  // 128 channels a warp
+        c = group * 128 + (ALN ? 4 * lane : lane);
+        if (ALN)
+            live = c < dim ? 4 : 0;  // dim is a multiple of four
+        else
+            live = c >= dim ? 0 : (dim - c + 31) / 32 < 4 ? (int)((dim - c + 31) / 32) : 4;
+    }
+    static __device__ __forceinline__ int step(int e) { return ALN ? e : 32 * e; }
 };
 
 // Weights and bias are f32 or the activations' type.
@@ -73,37 +118,64 @@ __device__ __forceinline__ int64_t live_len(const int32_t *lens, int64_t len, in
 
 // x at token t of a sequence (t >= -(W-1)): the state's before token 0, zeros
 // from the sequence's end on (what is stored there is not read).
-template <class S, int V>
-__device__ __forceinline__ void input_at(Lane<S, V> &v, const S *x, const S *state, const ConvDims &d, int64_t t,
-                                         int64_t n) {
+template <class S, bool ALN>
+__device__ __forceinline__ void input_at(Quad<S, ALN> &v, const S *x, const S *state, const ConvDims &d, int64_t t, int64_t n,
+                                         int live) {
     if (t < 0) {
         if (state != nullptr)
-            v.load(state + (t + d.width - 1) * d.dim);
+            v.load(state + (t + d.width - 1) * d.dim, live);
         else
-            v.fill(0.0f);
+            v.zero();
     } else if (t < n) {
-        v.load(x + t * d.xt);
+        v.load(x + t * d.xt, live);
     } else {
-        v.fill(0.0f);
+        v.zero();
+    }
+}
+// weights and bias of a lane's channels, two channels a register pair
+template <class S, bool ALN, int W>
+__device__ __forceinline__ void conv_params(const ConvDims &d, const ConvLane<ALN> &at, f32x2 (&w)[W][2], f32x2 (&bias)[2]) {
+    float b[4], k4[W][4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int64_t c = at.c + at.step(e);
+        const bool in = e < at.live;
+        b[e] = in && d.bias != nullptr ? param<S>(d.bias, c, d.wf32) : 0.0f;
+#pragma unroll
+        for (int k = 0; k < W; ++k)
+            k4[k][e] = in ? param<S>(d.weight, c * W + k, d.wf32) : 0.0f;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        bias[h] = pack2f(b[2 * h], b[2 * h + 1]);
+#pragma unroll
+        for (int k = 0; k < W; ++k)
+            w[k][h] = pack2f(k4[k][2 * h], k4[k][2 * h + 1]);
     }
 }
 
 // ---- forward ------------------------------------------------------------------------
 // Tokens per lane: at 32 the W-1 inputs read twice are a tenth of the
 // bytes and come from L2.
-constexpr int kConvSpan = 32;
-constexpr int kConvAhead = 8;  // tokens loaded together
+constexpr int kConvSpan = MT_XCN;
+#ifndef MT_XCA
+#define MT_XCA 8
+#endif
+constexpr int kConvAhead = MT_XCA;  // tokens loaded together, while as many before them are worked on
 
-template <class S, int V, int W>
-__global__ void __launch_bounds__(kConvThreads) k_conv(const S *x, S *out, S *state, ConvDims d, int64_t lanes,
+template <class S, bool ALN, int W, bool SILU>
+__global__ void __launch_bounds__(kConvThreads, MT_XCC) k_conv(const S *x, S *out, S *state, ConvDims d, int64_t groups,
                                                        int64_t spans) {
     pdl_prologue();
-    const int64_t i = (int64_t)blockIdx.x * kConvThreads + threadIdx.x;
-    const int64_t lane = i % lanes, bs = i / lanes;
+    const int64_t i = (int64_t)blockIdx.x * (kConvThreads / 32) + (threadIdx.x >> 5);
+    const int64_t group = i % groups, bs = i / groups;
     const int64_t span = bs % spans, b = bs / spans;
     if (b >= d.batch)
         return;
-    const int64_t c = lane * V;
+    ConvLane<ALN> at;
+    at.set(group, threadIdx.x & 31, d.dim);
+    if (at.live == 0)
+        return;
     const int64_t n = live_len(d.lens, d.len, b);
     const int64_t t0 = span * kConvSpan, t1 = t0 + kConvSpan < d.len ? t0 + kConvSpan : d.len;
     bool active = true;
@@ -112,100 +184,127 @@ __global__ void __launch_bounds__(kConvThreads) k_conv(const S *x, S *out, S *st
         const int64_t slot = slot_of(d.slots, d.nslots, b);
         active = slot >= 0;
         if (active && state != nullptr)
-            st = state + slot * (W - 1) * d.dim + c;
+            st = state + slot * (W - 1) * d.dim + at.c;
     }
-    const S *xs = x + b * d.xb + c;
-    S *os = out + b * d.ob + c;
-    float w[W][V], bias[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-        bias[e] = d.bias != nullptr ? param<S>(d.bias, c + e, d.wf32) : 0.0f;
-#pragma unroll
-        for (int k = 0; k < W; ++k)
-            w[k][e] = param<S>(d.weight, (c + e) * W + k, d.wf32);
-    }
-    Lane<S, V> h[W];  // h[0..W-2]: the inputs before the present one
+    const S *xs = x + b * d.xb + at.c;
+    S *os = out + b * d.ob + t0 * d.ot + at.c;
+    f32x2 w[W][2], bias[2];
+    conv_params<S, ALN, W>(d, at, w, bias);
+    f32x2 h[W][2];  // h[0..W-2]: the inputs before the present one
     const S *from = d.carry_in ? st : nullptr;
 #pragma unroll
-    for (int k = 0; k < W - 1; ++k)
-        input_at<S, V>(h[k], xs, from, d, t0 - (W - 1) + k, n);
-    for (int64_t tt = t0; tt < t1; tt += kConvAhead) {
-        Lane<S, V> v[kConvAhead];
+    for (int k = 0; k < W - 1; ++k) {
+        Quad<S, ALN> v;
+        input_at<S, ALN>(v, xs, from, d, t0 - (W - 1) + k, n, at.live);
+        v.widen(h[k]);
+    }
+    const int tokens = (int)(t1 - t0), here = !active || n <= t0 ? 0 : n < t1 ? (int)(n - t0) : tokens;  // that exist
+    const S *xt = xs + t0 * d.xt;
+    // token tt + j + kConvAhead is asked for as token tt + j is taken
+    Quad<S, ALN> ring[kConvAhead];
+#pragma unroll
+    for (int j = 0; j < kConvAhead; ++j) {
+        ring[j].zero();
+        if (j < here)
+            ring[j].load(xt + j * d.xt, at.live);
+    }
+    xt += kConvAhead * d.xt;
+    // FULL: every token of the batch, and of the next, exists
+    const auto batch = [&](int tt, auto full) {
+        constexpr bool FULL = decltype(full)::value;
 #pragma unroll
         for (int j = 0; j < kConvAhead; ++j) {
-            if (tt + j < n && tt + j < t1)
-                v[j].load(xs + (tt + j) * d.xt);
-            else
-                v[j].fill(0.0f);
-        }
+            ring[j].widen(h[W - 1]);
+            if (FULL) {
+                ring[j].load(xt + j * d.xt, at.live);
+            } else {
+                ring[j].zero();
+                if (tt + j + kConvAhead < here)
+                    ring[j].load(xt + j * d.xt, at.live);
+            }
+            f32x2 o[2];
 #pragma unroll
-        for (int j = 0; j < kConvAhead; ++j) {
-            if (tt + j < t1) {
-                h[W - 1] = v[j];
-                Lane<S, V> o;
-                const bool live = active && tt + j < n;
+            for (int e = 0; e < 2; ++e) {
+                f32x2 p = bias[e];
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    float p = bias[e];
-#pragma unroll
-                    for (int k = 0; k < W; ++k)
-                        p = fmaf(w[k][e], h[k].x[e], p);
-                    if (d.silu)
-                        p *= sigmoidf(p);
-                    o.x[e] = live ? p : 0.0f;
-                }
-                o.store(os + (tt + j) * d.ot);
+                for (int k = 0; k < W; ++k)
+                    p = fma2f(w[k][e], h[k][e], p);
+                if (SILU)
+                    p = mul2f(p, sigmoid_2f(p));
+                o[e] = FULL || tt + j < here ? p : 0ull;
 #pragma unroll
                 for (int k = 0; k < W - 1; ++k)
-                    h[k] = h[k + 1];
+                    h[k][e] = h[k + 1][e];
             }
+            Quad<S, ALN> v;
+            v.narrow(o);
+            if (FULL || tt + j < tokens)
+                v.store(os + j * d.ot, at.live);
         }
+        xt += kConvAhead * d.xt;
+        os += kConvAhead * d.ot;
+    };
+    for (int tt = 0; tt < tokens; tt += kConvAhead) {
+        if (tt + 2 * kConvAhead <= here)
+            batch(tt, std::true_type());
+        else
+            batch(tt, std::false_type());
     }
     // The lane of the first span is the only one that reads the state, so it
     // is also the one that writes it: the last W-1 inputs of the sequence.
     if (span == 0 && st != nullptr) {
-        Lane<S, V> last[W];
+        Quad<S, ALN> last[W];
 #pragma unroll
         for (int k = 0; k < W - 1; ++k)
-            input_at<S, V>(last[k], xs, from, d, n - (W - 1) + k, n);
+            input_at<S, ALN>(last[k], xs, from, d, n - (W - 1) + k, n, at.live);
 #pragma unroll
         for (int k = 0; k < W - 1; ++k)
-            last[k].store(st + k * d.dim);
+            last[k].store(st + k * d.dim, at.live);
     }
 }
 
 // ---- one token of each sequence --------------------------------------------------------
-template <class S, int V, int W>
-__global__ void __launch_bounds__(kConvThreads) k_conv_step(const S *x, S *out, S *state, ConvDims d, int64_t lanes) {
+template <class S, bool ALN, int W>
+__global__ void __launch_bounds__(kConvThreads) k_conv_step(const S *x, S *out, S *state, ConvDims d, int64_t groups) {
     pdl_prologue();
-    const int64_t i = (int64_t)blockIdx.x * kConvThreads + threadIdx.x;
-    const int64_t lane = i % lanes, b = i / lanes;
+    const int64_t i = (int64_t)blockIdx.x * (kConvThreads / 32) + (threadIdx.x >> 5);
+    const int64_t group = i % groups, b = i / groups;
     if (b >= d.batch)
         return;
-    const int64_t c = lane * V;
+    ConvLane<ALN> at;
+    at.set(group, threadIdx.x & 31, d.dim);
+    if (at.live == 0)
+        return;
     const int64_t slot = d.slots != nullptr || state != nullptr ? slot_of(d.slots, d.nslots, b) : b;
-    Lane<S, V> o;
-    o.fill(0.0f);
+    Quad<S, ALN> o;
+    o.zero();
     if (slot >= 0) {
-        S *st = state + slot * (W - 1) * d.dim + c;
-        Lane<S, V> h[W];
+        S *st = state + slot * (W - 1) * d.dim + at.c;
+        Quad<S, ALN> v[W];
 #pragma unroll
         for (int k = 0; k < W - 1; ++k)
-            h[k].load(st + k * d.dim);
-        h[W - 1].load(x + b * d.xb + c);
+            v[k].load(st + k * d.dim, at.live);
+        v[W - 1].load(x + b * d.xb + at.c, at.live);
+        f32x2 w[W][2], p[2], h[2];
+        conv_params<S, ALN, W>(d, at, w, p);
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-            float p = d.bias != nullptr ? param<S>(d.bias, c + e, d.wf32) : 0.0f;
+        for (int k = 0; k < W; ++k) {
+            v[k].widen(h);
 #pragma unroll
-            for (int k = 0; k < W; ++k)
-                p = fmaf(param<S>(d.weight, (c + e) * W + k, d.wf32), h[k].x[e], p);
-            o.x[e] = d.silu ? p * sigmoidf(p) : p;
+            for (int e = 0; e < 2; ++e)
+                p[e] = fma2f(w[k][e], h[e], p[e]);
         }
+        if (d.silu) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                p[e] = mul2f(p[e], sigmoid_2f(p[e]));
+        }
+        o.narrow(p);
 #pragma unroll
         for (int k = 0; k < W - 1; ++k)
-            h[k + 1].store(st + k * d.dim);
+            v[k + 1].store(st + k * d.dim, at.live);
     }
-    o.store(out + b * d.ob + c);
+    o.store(out + b * d.ob + at.c, at.live);
 }
 
 // ---- gradient ----------------------------------------------------------------------------
@@ -216,139 +315,160 @@ __global__ void __launch_bounds__(kConvThreads) k_conv_step(const S *x, S *out, 
 // too, without the sums. The sums of a span are 4(W+1) bytes against its
 // 6 * kGradSpan bytes of activations; they are added over a CTA's spans in
 // shared memory, written once per CTA and added by a second kernel in order.
-constexpr int kGradSpan = 64;
-constexpr int kGradLanes = 32, kGradSpans = 8;  // a CTA: 32 lanes of channels x 8 spans
-constexpr int kGradThreads = kGradLanes * kGradSpans;
+#ifndef MT_XCF
+#define MT_XCF 4
+#endif
+#ifndef MT_XCS
+#define MT_XCS 64
+#endif
+#ifndef MT_XCB
+#define MT_XCB 2
+#endif
+#ifndef MT_XCC
+#define MT_XCC 4
+#endif
+constexpr int kFew = MT_XCF;  // tokens loaded together
+constexpr int kGradSpan = MT_XCS;
+constexpr int kGradSpans = 8;  // a CTA: 128 channels x 8 spans, a warp a span
+constexpr int kGradThreads = 32 * kGradSpans;
 
 // out_t's derivative by p_t
-__device__ __forceinline__ float act_grad(float p, bool silu) {
-    if (!silu)
-        return 1.0f;
-    const float s = sigmoidf(p);
-    return s * fmaf(p, 1.0f - s, 1.0f);
+__device__ __forceinline__ f32x2 act_grad(f32x2 p) {
+    const f32x2 s = sigmoid_2f(p);
+    return mul2f(s, fma2f(p, add2f(both(1.0f), mul2f(both(-1.0f), s)), both(1.0f)));
 }
 
-template <class S, int V, int W>
-__global__ void __launch_bounds__(kGradThreads) k_conv_grad(const S *x, const S *dout, S *dx, const S *state, S *dstate,
-                                                            float *partial, ConvDims d, int64_t lane_blocks,
-                                                            int64_t span_blocks) {
-    __shared__ float s_sum[kGradSpans][kGradLanes * V + 1];
+template <class S, bool ALN, int W, bool SILU>
+__global__ void __launch_bounds__(kGradThreads, MT_XCB) k_conv_grad(const S *x, const S *dout, S *dx, const S *state, S *dstate,
+                                                            float *partial, ConvDims d, int64_t groups, int64_t span_blocks) {
+    __shared__ float s_sum[W + 1][kGradSpans][128];
     pdl_prologue();
-    const int lane = threadIdx.x % kGradLanes, sp = threadIdx.x / kGradLanes;
-    const int64_t lb = blockIdx.x % lane_blocks, rest = blockIdx.x / lane_blocks;
+    const int lane = threadIdx.x & 31, sp = threadIdx.x >> 5;
+    const int64_t group = blockIdx.x % groups, rest = blockIdx.x / groups;
     const int64_t sb = rest % span_blocks, b = rest / span_blocks;
-    const int64_t c = (lb * kGradLanes + lane) * V;
-    const bool on = c < d.dim;
-    float dw[W][V], db[V];
+    ConvLane<ALN> at;
+    at.set(group, lane, d.dim);
+    f32x2 sums[W + 1][2];  // dw, then dbias
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-        db[e] = 0.0f;
-#pragma unroll
-        for (int k = 0; k < W; ++k)
-            dw[k][e] = 0.0f;
-    }
+    for (int k = 0; k <= W; ++k)
+        sums[k][0] = sums[k][1] = 0ull;
     const int64_t t0 = (sb * kGradSpans + sp) * kGradSpan;
-    if (on && (t0 < d.len || (t0 == 0 && dstate != nullptr))) {
+    if (at.live > 0 && (t0 < d.len || (t0 == 0 && dstate != nullptr))) {
         const int64_t n = live_len(d.lens, d.len, b);
         const int64_t t1 = t0 + kGradSpan < d.len ? t0 + kGradSpan : d.len;
-        const S *xs = x + b * d.xb + c, *gs = dout + b * d.gb + c;
-        S *ds = dx + b * d.db + c;
-        const S *st = d.carry_in && state != nullptr ? state + b * (W - 1) * d.dim + c : nullptr;
-        float w[W][V], bias[V];
+        const S *xs = x + b * d.xb + at.c;
+        const S *st = d.carry_in && state != nullptr ? state + b * (W - 1) * d.dim + at.c : nullptr;
+        S *dst = t0 == 0 && dstate != nullptr ? dstate + b * (W - 1) * d.dim + at.c : nullptr;
+        f32x2 w[W][2], bias[2];
+        conv_params<S, ALN, W>(d, at, w, bias);
+        f32x2 h[W][2], q[W][2];  // q[j]: the sum so far of dx of token t-W+1+j (the newest begins at j = W-1)
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-            bias[e] = d.bias != nullptr ? param<S>(d.bias, c + e, d.wf32) : 0.0f;
-#pragma unroll
-            for (int k = 0; k < W; ++k)
-                w[k][e] = param<S>(d.weight, (c + e) * W + k, d.wf32);
+        for (int k = 0; k < W - 1; ++k) {
+            Quad<S, ALN> v;
+            input_at<S, ALN>(v, xs, st, d, t0 - (W - 1) + k, n, at.live);
+            v.widen(h[k]);
         }
-        Lane<S, V> h[W];
-        float q[W][V];  // q[j]: the sum so far of dx of token t-W+1+j (the newest begins at j = W-1)
-#pragma unroll
-        for (int k = 0; k < W - 1; ++k)
-            input_at<S, V>(h[k], xs, st, d, t0 - (W - 1) + k, n);
 #pragma unroll
         for (int k = 0; k < W; ++k)
+            q[k][0] = q[k][1] = 0ull;
+        const int tokens = (int)(t1 - t0), walk = tokens + W - 1;  // the last W-1 only finish this span's dx
+        const int here = n <= t0 ? 0 : n - t0 < walk ? (int)(n - t0) : walk;  // that exist
+        const S *xp = xs + t0 * d.xt, *gp = dout + b * d.gb + t0 * d.gt + at.c;
+        S *dp = dx + b * d.db + t0 * d.dt + at.c;
+        Quad<S, ALN> rx[kFew], rg[kFew];
 #pragma unroll
-            for (int e = 0; e < V; ++e)
-                q[k][e] = 0.0f;
-        // tokens t1 .. t1+W-2 only finish this span's dx
-        for (int64_t tt = t0; tt < t1 + W - 1; tt += 4) {
-            Lane<S, V> vx[4], vg[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int64_t t = tt + j;
-                if (t < n && t < t1 + W - 1) {
-                    vx[j].load(xs + t * d.xt);
-                    vg[j].load(gs + t * d.gt);
-                } else {
-                    vx[j].fill(0.0f);
-                    vg[j].fill(0.0f);
-                }
+        for (int j = 0; j < kFew; ++j) {
+            rx[j].zero();
+            rg[j].zero();
+            if (j < here) {
+                rx[j].load(xp + j * d.xt, at.live);
+                rg[j].load(gp + j * d.gt, at.live);
             }
+        }
+        xp += kFew * d.xt;
+        gp += kFew * d.gt;
+        // FULL: the batch's tokens are this span's, their dx too, and the next batch exists
+        const auto batch = [&](int tt, auto full) {
+            constexpr bool FULL = decltype(full)::value;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int64_t t = tt + j;
-                if (t < t1 + W - 1) {
-                    h[W - 1] = vx[j];
-                    Lane<S, V> o;
-#pragma unroll
-                    for (int e = 0; e < V; ++e) {
-                        float p = bias[e];
-#pragma unroll
-                        for (int k = 0; k < W; ++k)
-                            p = fmaf(w[k][e], h[k].x[e], p);
-                        const float g = vg[j].x[e] * act_grad(p, d.silu);
-                        if (t < t1) {
-                            db[e] += g;
-#pragma unroll
-                            for (int k = 0; k < W; ++k)
-                                dw[k][e] = fmaf(g, h[k].x[e], dw[k][e]);
-                        }
-                        // g_t reaches dx of tokens t-W+1+k with w_k
-#pragma unroll
-                        for (int k = 0; k < W; ++k)
-                            q[k][e] = fmaf(w[k][e], g, q[k][e]);
-                        o.x[e] = q[0][e];
-#pragma unroll
-                        for (int k = 0; k < W - 1; ++k)
-                            q[k][e] = q[k + 1][e];
-                        q[W - 1][e] = 0.0f;
-                    }
-                    const int64_t to = t - (W - 1);
-                    if (to >= t0) {
-                        if (to >= n)
-                            o.fill(0.0f);
-                        o.store(ds + to * d.dt);
-                    } else if (t0 == 0 && dstate != nullptr) {
-                        o.store(dstate + b * (W - 1) * d.dim + (to + W - 1) * d.dim + c);
-                    }
-#pragma unroll
-                    for (int k = 0; k < W - 1; ++k)
-                        h[k] = h[k + 1];
+            for (int j = 0; j < kFew; ++j) {
+                f32x2 g[2], o[2];
+                rx[j].widen(h[W - 1]);
+                rg[j].widen(g);
+                if (!FULL) {
+                    rx[j].zero();
+                    rg[j].zero();
                 }
+                if (FULL || tt + j + kFew < here) {
+                    rx[j].load(xp + j * d.xt, at.live);
+                    rg[j].load(gp + j * d.gt, at.live);
+                }
+                const bool own = FULL || tt + j < tokens;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    f32x2 p = bias[e];
+#pragma unroll
+                    for (int k = 0; k < W; ++k)
+                        p = fma2f(w[k][e], h[k][e], p);
+                    if (SILU)
+                        g[e] = mul2f(g[e], act_grad(p));
+                    const f32x2 gs = own ? g[e] : 0ull;
+                    sums[W][e] = add2f(sums[W][e], gs);
+#pragma unroll
+                    for (int k = 0; k < W; ++k) {
+                        sums[k][e] = fma2f(gs, h[k][e], sums[k][e]);
+                        q[k][e] = fma2f(w[k][e], g[e], q[k][e]);  // g_t reaches dx of tokens t-W+1+k with w_k
+                    }
+                    o[e] = q[0][e];
+#pragma unroll
+                    for (int k = 0; k < W - 1; ++k) {
+                        q[k][e] = q[k + 1][e];
+                        h[k][e] = h[k + 1][e];
+                    }
+                    q[W - 1][e] = 0ull;
+                }
+                const int to = tt + j - (W - 1);  // the token whose dx is done
+                if (!FULL && to >= here)
+                    o[0] = o[1] = 0ull;
+                Quad<S, ALN> v;
+                v.narrow(o);
+                if (FULL || (to >= 0 && to < tokens))
+                    v.store(dp + (j - (W - 1)) * d.dt, at.live);
+                else if (to < 0 && dst != nullptr)
+                    v.store(dst + (to + W - 1) * d.dim, at.live);
             }
+            xp += kFew * d.xt;
+            gp += kFew * d.gt;
+            dp += kFew * d.dt;
+        };
+        for (int tt = 0; tt < walk; tt += kFew) {
+            if (tt >= W - 1 && tt + kFew <= tokens && tt + 2 * kFew <= here)
+                batch(tt, std::true_type());
+            else
+                batch(tt, std::false_type());
         }
     }
-    // the CTA's sums, one quantity after the other
-    float *row = partial + (b * span_blocks + sb) * (W + 1) * d.dim;
 #pragma unroll
     for (int k = 0; k <= W; ++k) {
+        float v[4];
+        unpack2f(sums[k][0], v[0], v[1]);
+        unpack2f(sums[k][1], v[2], v[3]);
 #pragma unroll
-        for (int e = 0; e < V; ++e)
-            s_sum[sp][lane * V + e] = k < W ? dw[k < W ? k : 0][e] : db[e];
-        __syncthreads();
-        for (int i = threadIdx.x; i < kGradLanes * V; i += kGradThreads) {
-            const int64_t ch = lb * kGradLanes * V + i;
-            if (ch < d.dim) {
-                float s = 0.0f;
+        for (int e = 0; e < 4; ++e)
+            s_sum[k][sp][(ALN ? 4 * lane : lane) + at.step(e)] = v[e];
+    }
+    __syncthreads();
+    float *row = partial + (b * span_blocks + sb) * (W + 1) * d.dim;
+    for (int i = threadIdx.x; i < (W + 1) * 128; i += kGradThreads) {
+        const int k = i / 128, c = i % 128;
+        const int64_t ch = group * 128 + c;
+        if (ch < d.dim) {
+            float s = 0.0f;
 #pragma unroll
-                for (int j = 0; j < kGradSpans; ++j)
-                    s += s_sum[j][i];
-                row[k * d.dim + ch] = s;
-            }
+            for (int j = 0; j < kGradSpans; ++j)
+                s += s_sum[k][j][c];
+            row[k * d.dim + ch] = s;
         }
-        __syncthreads();
     }
 }
 
@@ -386,40 +506,40 @@ int64_t conv_grad_scratch_slots(int64_t batch, int64_t len, int64_t dim, int64_t
     return (batch * conv_span_blocks(len) * (width + 1) * dim + 1) / 2;
 }
 
-static bool fits(const void *p, int64_t a, int64_t b, int64_t e) {
-    return (uintptr_t)p % 16 == 0 && a % e == 0 && b % e == 0;
+static bool fits(const void *p, int64_t a, int64_t b, int64_t bytes) {  // of four values
+    return (uintptr_t)p % bytes == 0 && a % 4 == 0 && b % 4 == 0;
 }
 
-template <class S, int V, int W> static cudaError_t conv_go(const mt_conv_args &a, int what, const Launch &L) {
+template <class S, bool ALN, int W> static cudaError_t conv_go(const mt_conv_args &a, int what, const Launch &L) {
     const ConvDims d = conv_dims(a);
-    const int64_t lanes = a.dim / V;
+    const int64_t groups = (a.dim + 127) / 128;  // of channels: a warp's
     const S *x = static_cast<const S *>(a.x);
     S *state = static_cast<S *>(a.state);
     if (what == 0) {
         const int64_t spans = a.len > 0 ? (a.len + kConvSpan - 1) / kConvSpan : 1;
-        const int64_t grid = (a.batch * spans * lanes + kConvThreads - 1) / kConvThreads;
+        const int64_t grid = (a.batch * spans * groups + kConvThreads / 32 - 1) / (kConvThreads / 32);
         if (grid > INT32_MAX)
             return cudaErrorInvalidValue;
         note_launch();
-        return launch_pdl(k_conv<S, V, W>, (unsigned)grid, kConvThreads, 0, L.stream, x, static_cast<S *>(a.out), state, d, lanes, spans);
+        return launch_pdl(d.silu ? k_conv<S, ALN, W, true> : k_conv<S, ALN, W, false>, (unsigned)grid, kConvThreads, 0, L.stream, x, static_cast<S *>(a.out), state, d, groups, spans);
     }
     if (what == 1) {
-        const int64_t grid = (a.batch * lanes + kConvThreads - 1) / kConvThreads;
+        const int64_t grid = (a.batch * groups + kConvThreads / 32 - 1) / (kConvThreads / 32);
         if (grid > INT32_MAX)
             return cudaErrorInvalidValue;
         note_launch();
-        return launch_pdl(k_conv_step<S, V, W>, (unsigned)grid, kConvThreads, 0, L.stream, x, static_cast<S *>(a.out), state, d, lanes);
+        return launch_pdl(k_conv_step<S, ALN, W>, (unsigned)grid, kConvThreads, 0, L.stream, x, static_cast<S *>(a.out), state, d, groups);
     }
-    const int64_t lane_blocks = (lanes + kGradLanes - 1) / kGradLanes, span_blocks = conv_span_blocks(a.len);
-    const int64_t grid = a.batch * lane_blocks * span_blocks;
+    const int64_t span_blocks = conv_span_blocks(a.len);
+    const int64_t grid = a.batch * groups * span_blocks;
     if (grid > INT32_MAX)
         return cudaErrorInvalidValue;
     float *partial = static_cast<float *>(a.scratch);
     if (grid > 0) {
         note_launch();
-        const cudaError_t e = launch_pdl(k_conv_grad<S, V, W>, (unsigned)grid, kGradThreads, 0, L.stream, x,
+        const cudaError_t e = launch_pdl(d.silu ? k_conv_grad<S, ALN, W, true> : k_conv_grad<S, ALN, W, false>, (unsigned)grid, kGradThreads, 0, L.stream, x,
                                          static_cast<const S *>(a.dout), static_cast<S *>(a.dx), static_cast<const S *>(state),
-                                         static_cast<S *>(a.dstate), partial, d, lane_blocks, span_blocks);
+                                         static_cast<S *>(a.dstate), partial, d, groups, span_blocks);
         if (e != cudaSuccess)
             return e;
     }
@@ -437,24 +557,24 @@ template <class S, int V, int W> static cudaError_t conv_go(const mt_conv_args &
                               a.batch * span_blocks);
 }
 
-template <class S, int V> static cudaError_t conv_width(const mt_conv_args &a, int what, const Launch &L) {
+template <class S, bool ALN> static cudaError_t conv_width(const mt_conv_args &a, int what, const Launch &L) {
     switch (a.width) {
-    case 1: return conv_go<S, V, 1>(a, what, L);
-    case 2: return conv_go<S, V, 2>(a, what, L);
-    case 3: return conv_go<S, V, 3>(a, what, L);
-    case 4: return conv_go<S, V, 4>(a, what, L);
+    case 1: return conv_go<S, ALN, 1>(a, what, L);
+    case 2: return conv_go<S, ALN, 2>(a, what, L);
+    case 3: return conv_go<S, ALN, 3>(a, what, L);
+    case 4: return conv_go<S, ALN, 4>(a, what, L);
     default: return cudaErrorInvalidValue;
     }
 }
 
 template <class S> static cudaError_t conv_type(const mt_conv_args &a, int what, const Launch &L) {
-    constexpr int E = Codec<S>::E;
-    bool vec = a.dim % E == 0 && fits(a.x, a.x_batch, a.x_token, E) && fits(a.state, 0, 0, E);
+    constexpr int64_t v = 4 * sizeof(S);
+    bool aligned = a.dim % 4 == 0 && fits(a.x, a.x_batch, a.x_token, v) && fits(a.state, 0, 0, v);
     if (what == 2)
-        vec = vec && fits(a.dout, a.dout_batch, a.dout_token, E) && fits(a.dx, a.dx_batch, a.dx_token, E) && fits(a.dstate, 0, 0, E);
+        aligned = aligned && fits(a.dout, a.dout_batch, a.dout_token, v) && fits(a.dx, a.dx_batch, a.dx_token, v) && fits(a.dstate, 0, 0, v);
     else
-        vec = vec && fits(a.out, a.out_batch, a.out_token, E);
-    return vec ? conv_width<S, E>(a, what, L) : conv_width<S, 1>(a, what, L);
+        aligned = aligned && fits(a.out, a.out_batch, a.out_token, v);
+    return aligned ? conv_width<S, true>(a, what, L) : conv_width<S, false>(a, what, L);
 }
 
 static cudaError_t conv_any(const mt_conv_args &a, int what, const Launch &L) {

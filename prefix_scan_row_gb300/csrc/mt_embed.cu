@@ -138,11 +138,11 @@ cudaError_t embed_launch(const void *tokens, bool wide, int64_t n, const void *t
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortRows = 1024;  // most table rows per CTA: 32 warps x 1024 counts are 128 KB
-constexpr int kSortAhead = 8;
+constexpr int kSortAhead = 16;
 
 template <class Tok>
 __global__ void __launch_bounds__(kSortThreads) k_embed_sort(const Tok *tokens, int64_t ntokens, int64_t vocab,
-                                                             int rows, int32_t *start, int32_t *order) {
+                                                             int rows, int32_t *start, int32_t *order, int32_t *sorted) {
     extern __shared__ int32_t cnt[];  // [warps][rows]
     __shared__ int32_t s_warp[kSortWarps], s_less;
     pdl_prologue();
@@ -159,19 +159,26 @@ __global__ void __launch_bounds__(kSortThreads) k_embed_sort(const Tok *tokens, 
     const int64_t begin = per * warp < ntokens ? per * warp : ntokens;
     const int64_t end = begin + per < ntokens ? begin + per : ntokens;
     int32_t *mine = cnt + warp * rows;
+    // tokens as 32-bit numbers; any that names no row as -1, which is in no range and below none
+    const int lo32 = (int)lo;
+    const auto token = [&](int64_t i) {
+        if (i >= end)
+            return -1;
+        const Tok t = tokens[i];
+        return t >= 0 && t < (Tok)vocab ? (int)t : -1;
+    };
     int less = 0;
+    int t[kSortAhead];  // up to 32 * kSortAhead tokens a warp are read once for both passes
+    const bool once = per <= 32 * kSortAhead;
     for (int64_t i0 = begin; i0 < end; i0 += 32 * kSortAhead) {
-        int64_t t[kSortAhead];
+#pragma unroll
+        for (int k = 0; k < kSortAhead; ++k)
+            t[k] = token(i0 + 32 * k + lane);
 #pragma unroll
         for (int k = 0; k < kSortAhead; ++k) {
-            const int64_t i = i0 + 32 * k + lane;
-            t[k] = i < end ? (int64_t)tokens[i] : -1;
-        }
-#pragma unroll
-        for (int k = 0; k < kSortAhead; ++k) {
-            less += t[k] >= 0 && t[k] < lo;
-            if (t[k] >= lo && t[k] < hi)
-                atomicAdd(&mine[t[k] - lo], 1);
+            less += (unsigned)t[k] < (unsigned)lo32;
+            if ((unsigned)(t[k] - lo32) < (unsigned)live && t[k] >= 0)
+                atomicAdd(&mine[t[k] - lo32], 1);
         }
     }
     less = __reduce_add_sync(kFull, less);
@@ -181,6 +188,7 @@ __global__ void __launch_bounds__(kSortThreads) k_embed_sort(const Tok *tokens, 
     // one table row a thread (rows <= threads): its tokens before each warp's, and in all
     int total = 0;
     if (tid < live)
+#pragma unroll
         for (int w = 0; w < kSortWarps; ++w) {
             const int c = cnt[w * rows + tid];
             cnt[w * rows + tid] = total;
@@ -212,25 +220,25 @@ __global__ void __launch_bounds__(kSortThreads) k_embed_sort(const Tok *tokens, 
         start[lo + tid] = first;
         if (lo + tid + 1 == vocab)
             start[vocab] = first + total;
+#pragma unroll
         for (int w = 0; w < kSortWarps; ++w)
             cnt[w * rows + tid] += first;
     }
     __syncthreads();
     for (int64_t i0 = begin; i0 < end; i0 += 32 * kSortAhead) {
-        int64_t t[kSortAhead];
+        if (!once) {
 #pragma unroll
-        for (int k = 0; k < kSortAhead; ++k) {
-            const int64_t i = i0 + 32 * k + lane;
-            t[k] = i < end ? (int64_t)tokens[i] : -1;
+            for (int k = 0; k < kSortAhead; ++k)
+                t[k] = token(i0 + 32 * k + lane);
         }
 #pragma unroll
         for (int k = 0; k < kSortAhead; ++k) {
-            const bool in = t[k] >= lo && t[k] < hi;
+            const bool in = (unsigned)(t[k] - lo32) < (unsigned)live && t[k] >= 0;
             const unsigned any = __ballot_sync(kFull, in);
             if (any == 0)
                 continue;
             if (in) {
-                const int r = (int)(t[k] - lo);
+                const int r = t[k] - lo32;
                 const unsigned same = __match_any_sync(any, r);
                 const int rank = __popc(same & ((1u << lane) - 1u));
                 const int at = mine[r];
@@ -238,6 +246,7 @@ __global__ void __launch_bounds__(kSortThreads) k_embed_sort(const Tok *tokens, 
                 if (rank == 0)
                     mine[r] = at + __popc(same);
                 order[at + rank] = (int32_t)(i0 + 32 * k + lane);
+                sorted[at + rank] = t[k];
             }
             __syncwarp();
         }
@@ -245,49 +254,105 @@ __global__ void __launch_bounds__(kSortThreads) k_embed_sort(const Tok *tokens, 
 }
 
 // ---- the sums -----------------------------------------------------------------------
-template <class G, int E, bool VEC>
-__device__ __forceinline__ void put_row(G *row, int64_t col0, int64_t dim, int lane, const float (&x)[E], float scale,
-                                        bool accumulate) {
-    float v[E];
-    if (VEC) {  // E neighbouring columns, whole vectors
-        const int64_t c = col0 + lane * E;
-        if (c >= dim)
-            return;
-        constexpr int EG = Codec<G>::E;
-        constexpr int kStep = EG < E ? EG : E;
+// Columns of a row by one lane: two quads 128 apart (VEC: each a vector, of 8 or
+// 16 bytes, so that stores of f32 are whole sectors too), or eight a warp's width apart.
+template <bool VEC> struct Part {
+    static constexpr int kSpan = 256;  // columns of a warp
+    float x[8];
+    static __device__ __forceinline__ int64_t col(int64_t c0, int k, int lane) {
+        return VEC ? c0 + 128 * (k / 4) + 4 * lane + k % 4 : c0 + lane + 32 * k;
+    }
+    __device__ __forceinline__ void zero() {
 #pragma unroll
-        for (int b = 0; b < E; b += kStep) {
-            if constexpr (EG <= E) {
-                float y[EG];
-                if (accumulate) {
-                    Codec<G>::unpack(*reinterpret_cast<const uint4 *>(row + c + b), y);
-                } else {
+        for (int k = 0; k < 8; ++k)
+            x[k] = 0.0f;
+    }
+    // the same of a row in storage form
+    template <class S> struct Raw {
+        typename VecOf<S, 4>::T w[2];
+        __device__ __forceinline__ void load(const S *row, int64_t c0, int64_t dim, int lane) {
+            if (VEC) {
 #pragma unroll
-                    for (int k = 0; k < EG; ++k)
-                        y[k] = 0.0f;
+                for (int k = 0; k < 2; ++k) {
+                    const int64_t c = col(c0, 4 * k, lane);
+                    w[k] = *reinterpret_cast<const typename VecOf<S, 4>::T *>(row + (c < dim ? c : 0));  // past the end: not stored
                 }
+            } else {
+                S v[8];
 #pragma unroll
-                for (int k = 0; k < EG; ++k)
-                    y[k] = fmaf(scale, x[b + k], y[k]);
-                st_v4(reinterpret_cast<uint4 *>(row + c + b), Codec<G>::pack(y));
+                for (int k = 0; k < 8; ++k) {
+                    const int64_t c = col(c0, k, lane);
+                    v[k] = row[c < dim ? c : 0];
+                }
+                w[0] = *reinterpret_cast<typename VecOf<S, 4>::T *>(v);
+                w[1] = *reinterpret_cast<typename VecOf<S, 4>::T *>(v + 4);
             }
         }
-    } else {
+        __device__ __forceinline__ void add(Part &to) const {
 #pragma unroll
-        for (int k = 0; k < E; ++k) {
-            const int64_t c = col0 + lane + 32 * k;
-            if (c < dim) {
-                v[k] = accumulate ? Codec<G>::load1(row + c) : 0.0f;
-                Codec<G>::store1(row + c, fmaf(scale, x[k], v[k]));
+            for (int k = 0; k < 2; ++k) {
+                float v[4];
+                widen4<S>(w[k], v);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    to.x[4 * k + e] += v[e];
+            }
+        }
+    };
+    template <class S> __device__ __forceinline__ void load(const S *row, int64_t c0, int64_t dim, int lane) {
+        if (VEC) {
+#pragma unroll
+            for (int k = 0; k < 8; k += 4) {
+                const int64_t c = col(c0, k, lane);
+                float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                if (c < dim)
+                    widen4<S>(*reinterpret_cast<const typename VecOf<S, 4>::T *>(row + c), v);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    x[k + e] = v[e];
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int64_t c = col(c0, k, lane);
+                x[k] = c < dim ? Codec<S>::load1(row + c) : 0.0f;
             }
         }
     }
-}
+    template <class G>
+    __device__ __forceinline__ void store(G *row, int64_t c0, int64_t dim, int lane, float scale, bool accumulate) const {
+        Part old;
+        if (accumulate)
+            old.load(row, c0, dim, lane);
+        else
+            old.zero();
+        if (VEC) {
+#pragma unroll
+            for (int k = 0; k < 8; k += 4) {
+                const int64_t c = col(c0, k, lane);
+                float v[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    v[e] = fmaf(scale, x[k + e], old.x[k + e]);
+                if (c < dim)
+                    *reinterpret_cast<typename VecOf<G, 4>::T *>(row + c) = narrow4<G>(v);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int64_t c = col(c0, k, lane);
+                if (c < dim)
+                    Codec<G>::store1(row + c, fmaf(scale, x[k], old.x[k]));
+            }
+        }
+    }
+};
 
 struct EmbSumArgs {
-    const int32_t *start, *order;
+    const int32_t *start, *order, *sorted;
     float *partial;  // [pieces][2][dim]: of the run that came in, of the run that goes on
-    int64_t vocab, dim, pieces;
+    int32_t *last;   // [pieces]: the last piece of the run that begins here and goes on, or 0
+    int64_t vocab, dim, pieces, ntokens;
     int piece;
     float scale;
     int accumulate;
@@ -296,82 +361,86 @@ struct EmbSumArgs {
 
 constexpr int kSumThreads = 256;
 constexpr int kSumWarps = kSumThreads / 32;
-constexpr int kSumAhead = 4;  // rows of dout in flight per warp
+constexpr int kSumAhead = 8;  // rows of dout in flight per warp
 constexpr int kPieceMost = 1024;
+constexpr int kClearRows = 16;  // looked at together by a clearing warp
 
-// One CTA sums one piece of the sorted order, each warp its columns: it walks
-// the piece's rows with four of them in flight, and where the token changes
-// the run's sum leaves the registers. The dout rows are read once, so this
-// is bound by bytes: T*H of dout and V*H of the table's gradient, the larger part.
-template <class S, class G, class Tok, bool VEC>
-__global__ void __launch_bounds__(kSumThreads) k_embed_sum(const Tok *tokens, const S *dout, G *dtable, EmbSumArgs a) {
-    __shared__ int32_t s_pos[kPieceMost], s_tok[kPieceMost];
+// One CTA sums one piece of the sorted order, each warp its columns: it takes
+// the piece's rows a few at a time, all loaded before the first is added, and where the token
+// changes the run's sum leaves the registers. Where each sum goes is worked
+// out once for the piece, so a row costs its loads, its additions and one test. The dout rows are read once: bound
+// by bytes, T*H of dout and V*H of the table's gradient, the larger part.
+constexpr int kNowhere = -1, kHead = -2, kTail = -3;  // where a row's sum goes, but for a row of the table
+
+template <class S, class G, bool VEC>
+__global__ void __launch_bounds__(kSumThreads, 2) k_embed_sum(const S *dout, G *dtable, EmbSumArgs a) {
+    __shared__ int32_t s_pos[kPieceMost], s_to[kPieceMost], s_tok[kPieceMost];
     pdl_prologue();
-    using R = RowPart<S, VEC>;
-    constexpr int E = R::E;
+    using R = Part<VEC>;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if ((int64_t)blockIdx.x >= a.pieces) {  // rows that no token names
-        if (a.accumulate)
-            return;
-        float z[E];
-#pragma unroll
-        for (int k = 0; k < E; ++k)
-            z[k] = 0.0f;
-        const int64_t w0 = ((int64_t)blockIdx.x - a.pieces) * kSumWarps + warp;
-        for (int64_t v = w0; v < a.vocab; v += a.clear_ctas * kSumWarps)
-            if (a.start[v] == a.start[v + 1])
+    // pieces and clearing CTAs take turns, so that reading and writing overlap
+    const int64_t pair = blockIdx.x / 2, both = a.pieces < a.clear_ctas ? a.pieces : a.clear_ctas;
+    const bool clears = pair < both ? (blockIdx.x & 1) != 0 : a.clear_ctas > a.pieces;
+    const int64_t index = pair < both ? pair : (int64_t)blockIdx.x - both;
+    if (clears) {  // rows that no token names
+        R z;
+        z.zero();
+        for (int64_t v0 = (index * kSumWarps + warp) * kClearRows; v0 < a.vocab; v0 += a.clear_ctas * kSumWarps * kClearRows) {
+            const int64_t v = v0 + lane;
+            unsigned none = __ballot_sync(kFull, lane < kClearRows && v < a.vocab && a.start[v < a.vocab ? v : 0] == a.start[v < a.vocab ? v + 1 : 0]);
+            for (; none != 0; none &= none - 1) {
+                const int64_t row = v0 + __ffs(none) - 1;
                 for (int64_t c0 = 0; c0 < a.dim; c0 += R::kSpan)
-                    put_row<G, E, VEC>(dtable + v * a.dim, c0, a.dim, lane, z, 0.0f, false);
+                    z.store(dtable + row * a.dim, c0, a.dim, lane, 0.0f, false);
+            }
+        }
         return;
     }
     const int64_t total = a.start[a.vocab];
-    const int64_t p0 = (int64_t)blockIdx.x * a.piece;
-    if (p0 >= total)
+    const int64_t p0 = index * a.piece;
+    for (int i = tid; i < a.piece && p0 + i < a.ntokens; i += kSumThreads) {  // past the total: not used
+        s_pos[i] = a.order[p0 + i];
+        s_tok[i] = a.sorted[p0 + i];
+    }
+    if (p0 >= total) {
+        if (tid == 0)
+            a.last[index] = 0;
         return;
+    }
     const int n = (int)(total - p0 < a.piece ? total - p0 : a.piece);
+    __syncthreads();
     for (int i = tid; i < n; i += kSumThreads) {
-        const int32_t at = a.order[p0 + i];
-        s_pos[i] = at;
-        s_tok[i] = (int32_t)tokens[at];
+        const int32_t tok = s_tok[i];
+        int32_t to = kNowhere;
+        if (i + 1 == n || s_tok[i + 1] != tok) {
+            const int64_t from = a.start[tok], end = a.start[tok + 1];
+            to = from < p0 ? kHead : end > p0 + n ? kTail : tok;
+            if (i + 1 == n)  // a run that begins here and goes on is this piece's to join
+                a.last[index] = to == kTail ? (int32_t)((end - 1) / a.piece) : 0;
+        }
+        s_to[i] = to;
     }
     __syncthreads();
-    const bool comes_in = a.start[s_tok[0]] < p0;           // the first run began before this piece
-    const bool goes_on = a.start[s_tok[n - 1] + 1] > p0 + n;  // the last run ends after it
-    float *head = a.partial + (int64_t)blockIdx.x * 2 * a.dim, *tail = head + a.dim;
+    float *head = a.partial + index * 2 * a.dim, *tail = head + a.dim;
     for (int64_t c0 = (int64_t)warp * R::kSpan; c0 < a.dim; c0 += (int64_t)kSumWarps * R::kSpan) {
-        R buf[kSumAhead];
-#pragma unroll
-        for (int k = 0; k < kSumAhead; ++k)
-            if (k < n)
-                buf[k].load(dout + (int64_t)s_pos[k] * a.dim, c0, a.dim, lane);
-        float acc[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            acc[e] = 0.0f;
-        bool first = true;
+        R acc;
+        acc.zero();
         for (int i0 = 0; i0 < n; i0 += kSumAhead) {
+            typename R::template Raw<S> buf[kSumAhead];
+#pragma unroll
+            for (int k = 0; k < kSumAhead; ++k)
+                buf[k].load(dout + (int64_t)s_pos[i0 + k < n ? i0 + k : n - 1] * a.dim, c0, a.dim, lane);
 #pragma unroll
             for (int k = 0; k < kSumAhead; ++k) {
-                const int i = i0 + k;
-                if (i < n) {
-#pragma unroll
-                    for (int e = 0; e < E; ++e)
-                        acc[e] += buf[k].x[e];
-                    if (i + kSumAhead < n)
-                        buf[k].load(dout + (int64_t)s_pos[i + kSumAhead] * a.dim, c0, a.dim, lane);
-                    const int32_t tok = s_tok[i];
-                    const bool last = i + 1 == n;
-                    if (last || s_tok[i + 1] != tok) {
-                        if (first && comes_in)
-                            put_row<float, E, VEC>(head, c0, a.dim, lane, acc, 1.0f, false);
-                        else if (last && goes_on)
-                            put_row<float, E, VEC>(tail, c0, a.dim, lane, acc, 1.0f, false);
+                if (i0 + k < n) {
+                    buf[k].add(acc);
+                    const int32_t to = s_to[i0 + k];
+                    if (to != kNowhere) {
+                        if (to >= 0)
+                            acc.store(dtable + (int64_t)to * a.dim, c0, a.dim, lane, a.scale, a.accumulate);
                         else
-                            put_row<G, E, VEC>(dtable + (int64_t)tok * a.dim, c0, a.dim, lane, acc, a.scale, a.accumulate);
-                        first = false;
-#pragma unroll
-                        for (int e = 0; e < E; ++e)
-                            acc[e] = 0.0f;
+                            acc.store(to == kHead ? head : tail, c0, a.dim, lane, 1.0f, false);
+                        acc.zero();
                     }
                 }
             }
@@ -379,27 +448,62 @@ __global__ void __launch_bounds__(kSumThreads) k_embed_sum(const Tok *tokens, co
     }
 }
 
-// The run that begins in piece p and goes on: its sum over the pieces, in order.
-template <class G, class Tok>
-__global__ void __launch_bounds__(kSumThreads) k_embed_join(const Tok *tokens, G *dtable, EmbSumArgs a) {
+// Runs that go on: their sums over the pieces. A warp takes one of the CTA's eight
+// pieces, and 128 columns of the run that begins there; a run over more than
+// kFewPieces is left to all eight warps, of which each adds every eighth
+// piece, and the eight sums are added in order: a token that fills
+// hundreds of pieces is not one chain of loads.
+constexpr int kFewPieces = 12;
+
+template <class G>
+__global__ void __launch_bounds__(kSumThreads) k_embed_join(G *dtable, EmbSumArgs a) {
+    __shared__ float s_sum[kSumWarps][128];
     pdl_prologue();
-    const int64_t p = blockIdx.x;
-    const int64_t total = a.start[a.vocab];
-    const int64_t end = (p + 1) * a.piece;
-    if (end >= total)
-        return;
-    const int32_t tok = (int32_t)tokens[a.order[end - 1]];
-    const int64_t from = a.start[tok], to = a.start[tok + 1];
-    if (to <= end || from < p * a.piece)
-        return;
-    const int64_t q = (to - 1) / a.piece;  // its last piece
-    for (int64_t c = (int64_t)blockIdx.y * kSumThreads + threadIdx.x; c < a.dim; c += (int64_t)gridDim.y * kSumThreads) {
-        float s = a.partial[(p * 2 + 1) * a.dim + c];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t p0 = (int64_t)blockIdx.x * kSumWarps, c0 = (int64_t)blockIdx.y * 128 + lane;  // columns c0 + 32 k
+    const int32_t mine = lane < kSumWarps && p0 + lane < a.pieces ? a.last[p0 + lane] : 0;
+    const auto add = [&](int64_t from, int64_t to, int64_t first, int64_t by, float (&s)[4]) {
 #pragma unroll 4
-        for (int64_t k = p + 1; k <= q; ++k)
-            s += a.partial[k * 2 * a.dim + c];
-        G *at = dtable + (int64_t)tok * a.dim + c;
-        Codec<G>::store1(at, fmaf(a.scale, s, a.accumulate ? Codec<G>::load1(at) : 0.0f));
+        for (int64_t k = from; k <= to; k += by) {
+            const float *row = a.partial + (k == first ? k * 2 + 1 : k * 2) * a.dim;  // where it begins: the run that goes on
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                s[e] += c0 + 32 * e < a.dim ? row[c0 + 32 * e] : 0.0f;
+        }
+    };
+    const auto put = [&](int64_t p, const float (&s)[4]) {
+        G *row = dtable + (int64_t)a.sorted[(p + 1) * a.piece - 1] * a.dim;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (c0 + 32 * e < a.dim)
+                Codec<G>::store1(row + c0 + 32 * e, fmaf(a.scale, s[e], a.accumulate ? Codec<G>::load1(row + c0 + 32 * e) : 0.0f));
+    };
+    const int64_t q = __shfl_sync(kFull, mine, warp), p = p0 + warp;
+    if (q != 0 && q - p < kFewPieces) {
+        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        add(p, q, p, 1, s);
+        put(p, s);
+    }
+    unsigned many = __ballot_sync(kFull, mine != 0 && mine - (p0 + lane) >= kFewPieces);
+    for (; many != 0; many &= many - 1) {  // the same for all warps
+        const int i = __ffs(many) - 1;
+        const int64_t first = p0 + i, end = __shfl_sync(kFull, mine, i);
+        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        add(first + warp, end, first, kSumWarps, s);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            s_sum[warp][lane + 32 * e] = s[e];
+        __syncthreads();
+        if (warp == 0) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+#pragma unroll
+                for (int w = 1; w < kSumWarps; ++w)
+                    s[e] += s_sum[w][lane + 32 * e];
+            }
+            put(first, s);
+        }
+        __syncthreads();
     }
 }
 
@@ -410,14 +514,15 @@ EmbedGradPlan embed_grad_plan(int64_t tokens, int64_t vocab, int64_t dim) {
     rows = rows < 32 ? 32 : rows > kSortRows ? kSortRows : rows;
     p.rows_per_cta = rows;
     p.ctas = (vocab + rows - 1) / rows;
-    // short pieces spread a long run over the GPU; their partial sums stay few
-    p.piece = 32;
-    while (p.piece < kPieceMost && tokens / p.piece > 4096)
+    // short pieces spread the rows, and a long run, over the GPU; their partial sums stay few
+    p.piece = 8;
+    while (p.piece < kPieceMost && tokens / p.piece > 1024)
         p.piece *= 2;
     p.pieces = (tokens + p.piece - 1) / p.piece;
     p.start_slots = (vocab + 1 + 3) / 4 * 2;  // int32, 16-byte rounded
     p.order_slots = (tokens + 3) / 4 * 2;
     p.partial_slots = p.pieces * dim;  // two rows of f32 a piece
+    p.last_slots = (p.pieces + 3) / 4 * 2;
     return p;
 }
 
@@ -428,16 +533,22 @@ static cudaError_t embed_grad_go(const void *tokens, int64_t n, const void *dout
     EmbSumArgs a;
     int32_t *start = reinterpret_cast<int32_t *>(scratch);
     int32_t *order = reinterpret_cast<int32_t *>(scratch + p.start_slots);
+    int32_t *sorted = reinterpret_cast<int32_t *>(scratch + p.start_slots + p.order_slots);
     a.start = start;
     a.order = order;
-    a.partial = reinterpret_cast<float *>(scratch + p.start_slots + p.order_slots);
+    a.sorted = sorted;
+    a.last = reinterpret_cast<int32_t *>(scratch + p.start_slots + 2 * p.order_slots);
+    a.partial = reinterpret_cast<float *>(scratch + p.start_slots + 2 * p.order_slots + p.last_slots);
     a.vocab = vocab;
     a.dim = dim;
     a.pieces = p.pieces;
+    a.ntokens = n;
     a.piece = (int)p.piece;
     a.scale = scale;
     a.accumulate = accumulate;
-    a.clear_ctas = accumulate ? 0 : 2 * (int64_t)L.sm_count;
+    a.clear_ctas = accumulate ? 0 : (vocab + kClearRows * kSumWarps - 1) / (kClearRows * kSumWarps);
+    if (a.clear_ctas > 4 * (int64_t)L.sm_count)
+        a.clear_ctas = 4 * (int64_t)L.sm_count;
     const Tok *t = static_cast<const Tok *>(tokens);
     const S *d = static_cast<const S *>(dout);
     G *g = static_cast<G *>(dtable);
@@ -446,22 +557,30 @@ static cudaError_t embed_grad_go(const void *tokens, int64_t n, const void *dout
     if (e != cudaSuccess)
         return e;
     note_launch();
-    e = launch_pdl(k_embed_sort<Tok>, (unsigned)p.ctas, kSortThreads, smem, L.stream, t, n, vocab, (int)p.rows_per_cta, start, order);
+    e = launch_pdl(k_embed_sort<Tok>, (unsigned)p.ctas, kSortThreads, smem, L.stream, t, n, vocab, (int)p.rows_per_cta, start, order, sorted);
     if (e != cudaSuccess)
         return e;
-    const bool vec = dim % Codec<S>::E == 0 && dim % Codec<G>::E == 0 && (uintptr_t)dout % 16 == 0 &&
-                     (uintptr_t)dtable % 16 == 0 && sizeof(G) >= sizeof(S);
+    const bool vec = dim % 4 == 0 && (uintptr_t)dout % (4 * sizeof(S)) == 0 && (uintptr_t)dtable % (4 * sizeof(G)) == 0;
     const unsigned grid = (unsigned)(p.pieces + a.clear_ctas);
     if (grid > 0) {
         note_launch();
-        e = vec ? launch_pdl(k_embed_sum<S, G, Tok, true>, grid, kSumThreads, 0, L.stream, t, d, g, a)
-                : launch_pdl(k_embed_sum<S, G, Tok, false>, grid, kSumThreads, 0, L.stream, t, d, g, a);
+        e = vec ? launch_pdl(k_embed_sum<S, G, true>, grid, kSumThreads, 0, L.stream, d, g, a)
+                : launch_pdl(k_embed_sum<S, G, false>, grid, kSumThreads, 0, L.stream, d, g, a);
         if (e != cudaSuccess)
             return e;
     }
     if (p.pieces > 1) {
         note_launch();
-        e = launch_pdl(k_embed_join<G, Tok>, (unsigned)(p.pieces - 1), kSumThreads, 0, L.stream, t, g, a);
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)((p.pieces + kSumWarps - 1) / kSumWarps), (unsigned)((dim + 127) / 128));
+        cfg.blockDim = dim3(kSumThreads);
+        cfg.stream = L.stream;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        e = cudaLaunchKernelEx(&cfg, k_embed_join<G>, g, a);
     }
     return e;
 }

@@ -13,7 +13,7 @@ struct EmbedGradPlan {
     int64_t ctas;          // CTAs of the sort
     int64_t piece;         // sorted tokens per piece of the sum
     int64_t pieces;
-    int64_t start_slots, order_slots, partial_slots;  // 8-byte slots of the scratch's parts
+    int64_t start_slots, order_slots, last_slots, partial_slots;  // 8-byte slots of the scratch's parts
 };
 EmbedGradPlan embed_grad_plan(int64_t tokens, int64_t vocab, int64_t dim);
 cudaError_t embed_launch(const void *tokens, bool wide_tokens, int64_t ntokens, const void *table, int64_t vocab,

@@ -133,10 +133,10 @@ extern "C" int mt_embed(const void *tokens, int64_t ntokens, int token_dtype, co
 
 extern "C" int64_t mt_embed_grad_scratch_slots(int64_t ntokens, int64_t vocab, int64_t dim) {
     if (ntokens < 0 || vocab < 0 || dim < 0 || ntokens > INT32_MAX - 64 || vocab > INT32_MAX - 64 ||
-        product({ntokens, dim, 8}) < 0 || product({vocab, dim, 8}) < 0)
+        product({ntokens, dim, 8}) < 0 || product({vocab, dim, 8}) < 0 || dim > 65535 * 32)
         return -1;
     const EmbedGradPlan p = embed_grad_plan(ntokens, vocab, dim);
-    return p.start_slots + p.order_slots + p.partial_slots;
+    return p.start_slots + 2 * p.order_slots + p.last_slots + p.partial_slots;
 }
 
 extern "C" int mt_embed_grad(const void *tokens, int64_t ntokens, int token_dtype, const void *dout, int dtype,
