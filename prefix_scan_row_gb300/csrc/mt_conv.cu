@@ -17,12 +17,6 @@
 namespace mt {
 
 constexpr int kConvThreads = 128;
-#ifndef MT_XCC
-#define MT_XCC 6
-#endif
-#ifndef MT_XCN
-#define MT_XCN 32
-#endif
 
 // Four values of one lane in storage form: neighbouring channels moved as one
 // (ALN), or channels 32 apart (rows that no vector fits), of which `live` exist.
@@ -69,6 +63,44 @@ template <class S, bool ALN> struct Quad {
         w.w = narrow4<S>(v);
     }
 };
+// Tokens on their way to a lane: GROUPS groups of EACH quads, asked for in
+// order and taken in order. Quads that are vectors are copied into the lane's
+// own places in shared memory, so no register waits for them and the whole ring is in flight;
+// the others are loaded one group ahead.
+template <class S, bool ALN, int GROUPS, int EACH> struct Ring {
+    static constexpr int kBytes = ALN ? GROUPS * EACH * 4 * (int)sizeof(S) : 0;  // of a lane
+    char *mine;  // the lane's place in the first quad; quads lie 32 lanes apart
+    Quad<S, ALN> next[ALN ? 1 : EACH];
+    __device__ __forceinline__ void set(char *warp, int lane) { mine = warp + lane * 4 * (int)sizeof(S); }
+    __device__ __forceinline__ void ask(int group, const S *from, int64_t stride, int left, int live) {
+        if constexpr (ALN) {
+#pragma unroll
+            for (int j = 0; j < EACH; ++j)
+                cp_async_zfill<4 * sizeof(S)>(smem_addr(mine) + (group % GROUPS * EACH + j) * 32 * 4 * (int)sizeof(S),
+                                              j < left ? from + j * stride : from, j < left);
+            cp_async_commit();
+        } else {
+#pragma unroll
+            for (int j = 0; j < EACH; ++j) {
+                next[j].zero();
+                if (j < left)
+                    next[j].load(from + j * stride, live);
+            }
+        }
+    }
+    __device__ __forceinline__ void take(int group, Quad<S, ALN> (&v)[EACH]) {
+        if constexpr (ALN) {
+#pragma unroll
+            for (int j = 0; j < EACH; ++j)
+                v[j].w.w = *reinterpret_cast<const typename VecOf<S, 4>::T *>(mine + (group % GROUPS * EACH + j) * 32 * 4 * (int)sizeof(S));
+        } else {
+#pragma unroll
+            for (int j = 0; j < EACH; ++j)
+                v[j] = next[j];
+        }
+    }
+};
+
 // A lane's first channel, how many it has, and the distance between them.
 template <bool ALN> struct ConvLane {
     int64_t c;
@@ -157,23 +189,23 @@ __device__ __forceinline__ void conv_params(const ConvDims &d, const ConvLane<AL
 // ---- forward ------------------------------------------------------------------------
 // Tokens per lane: at 32 the W-1 inputs read twice are a tenth of the
 // bytes and come from L2.
-constexpr int kConvSpan = MT_XCN;
-#ifndef MT_XCA
-#define MT_XCA 8
-#endif
-constexpr int kConvAhead = MT_XCA;  // tokens loaded together, while as many before them are worked on
+constexpr int kConvSpan = 64;
+constexpr int kConvAhead = 4, kConvGroups = 4;  // tokens of a group, groups on their way
 
 template <class S, bool ALN, int W, bool SILU>
-__global__ void __launch_bounds__(kConvThreads, MT_XCC) k_conv(const S *x, S *out, S *state, ConvDims d, int64_t groups,
+__global__ void __launch_bounds__(kConvThreads, 5) k_conv(const S *x, S *out, S *state, ConvDims d, int64_t groups,
                                                        int64_t spans) {
     pdl_prologue();
+    using Rng = Ring<S, ALN, kConvGroups, kConvAhead>;
+    __shared__ __align__(16) char s_ring[ALN ? kConvThreads * Rng::kBytes : 16];
+    Rng ring;
     const int64_t i = (int64_t)blockIdx.x * (kConvThreads / 32) + (threadIdx.x >> 5);
-    const int64_t group = i % groups, bs = i / groups;
+    const int64_t cgroup = i % groups, bs = i / groups;
     const int64_t span = bs % spans, b = bs / spans;
     if (b >= d.batch)
         return;
     ConvLane<ALN> at;
-    at.set(group, threadIdx.x & 31, d.dim);
+    at.set(cgroup, threadIdx.x & 31, d.dim);
     if (at.live == 0)
         return;
     const int64_t n = live_len(d.lens, d.len, b);
@@ -200,28 +232,23 @@ __global__ void __launch_bounds__(kConvThreads, MT_XCC) k_conv(const S *x, S *ou
     }
     const int tokens = (int)(t1 - t0), here = !active || n <= t0 ? 0 : n < t1 ? (int)(n - t0) : tokens;  // that exist
     const S *xt = xs + t0 * d.xt;
-    // token tt + j + kConvAhead is asked for as token tt + j is taken
-    Quad<S, ALN> ring[kConvAhead];
+    constexpr int kDeep = ALN ? kConvGroups : 1;
+    ring.set(s_ring + (threadIdx.x >> 5) * 32 * Rng::kBytes, threadIdx.x & 31);
 #pragma unroll
-    for (int j = 0; j < kConvAhead; ++j) {
-        ring[j].zero();
-        if (j < here)
-            ring[j].load(xt + j * d.xt, at.live);
-    }
-    xt += kConvAhead * d.xt;
-    // FULL: every token of the batch, and of the next, exists
-    const auto batch = [&](int tt, auto full) {
-        constexpr bool FULL = decltype(full)::value;
+    for (int g = 0; g < kDeep; ++g)
+        ring.ask(g, xt + g * kConvAhead * d.xt, d.xt, here - g * kConvAhead, at.live);
+    xt += kDeep * kConvAhead * d.xt;
+    int group = 0;
+    for (int tt = 0; tt < tokens; tt += kConvAhead, ++group) {
+        Quad<S, ALN> v[kConvAhead];
+        if (ALN)
+            cp_async_wait<kDeep - 1>();
+        ring.take(group, v);
+        ring.ask(group, xt, d.xt, here - tt - kDeep * kConvAhead, at.live);  // in the place of what was taken
+        xt += kConvAhead * d.xt;
 #pragma unroll
         for (int j = 0; j < kConvAhead; ++j) {
-            ring[j].widen(h[W - 1]);
-            if (FULL) {
-                ring[j].load(xt + j * d.xt, at.live);
-            } else {
-                ring[j].zero();
-                if (tt + j + kConvAhead < here)
-                    ring[j].load(xt + j * d.xt, at.live);
-            }
+            v[j].widen(h[W - 1]);
             f32x2 o[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -231,24 +258,16 @@ __global__ void __launch_bounds__(kConvThreads, MT_XCC) k_conv(const S *x, S *ou
                     p = fma2f(w[k][e], h[k][e], p);
                 if (SILU)
                     p = mul2f(p, sigmoid_2f(p));
-                o[e] = FULL || tt + j < here ? p : 0ull;
+                o[e] = tt + j < here ? p : 0ull;
 #pragma unroll
                 for (int k = 0; k < W - 1; ++k)
                     h[k][e] = h[k + 1][e];
             }
-            Quad<S, ALN> v;
-            v.narrow(o);
-            if (FULL || tt + j < tokens)
-                v.store(os + j * d.ot, at.live);
+            v[j].narrow(o);
+            if (tt + j < tokens)
+                v[j].store(os, at.live);
+            os += d.ot;
         }
-        xt += kConvAhead * d.xt;
-        os += kConvAhead * d.ot;
-    };
-    for (int tt = 0; tt < tokens; tt += kConvAhead) {
-        if (tt + 2 * kConvAhead <= here)
-            batch(tt, std::true_type());
-        else
-            batch(tt, std::false_type());
     }
     // The lane of the first span is the only one that reads the state, so it
     // is also the one that writes it: the last W-1 inputs of the sequence.
@@ -315,20 +334,8 @@ __global__ void __launch_bounds__(kConvThreads) k_conv_step(const S *x, S *out, 
 // too, without the sums. The sums of a span are 4(W+1) bytes against its
 // 6 * kGradSpan bytes of activations; they are added over a CTA's spans in
 // shared memory, written once per CTA and added by a second kernel in order.
-#ifndef MT_XCF
-#define MT_XCF 4
-#endif
-#ifndef MT_XCS
-#define MT_XCS 64
-#endif
-#ifndef MT_XCB
-#define MT_XCB 2
-#endif
-#ifndef MT_XCC
-#define MT_XCC 4
-#endif
-constexpr int kFew = MT_XCF;  // tokens loaded together
-constexpr int kGradSpan = MT_XCS;
+constexpr int kFew = 4, kGradGroups = 2;  // tokens of a group, groups on their way
+constexpr int kGradSpan = 64;
 constexpr int kGradSpans = 8;  // a CTA: 128 channels x 8 spans, a warp a span
 constexpr int kGradThreads = 32 * kGradSpans;
 
@@ -339,15 +346,19 @@ __device__ __forceinline__ f32x2 act_grad(f32x2 p) {
 }
 
 template <class S, bool ALN, int W, bool SILU>
-__global__ void __launch_bounds__(kGradThreads, MT_XCB) k_conv_grad(const S *x, const S *dout, S *dx, const S *state, S *dstate,
+__global__ void __launch_bounds__(kGradThreads, 2) k_conv_grad(const S *x, const S *dout, S *dx, const S *state, S *dstate,
                                                             float *partial, ConvDims d, int64_t groups, int64_t span_blocks) {
-    __shared__ float s_sum[W + 1][kGradSpans][128];
+    using Rng = Ring<S, ALN, kGradGroups, kFew>;
+    // the rings, and after them the sums
+    constexpr int kRings = ALN ? 2 * kGradThreads * Rng::kBytes : 16, kSums = (W + 1) * kGradSpans * 128 * 4;
+    __shared__ __align__(16) char s_ring[kRings > kSums ? kRings : kSums];
+    float(*s_sum)[kGradSpans][128] = reinterpret_cast<float(*)[kGradSpans][128]>(s_ring);
     pdl_prologue();
     const int lane = threadIdx.x & 31, sp = threadIdx.x >> 5;
-    const int64_t group = blockIdx.x % groups, rest = blockIdx.x / groups;
+    const int64_t cgroup = blockIdx.x % groups, rest = blockIdx.x / groups;
     const int64_t sb = rest % span_blocks, b = rest / span_blocks;
     ConvLane<ALN> at;
-    at.set(group, lane, d.dim);
+    at.set(cgroup, lane, d.dim);
     f32x2 sums[W + 1][2];  // dw, then dbias
 #pragma unroll
     for (int k = 0; k <= W; ++k)
@@ -375,35 +386,35 @@ __global__ void __launch_bounds__(kGradThreads, MT_XCB) k_conv_grad(const S *x, 
         const int here = n <= t0 ? 0 : n - t0 < walk ? (int)(n - t0) : walk;  // that exist
         const S *xp = xs + t0 * d.xt, *gp = dout + b * d.gb + t0 * d.gt + at.c;
         S *dp = dx + b * d.db + t0 * d.dt + at.c;
-        Quad<S, ALN> rx[kFew], rg[kFew];
+        constexpr int kDeep = ALN ? kGradGroups : 1;
+        Rng rx, rg;
+        rx.set(s_ring + sp * 64 * Rng::kBytes, lane);
+        rg.set(s_ring + (sp * 64 + 32) * Rng::kBytes, lane);
 #pragma unroll
-        for (int j = 0; j < kFew; ++j) {
-            rx[j].zero();
-            rg[j].zero();
-            if (j < here) {
-                rx[j].load(xp + j * d.xt, at.live);
-                rg[j].load(gp + j * d.gt, at.live);
-            }
+        for (int g = 0; g < kDeep; ++g) {
+            rx.ask(g, xp + g * kFew * d.xt, d.xt, here - g * kFew, at.live);
+            rg.ask(g, gp + g * kFew * d.gt, d.gt, here - g * kFew, at.live);
         }
-        xp += kFew * d.xt;
-        gp += kFew * d.gt;
-        // FULL: the batch's tokens are this span's, their dx too, and the next batch exists
-        const auto batch = [&](int tt, auto full) {
-            constexpr bool FULL = decltype(full)::value;
+        xp += kDeep * kFew * d.xt;
+        gp += kDeep * kFew * d.gt;
+        dp -= (W - 1) * d.dt;
+        int group = 0;
+        for (int tt = 0; tt < walk; tt += kFew, ++group) {
+            Quad<S, ALN> vx[kFew], vg[kFew];
+            if (ALN)
+                cp_async_wait<2 * kDeep - 2>();
+            rx.take(group, vx);
+            rg.take(group, vg);
+            rx.ask(group, xp, d.xt, here - tt - kDeep * kFew, at.live);  // in the place of what was taken
+            rg.ask(group, gp, d.gt, here - tt - kDeep * kFew, at.live);
+            xp += kFew * d.xt;
+            gp += kFew * d.gt;
 #pragma unroll
             for (int j = 0; j < kFew; ++j) {
                 f32x2 g[2], o[2];
-                rx[j].widen(h[W - 1]);
-                rg[j].widen(g);
-                if (!FULL) {
-                    rx[j].zero();
-                    rg[j].zero();
-                }
-                if (FULL || tt + j + kFew < here) {
-                    rx[j].load(xp + j * d.xt, at.live);
-                    rg[j].load(gp + j * d.gt, at.live);
-                }
-                const bool own = FULL || tt + j < tokens;
+                vx[j].widen(h[W - 1]);
+                vg[j].widen(g);
+                const bool own = tt + j < tokens;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     f32x2 p = bias[e];
@@ -428,26 +439,19 @@ __global__ void __launch_bounds__(kGradThreads, MT_XCB) k_conv_grad(const S *x, 
                     q[W - 1][e] = 0ull;
                 }
                 const int to = tt + j - (W - 1);  // the token whose dx is done
-                if (!FULL && to >= here)
+                if (to >= here)
                     o[0] = o[1] = 0ull;
-                Quad<S, ALN> v;
-                v.narrow(o);
-                if (FULL || (to >= 0 && to < tokens))
-                    v.store(dp + (j - (W - 1)) * d.dt, at.live);
+                vg[j].narrow(o);
+                if (to >= 0 && to < tokens)
+                    vg[j].store(dp, at.live);
                 else if (to < 0 && dst != nullptr)
-                    v.store(dst + (to + W - 1) * d.dim, at.live);
+                    vg[j].store(dst + (to + W - 1) * d.dim, at.live);
+                dp += d.dt;
             }
-            xp += kFew * d.xt;
-            gp += kFew * d.gt;
-            dp += kFew * d.dt;
-        };
-        for (int tt = 0; tt < walk; tt += kFew) {
-            if (tt >= W - 1 && tt + kFew <= tokens && tt + 2 * kFew <= here)
-                batch(tt, std::true_type());
-            else
-                batch(tt, std::false_type());
         }
     }
+    cp_async_wait_all();
+    __syncthreads();  // the rings are done with
 #pragma unroll
     for (int k = 0; k <= W; ++k) {
         float v[4];
@@ -461,7 +465,7 @@ __global__ void __launch_bounds__(kGradThreads, MT_XCB) k_conv_grad(const S *x, 
     float *row = partial + (b * span_blocks + sb) * (W + 1) * d.dim;
     for (int i = threadIdx.x; i < (W + 1) * 128; i += kGradThreads) {
         const int k = i / 128, c = i % 128;
-        const int64_t ch = group * 128 + c;
+        const int64_t ch = cgroup * 128 + c;
         if (ch < d.dim) {
             float s = 0.0f;
 #pragma unroll

@@ -72,6 +72,19 @@ template <class S> __device__ __forceinline__ void store4(S *p, const float (&x)
     }
 }
 
+// ---- asynchronous copies to shared memory ------------------------------------------
+// Zeros where `in` is false (the source is then not read).
+template <int BYTES> __device__ __forceinline__ void cp_async_zfill(uint32_t dst, const void *src, bool in) {
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" :: "r"(dst), "l"(src), "r"(in ? BYTES : 0), "n"(BYTES) : "memory");
+}
+
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// until at most LEFT of the thread's groups are on their way
+template <int LEFT> __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(LEFT) : "memory"); }
+
 // ---- scalar functions ---------------------------------------------------------
 __device__ __forceinline__ float ex2f(float x) {
     float y;
@@ -159,5 +172,13 @@ __device__ __forceinline__ f32x2 softplus_2f(f32x2 x) {
     return fma2f(add2f(s, s), p, pack2f(fmaxf(a, 0.0f), fmaxf(b, 0.0f)));
 }
 __device__ __forceinline__ f32x2 sigmoid_2f(f32x2 x) { return rcp_2f(add2f(both(1.0f), ex2_2f(mul2f(both(-kLog2e), x)))); }
+
+// a where yes, else b
+__device__ __forceinline__ f32x2 choose_2f(bool yes, f32x2 a, f32x2 b) {
+    float a0, a1, b0, b1;
+    unpack2f(a, a0, a1);
+    unpack2f(b, b0, b1);
+    return pack2f(yes ? a0 : b0, yes ? a1 : b1);
+}
 
 }  // namespace mt

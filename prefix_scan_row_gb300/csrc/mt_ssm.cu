@@ -9,15 +9,12 @@ namespace mt {
 // device (scratch is sized on the host), so it counts GB300's 152 SMs.
 constexpr int64_t kSsmSms = 152;
 constexpr int64_t kEnoughWarps = kSsmSms * 5;   // from here on the tokens are not cut
-#ifndef MT_XT
-#define MT_XT 24
+constexpr int64_t kTargetWarps = kSsmSms * 24;  // what a cut aims at
+constexpr int64_t kTargetCtas = kSsmSms * 9;    // the same for the gradient's CTAs
+#ifndef MT_XL
+#define MT_XL 64
 #endif
-constexpr int64_t kTargetWarps = kSsmSms * MT_XT;  // what a cut aims at
-#ifndef MT_XGT
-#define MT_XGT 9
-#endif
-constexpr int64_t kTargetCtas = kSsmSms * MT_XGT;    // the same for the gradient's CTAs
-constexpr int64_t kLeastSegment = 64;           // tokens: below, a carry costs more than it frees
+constexpr int64_t kLeastSegment = MT_XL;           // tokens: below, a carry costs more than it frees
 
 SsmPlan ssm_plan(int64_t batch, int64_t len, int64_t dim, int64_t nstate, int64_t groups, bool grad) {
     SsmPlan p;

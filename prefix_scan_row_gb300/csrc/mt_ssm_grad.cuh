@@ -29,10 +29,6 @@
 
 namespace mt {
 
-#ifndef MT_XG
-#define MT_XG 3
-#endif
-
 __device__ __forceinline__ void mark_store(float4 *m, int lane, const Pairs &h) {
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
@@ -109,7 +105,7 @@ template <class S, int P> struct GradSmem {
 };
 
 template <class S, int P, bool ALN>
-__global__ void __launch_bounds__(kSsmThreads, sizeof(S) == 2 && P <= 8 ? MT_XG : 2) k_ssm_grad(const __grid_constant__ SsmArgs a) {
+__global__ void __launch_bounds__(kSsmThreads, sizeof(S) == 2 && P <= 8 ? 3 : 2) k_ssm_grad(const __grid_constant__ SsmArgs a) {
     extern __shared__ float4 smem4[];
     using M = GradSmem<S, P>;
     using R = typename M::R;

@@ -21,27 +21,8 @@
 namespace mt {
 
 constexpr int kStep = kSsmTile;  // tokens per stage, and per checkpoint
-#ifndef MT_XF
-#define MT_XF 3
-#endif
-#ifndef MT_XC
-#define MT_XC 3
-#endif
-#ifndef MT_XA
-#define MT_XA 4
-#endif
-constexpr int kAhead = MT_XA;
-#ifndef MT_XN
-#define MT_XN 1
-#endif
-constexpr int NC = MT_XN;  // channels per lane  // tokens whose step sizes are made together
-
-template <int BYTES> __device__ __forceinline__ void cp_async_zfill(uint32_t dst, const void *src, bool in) {
-    if constexpr (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" :: "r"(dst), "l"(src), "r"(in ? BYTES : 0), "n"(BYTES) : "memory");
-}
+constexpr int kAhead = 4;         // tokens whose step sizes are made together
+constexpr int kPromptCtas = 3;    // CTAs an SM: at 4 (128 registers) a lane's schedule costs more than the warps give
 
 // ROWS rows of up to `values` <= MOST values each, by 32-bit words: the words that a row's
 // live values touch, to dst + row * pitch (16-bit values that start in the middle of a word stay
@@ -296,7 +277,6 @@ template <class S, int NP> struct States8 {
         }
     }
 };
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
 // Bytes of shared memory per warp: two stages of 3 activations and `shared` of
 // B and C in storage form, and those widened.
@@ -318,7 +298,7 @@ __device__ __forceinline__ f32x2 pair_of(const float *p, int64_t ch, int cl) {
 // first state). REV: the same of the adjoint, r = a (r + C g) from the last token
 // down. One exponential and three multiply-adds a pair; no output.
 template <class S, int K, int P, bool REV, bool ALN>
-__global__ void __launch_bounds__(kSsmThreads, MT_XC) k_ssm_carry(const __grid_constant__ SsmArgs a, int64_t warps) {
+__global__ void __launch_bounds__(kSsmThreads, kPromptCtas) k_ssm_carry(const __grid_constant__ SsmArgs a, int64_t warps) {
     using Q = PromptPlace<K, P>;
     using M = PromptSmem<S, K, P, 1>;
     using R = typename M::R;
@@ -405,7 +385,7 @@ __global__ void __launch_bounds__(kSsmThreads, MT_XC) k_ssm_carry(const __grid_c
             R::no_steps(raw, left, lane, softplus);
         St::widen(sb, raw + 3 * R::kBytes, bp, bt, t0, left, (int)N, lane, ALN);
         __syncwarp();
-#pragma unroll 1
+#pragma unroll
         for (int ii = 0; ii < kStep; ii += kAhead) {
             const int i = REV ? kStep - kAhead - ii : ii;
             f32x2 d[kAhead], x[kAhead];
@@ -414,16 +394,15 @@ __global__ void __launch_bounds__(kSsmThreads, MT_XC) k_ssm_carry(const __grid_c
                 d[j] = add2f(R::read(raw, i + j, cq), bias);
                 x[j] = R::read(raw + R::kBytes, i + j, cq);
             }
-            if (softplus) {
+            // chosen, not branched on: a branch would keep one group's work from the next one's
 #pragma unroll
-                for (int j = 0; j < kAhead; ++j)
-                    d[j] = softplus_2f(d[j]);
-            }
-            if (gated) {
+            for (int j = 0; j < kAhead; ++j)
+                d[j] = choose_2f(softplus, softplus_2f(d[j]), d[j]);
+            if (REV) {
 #pragma unroll
                 for (int j = 0; j < kAhead; ++j) {
                     const f32x2 z = R::read(raw + 2 * R::kBytes, i + j, cq);
-                    x[j] = mul2f(x[j], mul2f(z, sigmoid_2f(z)));
+                    x[j] = choose_2f(gated, mul2f(x[j], mul2f(z, sigmoid_2f(z))), x[j]);
                 }
             }
             const float *row = sb + i * NP + at.n0;
@@ -503,7 +482,7 @@ __global__ void __launch_bounds__(256) k_ssm_chain(const __grid_constant__ SsmAr
 
 // ---- forward -----------------------------------------------------------------------------
 template <class S, int K, int P, bool ALN>
-__global__ void __launch_bounds__(kSsmThreads, MT_XF) k_ssm(const __grid_constant__ SsmArgs a, int64_t warps) {
+__global__ void __launch_bounds__(kSsmThreads, kPromptCtas) k_ssm(const __grid_constant__ SsmArgs a, int64_t warps) {
     using Q = PromptPlace<K, P>;
     constexpr int NP = Q::NP;
     using M = PromptSmem<S, K, P, 2>;
@@ -595,7 +574,7 @@ __global__ void __launch_bounds__(kSsmThreads, MT_XF) k_ssm(const __grid_constan
         St::widen(sb, raw + 3 * R::kBytes, bp, a.p.B_token, t0, left, (int)N, lane, ALN);
         St::widen(sc, raw + 3 * R::kBytes + St::kBytes, cp, a.p.C_token, t0, left, (int)N, lane, ALN);
         __syncwarp();
-#pragma unroll 1
+#pragma unroll
         for (int i = 0; i < kStep; i += kAhead) {
             f32x2 d[kAhead], u[kAhead], y[kAhead];
 #pragma unroll
@@ -603,11 +582,9 @@ __global__ void __launch_bounds__(kSsmThreads, MT_XF) k_ssm(const __grid_constan
                 d[j] = add2f(R::read(raw, i + j, cq), bias);
                 u[j] = R::read(raw + R::kBytes, i + j, cq);
             }
-            if (softplus) {
 #pragma unroll
-                for (int j = 0; j < kAhead; ++j)
-                    d[j] = softplus_2f(d[j]);
-            }
+            for (int j = 0; j < kAhead; ++j)
+                d[j] = choose_2f(softplus, softplus_2f(d[j]), d[j]);
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) {
                 f32x2 acc[2] = {0ull, 0ull};
@@ -643,12 +620,10 @@ __global__ void __launch_bounds__(kSsmThreads, MT_XF) k_ssm(const __grid_constan
                 }
                 y[j] = fma2f(skip, u[j], pack2f(s[0], s[1]));
             }
-            if (gated) {
 #pragma unroll
-                for (int j = 0; j < kAhead; ++j) {
-                    const f32x2 z = R::read(raw + 2 * R::kBytes, i + j, cq);
-                    y[j] = mul2f(y[j], mul2f(z, sigmoid_2f(z)));
-                }
+            for (int j = 0; j < kAhead; ++j) {
+                const f32x2 z = R::read(raw + 2 * R::kBytes, i + j, cq);
+                y[j] = choose_2f(gated, mul2f(y[j], mul2f(z, sigmoid_2f(z))), y[j]);
             }
             // into the place of delta, which every lane of the pair has used
             if (P == 1 || writer) {
