@@ -11,10 +11,7 @@ constexpr int64_t kSsmSms = 152;
 constexpr int64_t kEnoughWarps = kSsmSms * 5;   // from here on the tokens are not cut
 constexpr int64_t kTargetWarps = kSsmSms * 24;  // what a cut aims at
 constexpr int64_t kTargetCtas = kSsmSms * 9;    // the same for the gradient's CTAs
-#ifndef MT_XL
-#define MT_XL 64
-#endif
-constexpr int64_t kLeastSegment = MT_XL;           // tokens: below, a carry costs more than it frees
+constexpr int64_t kLeastSegment = 16;           // tokens: a warp alone takes as long for a token as the chain of carries does
 
 SsmPlan ssm_plan(int64_t batch, int64_t len, int64_t dim, int64_t nstate, int64_t groups, bool grad) {
     SsmPlan p;
@@ -72,9 +69,10 @@ static SsmArgs ssm_args(const mt_ssm_args &p, bool grad) {
     a.ntiles = (p.len + kSsmTile - 1) / kSsmTile;
     a.gdim = p.dim / p.groups;
     const int64_t v = p.dtype == MT_F32 ? 16 : 8;  // bytes of four values
-    a.aligned = channels_fit(p, grad, a.gdim, p.dtype == MT_F32 ? 4 : 8) && p.nstate % 4 == 0 && fits(p.A, 0, 0, 16) &&
-                fits(p.state, 0, 0, 16) && fits(p.checkpoints, 0, 0, 16) && fits(p.dfinal, 0, 0, 16) && fits(p.dinit, 0, 0, 16) &&
-                fits(p.B, p.B_batch, p.B_token, v) && fits(p.C, p.C_batch, p.C_token, v);
+    a.nvec = p.nstate % 4 == 0 && fits(p.A, 0, 0, 16) && fits(p.state, 0, 0, 16) && fits(p.checkpoints, 0, 0, 16) &&
+             fits(p.dfinal, 0, 0, 16) && fits(p.dinit, 0, 0, 16);
+    a.bvec = p.nstate % 4 == 0 && fits(p.B, p.B_batch, p.B_token, v) && fits(p.C, p.C_batch, p.C_token, v);
+    a.aligned = a.nvec && a.bvec && channels_fit(p, grad, a.gdim, p.dtype == MT_F32 ? 4 : 8);
     uint64_t *s = static_cast<uint64_t *>(p.scratch);
     a.carry = a.decay = a.shared = a.dA_part = a.dD_part = a.dbias_part = nullptr;
     if (s != nullptr) {

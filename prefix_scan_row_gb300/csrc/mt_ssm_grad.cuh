@@ -141,13 +141,13 @@ __global__ void __launch_bounds__(kSsmThreads, sizeof(S) == 2 && P <= 8 ? 3 : 2)
     const int64_t stop = begin + a.plan.seg_len < a.p.len ? begin + a.plan.seg_len : a.p.len;
     const int64_t end = n < stop ? n : stop;
     Pairs A, r, dA;
-    A.load(a.p.A + at.ch * N, N, at.n0, at.cl, ALN, kLog2e);
+    A.load(a.p.A + at.ch * N, N, at.n0, at.cl, ALN || a.nvec, kLog2e);
     dA.zero();
     r.zero();
     if (SEG > 1)
-        r.load(a.carry + ((at.b * SEG + at.s) * a.p.dim + at.ch) * N, N, at.n0, at.cl, ALN);
+        r.load(a.carry + ((at.b * SEG + at.s) * a.p.dim + at.ch) * N, N, at.n0, at.cl, ALN || a.nvec);
     else if (a.p.dfinal != nullptr)
-        r.load(a.p.dfinal + (at.b * a.p.dim + at.ch) * N, N, at.n0, at.cl, ALN);
+        r.load(a.p.dfinal + (at.b * a.p.dim + at.ch) * N, N, at.n0, at.cl, ALN || a.nvec);
     // the elementwise parts: a lane has a channel pair, and every kTok-th token
     constexpr int kPairs = CW / 2 < 32 ? CW / 2 : 32, kTok = 32 / kPairs;
     const int ec = lane % kPairs * 2, et = lane / kPairs;
@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kSsmThreads, sizeof(S) == 2 && P <= 8 ? 3 : 2)
         }
         if (warp < 2) {  // warp 0 brings B, warp 1 C
             const uint32_t ks = smem_addr(kept) + ((k & 1) * 2 + warp) * St::kBytes;
-            St::fetch(ks, warp == 0 ? bp : cp, warp == 0 ? a.p.B_token : a.p.C_token, t0, left, (int)N, lane, ALN);
+            St::fetch(ks, warp == 0 ? bp : cp, warp == 0 ? a.p.B_token : a.p.C_token, t0, left, (int)N, lane, ALN || a.bvec);
         }
         cp_async_commit();
     };
@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(kSsmThreads, sizeof(S) == 2 && P <= 8 ? 3 : 2)
         const int left = end - t0 < kStep ? (int)(end - t0) : kStep;
         if (warp < 2)
             St::widen(wide + ((k & 1) * 2 + warp) * (kStep * NP), kept + ((k & 1) * 2 + warp) * St::kBytes, warp == 0 ? bp : cp,
-                      warp == 0 ? a.p.B_token : a.p.C_token, t0, left, (int)N, lane, ALN);
+                      warp == 0 ? a.p.B_token : a.p.C_token, t0, left, (int)N, lane, ALN || a.bvec);
     };
     if (tiles > 0) {
         fetch(tiles - 1);
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(kSsmThreads, sizeof(S) == 2 && P <= 8 ? 3 : 2)
         if (left < kStep)
             R::no_steps(raw, left, lane, softplus);
         Pairs h;
-        h.load(a.p.checkpoints + ((at.b * a.ntiles + t0 / kStep) * a.p.dim + at.ch) * N, N, at.n0, at.cl, ALN);
+        h.load(a.p.checkpoints + ((at.b * a.ntiles + t0 / kStep) * a.p.dim + at.ch) * N, N, at.n0, at.cl, ALN || a.nvec);
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < (kStep + kTok - 1) / kTok; ++i) {
@@ -398,9 +398,9 @@ __global__ void __launch_bounds__(kSsmThreads, sizeof(S) == 2 && P <= 8 ? 3 : 2)
                 Codec<S>::store1(static_cast<S *>(a.p.dz) + at.b * a.p.dz_batch + t * a.p.dz_token + cb + c, 0.0f);
         }
     if (at.s == 0 && a.p.dinit != nullptr)
-        r.store(a.p.dinit + (at.b * a.p.dim + at.ch) * N, N, at.n0, at.cl, ALN);
+        r.store(a.p.dinit + (at.b * a.p.dim + at.ch) * N, N, at.n0, at.cl, ALN || a.nvec);
     const int64_t part = at.b * SEG + at.s;
-    dA.store(a.dA_part + (part * a.p.dim + at.ch) * N, N, at.n0, at.cl, ALN);
+    dA.store(a.dA_part + (part * a.p.dim + at.ch) * N, N, at.n0, at.cl, ALN || a.nvec);
     float v[4];
     unpack2f(dskip, v[0], v[1]);
     unpack2f(dbias, v[2], v[3]);
@@ -445,14 +445,14 @@ __global__ void __launch_bounds__(256) k_ssm_grad_join(const __grid_constant__ S
         } else if (i < shared + params) {
             const int64_t j = i - shared;
             float v = 0.0f;
-#pragma unroll 4
+#pragma unroll 16
             for (int64_t k = 0; k < parts; ++k)
                 v += a.dA_part[k * params + j];
             a.p.dA[j] = v;
         } else {
             const int64_t j = i - shared - params;
             float v = 0.0f, w = 0.0f;
-#pragma unroll 4
+#pragma unroll 8
             for (int64_t k = 0; k < parts; ++k) {
                 v += a.dD_part[k * D + j];
                 w += a.dbias_part[k * D + j];

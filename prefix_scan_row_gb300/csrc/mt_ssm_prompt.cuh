@@ -30,21 +30,28 @@ constexpr int kPromptCtas = 3;    // CTAs an SM: at 4 (128 registers) a lane's s
 template <class S, int ROWS, int MOST>
 __device__ __forceinline__ void copy_words(uint32_t dst, int pitch, const S *base, int64_t stride, int64_t t0, int left, int values,
                                            int lane) {
-    constexpr int kWords = sizeof(S) == 4 ? MOST : MOST / 2 + 1;
+    constexpr int kWords = sizeof(S) == 4 ? MOST : MOST / 2 + 1, kEach = 32 / ROWS;  // lanes of a row
+    const int t = lane / kEach, w0 = lane % kEach;
+    const uintptr_t at = (uintptr_t)(base + (t0 + t) * stride), from = (at & ~(uintptr_t)3) + 4 * w0;
+    const uint32_t to = dst + t * pitch + 4 * w0;
+    // words of the row from this lane's first on
+    const int words = t < left && values > 0 ? (int)((at + values * sizeof(S) + 3 - from) >> 2) : 0;
 #pragma unroll
-    for (int i = 0; i < (ROWS * kWords + 31) / 32; ++i) {
-        const int t = (32 * i + lane) / kWords, w = (32 * i + lane) % kWords;
-        const S *row = base + (t0 + t) * stride;
+    for (int w = 0; w < kWords; w += kEach) {
         if constexpr (sizeof(S) == 4) {
-            const bool in = t < left && w < values;
-            if (t < ROWS)
-                cp_async_zfill<4>(dst + t * pitch + 4 * w, in ? row + w : base, in);
+            if (MOST % kEach == 0 || w + w0 < MOST)
+                cp_async_zfill<4>(to + 4 * w, w < words ? (const void *)(from + 4 * w) : (const void *)base, w < words);
         } else {
-            const uintptr_t at = (uintptr_t)row, from = at & ~(uintptr_t)3;
-            if (t < left && values > 0 && from + 4 * w < at + 2 * values)
-                cp_async_zfill<4>(dst + t * pitch + 4 * w, (const void *)(from + 4 * w), true);
+            if (w < words)
+                cp_async_zfill<4>(to + 4 * w, (const void *)(from + 4 * w), true);
         }
     }
+}
+// How far into its first word row t of a tensor starts, in bytes.
+template <class S> __device__ __forceinline__ uint32_t row_skip(const S *base, int64_t stride, int64_t t) {
+    if (sizeof(S) == 4)
+        return 0u;
+    return ((uint32_t)(uintptr_t)base + (uint32_t)t * (uint32_t)stride * (uint32_t)sizeof(S)) & 3u;
 }
 
 // A warp's CW channels of kStep tokens in shared memory, in storage form and
@@ -88,7 +95,7 @@ template <class S, int CW> struct Rows8 {
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
             const int t = lane / kLanes + i * kTok;
-            const S *p = reinterpret_cast<const S *>(rows + (t < kStep ? t : 0) * kPitch + ((uintptr_t)(base + (t0 + t) * stride) & 3u)) + c;
+            const S *p = reinterpret_cast<const S *>(rows + (t < kStep ? t : 0) * kPitch + row_skip(base, stride, t0 + t)) + c;
             v[i][0] = t < left && c < channels ? p[0] : S(0.0f);
             v[i][1] = t < left && c + 1 < channels ? p[1] : S(0.0f);
         }
@@ -142,11 +149,16 @@ template <class S, int CW> struct Rows8 {
     }
     static __device__ __forceinline__ void put_each(const char *rows, S *base, int64_t stride, int64_t t0, int left, int channels,
                                                     int lane) {
+        constexpr int kRow = CW < 32 ? CW : 32, kTok = 32 / kRow;  // lanes of a token, tokens together
+        const int c0 = lane % kRow;
+        S *to = base + (t0 + lane / kRow) * stride + c0;
 #pragma unroll
-        for (int i = 0; i < (kStep * CW + 31) / 32; ++i) {
-            const int t = (32 * i + lane) / CW, c = (32 * i + lane) % CW;
-            if (t < left && c < channels)
-                base[(t0 + t) * stride + c] = reinterpret_cast<const S *>(rows + t * kPitch)[c];
+        for (int t = lane / kRow; t < kStep; t += kTok) {
+#pragma unroll
+            for (int c = 0; c < CW; c += kRow)
+                if (t < left && c0 + c < channels)
+                    to[c] = reinterpret_cast<const S *>(rows + t * kPitch)[c0 + c];
+            to += kTok * stride;
         }
     }
 };
@@ -267,8 +279,8 @@ template <class S, int NP> struct States8 {
                 if (vec) {
                     w.load(reinterpret_cast<const S *>(raw) + 4 * v, true, 4);
                 } else {
-                    const int skip = sizeof(S) == 4 ? 0 : (int)((uintptr_t)(base + (t0 + t) * stride) & 3u);
-                    w.load(reinterpret_cast<const S *>(raw + t * kPitch + skip) + s, false, live(left, t, s, nstate));
+                    const char *row = raw + t * kPitch + row_skip(base, stride, t0 + t);
+                    w.load(reinterpret_cast<const S *>(row) + s, false, live(left, t, s, nstate));
                 }
                 float x[4];
                 w.widen(x);
@@ -318,16 +330,16 @@ __global__ void __launch_bounds__(kSsmThreads, kPromptCtas) k_ssm_carry(const __
     const int64_t begin = at.s * a.plan.seg_len;
     const int64_t end = begin + a.plan.seg_len < n ? begin + a.plan.seg_len : n;
     Rows<K> A, h;
-    A.load(a.p.A + at.ch * N, N, at.n0, at.cl, ALN, kLog2e);
+    A.load(a.p.A + at.ch * N, N, at.n0, at.cl, ALN || a.nvec, kLog2e);
     h.zero();
     if (!REV && at.s == 0) {
         const int64_t slot = ssm_slot(a, at.b);
         if (a.p.carry_in && a.p.state != nullptr && slot >= 0)
-            h.load(a.p.state + (slot * a.p.dim + at.ch) * N, N, at.n0, at.cl, ALN);
+            h.load(a.p.state + (slot * a.p.dim + at.ch) * N, N, at.n0, at.cl, ALN || a.nvec);
         // the state is written by the next launch's last segment while its first
         // one starts: that one reads this copy, in the place of the last carry
         const int64_t spare = (at.b * a.plan.segments + a.plan.segments - 1) * a.p.dim + at.ch;
-        h.store(a.carry + spare * N, N, at.n0, at.cl, ALN);
+        h.store(a.carry + spare * N, N, at.n0, at.cl, ALN || a.nvec);
     }
     f32x2 sum = 0ull;
     const f32x2 bias = pair_of(a.p.delta_bias, at.ch, at.cl);
@@ -360,7 +372,7 @@ __global__ void __launch_bounds__(kSsmThreads, kPromptCtas) k_ssm_carry(const __
             if (gated)
                 R::fetch_words(to + 2 * R::kBytes, zp, zt, t0, left, at.channels, lane);
         }
-        St::fetch(to + 3 * R::kBytes, bp, bt, t0, left, (int)N, lane, ALN);
+        St::fetch(to + 3 * R::kBytes, bp, bt, t0, left, (int)N, lane, ALN || a.bvec);
         cp_async_commit();
     };
     if (steps > 0)
@@ -383,7 +395,7 @@ __global__ void __launch_bounds__(kSsmThreads, kPromptCtas) k_ssm_carry(const __
         }
         if (left < kStep)
             R::no_steps(raw, left, lane, softplus);
-        St::widen(sb, raw + 3 * R::kBytes, bp, bt, t0, left, (int)N, lane, ALN);
+        St::widen(sb, raw + 3 * R::kBytes, bp, bt, t0, left, (int)N, lane, ALN || a.bvec);
         __syncwarp();
 #pragma unroll
         for (int ii = 0; ii < kStep; ii += kAhead) {
@@ -432,7 +444,7 @@ __global__ void __launch_bounds__(kSsmThreads, kPromptCtas) k_ssm_carry(const __
         }
     }
     const int64_t row = (at.b * a.plan.segments + at.s) * a.p.dim + at.ch;
-    h.store(a.carry + row * N, N, at.n0, at.cl, ALN);
+    h.store(a.carry + row * N, N, at.n0, at.cl, ALN || a.nvec);
     float s[2];
     unpack2f(sum, s[0], s[1]);
     if (lane % P == 0)
@@ -507,12 +519,12 @@ __global__ void __launch_bounds__(kSsmThreads, kPromptCtas) k_ssm(const __grid_c
     const int64_t end = n < stop ? n : stop;
     float *state = a.p.state != nullptr && active ? a.p.state + (slot * a.p.dim + at.ch) * N : nullptr;
     Rows<K> A, h;
-    A.load(a.p.A + at.ch * N, N, at.n0, at.cl, ALN, kLog2e);
+    A.load(a.p.A + at.ch * N, N, at.n0, at.cl, ALN || a.nvec, kLog2e);
     h.zero();
     if (a.plan.segments > 1)
-        h.load(a.carry + ((at.b * a.plan.segments + at.s) * a.p.dim + at.ch) * N, N, at.n0, at.cl, ALN);
+        h.load(a.carry + ((at.b * a.plan.segments + at.s) * a.p.dim + at.ch) * N, N, at.n0, at.cl, ALN || a.nvec);
     else if (a.p.carry_in && state != nullptr)
-        h.load(state, N, at.n0, at.cl, ALN);
+        h.load(state, N, at.n0, at.cl, ALN || a.nvec);
     const f32x2 bias = pair_of(a.p.delta_bias, at.ch, at.cl), skip = pair_of(a.p.D, at.ch, at.cl);
     const S *dp = static_cast<const S *>(a.p.delta) + at.b * a.p.delta_batch + at.cw;
     const S *up = static_cast<const S *>(a.p.u) + at.b * a.p.u_batch + at.cw;
@@ -545,8 +557,8 @@ __global__ void __launch_bounds__(kSsmThreads, kPromptCtas) k_ssm(const __grid_c
             if (gated)
                 R::fetch_words(to + 2 * R::kBytes, zp, a.p.z_token, t0, left, at.channels, lane);
         }
-        St::fetch(to + 3 * R::kBytes, bp, a.p.B_token, t0, left, (int)N, lane, ALN);
-        St::fetch(to + 3 * R::kBytes + St::kBytes, cp, a.p.C_token, t0, left, (int)N, lane, ALN);
+        St::fetch(to + 3 * R::kBytes, bp, a.p.B_token, t0, left, (int)N, lane, ALN || a.bvec);
+        St::fetch(to + 3 * R::kBytes + St::kBytes, cp, a.p.C_token, t0, left, (int)N, lane, ALN || a.bvec);
         cp_async_commit();
     };
     if (steps > 0)
@@ -556,7 +568,7 @@ __global__ void __launch_bounds__(kSsmThreads, kPromptCtas) k_ssm(const __grid_c
     for (int k = 0; k < steps; ++k, t0 += kStep) {
         char *raw = stage + (k & 1) * M::kStage;
         if (a.p.checkpoints != nullptr)
-            h.store(a.p.checkpoints + ((at.b * a.ntiles + t0 / kStep) * a.p.dim + at.ch) * N, N, at.n0, at.cl, ALN);
+            h.store(a.p.checkpoints + ((at.b * a.ntiles + t0 / kStep) * a.p.dim + at.ch) * N, N, at.n0, at.cl, ALN || a.nvec);
         cp_async_wait_all();
         __syncwarp();  // everyone's copies are here, and nobody reads the other stage any more
         if (k + 1 < steps)
@@ -571,8 +583,8 @@ __global__ void __launch_bounds__(kSsmThreads, kPromptCtas) k_ssm(const __grid_c
         }
         if (left < kStep)
             R::no_steps(raw, left, lane, softplus);
-        St::widen(sb, raw + 3 * R::kBytes, bp, a.p.B_token, t0, left, (int)N, lane, ALN);
-        St::widen(sc, raw + 3 * R::kBytes + St::kBytes, cp, a.p.C_token, t0, left, (int)N, lane, ALN);
+        St::widen(sb, raw + 3 * R::kBytes, bp, a.p.B_token, t0, left, (int)N, lane, ALN || a.bvec);
+        St::widen(sc, raw + 3 * R::kBytes + St::kBytes, cp, a.p.C_token, t0, left, (int)N, lane, ALN || a.bvec);
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < kStep; i += kAhead) {
@@ -644,7 +656,7 @@ __global__ void __launch_bounds__(kSsmThreads, kPromptCtas) k_ssm(const __grid_c
         for (int c = lane; c < at.channels; c += 32)
             Codec<S>::store1(op + t * a.p.out_token + c, 0.0f);
     if (state != nullptr && at.s == a.plan.segments - 1)
-        h.store(state, N, at.n0, at.cl, ALN);
+        h.store(state, N, at.n0, at.cl, ALN || a.nvec);
 }
 
 // ---- launches ------------------------------------------------------------------------------
