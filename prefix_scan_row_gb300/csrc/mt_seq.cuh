@@ -88,12 +88,8 @@ template <int LEFT> __device__ __forceinline__ void cp_async_wait() { asm volati
 // ---- scalar functions ---------------------------------------------------------
 __device__ __forceinline__ float ex2f(float x) {
     float y;
-#ifdef MT_XE
-    return exp2f(x);
-#else
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
-#endif
 }
 __device__ __forceinline__ float rcpf(float x) {
     float y;

@@ -346,6 +346,7 @@ __global__ void __launch_bounds__(kSsmThreads, sizeof(S) == 2 && P <= 8 ? 3 : 2)
         }
         if (k > 0)
             widen(k - 1);
+        f32x2 tskip = 0ull, tbias = 0ull;  // of the tile: added to the segment's as one, which halves their rounding
 #pragma unroll
         for (int i = 0; i < (kStep + kTok - 1) / kTok; ++i) {
             const int t = et + i * kTok;
@@ -361,8 +362,8 @@ __global__ void __launch_bounds__(kSsmThreads, sizeof(S) == 2 && P <= 8 ? 3 : 2)
                     xd = mul2f(xd, sigmoid_2f(add2f(R::read(raw, t, ec), bias)));
                 R::write(raw, t, ec, xd);
                 if (t < left) {
-                    dskip = fma2f(gy, u, dskip);
-                    dbias = add2f(dbias, xd);
+                    tskip = fma2f(gy, u, tskip);
+                    tbias = add2f(tbias, xd);
                 }
                 if (gated) {
                     const f32x2 z = R::read(raw + 3 * R::kBytes, t, ec), o = R::read(raw + 2 * R::kBytes, t, ec), s = sigmoid_2f(z);
@@ -371,6 +372,8 @@ __global__ void __launch_bounds__(kSsmThreads, sizeof(S) == 2 && P <= 8 ? 3 : 2)
                 }
             }
         }
+        dskip = add2f(dskip, tskip);
+        dbias = add2f(dbias, tbias);
         __syncwarp();
         {
             const int64_t tl = t0 + R::token(lane);
@@ -414,6 +417,22 @@ __global__ void __launch_bounds__(kSsmThreads, sizeof(S) == 2 && P <= 8 ? 3 : 2)
     }
 }
 
+// rows values `stride` apart, in eight sums that are then added in pairs: the
+// loads are in flight together, and rounding grows with the logarithm of what is added.
+__device__ __forceinline__ float sum_rows(const float *p, int64_t stride, int64_t rows) {
+    float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    int64_t k = 0;
+    for (; k + 8 <= rows; k += 8)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[e] += p[(k + e) * stride];
+#pragma unroll
+    for (int e = 0; e < 7; ++e)
+        if (k + e < rows)
+            v[e] += p[(k + e) * stride];
+    return ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+}
+
 // The sums over CTAs of dB and dC (rounded once, here), and over sequences and
 // segments of dA, dD and the bias's gradient, each in a fixed order.
 template <class S>
@@ -432,31 +451,18 @@ __global__ void __launch_bounds__(256) k_ssm_grad_join(const __grid_constant__ S
             const int64_t g = q % G;
             q /= G;
             const int64_t t = q % L, b = q / L;
-            float v = 0.0f;
-            if (t < ssm_len(a, b)) {
-                const float *p = a.shared + ((g * a.plan.ctiles * B + b) * L + t) * (2 * np) + which * np + s;
-#pragma unroll 8
-                for (int64_t k = 0; k < a.plan.ctiles; ++k)
-                    v += p[k * B * L * (2 * np)];
-            }
+            const float v = t < ssm_len(a, b) ? sum_rows(a.shared + ((g * a.plan.ctiles * B + b) * L + t) * (2 * np) + which * np + s,
+                                                         B * L * (2 * np), a.plan.ctiles)
+                                              : 0.0f;
             S *to = which ? static_cast<S *>(a.p.dC) + b * a.p.dC_batch + t * a.p.dC_token
                           : static_cast<S *>(a.p.dB) + b * a.p.dB_batch + t * a.p.dB_token;
             Codec<S>::store1(to + g * N + s, v);
         } else if (i < shared + params) {
             const int64_t j = i - shared;
-            float v = 0.0f;
-#pragma unroll 16
-            for (int64_t k = 0; k < parts; ++k)
-                v += a.dA_part[k * params + j];
-            a.p.dA[j] = v;
+            a.p.dA[j] = sum_rows(a.dA_part + j, params, parts);
         } else {
             const int64_t j = i - shared - params;
-            float v = 0.0f, w = 0.0f;
-#pragma unroll 8
-            for (int64_t k = 0; k < parts; ++k) {
-                v += a.dD_part[k * D + j];
-                w += a.dbias_part[k * D + j];
-            }
+            const float v = sum_rows(a.dD_part + j, D, parts), w = sum_rows(a.dbias_part + j, D, parts);
             if (a.p.dD != nullptr)
                 a.p.dD[j] = v;
             if (a.p.ddelta_bias != nullptr)
