@@ -72,18 +72,21 @@ template <class S, bool ALN, int GROUPS, int EACH> struct Ring {
     char *mine;  // the lane's place in the first quad; quads lie 32 lanes apart
     Quad<S, ALN> next[ALN ? 1 : EACH];
     __device__ __forceinline__ void set(char *warp, int lane) { mine = warp + lane * 4 * (int)sizeof(S); }
-    __device__ __forceinline__ void ask(int group, const S *from, int64_t stride, int left, int live) {
+    // ALL: all EACH tokens exist
+    template <bool ALL> __device__ __forceinline__ void ask(int group, const S *from, int64_t stride, int left, int live) {
         if constexpr (ALN) {
+            const uint32_t to = smem_addr(mine) + group % GROUPS * (EACH * 32 * 4 * (int)sizeof(S));
 #pragma unroll
-            for (int j = 0; j < EACH; ++j)
-                cp_async_zfill<4 * sizeof(S)>(smem_addr(mine) + (group % GROUPS * EACH + j) * 32 * 4 * (int)sizeof(S),
-                                              j < left ? from + j * stride : from, j < left);
+            for (int j = 0; j < EACH; ++j) {
+                const bool in = ALL || j < left;
+                cp_async_zfill<4 * sizeof(S)>(to + j * 32 * 4 * (int)sizeof(S), in ? from + j * stride : from, in);
+            }
             cp_async_commit();
         } else {
 #pragma unroll
             for (int j = 0; j < EACH; ++j) {
                 next[j].zero();
-                if (j < left)
+                if (ALL || j < left)
                     next[j].load(from + j * stride, live);
             }
         }
@@ -236,15 +239,17 @@ __global__ void __launch_bounds__(kConvThreads, 5) k_conv(const S *x, S *out, S 
     ring.set(s_ring + (threadIdx.x >> 5) * 32 * Rng::kBytes, threadIdx.x & 31);
 #pragma unroll
     for (int g = 0; g < kDeep; ++g)
-        ring.ask(g, xt + g * kConvAhead * d.xt, d.xt, here - g * kConvAhead, at.live);
+        ring.template ask<false>(g, xt + g * kConvAhead * d.xt, d.xt, here - g * kConvAhead, at.live);
     xt += kDeep * kConvAhead * d.xt;
     int group = 0;
-    for (int tt = 0; tt < tokens; tt += kConvAhead, ++group) {
+    // FULL: the batch's tokens, and those asked for, all exist
+    const auto batch = [&](int tt, auto full) {
+        constexpr bool FULL = decltype(full)::value;
         Quad<S, ALN> v[kConvAhead];
         if (ALN)
             cp_async_wait<kDeep - 1>();
         ring.take(group, v);
-        ring.ask(group, xt, d.xt, here - tt - kDeep * kConvAhead, at.live);  // in the place of what was taken
+        ring.template ask<FULL>(group, xt, d.xt, here - tt - kDeep * kConvAhead, at.live);  // in the place of what was taken
         xt += kConvAhead * d.xt;
 #pragma unroll
         for (int j = 0; j < kConvAhead; ++j) {
@@ -258,16 +263,22 @@ __global__ void __launch_bounds__(kConvThreads, 5) k_conv(const S *x, S *out, S 
                     p = fma2f(w[k][e], h[k][e], p);
                 if (SILU)
                     p = mul2f(p, sigmoid_2f(p));
-                o[e] = tt + j < here ? p : 0ull;
+                o[e] = FULL || tt + j < here ? p : 0ull;
 #pragma unroll
                 for (int k = 0; k < W - 1; ++k)
                     h[k][e] = h[k + 1][e];
             }
             v[j].narrow(o);
-            if (tt + j < tokens)
+            if (FULL || tt + j < tokens)
                 v[j].store(os, at.live);
             os += d.ot;
         }
+    };
+    for (int tt = 0; tt < tokens; tt += kConvAhead, ++group) {
+        if (tt + (kDeep + 1) * kConvAhead <= here)
+            batch(tt, std::true_type());
+        else
+            batch(tt, std::false_type());
     }
     // The lane of the first span is the only one that reads the state, so it
     // is also the one that writes it: the last W-1 inputs of the sequence.
@@ -392,21 +403,23 @@ __global__ void __launch_bounds__(kGradThreads, 2) k_conv_grad(const S *x, const
         rg.set(s_ring + (sp * 64 + 32) * Rng::kBytes, lane);
 #pragma unroll
         for (int g = 0; g < kDeep; ++g) {
-            rx.ask(g, xp + g * kFew * d.xt, d.xt, here - g * kFew, at.live);
-            rg.ask(g, gp + g * kFew * d.gt, d.gt, here - g * kFew, at.live);
+            rx.template ask<false>(g, xp + g * kFew * d.xt, d.xt, here - g * kFew, at.live);
+            rg.template ask<false>(g, gp + g * kFew * d.gt, d.gt, here - g * kFew, at.live);
         }
         xp += kDeep * kFew * d.xt;
         gp += kDeep * kFew * d.gt;
         dp -= (W - 1) * d.dt;
         int group = 0;
-        for (int tt = 0; tt < walk; tt += kFew, ++group) {
+        // FULL: the batch's tokens are this span's, their dx too, and those asked for exist
+        const auto batch = [&](int tt, auto full) {
+            constexpr bool FULL = decltype(full)::value;
             Quad<S, ALN> vx[kFew], vg[kFew];
             if (ALN)
                 cp_async_wait<2 * kDeep - 2>();
             rx.take(group, vx);
             rg.take(group, vg);
-            rx.ask(group, xp, d.xt, here - tt - kDeep * kFew, at.live);  // in the place of what was taken
-            rg.ask(group, gp, d.gt, here - tt - kDeep * kFew, at.live);
+            rx.template ask<FULL>(group, xp, d.xt, here - tt - kDeep * kFew, at.live);  // in the place of what was taken
+            rg.template ask<FULL>(group, gp, d.gt, here - tt - kDeep * kFew, at.live);
             xp += kFew * d.xt;
             gp += kFew * d.gt;
 #pragma unroll
@@ -414,7 +427,7 @@ __global__ void __launch_bounds__(kGradThreads, 2) k_conv_grad(const S *x, const
                 f32x2 g[2], o[2];
                 vx[j].widen(h[W - 1]);
                 vg[j].widen(g);
-                const bool own = tt + j < tokens;
+                const bool own = FULL || tt + j < tokens;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     f32x2 p = bias[e];
@@ -439,15 +452,21 @@ __global__ void __launch_bounds__(kGradThreads, 2) k_conv_grad(const S *x, const
                     q[W - 1][e] = 0ull;
                 }
                 const int to = tt + j - (W - 1);  // the token whose dx is done
-                if (to >= here)
+                if (!FULL && to >= here)
                     o[0] = o[1] = 0ull;
                 vg[j].narrow(o);
-                if (to >= 0 && to < tokens)
+                if (FULL || (to >= 0 && to < tokens))
                     vg[j].store(dp, at.live);
                 else if (to < 0 && dst != nullptr)
                     vg[j].store(dst + (to + W - 1) * d.dim, at.live);
                 dp += d.dt;
             }
+        };
+        for (int tt = 0; tt < walk; tt += kFew, ++group) {
+            if (tt >= W - 1 && tt + kFew <= tokens && tt + (kDeep + 1) * kFew <= here)
+                batch(tt, std::true_type());
+            else
+                batch(tt, std::false_type());
         }
     }
     cp_async_wait_all();
