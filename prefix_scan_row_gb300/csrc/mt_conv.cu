@@ -567,16 +567,7 @@ template <class S, bool ALN, int W> static cudaError_t conv_go(const mt_conv_arg
             return e;
     }
     note_launch();
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((a.dim + 31) / 32), (unsigned)(W + 1));
-    cfg.blockDim = dim3(256);
-    cfg.stream = L.stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_conv_grad_join, (const float *)partial, a.dweight, a.dbias, (int64_t)a.dim, (int64_t)W,
+    return launch_pdl_2d(k_conv_grad_join, dim3((unsigned)((a.dim + 31) / 32), (unsigned)(W + 1)), 256, L.stream, (const float *)partial, a.dweight, a.dbias, (int64_t)a.dim, (int64_t)W,
                               a.batch * span_blocks);
 }
 

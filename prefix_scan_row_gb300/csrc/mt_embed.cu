@@ -571,16 +571,7 @@ static cudaError_t embed_grad_go(const void *tokens, int64_t n, const void *dout
     }
     if (p.pieces > 1) {
         note_launch();
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)((p.pieces + kSumWarps - 1) / kSumWarps), (unsigned)((dim + 127) / 128));
-        cfg.blockDim = dim3(kSumThreads);
-        cfg.stream = L.stream;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        e = cudaLaunchKernelEx(&cfg, k_embed_join<G>, g, a);
+        e = launch_pdl_2d(k_embed_join<G>, dim3((unsigned)((p.pieces + kSumWarps - 1) / kSumWarps), (unsigned)((dim + 127) / 128)), kSumThreads, L.stream, g, a);
     }
     return e;
 }

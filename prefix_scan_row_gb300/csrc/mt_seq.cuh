@@ -14,6 +14,21 @@ namespace mt {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
+// launch_pdl for grids of two dimensions.
+template <class... KArgs, class... Args>
+static cudaError_t launch_pdl_2d(void (*kernel)(KArgs...), dim3 grid, unsigned block, cudaStream_t stream, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(block);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
+
 // ---- V neighbouring values --------------------------------------------------
 // load_n / store_n move V values as one vector access when `vec` (then p is
 // aligned to V values) and otherwise value by value; `live` values exist, the

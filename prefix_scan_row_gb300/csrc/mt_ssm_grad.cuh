@@ -422,10 +422,21 @@ __global__ void __launch_bounds__(kSsmThreads, sizeof(S) == 2 && P <= 8 ? 3 : 2)
 __device__ __forceinline__ float sum_rows(const float *p, int64_t stride, int64_t rows) {
     float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
     int64_t k = 0;
-    for (; k + 8 <= rows; k += 8)
+    for (; k + 16 <= rows; k += 16) {
+        float x[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            x[e] = p[(k + e) * stride];
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            v[e % 8] += x[e];
+    }
+    if (k + 8 <= rows) {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             v[e] += p[(k + e) * stride];
+        k += 8;
+    }
 #pragma unroll
     for (int e = 0; e < 7; ++e)
         if (k + e < rows)

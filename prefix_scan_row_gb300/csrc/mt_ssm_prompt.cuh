@@ -457,36 +457,37 @@ __global__ void __launch_bounds__(kSsmThreads, kPromptCtas) k_ssm_carry(const __
 // Carries to first states: a lane a (channel, state) pair goes over the segments in
 // order (REV: from the last down), and each carry is replaced by the state (REV:
 // the adjoint) that its segment starts from. The loads do not depend on the
-// states, so eight are in flight; done by every warp of the forward kernel
+// states, so kMany are in flight (16 for many segments, 8 where more threads count for more); done by every warp of the forward kernel
 // for itself instead, 57 segments took 20 of its 140 us.
-template <bool REV>
+template <bool REV, int kMany>
 __global__ void __launch_bounds__(256) k_ssm_chain(const __grid_constant__ SsmArgs a) {
     pdl_prologue();
-    const int64_t per = a.p.dim * a.p.nstate, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= a.p.batch * per)
+    const int64_t per = a.p.dim * a.p.nstate, e = (int64_t)blockIdx.x * 256 + threadIdx.x, S = a.plan.segments;
+    if (e >= per)
         return;
-    const int64_t b = i / per, e = i % per, ch = e / a.p.nstate, S = a.plan.segments;
-    float *c = a.carry + b * S * per + e;
-    const float *sum = a.decay + b * S * a.p.dim + ch;
+    const int64_t ch = per <= 0xffffffffll ? (uint32_t)e / (uint32_t)a.p.nstate : e / a.p.nstate;
     const float A = a.p.A[e] * kLog2e;
-    constexpr int kMany = 8;
-    // forward: segment 0 starts from the copy in the last place, and its carry already holds it
-    float h = REV ? (a.p.dfinal != nullptr ? a.p.dfinal[i] : 0.0f) : c[(S - 1) * per];
-    for (int64_t j0 = 0; j0 < S; j0 += kMany) {
-        float next[kMany], dec[kMany];
+    for (int64_t b = blockIdx.y; b < a.p.batch; b += gridDim.y) {
+        float *c = a.carry + b * S * per + e;
+        const float *sum = a.decay + b * S * a.p.dim + ch;
+        // forward: segment 0 starts from the copy in the last place, and its carry already holds it
+        float h = REV ? (a.p.dfinal != nullptr ? a.p.dfinal[b * per + e] : 0.0f) : c[(S - 1) * per];
+        for (int64_t j0 = 0; j0 < S; j0 += kMany) {
+            float next[kMany], dec[kMany];
 #pragma unroll
-        for (int k = 0; k < kMany; ++k) {
-            const int64_t j = j0 + k, s = REV ? S - 1 - j : j;
-            const bool in = j < S - 1;  // the last one's carry goes nowhere
-            next[k] = in ? c[s * per] : 0.0f;
-            dec[k] = in && (REV || s > 0) ? sum[s * a.p.dim] : 0.0f;
-        }
+            for (int k = 0; k < kMany; ++k) {
+                const int64_t j = j0 + k, s = REV ? S - 1 - j : j;
+                const bool in = j < S - 1;  // the last one's carry goes nowhere
+                next[k] = in ? c[s * per] : 0.0f;
+                dec[k] = in && (REV || s > 0) ? sum[s * a.p.dim] : 0.0f;
+            }
 #pragma unroll
-        for (int k = 0; k < kMany; ++k) {
-            const int64_t j = j0 + k, s = REV ? S - 1 - j : j;
-            if (j < S) {
-                c[s * per] = h;
-                h = !REV && s == 0 ? next[k] : fmaf(ex2f(A * dec[k]), h, next[k]);
+            for (int k = 0; k < kMany; ++k) {
+                const int64_t j = j0 + k, s = REV ? S - 1 - j : j;
+                if (j < S) {
+                    c[s * per] = h;
+                    h = !REV && s == 0 ? next[k] : fmaf(ex2f(A * dec[k]), h, next[k]);
+                }
             }
         }
     }
@@ -668,7 +669,7 @@ template <class S, int K, int P, bool REV, bool ALN> static cudaError_t carry_go
     SsmArgs c = a;
     c.plan.ctiles = (a.gdim + 64 / P - 1) / (64 / P);
     const int64_t warps = a.p.batch * a.p.groups * c.plan.ctiles * (a.plan.segments - 1);
-    const int64_t grid = (warps + kSsmWarps - 1) / kSsmWarps, chain = (a.p.batch * a.p.dim * a.p.nstate + 255) / 256;
+    const int64_t grid = (warps + kSsmWarps - 1) / kSsmWarps, chain = (a.p.dim * a.p.nstate + 255) / 256;
     if (grid > INT32_MAX || chain > INT32_MAX)
         return cudaErrorInvalidValue;
     const size_t smem = kSsmWarps * PromptSmem<S, K, P, 1>::kBytes;
@@ -680,7 +681,7 @@ template <class S, int K, int P, bool REV, bool ALN> static cudaError_t carry_go
     if (e != cudaSuccess)
         return e;
     note_launch();
-    return launch_pdl(k_ssm_chain<REV>, (unsigned)chain, 256, 0, L.stream, a);
+    return launch_pdl_2d(a.plan.segments > 16 ? k_ssm_chain<REV, 16> : k_ssm_chain<REV, 8>, dim3((unsigned)chain, (unsigned)(a.p.batch < 65535 ? a.p.batch : 65535)), 256, L.stream, a);
 }
 template <class S, int K, int P, bool ALN> static cudaError_t prompt_go(const SsmArgs &a, const Launch &L) {
     cudaError_t e;
