@@ -200,31 +200,25 @@ template <int P> struct SsmPlace {
 // P lanes share a channel, four states each: the state is read and written once
 // (8 bytes a pair) and everything else is small beside it; bound by bytes. A lane takes
 // its channel of SEQ sequences, so A and the parameters are read once for them and
-// their states are in flight together (64 sequences of 4096 channels x 16 states: 10.7 us one by one).
-template <class S, int P, int SEQ>
-__global__ void __launch_bounds__(256) k_ssm_step(const __grid_constant__ SsmArgs a) {
-    pdl_prologue();
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int p = (int)(i % P);
-    const int64_t ch = (i / P) % a.p.dim, b0 = i / P / a.p.dim * SEQ;
-    const int64_t N = a.p.nstate;
+// their states are in flight together: 64 sequences of 4096 channels x 16 states, 36 MB, take 10.7 us.
+// ALL: every sequence has a state and all values move as vectors, so that nothing stands between the loads.
+template <class S, int P, int SEQ, bool ALL>
+__device__ __forceinline__ void step_lane(const SsmArgs &a, int64_t b0, int64_t ch, int p, float *const (&sp)[SEQ], bool vec, int live) {
+    const int64_t N = a.p.nstate, g = ch / a.gdim;
     const int n0 = 4 * p;
-    const int live = N - n0 < 0 ? 0 : N - n0 > 4 ? 4 : (int)(N - n0);
-    const bool vec = a.nvec && live == 4;
-    const int64_t g = ch / a.gdim;
-    float *sp[SEQ];
-    float h[SEQ][4], A[4] = {0.0f, 0.0f, 0.0f, 0.0f}, y[SEQ], u[SEQ], d[SEQ];
+    float h[SEQ][4], A[4] = {0.0f, 0.0f, 0.0f, 0.0f}, y[SEQ], u[SEQ], d[SEQ], z[SEQ];
     Raw4<S> rb[SEQ], rc[SEQ];
 #pragma unroll
     for (int s = 0; s < SEQ; ++s) {
-        const int64_t b = b0 + s, slot = b < a.p.batch ? ssm_slot(a, b) : -1;
-        sp[s] = slot >= 0 ? a.p.state + (slot * a.p.dim + ch) * N + n0 : nullptr;
-        y[s] = u[s] = d[s] = 0.0f;
+        const int64_t b = b0 + s;
+        y[s] = u[s] = d[s] = z[s] = 0.0f;
+        if (!ALL) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            h[s][k] = 0.0f;
-        if (sp[s] != nullptr) {
-            if (vec) {
+            for (int k = 0; k < 4; ++k)
+                h[s][k] = 0.0f;
+        }
+        if (ALL || sp[s] != nullptr) {
+            if (ALL || vec) {
                 lds4(sp[s], h[s]);
             } else {
 #pragma unroll
@@ -234,12 +228,14 @@ __global__ void __launch_bounds__(256) k_ssm_step(const __grid_constant__ SsmArg
             }
             u[s] = Codec<S>::load1(static_cast<const S *>(a.p.u) + b * a.p.u_batch + ch);
             d[s] = Codec<S>::load1(static_cast<const S *>(a.p.delta) + b * a.p.delta_batch + ch);
-            rb[s].load(static_cast<const S *>(a.p.B) + b * a.p.B_batch + g * N + n0, a.bvec, live);
-            rc[s].load(static_cast<const S *>(a.p.C) + b * a.p.C_batch + g * N + n0, a.bvec, live);
+            rb[s].load(static_cast<const S *>(a.p.B) + b * a.p.B_batch + g * N + n0, ALL || a.bvec, ALL ? 4 : live);
+            rc[s].load(static_cast<const S *>(a.p.C) + b * a.p.C_batch + g * N + n0, ALL || a.bvec, ALL ? 4 : live);
+            if (a.p.z != nullptr)
+                z[s] = Codec<S>::load1(static_cast<const S *>(a.p.z) + b * a.p.z_batch + ch);
         }
     }
     const float *ap = a.p.A + ch * N + n0;
-    if (vec) {
+    if (ALL || vec) {
         lds4(ap, A);
     } else {
 #pragma unroll
@@ -250,7 +246,7 @@ __global__ void __launch_bounds__(256) k_ssm_step(const __grid_constant__ SsmArg
     const float bias = a.p.delta_bias != nullptr ? a.p.delta_bias[ch] : 0.0f, skip = a.p.D != nullptr ? a.p.D[ch] : 0.0f;
 #pragma unroll
     for (int s = 0; s < SEQ; ++s) {
-        if (sp[s] != nullptr) {
+        if (ALL || sp[s] != nullptr) {
             float bb[4], cc[4];
             rb[s].widen(bb);
             rc[s].widen(cc);
@@ -262,7 +258,7 @@ __global__ void __launch_bounds__(256) k_ssm_step(const __grid_constant__ SsmArg
                 h[s][k] = fmaf(ex2f(d[s] * (A[k] * kLog2e)), h[s][k], d[s] * u[s] * bb[k]);
                 y[s] = fmaf(cc[k], h[s][k], y[s]);
             }
-            if (vec) {
+            if (ALL || vec) {
                 *reinterpret_cast<float4 *>(sp[s]) = make_float4(h[s][0], h[s][1], h[s][2], h[s][3]);
             } else {
 #pragma unroll
@@ -270,20 +266,45 @@ __global__ void __launch_bounds__(256) k_ssm_step(const __grid_constant__ SsmArg
                     if (k < live)
                         sp[s][k] = h[s][k];
             }
-        }
-#pragma unroll
-        for (int m = 1; m < P; m <<= 1)
-            y[s] += __shfl_xor_sync(kFull, y[s], m);
-        const int64_t b = b0 + s;
-        if (p == 0 && b < a.p.batch) {
-            float o = fmaf(skip, u[s], y[s]);
-            if (sp[s] != nullptr && a.p.z != nullptr) {
-                const float z = Codec<S>::load1(static_cast<const S *>(a.p.z) + b * a.p.z_batch + ch);
-                o *= z * sigmoidf(z);
-            }
-            Codec<S>::store1(static_cast<S *>(a.p.out) + b * a.p.out_batch + ch, sp[s] != nullptr ? o : 0.0f);
+            y[s] = p == 0 ? fmaf(skip, u[s], y[s]) : y[s];
         }
     }
+    // the sums over states, by all lanes of the channel
+    const unsigned with = P == 32 ? kFull : ((1u << (P % 32)) - 1u) << ((threadIdx.x & 31) / P * P);
+#pragma unroll
+    for (int s = 0; s < SEQ; ++s) {
+#pragma unroll
+        for (int m = 1; m < P; m <<= 1)
+            y[s] += __shfl_xor_sync(with, y[s], m);
+        const int64_t b = b0 + s;
+        if (p == 0 && (ALL || b < a.p.batch)) {
+            if (a.p.z != nullptr)
+                y[s] *= z[s] * sigmoidf(z[s]);
+            Codec<S>::store1(static_cast<S *>(a.p.out) + b * a.p.out_batch + ch, ALL || sp[s] != nullptr ? y[s] : 0.0f);
+        }
+    }
+}
+
+template <class S, int P, int SEQ>
+__global__ void __launch_bounds__(256) k_ssm_step(const __grid_constant__ SsmArgs a) {
+    pdl_prologue();
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int p = (int)(i % P);
+    const int64_t ch = (i / P) % a.p.dim, b0 = i / P / a.p.dim * SEQ;
+    const int64_t left = a.p.nstate - 4 * p;
+    const int live = left < 0 ? 0 : left > 4 ? 4 : (int)left;
+    float *sp[SEQ];
+    bool all = a.nvec && a.bvec && a.p.nstate == 4 * P;  // the same for all lanes of a channel
+#pragma unroll
+    for (int s = 0; s < SEQ; ++s) {
+        const int64_t slot = b0 + s < a.p.batch ? ssm_slot(a, b0 + s) : -1;
+        sp[s] = slot >= 0 ? a.p.state + (slot * a.p.dim + ch) * a.p.nstate + 4 * p : nullptr;
+        all = all && slot >= 0;
+    }
+    if (all)
+        step_lane<S, P, SEQ, true>(a, b0, ch, p, sp, true, 4);
+    else
+        step_lane<S, P, SEQ, false>(a, b0, ch, p, sp, a.nvec && live == 4, live);
 }
 
 template <class S, int P, int SEQ> static cudaError_t step_seq(const SsmArgs &a, const Launch &L) {
@@ -293,9 +314,9 @@ template <class S, int P, int SEQ> static cudaError_t step_seq(const SsmArgs &a,
     note_launch();
     return launch_pdl(k_ssm_step<S, P, SEQ>, (unsigned)grid, 256, 0, L.stream, a);
 }
-// four sequences a lane where that still fills the SMs
+// two sequences a lane where that still fills the SMs (one measured 11.2 us there, four 11.8)
 template <class S, int P> static cudaError_t step_go(const SsmArgs &a, const Launch &L) {
-    return a.p.batch * a.p.dim * P >= 4 * 1024 * (int64_t)L.sm_count ? step_seq<S, P, 4>(a, L) : step_seq<S, P, 1>(a, L);
+    return a.p.batch * a.p.dim * P >= 2 * 2048 * (int64_t)L.sm_count ? step_seq<S, P, 2>(a, L) : step_seq<S, P, 1>(a, L);
 }
 template <class S> static cudaError_t step_states(const SsmArgs &a, const Launch &L) {
     switch (a.plan.lanes) {

@@ -120,8 +120,8 @@ def test_host_memory_is_refused(mt):
     assert e.value.code == mt.MT_ERR_MEMORY
 
 
-def test_four_sequences_a_lane(mt):
-    """The single-token form with enough channels that a lane takes several sequences; their number is no multiple of four."""
+def test_several_sequences_a_lane(mt):
+    """The single-token form with enough channels that a lane takes several sequences; their number is odd."""
     b, d, n = 5, 32768, 16
     x = Inputs(torch.bfloat16, b, 1, d, n)
     slots = torch.tensor([3, -1, 0, 4, 9], dtype=torch.int32)
