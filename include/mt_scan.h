@@ -322,7 +322,7 @@ uint64_t mt_scan_launches(void);
 const char *mt_scan_strerror(int code);
 
 /* 1 in the bounds-checked build of the library (libmtscan_checked.so, whose
- * kernels check every global store and shared-memory access against its
+ * scan kernels check every global store and shared-memory access against its
  * buffer and report a bad one as MT_ERR_BOUNDS instead of making it), 0 in
  * the ordinary one. */
 int mt_scan_build_checked(void);

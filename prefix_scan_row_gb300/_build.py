@@ -5,7 +5,7 @@ Each .cu file is compiled by nvcc in parallel, then linked into one shared
 library next to this file. The CUDA runtime is linked statically, so the
 library loads without any library path set up. The checked library is the
 same sources compiled with MT_CHECKED=1: every global store and shared-memory
-access of its kernels is checked against its buffer first, and a bad one is
+access of its scan kernels is checked against its buffer first, and a bad one is
 skipped and reported as MT_ERR_BOUNDS by mt_scan_status() (a debugging and
 test build; the ordinary library is the product).
 """
