@@ -170,6 +170,14 @@ __device__ __forceinline__ f32x2 rcp_2f(f32x2 v) {
     unpack2f(v, a, b);
     return pack2f(rcpf(a), rcpf(b));
 }
+// Exponent of a decay, d * A in powers of two. The unit's exponential is low by about 2e-8 of its
+// value on average (measured, decays of 0.5 to 0.997), and a state that remembers n tokens sees
+// that n times. The constant takes it back in a multiply-add where the product alone would be as
+// dear: dA's error falls from 7.7e-7 to 3.0e-7 over 4 x 1024 tokens of 1024 channels, for no time.
+// Up to 8e-8 the unit's answer is 1 exactly, so a token with d = 0 still leaves the state alone.
+constexpr float kExponentLow = 2.6e-8f;
+__device__ __forceinline__ f32x2 exponent2f(f32x2 d, f32x2 A) { return fma2f(d, A, both(kExponentLow)); }
+
 // softplusf and sigmoidf of two values: half the multiply-add instructions.
 __device__ __forceinline__ f32x2 softplus_2f(f32x2 x) {
     float a, b;

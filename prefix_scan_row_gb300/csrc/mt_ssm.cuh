@@ -163,8 +163,8 @@ __device__ __forceinline__ void advance(Pairs &h, const Pairs &A, const float (&
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
         const f32x2 d2 = pack2f(dt[c], dt[c]), x2 = pack2f(du[c], du[c]);
-        h.v[c][0] = fma2f(ex2_2f(mul2f(d2, A.v[c][0])), h.v[c][0], mul2f(x2, b0));
-        h.v[c][1] = fma2f(ex2_2f(mul2f(d2, A.v[c][1])), h.v[c][1], mul2f(x2, b1));
+        h.v[c][0] = fma2f(ex2_2f(exponent2f(d2, A.v[c][0])), h.v[c][0], mul2f(x2, b0));
+        h.v[c][1] = fma2f(ex2_2f(exponent2f(d2, A.v[c][1])), h.v[c][1], mul2f(x2, b1));
         if (OUT) {
             float lo, hi;
             unpack2f(fma2f(c1, h.v[c][1], mul2f(c0, h.v[c][0])), lo, hi);
@@ -255,7 +255,7 @@ __device__ __forceinline__ void step_lane(const SsmArgs &a, int64_t b0, int64_t 
                 d[s] = softplusf(d[s]);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                h[s][k] = fmaf(ex2f(d[s] * (A[k] * kLog2e)), h[s][k], d[s] * u[s] * bb[k]);
+                h[s][k] = fmaf(ex2f(fmaf(d[s], A[k] * kLog2e, kExponentLow)), h[s][k], d[s] * u[s] * bb[k]);
                 y[s] = fmaf(cc[k], h[s][k], y[s]);
             }
             if (ALL || vec) {

@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(kSsmThreads, sizeof(S) == 2 && P <= 8 ? 3 : 2)
                     const f32x2 d2 = both(d[e]), x2 = both(x[e]);
 #pragma unroll
                     for (int s = 0; s < 2; ++s) {
-                        dec[j].v[e][s] = ex2_2f(mul2f(d2, A.v[e][s]));
+                        dec[j].v[e][s] = ex2_2f(exponent2f(d2, A.v[e][s]));
                         hs[j].v[e][s] = fma2f(dec[j].v[e][s], hs[j].v[e][s], mul2f(x2, b[s]));
                     }
                 }

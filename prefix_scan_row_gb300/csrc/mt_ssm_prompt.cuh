@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(kSsmThreads, kPromptCtas) k_ssm_carry(const __
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             f32x2 &hv = h.v[c][2 * q + e];
-                            const f32x2 dec = ex2_2f(mul2f(d2[c], A.v[c][2 * q + e]));
+                            const f32x2 dec = ex2_2f(exponent2f(d2[c], A.v[c][2 * q + e]));
                             hv = REV ? mul2f(dec, fma2f(x2[c], b[e], hv)) : fma2f(dec, hv, mul2f(x2[c], b[e]));
                         }
                     }
@@ -616,7 +616,7 @@ __global__ void __launch_bounds__(kSsmThreads, kPromptCtas) k_ssm(const __grid_c
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             f32x2 &hv = h.v[c][2 * q + e];
-                            hv = fma2f(ex2_2f(mul2f(d2[c], A.v[c][2 * q + e])), hv, mul2f(x2[c], bb[e]));
+                            hv = fma2f(ex2_2f(exponent2f(d2[c], A.v[c][2 * q + e])), hv, mul2f(x2[c], bb[e]));
                             acc[c] = fma2f(cc[e], hv, acc[c]);
                         }
                     }
