@@ -9,7 +9,8 @@
 // shared memory and reads them back as broadcasts, half a clock per value
 // and 64 channels. (A lane of 4 channels x 4 states, the gradient's shape, reads B and C with 4
 // addresses a warp, at twice the cost, and needs 12 operations a token for the sum over lanes; it
-// measured 347 us where this takes less than half, one prompt of 16384 tokens x 2048 channels.)
+// measured 347 us for one prompt of 16384 tokens x 2048 channels with 16 states, bf16, where
+// this takes 229: carries, chain and forward pass. 16 states of one channel a lane: 291.)
 //
 // Latency: u, delta, z, B and C of the next 8 tokens are copied into shared memory (cp.async, in
 // storage form, so that no register holds them) while 8 are worked on; and the
@@ -22,7 +23,7 @@ namespace mt {
 
 constexpr int kStep = kSsmTile;  // tokens per stage, and per checkpoint
 constexpr int kAhead = 4;         // tokens whose step sizes are made together
-constexpr int kPromptCtas = 3;    // CTAs an SM: at 4 (128 registers) a lane's schedule costs more than the warps give
+constexpr int kPromptCtas = 3;    // CTAs an SM: 16 warps at 128 registers measured 294 us against 261 at 12 of 168 (same code)
 
 // ROWS rows of up to `values` <= MOST values each, by 32-bit words: the words that a row's
 // live values touch, to dst + row * pitch (16-bit values that start in the middle of a word stay
@@ -454,40 +455,117 @@ __global__ void __launch_bounds__(kSsmThreads, kPromptCtas) k_ssm_carry(const __
                 a.decay[row + c] = s[c];
 }
 
-// Carries to first states: a lane a (channel, state) pair goes over the segments in
-// order (REV: from the last down), and each carry is replaced by the state (REV:
-// the adjoint) that its segment starts from. The loads do not depend on the
-// states, so kMany are in flight (16 for many segments, 8 where more threads count for more); done by every warp of the forward kernel
-// for itself instead, 57 segments took 20 of its 140 us.
-template <bool REV, int kMany>
-__global__ void __launch_bounds__(256) k_ssm_chain(const __grid_constant__ SsmArgs a) {
+// Carries to first states: each carry is replaced by the state (REV: the adjoint)
+// that its segment starts from. A lane holds V states of a channel over kChain segments, whose
+// loads are all in flight at once, and up to 16 warps of a CTA hold the segments after one another: each
+// combines its own, and goes over the sums of those before it, so the loads of 128
+// segments are waited for once. 9 us (caches empty) for 8 sequences of 7 segments of 65536 states; a lane that
+// walked down all segments of one state took 30, more in the addresses than in the sums.
+constexpr int kChain = 8, kChainMost = 16;
+struct ChainPlan {
+    int chunks, lanes;  // of a CTA: groups of kChain segments, and lanes of a group
+};
+static inline ChainPlan chain_plan(int64_t segments) {
+    int c = 1;
+    while (c < kChainMost && (int64_t)c * kChain < segments)
+        c *= 2;
+    return {c, c < 8 ? 256 / c : 32};
+}
+template <int V> __device__ __forceinline__ void get_states(const float *p, float (&x)[V]) {
+    if constexpr (V == 4)
+        lds4(p, x);
+    else
+        x[0] = *p;
+}
+template <int V> __device__ __forceinline__ void put_states(float *p, const float (&x)[V]) {
+    if constexpr (V == 4)
+        *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
+    else
+        *p = x[0];
+}
+template <bool REV, int V>
+__global__ void __launch_bounds__(32 * kChainMost) k_ssm_chain(const __grid_constant__ SsmArgs a, int lanes, int chunks) {
+    __shared__ float s_h[32 * kChainMost * V], s_sum[32 * kChainMost];
     pdl_prologue();
-    const int64_t per = a.p.dim * a.p.nstate, e = (int64_t)blockIdx.x * 256 + threadIdx.x, S = a.plan.segments;
-    if (e >= per)
-        return;
-    const int64_t ch = per <= 0xffffffffll ? (uint32_t)e / (uint32_t)a.p.nstate : e / a.p.nstate;
-    const float A = a.p.A[e] * kLog2e;
-    for (int64_t b = blockIdx.y; b < a.p.batch; b += gridDim.y) {
-        float *c = a.carry + b * S * per + e;
-        const float *sum = a.decay + b * S * a.p.dim + ch;
-        // forward: segment 0 starts from the copy in the last place, and its carry already holds it
-        float h = REV ? (a.p.dfinal != nullptr ? a.p.dfinal[b * per + e] : 0.0f) : c[(S - 1) * per];
-        for (int64_t j0 = 0; j0 < S; j0 += kMany) {
-            float next[kMany], dec[kMany];
+    const int chunk = threadIdx.x / lanes, x = threadIdx.x - chunk * lanes;
+    const int64_t per = a.p.dim * a.p.nstate, S = a.plan.segments, mine = ((int64_t)blockIdx.x * lanes + x) * V;
+    const bool in = mine < per;
+    const int64_t e = in ? mine : 0, ch = per <= 0xffffffffll ? (uint32_t)e / (uint32_t)a.p.nstate : e / a.p.nstate;
+    const int64_t by = REV ? -per : per, sum_by = REV ? -a.p.dim : a.p.dim;
+    float A[V];
+    get_states<V>(a.p.A + e, A);
 #pragma unroll
-            for (int k = 0; k < kMany; ++k) {
-                const int64_t j = j0 + k, s = REV ? S - 1 - j : j;
-                const bool in = j < S - 1;  // the last one's carry goes nowhere
-                next[k] = in ? c[s * per] : 0.0f;
-                dec[k] = in && (REV || s > 0) ? sum[s * a.p.dim] : 0.0f;
+    for (int v = 0; v < V; ++v)
+        A[v] *= kLog2e;
+    for (int64_t b = blockIdx.y; b < a.p.batch; b += gridDim.y) {
+        float *c = a.carry + (b * S + (REV ? S - 1 : 0)) * per + e;
+        const float *sum = a.decay + (b * S + (REV ? S - 1 : 0)) * a.p.dim + ch;
+        // forward: segment 0 starts from the copy in the last place, and its carry already holds it
+        float h[V] = {};
+        if (!REV)
+            get_states<V>(c + (S - 1) * per, h);
+        else if (a.p.dfinal != nullptr)
+            get_states<V>(a.p.dfinal + b * per + e, h);
+        for (int64_t first = 0; first < S; first += (int64_t)chunks * kChain) {
+            const int64_t j0 = first + chunk * kChain;
+            const int live = S - 1 - j0 < kChain ? (int)(S - 1 - j0) : kChain;  // the last one's carry goes nowhere
+            float next[kChain][V], dec[kChain];
+#pragma unroll
+            for (int k = 0; k < kChain; ++k) {
+                dec[k] = 0.0f;
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    next[k][v] = 0.0f;
+                if (k < live) {
+                    get_states<V>(c + (j0 + k) * by, next[k]);
+                    dec[k] = sum[(j0 + k) * sum_by];
+                }
+            }
+            const auto advance = [&](int k) {
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    h[v] = !REV && k == 0 && j0 == 0 ? next[k][v] : fmaf(ex2f(A[v] * dec[k]), h[v], next[k][v]);
+            };
+            float past[V];  // the state after all of the CTA's chunks
+            if (chunks > 1) {
+                float all = 0.0f;
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    past[v] = h[v];
+                    h[v] = chunk == 0 ? h[v] : 0.0f;
+                }
+#pragma unroll
+                for (int k = 0; k < kChain; ++k) {
+                    advance(k);
+                    all += dec[k];
+                }
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    s_h[v * lanes * chunks + threadIdx.x] = h[v];
+                s_sum[threadIdx.x] = all;
+                __syncthreads();
+                for (int i = 0; i < chunks; ++i) {
+                    const float d = s_sum[i * lanes + x];
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        if (i == chunk)
+                            h[v] = past[v];
+                        const float y = s_h[v * lanes * chunks + i * lanes + x];
+                        past[v] = i == 0 ? y : fmaf(ex2f(A[v] * d), past[v], y);
+                    }
+                }
+                __syncthreads();  // the sums are read, and every lane has the copy in the last place
             }
 #pragma unroll
-            for (int k = 0; k < kMany; ++k) {
-                const int64_t j = j0 + k, s = REV ? S - 1 - j : j;
-                if (j < S) {
-                    c[s * per] = h;
-                    h = !REV && s == 0 ? next[k] : fmaf(ex2f(A * dec[k]), h, next[k]);
-                }
+            for (int k = 0; k < kChain; ++k) {
+                if (in && k <= live)
+                    put_states<V>(c + (j0 + k) * by, h);
+                advance(k);
+            }
+            if (chunks > 1) {  // one chunk alone takes all segments in one turn
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    h[v] = past[v];
             }
         }
     }
@@ -669,7 +747,9 @@ template <class S, int K, int P, bool REV, bool ALN> static cudaError_t carry_go
     SsmArgs c = a;
     c.plan.ctiles = (a.gdim + 64 / P - 1) / (64 / P);
     const int64_t warps = a.p.batch * a.p.groups * c.plan.ctiles * (a.plan.segments - 1);
-    const int64_t grid = (warps + kSsmWarps - 1) / kSsmWarps, chain = (a.p.dim * a.p.nstate + 255) / 256;
+    const ChainPlan at = chain_plan(a.plan.segments);
+    const int64_t each = a.nvec ? 4 : 1;
+    const int64_t grid = (warps + kSsmWarps - 1) / kSsmWarps, chain = (a.p.dim * a.p.nstate + at.lanes * each - 1) / (at.lanes * each);
     if (grid > INT32_MAX || chain > INT32_MAX)
         return cudaErrorInvalidValue;
     const size_t smem = kSsmWarps * PromptSmem<S, K, P, 1>::kBytes;
@@ -681,7 +761,8 @@ template <class S, int K, int P, bool REV, bool ALN> static cudaError_t carry_go
     if (e != cudaSuccess)
         return e;
     note_launch();
-    return launch_pdl_2d(a.plan.segments > 16 ? k_ssm_chain<REV, 16> : k_ssm_chain<REV, 8>, dim3((unsigned)chain, (unsigned)(a.p.batch < 65535 ? a.p.batch : 65535)), 256, L.stream, a);
+    return launch_pdl_2d(a.nvec ? k_ssm_chain<REV, 4> : k_ssm_chain<REV, 1>, dim3((unsigned)chain, (unsigned)(a.p.batch < 65535 ? a.p.batch : 65535)),
+                         (unsigned)(at.lanes * at.chunks), L.stream, a, at.lanes, at.chunks);
 }
 template <class S, int K, int P, bool ALN> static cudaError_t prompt_go(const SsmArgs &a, const Launch &L) {
     cudaError_t e;

@@ -308,3 +308,13 @@ def test_same_bits_each_time_and_on_another_stream(mt):
     side.synchronize()
     for k in a:
         assert torch.equal(a[k], b[k]) and torch.equal(a[k], c[k]), k
+
+
+@pytest.mark.parametrize("n", [3, 4])
+@pytest.mark.parametrize("length,lens", [(140, None), (1040, None), (2064, [2064, 1041]), (4243, None), (4243, [2050, 4243])],
+                         ids=lambda v: "full" if v is None else "ragged" if isinstance(v, list) else str(v))
+def test_many_segments(mt, n, length, lens):
+    """A token axis of 9 to 266 segments: the carries meet over more turns and more warps than one."""
+    x = Inputs(torch.float32, 2, length, 6, n, lens=None if lens is None else torch.tensor(lens, dtype=torch.int32))
+    check_forward(x, *x.forward(mt))
+    check_gradient(x, x.gradient(mt))
