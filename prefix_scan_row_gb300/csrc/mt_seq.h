@@ -33,11 +33,11 @@ constexpr int kSsmTile = 8;  // tokens per checkpoint
 struct SsmPlan {
     int lanes;         // lanes that share a channel's states, four states each
     int64_t segments;  // pieces of the token axis that run side by side
-    int64_t seg_len;   // tokens per segment, a multiple of 16
+    int64_t seg_len;   // tokens per segment, a multiple of 8
     int64_t ctiles;    // channel tiles per group (forward: of a warp; gradient: of a CTA)
     int64_t carry_slots, decay_slots, shared_slots, param_slots;  // 8-byte slots of the scratch's parts
 };
-SsmPlan ssm_plan(int64_t batch, int64_t len, int64_t dim, int64_t nstate, int64_t groups, bool grad);
+SsmPlan ssm_plan(int64_t batch, int64_t len, int64_t dim, int64_t nstate, int64_t groups, bool grad, bool lens);
 cudaError_t ssm_launch(const mt_ssm_args &a, const Launch &L);
 cudaError_t ssm_grad_launch(const mt_ssm_args &a, const Launch &L);
 cudaError_t ssm_step_launch(const mt_ssm_args &a, const Launch &L);

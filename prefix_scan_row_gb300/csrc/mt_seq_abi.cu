@@ -242,8 +242,13 @@ extern "C" int64_t mt_selective_scan_scratch_slots(int64_t batch, int64_t len, i
         product({batch, len, dim, nstate, 16}) < 0 || product({batch, len, groups, nstate, 16}) < 0 ||
         product({batch, dim, nstate, 16}) < 0)
         return -1;
-    const SsmPlan p = ssm_plan(batch, len, dim, nstate, groups, grad != 0);
-    return p.carry_slots + p.decay_slots + p.shared_slots + p.param_slots;
+    int64_t most = 0;  // of the plans with live lengths and without
+    for (const bool lens : {false, true}) {
+        const SsmPlan p = ssm_plan(batch, len, dim, nstate, groups, grad != 0, lens);
+        const int64_t slots = p.carry_slots + p.decay_slots + p.shared_slots + p.param_slots;
+        most = slots > most ? slots : most;
+    }
+    return most;
 }
 
 extern "C" int64_t mt_selective_scan_checkpoint_slots(int64_t batch, int64_t len, int64_t dim, int64_t nstate) {

@@ -4,16 +4,40 @@
 
 namespace mt {
 
-// Warps that keep an SM's arithmetic busy: a lane has 16 independent
-// recurrences, so a few warps a scheduler suffice. The plan must not ask the
-// device (scratch is sized on the host), so it counts GB300's 152 SMs.
+// The tokens are cut where the uncut work would leave SMs with less than it takes to keep
+// their arithmetic busy: a lane has 32 independent recurrences, so that is little. Three
+// CTAs of an SM run at once. The plan must not ask the device (scratch is sized on the host), so it
+// counts GB300's 152 SMs.
 constexpr int64_t kSsmSms = 152;
-constexpr int64_t kEnoughWarps = kSsmSms * 5;   // from here on the tokens are not cut
-constexpr int64_t kTargetWarps = kSsmSms * 24;  // what a cut aims at
-constexpr int64_t kTargetCtas = kSsmSms * 9;    // the same for the gradient's CTAs
-constexpr int64_t kLeastSegment = 16;           // tokens: a warp alone takes as long for a token as the chain of carries does
+constexpr int64_t kEnoughWarps = kSsmSms * 5;  // from here on the tokens are not cut
+constexpr int64_t kEnoughCtas = kSsmSms * 3;   // the same for the gradient's CTAs
+constexpr int64_t kResident = 3, kMostCtas = 12;  // CTAs of an SM: at once, and all that a cut aims at
+constexpr int64_t kLeastSegment = 16;  // tokens: at least 64 measured 100 us where 16 take 30 (2 x 700 tokens, 301 channels)
+constexpr int64_t kSegmentStart = 8;   // tokens' time that a segment's first loads and its carry take
 
-SsmPlan ssm_plan(int64_t batch, int64_t len, int64_t dim, int64_t nstate, int64_t groups, bool grad) {
+// Tokens of a segment, `units` / per_cta CTAs working on one. The time is that of the SM with the
+// most CTAs, so of the cuts into 3 to 12 CTAs an SM the one is taken that makes it the least. Where
+// lengths differ, CTAs end at any time and half a segment is left at the end, which favours short ones.
+// 8 x 1027 tokens x 4096 channels: ragged, 80 tokens 189 us and 152 195; full, 241 and 240. A gradient over
+// 4 x 2048 tokens x 4096 channels: 80 tokens in its forward pass 1000 us, 296 981; 16384 tokens x 2048: 288 229, 144 234.
+static int64_t ssm_segment(int64_t len, int64_t units, int64_t per_cta, bool lens) {
+    const int64_t wave = kSsmSms * per_cta;
+    int64_t best = len, least = INT64_MAX;
+    for (int64_t r = kResident; r <= kMostCtas; ++r) {
+        const int64_t s = r * wave / units;
+        int64_t seg = s > 0 ? ((len + s - 1) / s + kSsmTile - 1) / kSsmTile * kSsmTile : len;
+        seg = seg < kLeastSegment ? kLeastSegment : seg;
+        const int64_t busy = (units * ((len + seg - 1) / seg) + wave - 1) / wave;
+        const int64_t cost = (busy < kResident ? kResident : busy) * (seg + kSegmentStart) + (lens ? seg / 2 : 0);
+        if (cost < least) {
+            least = cost;
+            best = seg;
+        }
+    }
+    return best;
+}
+
+SsmPlan ssm_plan(int64_t batch, int64_t len, int64_t dim, int64_t nstate, int64_t groups, bool grad, bool lens) {
     SsmPlan p;
     p.lanes = 2;
     while (p.lanes < 32 && 4 * p.lanes < nstate)
@@ -23,17 +47,13 @@ SsmPlan ssm_plan(int64_t batch, int64_t len, int64_t dim, int64_t nstate, int64_
     const int64_t channels = grad ? 128 / p.lanes * kSsmWarps : nstate <= 16 ? 64 : nstate <= 32 ? 32 : nstate <= 64 ? 16 : 8;
     p.ctiles = (gdim + channels - 1) / channels;
     const int64_t units = batch * groups * p.ctiles;  // warps or CTAs of one segment
-    const int64_t enough = grad ? kSsmSms * 3 : kEnoughWarps, target = grad ? kTargetCtas : kTargetWarps;
     p.segments = 1;
-    p.seg_len = len > 0 ? (len + 15) / 16 * 16 : 16;
-    if (units > 0 && units < enough && len > kLeastSegment) {
-        int64_t s = target / units;
-        const int64_t most = len / kLeastSegment;
-        if (s > most)
-            s = most;
-        if (s > 1) {
-            p.seg_len = ((len + s - 1) / s + 15) / 16 * 16;
-            p.segments = (len + p.seg_len - 1) / p.seg_len;
+    p.seg_len = len > 0 ? (len + kSsmTile - 1) / kSsmTile * kSsmTile : kSsmTile;
+    if (units > 0 && units < (grad ? kEnoughCtas : kEnoughWarps) && len > kLeastSegment) {
+        const int64_t seg = ssm_segment(len, units, grad ? 1 : kSsmWarps, lens);
+        if (seg < len) {
+            p.seg_len = seg;
+            p.segments = (len + seg - 1) / seg;
         }
     }
     const int64_t cut = p.segments > 1 ? batch * p.segments * dim : 0;
@@ -65,7 +85,7 @@ static bool channels_fit(const mt_ssm_args &p, bool grad, int64_t gdim, int64_t 
 static SsmArgs ssm_args(const mt_ssm_args &p, bool grad) {
     SsmArgs a;
     a.p = p;
-    a.plan = ssm_plan(p.batch, p.len, p.dim, p.nstate, p.groups, grad);
+    a.plan = ssm_plan(p.batch, p.len, p.dim, p.nstate, p.groups, grad, p.lens != nullptr);
     a.ntiles = (p.len + kSsmTile - 1) / kSsmTile;
     a.gdim = p.dim / p.groups;
     const int64_t v = p.dtype == MT_F32 ? 16 : 8;  // bytes of four values
