@@ -123,7 +123,7 @@ def test_embed_refusals():
 
 
 def test_scratch_sizes():
-    assert mt.mt_selective_scan_scratch_slots(8, 2048, 4096, 16) == 0  # enough channels: the tokens are not cut
+    assert mt.mt_selective_scan_scratch_slots(16, 2048, 4096, 16) == 0  # enough channels: the tokens are not cut
     assert mt.mt_selective_scan_scratch_slots(1, 2048, 64, 16) > 0
     assert mt.mt_selective_scan_checkpoint_slots(2, 33, 10, 5) == (2 * 3 * 10 * 5 + 1) // 2
     for bad in ((-1, 1, 1, 1), (1, 1, 1, 129), (1, 1, 1, 0)):
