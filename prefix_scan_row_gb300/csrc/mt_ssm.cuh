@@ -1,5 +1,5 @@
-// mt_ssm.cuh -- the selective state space scan: forward, gradient and
-// single-token kernels, instantiated per activation type (mt_ssm_*.cu).
+// mt_ssm.cuh -- the selective state space scan: what its kernels share, and the
+// single-token kernel, instantiated per activation type (mt_ssm_*.cu).
 //
 //   Delta = softplus(delta + delta_bias),  a_t[d,n] = exp(Delta_t[d] A[d,n])
 //   h_t[d,n] = a_t[d,n] h_{t-1}[d,n] + Delta_t[d] u_t[d] B_t[n]
@@ -9,26 +9,20 @@
 // whose products of a are exp(A * sum of Delta): the carry of a span of tokens is
 // one state and one sum of steps per channel.
 //
-// Work split. A lane keeps 4 channels x 4 states in registers, P lanes share
-// a channel group (4P states), so a warp holds 128/P channels. Per token
-// a lane reads Delta and Delta*u of its 4 channels and B and C of its 4 states from
-// shared memory, four 16-byte reads for 16 (channel, state) pairs: fewer
-// channels a lane would make the reads, more would make the registers, the
-// limit. The sum over states is 4 values over P lanes, exchanged so that every
-// step halves the values that are left. A warp works through tiles of 16
-// tokens on its own: it widens u and delta of the tile into shared memory, walks
-// the 16 tokens, and gates and stores the tile.
-//
 // Bound: per (token, channel, state) one exponential and four multiply-adds
-// (Delta*A, the input, the recurrence, the output); the exponentials run at 32
-// and packed multiply-adds at 128 a clock and SM, so at 16 states a warp's token
-// costs 16 clocks of either against 8 bytes per channel of HBM traffic
-// (4.8 clocks at 16-bit storage): arithmetic, not bandwidth.
+// (Delta*A, the input, the recurrence, the output). The exponentials run at 30.5 and
+// packed multiply-adds at up to 128 a clock and SM, so a token of 64 channels x 16 states
+// takes 34 clocks of an SM against 24 of HBM traffic at 16-bit storage (8 bytes a channel),
+// and in the carry pass as many again against 12: arithmetic, not bandwidth. With one token a
+// sequence the states themselves are read and written, and it is bandwidth again.
 //
 // Few channels do not fill the GPU: the tokens are then cut into segments that
 // run side by side, after a pass that computes each segment's carry (a state
 // from zero, and the sum of steps); a segment's first state is the combination of
 // the carries before it.
+//
+// Here are the parts that prompts and gradients share, and the single-token kernel; the
+// other kernels say how they split their work.
 #pragma once
 
 #include <type_traits>

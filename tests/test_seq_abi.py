@@ -125,7 +125,7 @@ def test_embed_refusals():
 def test_scratch_sizes():
     assert mt.mt_selective_scan_scratch_slots(16, 2048, 4096, 16) == 0  # enough channels: the tokens are not cut
     assert mt.mt_selective_scan_scratch_slots(1, 2048, 64, 16) > 0
-    assert mt.mt_selective_scan_checkpoint_slots(2, 33, 10, 5) == (2 * 3 * 10 * 5 + 1) // 2
+    assert mt.mt_selective_scan_checkpoint_slots(2, 33, 10, 5) == (2 * 5 * 10 * 5 + 1) // 2  # a state every 8 tokens
     for bad in ((-1, 1, 1, 1), (1, 1, 1, 129), (1, 1, 1, 0)):
         with pytest.raises(ValueError):
             mt.mt_selective_scan_checkpoint_slots(*bad)
