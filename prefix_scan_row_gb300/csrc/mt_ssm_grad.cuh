@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kSsmThreads, sizeof(S) == 2 && P <= 8 ? 3 : 2)
             __syncwarp();
         }
         if (left < kStep)
-            R::no_steps(raw, left, lane, softplus);
+            R::no_steps(raw, left, lane);
         Pairs h;
         h.load(a.p.checkpoints + ((at.b * a.ntiles + t0 / kStep) * a.p.dim + at.ch) * N, N, at.n0, at.cl, ALN || a.nvec);
         __syncwarp();
@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kSsmThreads, sizeof(S) == 2 && P <= 8 ? 3 : 2)
             const int t = et + i * kTok;
             if (kTok <= kStep || t < kStep) {
                 f32x2 d = add2f(R::read(raw, t, ec), bias);
-                if (softplus)
+                if (softplus || t >= left)
                     d = softplus_2f(d);
                 const f32x2 u = R::read(raw + R::kBytes, t, ec);
                 f32x2 o = R::read(raw + 2 * R::kBytes, t, ec);

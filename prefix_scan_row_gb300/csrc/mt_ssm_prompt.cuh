@@ -132,11 +132,12 @@ template <class S, int CW> struct Rows8 {
             *reinterpret_cast<uint32_t *>(row) = Codec<S>::pack2(a, b);
         }
     }
-    // tokens left .. kStep - 1 of a stage of delta: steps of 0, as softplus(-inf) (or 0 itself) gives them
-    static __device__ __forceinline__ void no_steps(char *rows, int left, int lane, bool softplus) {
+    // tokens left .. kStep - 1 of a stage of delta: -inf, of which softplus (after any bias) makes the step 0 that they
+    // take. So they go through softplus where the live tokens have none, too: a 0 here would come out as the bias
+    static __device__ __forceinline__ void no_steps(char *rows, int left, int lane) {
         for (int t = left; t < kStep; ++t)
             for (int c = lane; c < CW; c += 32)
-                Codec<S>::store1(reinterpret_cast<S *>(rows + t * kPitch) + c, softplus ? __int_as_float((int)0xff800000u) : 0.0f);
+                Codec<S>::store1(reinterpret_cast<S *>(rows + t * kPitch) + c, __int_as_float((int)0xff800000u));
     }
     // the rows of the `left` tokens to global memory
     static __device__ __forceinline__ void put16(const char *rows, S *at, int64_t stride, int left, bool in, int lane) {
@@ -395,7 +396,7 @@ __global__ void __launch_bounds__(kSsmThreads, kPromptCtas) k_ssm_carry(const __
             __syncwarp();
         }
         if (left < kStep)
-            R::no_steps(raw, left, lane, softplus);
+            R::no_steps(raw, left, lane);
         St::widen(sb, raw + 3 * R::kBytes, bp, bt, t0, left, (int)N, lane, ALN || a.bvec);
         __syncwarp();
 #pragma unroll
@@ -410,7 +411,7 @@ __global__ void __launch_bounds__(kSsmThreads, kPromptCtas) k_ssm_carry(const __
             // chosen, not branched on: a branch would keep one group's work from the next one's
 #pragma unroll
             for (int j = 0; j < kAhead; ++j)
-                d[j] = choose_2f(softplus, softplus_2f(d[j]), d[j]);
+                d[j] = choose_2f(softplus || i + j >= left, softplus_2f(d[j]), d[j]);
             if (REV) {
 #pragma unroll
                 for (int j = 0; j < kAhead; ++j) {
@@ -661,7 +662,7 @@ __global__ void __launch_bounds__(kSsmThreads, kPromptCtas) k_ssm(const __grid_c
             __syncwarp();
         }
         if (left < kStep)
-            R::no_steps(raw, left, lane, softplus);
+            R::no_steps(raw, left, lane);
         St::widen(sb, raw + 3 * R::kBytes, bp, a.p.B_token, t0, left, (int)N, lane, ALN || a.bvec);
         St::widen(sc, raw + 3 * R::kBytes + St::kBytes, cp, a.p.C_token, t0, left, (int)N, lane, ALN || a.bvec);
         __syncwarp();
@@ -675,7 +676,7 @@ __global__ void __launch_bounds__(kSsmThreads, kPromptCtas) k_ssm(const __grid_c
             }
 #pragma unroll
             for (int j = 0; j < kAhead; ++j)
-                d[j] = choose_2f(softplus, softplus_2f(d[j]), d[j]);
+                d[j] = choose_2f(softplus || i + j >= left, softplus_2f(d[j]), d[j]);
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) {
                 f32x2 acc[2] = {0ull, 0ull};
