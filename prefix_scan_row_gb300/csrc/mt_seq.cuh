@@ -29,16 +29,13 @@ static cudaError_t launch_pdl_2d(void (*kernel)(KArgs...), dim3 grid, unsigned b
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
-// ---- V neighbouring values --------------------------------------------------
-// load_n / store_n move V values as one vector access when `vec` (then p is
-// aligned to V values) and otherwise value by value; `live` values exist, the
-// others load as 0 and are not stored.
+// ---- four neighbouring values -------------------------------------------------
+// as one vector access when `vec` (then p is aligned to four values) and all four
+// are `live`, otherwise value by value; those that do not exist load as 0.
 template <class S, int V> struct VecOf;
 template <> struct VecOf<float, 4> { using T = uint4; };
 template <> struct VecOf<__nv_bfloat16, 4> { using T = uint2; };
 template <> struct VecOf<__half, 4> { using T = uint2; };
-template <> struct VecOf<__nv_bfloat16, 8> { using T = uint4; };
-template <> struct VecOf<__half, 8> { using T = uint4; };
 
 template <class S> __device__ __forceinline__ void widen4(const typename VecOf<S, 4>::T &w, float (&x)[4]);
 template <> __device__ __forceinline__ void widen4<float>(const uint4 &w, float (&x)[4]) { Codec<float>::unpack(w, x); }
@@ -76,16 +73,6 @@ template <class S> struct Raw4 {
     }
     __device__ __forceinline__ void widen(float (&x)[4]) const { widen4<S>(w, x); }
 };
-template <class S> __device__ __forceinline__ void store4(S *p, const float (&x)[4], bool vec, int live) {
-    if (vec && live == 4) {
-        *reinterpret_cast<typename VecOf<S, 4>::T *>(p) = narrow4<S>(x);
-    } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (k < live)
-                Codec<S>::store1(p + k, x[k]);
-    }
-}
 
 // ---- asynchronous copies to shared memory ------------------------------------------
 // Zeros where `in` is false (the source is then not read).

@@ -255,12 +255,12 @@ __global__ void __launch_bounds__(kSsmThreads, sizeof(S) == 2 && P <= 8 ? 3 : 2)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int t = 2 * qt + j;
-                float d[4], x[4], none[4];
+                float d[4], x[4];
                 f32x2 b0, b1;
                 lds4(dt + t * CW + wo, d);
                 lds4(du + t * CW + wo, x);
                 lds_pairs(sb + t * NP + no, b0, b1);
-                advance<false>(h, A, d, x, b0, b1, 0ull, 0ull, none);
+                advance(h, A, d, x, b0, b1);
             }
             mark_store(marks + (qt + 1) * 128, lane, h);
         }
