@@ -475,7 +475,8 @@ int mt_causal_conv_step(const mt_conv_args *args, void *stream);
 
 /* mt_causal_conv_grad -- gradients of mt_causal_conv by x, weight, bias and
  * (dstate) the first state, from dout. The state is only read here, row b for
- * sequence b (slots must be NULL): it holds what it held before the forward call. out is ignored. */
+ * sequence b (slots must be NULL): it holds what it held before the forward call. out is ignored.
+ * The state that the forward call leaves counts as a constant: a gradient by it is not taken in. */
 int mt_causal_conv_grad(const mt_conv_args *args, void *stream);
 int64_t mt_causal_conv_grad_scratch_slots(int64_t batch, int64_t len, int64_t dim, int64_t width);
 

@@ -192,7 +192,8 @@ __device__ __forceinline__ void conv_params(const ConvDims &d, const ConvLane<AL
 // ---- forward ------------------------------------------------------------------------
 // Tokens per lane: at 64 the W-1 inputs read twice are a twentieth of the
 // bytes and come from L2. 32 tokens a lane measured 54 us where 64 and 128 take 47 (4 x 4096 tokens x 4096
-// channels, bf16, W = 4: 268 MB, 86 % of the copy's rate).
+// channels, bf16, W = 4: 268 MB, 85 % of the copy's rate). Rows that fit no vector (4095 channels) are loaded value by value, one group
+// ahead: 68 us (58 %), in f32 90 against 84 (87 and 94 %).
 constexpr int kConvSpan = 64;
 constexpr int kConvAhead = 4, kConvGroups = 4;  // tokens of a group, groups on their way
 
@@ -346,9 +347,13 @@ __global__ void __launch_bounds__(kConvThreads) k_conv_step(const S *x, S *out, 
 // too, without the sums. The sums of a span are 4(W+1) bytes against its
 // 6 * kGradSpan bytes of activations; they are added over a CTA's spans in
 // shared memory, written once per CTA and added by a second kernel in order.
-// 30 us for 2 x 4099 tokens x 2048 channels, f16, W = 4 (101 MB, 15 us of the copy's rate): bound by
-// issue, 98 instructions a lane and token. Spans of 16, 32 and 128 tokens measured 45, 38 and 62 us
-// where 64 took 36: shorter ones walk the W-1 tokens past the end more often, longer ones leave warps out.
+// 30 us for 2 x 4099 tokens x 2048 channels, f16, W = 4 (101 MB, 15 us of the copy's rate; 3.3 TB/s). Its 98 instructions a lane
+// and token are 11 us of the SMs' issue slots (47 % busy), so neither those nor the bytes bound it, but the cut: 288 CTAs of 512 tokens x
+// 128 channels, of which 32 hold three tokens and the others lie two or one on 152 SMs, 13 warps an SM (128 registers), each a chain of 67 tokens.
+// 8 x 4096 tokens x 4096 channels (2048 CTAs) reach 4.6 TB/s, one sequence of 2048 tokens x 1024 channels (32 CTAs) takes 18.7 us.
+// Spans of 16, 32 and 128 tokens measured 45, 38 and 62 us where 64 took 36: shorter ones walk the W-1 tokens past the end more often,
+// longer ones leave warps out. Rows that fit no vector: 47 us with 2047 channels (f32 73 against 40). With W = 4 that form keeps more than 128
+// registers a thread, and spills 100 bytes (f32 316).
 constexpr int kFew = 4, kGradGroups = 2;  // tokens of a group, groups on their way
 constexpr int kGradSpan = 64;
 constexpr int kGradSpans = 8;  // a CTA: 128 channels x 8 spans, a warp a span

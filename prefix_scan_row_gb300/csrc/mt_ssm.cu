@@ -8,6 +8,15 @@ namespace mt {
 // their arithmetic busy: a lane has 32 independent recurrences, so that is little. Three
 // CTAs of an SM run at once. The plan must not ask the device (scratch is sized on the host), so it
 // counts GB300's 152 SMs.
+// Both sides of the two lines, us, bf16, 4096 channels x 16 states, every plan forced uncut / left to ssm_segment:
+//   sequences (warps of a prompt, CTAs of a gradient)   8 (512, 256)   12 (768, 384)   16 (1024, 512)   24 (1536, 768)   32 (2048, 1024)
+//   prompt, 512 tokens                                   108 / 126       161 / 178       221 / 229        228 / 327        309 / 388
+//   prompt, 2048 tokens                                  411 / 449       621 / 631       859 / 835        886 / 1201      1206 / 1455
+//   the same with checkpoints                            524 / 503       751 / 710      1022 / 945       1053 / 1356      1463 / 1667
+//   gradient, 512 tokens                                 511 / 381       524 / 546       779 / 733       1024 / 1042      1253 / 1253
+//   gradient, 2048 tokens                               2001 / 1434     2061 / 2071     3055 / 2820      4044 / 4045      4934 / 4934
+// A single line is right at both ends and not between: it costs prompts up to 18 % at 8 sequences (cut) and, where the
+// last wave is half empty, up to 8 % at 16 (uncut).
 constexpr int64_t kSsmSms = 152;
 constexpr int64_t kEnoughWarps = kSsmSms * 5;  // from here on the tokens are not cut
 constexpr int64_t kEnoughCtas = kSsmSms * 3;   // the same for the gradient's CTAs

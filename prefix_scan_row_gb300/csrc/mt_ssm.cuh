@@ -14,7 +14,7 @@
 // packed multiply-adds at up to 128 a clock and SM, so a token of 64 channels x 16 states
 // takes 34 clocks of an SM against 24 of HBM traffic at 16-bit storage (8 bytes a channel),
 // and in the carry pass as many again against 12: arithmetic, not bandwidth. With one token a
-// sequence the states themselves are read and written, and it is bandwidth again.
+// sequence the states themselves are read and written, and bytes count again.
 //
 // Few channels do not fill the GPU: the tokens are then cut into segments that
 // run side by side, after a pass that computes each segment's carry (a state
@@ -179,9 +179,11 @@ template <int P> struct SsmPlace {
 
 // ---- one token of each sequence --------------------------------------------------------
 // P lanes share a channel, four states each: the state is read and written once
-// (8 bytes a pair) and everything else is small beside it; bound by bytes. A lane takes
-// its channel of SEQ sequences, so A and the parameters are read once for them and
-// their states are in flight together: 64 sequences of 4096 channels x 16 states, 36 MB, take 10.7 us.
+// (8 bytes a pair) and everything else is small beside it. A lane takes its channel of SEQ sequences, so A
+// and the parameters are read once for them and their states are in flight together. 64 sequences of 4096 channels x 16
+// states, 36 MB, take 10.7 us in a CUDA graph (states of 16 batches in turn; 8.8 for one that stays in L2): 3.4 TB/s, half of
+// the copy's rate. 16 sequences take 4.2 us (2.2 TB/s), 128 take 18.8 (3.8): what is left is the latency of short CTAs
+// that each load, compute and store once (27 warps an SM, issue 62 %), not the bytes.
 // ALL: every sequence has a state and all values move as vectors, so that nothing stands between the loads.
 template <class S, int P, int SEQ, bool ALL>
 __device__ __forceinline__ void step_lane(const SsmArgs &a, int64_t b0, int64_t ch, int p, float *const (&sp)[SEQ], bool vec, int live) {

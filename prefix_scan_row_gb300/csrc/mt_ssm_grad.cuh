@@ -24,9 +24,10 @@
 // (no atomics, so the same bits every time). dA, dD and the bias's gradient stay in registers over a
 // segment and are added over sequences and segments by the same kernel.
 //
-// Bound by issue: 390 warp instructions a token of 32 channels at 16 states, of which the
-// recurrences are 143 packed multiply-adds. 310 us of 4 x 1024 tokens x 4096 channels, bf16 (a tile of 16
-// tokens with 8 x 2 tokens' states and decays made twice: 481; channel pairs for state pairs: 316).
+// 390 warp instructions a token of 32 channels at 16 states, of which the recurrences are 143 packed multiply-adds. 310 us
+// of 4 x 1024 tokens x 4096 channels, bf16 (a tile of 16 tokens with 8 x 2 tokens' states and decays made twice: 481; channel pairs
+// for state pairs: 316). Issue is 55 % busy, FMA 46, XU 20, DRAM 15: bound by how far 11 warps an SM (168 registers, 75 KB a CTA)
+// cover an instruction's wait for the one before (1.0 of a warp's cycles between two instructions; shared memory 0.65, math pipes 0.5).
 #pragma once
 
 #include "mt_ssm_prompt.cuh"

@@ -5,12 +5,12 @@
 // states in registers (K of them; P lanes share a channel pair when there are
 // more), so at up to 16 states the sum over states never leaves the lane and a
 // channel's step size, gate and output are made where they are used. B and C
-// are the same for all channels of a group: a warp widens 16 tokens of them into
+// are the same for all channels of a group: a warp widens 8 tokens of them into
 // shared memory and reads them back as broadcasts, half a clock per value
 // and 64 channels. (A lane of 4 channels x 4 states, the gradient's shape, reads B and C with 4
 // addresses a warp, at twice the cost, and needs 12 operations a token for the sum over lanes; it
 // measured 347 us for one prompt of 16384 tokens x 2048 channels with 16 states, bf16, where
-// this takes 229: carries, chain and forward pass. 16 states of one channel a lane: 291.)
+// this takes 227: carries, chain and forward pass. 16 states of one channel a lane: 291.)
 //
 // Latency: u, delta, z, B and C of the next 8 tokens are copied into shared memory (cp.async, in
 // storage form, so that no register holds them) while 8 are worked on; and the
