@@ -374,8 +374,8 @@ int mt_scan_rows_noalloc(const void *inp, void *out, int64_t rows, int64_t n, in
 
 /* ------------------------------------------------------------------------
  * Operators of sequence models: the embedding lookup, the short causal
- * convolution and the selective state space scan, forward, backward and for
- * single tokens. They follow the rules above: caller-owned device memory,
+ * convolution, the selective state space scan and the gated scan, forward, backward and for
+ * single tokens; a beam search's selection, and copies between slots of state pools. They follow the rules above: caller-owned device memory,
  * work enqueued on `stream` only, host-checkable mistakes refused before any
  * launch, f32 arithmetic with one rounding at each store. Every sum has a
  * fixed order, so a call gives the same bits each time. No call waits
@@ -561,6 +561,149 @@ int mt_selective_scan_grad(const mt_ssm_args *args, void *stream);
  * (grad nonzero), and of the checkpoints; -1 for a size out of range. */
 int64_t mt_selective_scan_scratch_slots(int64_t batch, int64_t len, int64_t dim, int64_t nstate, int64_t groups, int grad);
 int64_t mt_selective_scan_checkpoint_slots(int64_t batch, int64_t len, int64_t dim, int64_t nstate);
+
+/*
+ * mt_gated_args -- arguments of the gated scan calls. Every field is eight
+ * bytes wide; strides count elements; optional pointers may be NULL. With
+ * sigma the logistic function, for every channel d by itself
+ *   s_t = sigma(r_t)
+ *   with rate:     a_t = exp(-rate[d] * s_t),  w_t = sqrt(1 - a_t^2)
+ *   without rate:  a_t = 1 - s_t,              w_t = s_t
+ *   h_t = a_t * h_{t-1} + w_t * v_t,   v_t = sigma(i_t) * x_t, or x_t without i
+ *   out_t = h_t, or h_t * z_t * sigma(z_t) with z
+ * Where w_t is 0 (s_t or rate[d] so small that 1 - a_t^2 is) its derivative counts as 0.
+ */
+typedef struct {
+    int64_t dtype;                 /* all activations and their gradients: MT_F32, MT_BF16 or MT_F16 */
+    int64_t batch, len, dim;       /* mt_gated_scan_step: len is ignored (one token) */
+    int64_t carry_in;              /* nonzero: the state before token 0 is the pool's; zero: it is 0 */
+    int64_t nslots;                /* rows of the state pool (batch without slots) */
+    const void *x;                 /* [batch, len, dim] */
+    int64_t x_batch, x_token;
+    const void *r;                 /* [batch, len, dim]: the gate of the recurrence */
+    int64_t r_batch, r_token;
+    const void *i;                 /* [batch, len, dim], optional: the gate of the input */
+    int64_t i_batch, i_token;
+    const void *z;                 /* [batch, len, dim], optional: the gate of the output */
+    int64_t z_batch, z_token;
+    const float *rate;             /* [dim], optional, 0 or more */
+    float *state;                  /* [nslots, dim] contiguous */
+    const int32_t *slots, *lens;   /* optional */
+    void *out;                     /* [batch, len, dim] */
+    int64_t out_batch, out_token;
+    float *checkpoints;            /* mt_gated_scan_checkpoint_slots(...) slots: written by the scan where given
+                                      (slots must then be NULL), read by the gradient */
+    /* mt_gated_scan_grad only */
+    void *scratch;                 /* mt_gated_scan_scratch_slots(...) slots, 16-byte aligned; needed with drate */
+    const void *dout;              /* [batch, len, dim] */
+    int64_t dout_batch, dout_token;
+    void *dx;
+    int64_t dx_batch, dx_token;
+    void *dr;
+    int64_t dr_batch, dr_token;
+    void *di;                      /* required with i */
+    int64_t di_batch, di_token;
+    void *dz;                      /* required with z */
+    int64_t dz_batch, dz_token;
+    float *drate;                  /* [dim], optional, only with rate */
+    const float *dfinal;           /* [batch, dim], optional: gradient of the last states */
+    float *dinit;                  /* [batch, dim], optional: gradient of the first states */
+} mt_gated_args;
+
+/*
+ * mt_gated_scan -- the gated scan of whole prompts. `state` is optional; if
+ * given it is read (with carry_in) and left holding the state after each
+ * sequence's last live token. scratch .. dinit are ignored.
+ * Errors of the three calls: MT_ERR_ARG, MT_ERR_DTYPE, MT_ERR_ALIAS,
+ * MT_ERR_ALIGN, MT_ERR_MEMORY, MT_ERR_CUDA.
+ */
+int mt_gated_scan(const mt_gated_args *args, void *stream);
+
+/* mt_gated_scan_step -- one token of each sequence: x, r, i, z and out are
+ * [batch, dim] (the _batch strides count); state is required and updated in
+ * place (carry_in, lens and checkpoints are ignored). */
+int mt_gated_scan_step(const mt_gated_args *args, void *stream);
+
+/* mt_gated_scan_grad -- every gradient of mt_gated_scan from dout (and dfinal),
+ * with the checkpoints that the forward call of the same arguments wrote.
+ * state, slots, carry_in and out are ignored (the first states are in the
+ * checkpoints; slots must be NULL). */
+int mt_gated_scan_grad(const mt_gated_args *args, void *stream);
+
+/* 8-byte slots of mt_gated_scan_grad's scratch and of the checkpoints; -1 for a size out of range. */
+int64_t mt_gated_scan_scratch_slots(int64_t batch, int64_t len, int64_t dim);
+int64_t mt_gated_scan_checkpoint_slots(int64_t batch, int64_t len, int64_t dim);
+
+/*
+ * mt_beam_args -- arguments of mt_beam_select. Every field is eight bytes
+ * wide; strides count elements; optional pointers may be NULL.
+ */
+typedef struct {
+    int64_t dtype;                 /* logits: MT_F32, MT_BF16 or MT_F16 */
+    int64_t batch;
+    int64_t beams;                 /* beams that there are, 1..32 */
+    int64_t beams_out;             /* beams to go on with, 1..32, at most beams * vocab */
+    int64_t vocab;                 /* 1 or more, below 2^31 */
+    int64_t eos;                   /* the token that ends a sequence; negative: none does */
+    const void *logits;            /* [batch, beams, vocab], vocab contiguous */
+    int64_t logits_batch, logits_beam;
+    const float *prior;            /* [batch, beams], optional: the beams' scores (0 without) */
+    const uint8_t *finished;       /* [batch, beams], optional: nonzero for a beam that has ended; needs eos */
+    int32_t *tokens, *parents;     /* [batch, beams_out] */
+    float *scores;                 /* [batch, beams_out]; may be prior where beams == beams_out */
+    uint8_t *finished_out;         /* [batch, beams_out], optional; may be finished where beams == beams_out */
+    int32_t *slots;                /* [batch, max(beams, beams_out)], optional: updated in place */
+    int32_t *src, *dst;            /* [batch, beams_out], required with slots */
+    void *scratch;                 /* mt_beam_select_scratch_slots(...) slots, 16-byte aligned */
+} mt_beam_args;
+
+/*
+ * mt_beam_select -- one step of a beam search: of every sequence's beams x
+ * vocab continuations (k, v), whose scores are
+ *   prior[k] + logits[k, v] - log(sum over v' of exp(logits[k, v']))
+ * the beams_out best ones, best first; equal scores by the lowest k, then the
+ * lowest v. parents[j] = k, tokens[j] = v, scores[j] the score. All arrays but
+ * logits are contiguous. Scores of different beams are compared in 64 bits, those
+ * of one beam by their logits; they are rounded once, at the store.
+ *
+ * Logits: NaN counts as -inf (a token that may not come next), +inf as the
+ * largest finite f32. A beam whose logits are all -inf, or whose prior is -inf or
+ * NaN, has no continuation: all its scores are -inf, and only fill places that
+ * no others take. +inf as a prior counts as the largest finite f32.
+ * A finished beam has one continuation, (k, eos), with the beam's prior as its score; its logits
+ * are not read. finished_out[j] is 1 where the beam was finished or v is eos.
+ *
+ * slots names each beam's row in pools of states (mt_state_copy): the first
+ * `beams` of a sequence's row are its beams', the others are spare, and all are
+ * different. A beam's first child goes on in its slot; the other children, in
+ * order, take the slots that no child goes on in, in order, and src[j], dst[j] say which row
+ * is to be copied where (-1, -1 for a child that stays). Afterwards
+ * slots[j] is beam j's for j < beams_out, the spare ones follow in order.
+ * Errors: MT_ERR_ARG, MT_ERR_DTYPE, MT_ERR_ALIAS, MT_ERR_ALIGN, MT_ERR_MEMORY, MT_ERR_CUDA.
+ */
+int mt_beam_select(const mt_beam_args *args, void *stream);
+
+/* 8-byte scratch slots of mt_beam_select; -1 for a size out of range. */
+int64_t mt_beam_select_scratch_slots(int64_t batch, int64_t beams, int64_t beams_out, int64_t vocab);
+
+/* A pool of state rows: row s of plane l begins at base + l * plane_stride + s * row_stride (bytes). */
+typedef struct {
+    void *base;
+    int64_t nslots, row_bytes, row_stride;  /* row_stride at least row_bytes */
+    int64_t planes, plane_stride;           /* a layer each, say; plane_stride at least row_bytes; 1 plane: any */
+} mt_pool;
+#define MT_MOST_POOLS 16
+
+/*
+ * mt_state_copy -- copies rows of state pools: for every pair i below `pairs`,
+ * every pool (1..MT_MOST_POOLS, a host array) and every plane of it, row dst[i] becomes a copy of
+ * row src[i]. A pair does nothing in a pool where src[i] or dst[i] is outside it.
+ * One src may be copied to several dst (a fork). No dst may be named twice,
+ * nor be the src of another pair; src[i] == dst[i] does nothing.
+ * src, dst: device int32 arrays. Errors: MT_ERR_ARG, MT_ERR_ALIAS (a base that is src or dst), MT_ERR_ALIGN,
+ * MT_ERR_MEMORY, MT_ERR_CUDA.
+ */
+int mt_state_copy(const int32_t *src, const int32_t *dst, int64_t pairs, const mt_pool *pools, int64_t npools, void *stream);
 
 #ifdef __cplusplus
 }

@@ -33,9 +33,16 @@ Operators of sequence models (activations [batch, len, dim], f32/bf16/f16):
   bias and SiLU.
 * ``mt_selective_scan(u, delta, A, B, C, out, ...)``, ``mt_selective_scan_step``
   and ``mt_selective_scan_grad`` -- selective state space scan with gate.
+* ``mt_gated_scan(x, r, out, ...)``, ``mt_gated_scan_step`` and
+  ``mt_gated_scan_grad`` -- gated linear recurrence of every channel by itself.
+* ``mt_beam_select(logits, tokens, parents, scores, scratch, ...)`` -- one step
+  of a beam search over beams and vocabulary, and the slots of its beams' states.
+* ``mt_state_copy(src, dst, pools, axis)`` -- copies rows between slots of state
+  pools: forks, and the states that follow a beam search's beams.
 * their scratch sizes: ``mt_embed_grad_scratch_slots``,
-  ``mt_causal_conv_grad_scratch_slots``, ``mt_selective_scan_scratch_slots`` and
-  ``mt_selective_scan_checkpoint_slots``, in 8-byte slots.
+  ``mt_causal_conv_grad_scratch_slots``, ``mt_selective_scan_scratch_slots``,
+  ``mt_selective_scan_checkpoint_slots``, ``mt_gated_scan_scratch_slots``,
+  ``mt_gated_scan_checkpoint_slots`` and ``mt_beam_select_scratch_slots``, in 8-byte slots.
 """
 from __future__ import annotations
 
@@ -60,6 +67,7 @@ MT_ERR_TOO_LARGE = -7
 MT_ERR_MEMORY = -8
 MT_ERR_BOUNDS = -9
 MT_NOALLOC_SCRATCH_BYTES = 1 << 20
+MT_MOST_POOLS = 16
 
 DTYPE_CODE = {torch.float32: MT_F32, torch.bfloat16: MT_BF16, torch.float16: MT_F16,
               torch.int32: MT_I32, torch.int64: MT_I64, torch.uint32: MT_U32, torch.uint64: MT_U64,
@@ -72,7 +80,9 @@ EXPORTS = ("mt_scan_rows", "mt_scan_rows_op", "mt_exclusive_scan", "mt_inclusive
            "mt_scan_rows_noalloc", "mt_scan_rows_scratch_slots", "mt_scan_build_checked",
            "mt_embed", "mt_embed_grad", "mt_embed_grad_scratch_slots", "mt_causal_conv", "mt_causal_conv_step",
            "mt_causal_conv_grad", "mt_causal_conv_grad_scratch_slots", "mt_selective_scan", "mt_selective_scan_step",
-           "mt_selective_scan_grad", "mt_selective_scan_scratch_slots", "mt_selective_scan_checkpoint_slots")
+           "mt_selective_scan_grad", "mt_selective_scan_scratch_slots", "mt_selective_scan_checkpoint_slots",
+           "mt_gated_scan", "mt_gated_scan_step", "mt_gated_scan_grad", "mt_gated_scan_scratch_slots",
+           "mt_gated_scan_checkpoint_slots", "mt_beam_select", "mt_beam_select_scratch_slots", "mt_state_copy")
 
 
 class ScanError(RuntimeError):
@@ -128,10 +138,16 @@ def _load(path: str):
     L.mt_selective_scan_scratch_slots.argtypes = [i64, i64, i64, i64, i64, i32]
     L.mt_selective_scan_checkpoint_slots.argtypes = [i64, i64, i64, i64]
     for name in ("mt_embed_grad_scratch_slots", "mt_causal_conv_grad_scratch_slots",
-                 "mt_selective_scan_scratch_slots", "mt_selective_scan_checkpoint_slots"):
+                 "mt_selective_scan_scratch_slots", "mt_selective_scan_checkpoint_slots",
+                 "mt_gated_scan_scratch_slots", "mt_gated_scan_checkpoint_slots", "mt_beam_select_scratch_slots"):
         getattr(L, name).restype = i64
+    L.mt_gated_scan_scratch_slots.argtypes = L.mt_gated_scan_checkpoint_slots.argtypes = [i64, i64, i64]
+    L.mt_beam_select_scratch_slots.argtypes = [i64, i64, i64, i64]
+    L.mt_state_copy.argtypes = [p, p, i64, args, i64, p]
+    L.mt_state_copy.restype = i32
     for name in ("mt_causal_conv", "mt_causal_conv_step", "mt_causal_conv_grad", "mt_selective_scan",
-                 "mt_selective_scan_step", "mt_selective_scan_grad"):
+                 "mt_selective_scan_step", "mt_selective_scan_grad", "mt_gated_scan", "mt_gated_scan_step",
+                 "mt_gated_scan_grad", "mt_beam_select"):
         getattr(L, name).argtypes = [args, p]
         getattr(L, name).restype = i32
     return L
@@ -163,9 +179,12 @@ def _contiguous(**tensors) -> None:
             raise ValueError(f"{name} must be contiguous")
 
 
-# The argument blocks mt_conv_args and mt_ssm_args: eight bytes a field.
+# The argument blocks mt_conv_args, mt_ssm_args, mt_gated_args and mt_beam_args, and mt_pool: eight bytes a field.
 _CONV_ARGS = struct.Struct("=30q")
 _SSM_ARGS = struct.Struct("=58q")
+_GATED_ARGS = struct.Struct("=45q")
+_BEAM_ARGS = struct.Struct("=19q")
+_POOL = struct.Struct("=6q")
 _NO_ACT = (0, 0, 0)  # an activation that is absent: pointer, batch and token strides
 
 
@@ -207,8 +226,8 @@ def _pool(name, state, row, dtype, batch, slots):
     """The pointer and the number of rows of a pool of states."""
     if state is None:
         return 0, batch
-    if state.dtype != dtype or state.dim() != 3 or tuple(state.shape[1:]) != row or not state.is_contiguous():
-        raise ValueError(f"{name} must be contiguous [slots, {row[0]}, {row[1]}] of {dtype}")
+    if state.dtype != dtype or state.dim() != 1 + len(row) or tuple(state.shape[1:]) != row or not state.is_contiguous():
+        raise ValueError(f"{name} must be contiguous [slots, {', '.join(map(str, row))}] of {dtype}")
     if slots is None and state.shape[0] < batch:
         raise ValueError(f"{name} needs a row for every sequence")
     return state.data_ptr(), state.shape[0]
@@ -562,6 +581,120 @@ class Library:
             _flat("dD", dD, (dim,), f32), _flat("ddelta_bias", ddelta_bias, (dim,), f32), _flat("dfinal", dfinal, states, f32),
             _flat("dinit", dinit, states, f32)), _stream(stream)), "mt_selective_scan_grad")
 
+    def mt_gated_scan_scratch_slots(self, batch: int, length: int, dim: int) -> int:
+        return self._slots(self.lib.mt_gated_scan_scratch_slots(batch, length, dim), "mt_gated_scan_scratch_slots")
+
+    def mt_gated_scan_checkpoint_slots(self, batch: int, length: int, dim: int) -> int:
+        return self._slots(self.lib.mt_gated_scan_checkpoint_slots(batch, length, dim), "mt_gated_scan_checkpoint_slots")
+
+    def mt_gated_scan(self, x: torch.Tensor, r: torch.Tensor, out: torch.Tensor, i=None, z=None, rate=None, state=None,
+                      carry_in: bool = False, slots=None, lens=None, checkpoints=None, stream=None) -> None:
+        """The gated recurrence over whole prompts: x, the gates r (of the recurrence),
+        i (of the input) and z (of the output), and out [batch, len, dim]; rate [dim]
+        f32 for decays exp(-rate sigmoid(r)), without it they are 1 - sigmoid(r).
+        `state` [slots, dim] f32 is left holding each sequence's last state and, with
+        carry_in, gives its first; `checkpoints` are written for mt_gated_scan_grad."""
+        batch, length, dim = shape = tuple(x.shape)
+        dt, f32 = x.dtype, torch.float32
+        sp, nslots = _pool("state", state, (dim,), f32, batch, slots)
+        ck = 0
+        if checkpoints is not None:
+            ck = _scratch("checkpoints", checkpoints, self.mt_gated_scan_checkpoint_slots(batch, length, dim))
+        _check(self.lib.mt_gated_scan(_GATED_ARGS.pack(
+            DTYPE_CODE.get(dt, -99), batch, length, dim, bool(carry_in), nslots, *_act("x", x, shape, dt), *_act("r", r, shape, dt),
+            *(_NO_ACT if i is None else _act("i", i, shape, dt)), *(_NO_ACT if z is None else _act("z", z, shape, dt)),
+            _flat("rate", rate, (dim,), f32), sp, _flat("slots", slots, (batch,), torch.int32),
+            _flat("lens", lens, (batch,), torch.int32), *_act("out", out, shape, dt), ck, 0, *_NO_ACT * 5, 0, 0, 0),
+            _stream(stream)), "mt_gated_scan")
+
+    def mt_gated_scan_step(self, x: torch.Tensor, r: torch.Tensor, state: torch.Tensor, out: torch.Tensor, i=None, z=None,
+                           rate=None, slots=None, stream=None) -> None:
+        """One token of each sequence: x, r, i, z and out [batch, dim]; state is updated in place."""
+        batch, dim = shape = tuple(x.shape)
+        dt, f32 = x.dtype, torch.float32
+        sp, nslots = _pool("state", state, (dim,), f32, batch, slots)
+        _check(self.lib.mt_gated_scan_step(_GATED_ARGS.pack(
+            DTYPE_CODE.get(dt, -99), batch, 1, dim, 0, nslots, *_act_step("x", x, shape, dt), *_act_step("r", r, shape, dt),
+            *(_NO_ACT if i is None else _act_step("i", i, shape, dt)), *(_NO_ACT if z is None else _act_step("z", z, shape, dt)),
+            _flat("rate", rate, (dim,), f32), sp, _flat("slots", slots, (batch,), torch.int32), 0,
+            *_act_step("out", out, shape, dt), 0, 0, *_NO_ACT * 5, 0, 0, 0), _stream(stream)), "mt_gated_scan_step")
+
+    def mt_gated_scan_grad(self, x: torch.Tensor, r: torch.Tensor, dout: torch.Tensor, checkpoints: torch.Tensor,
+                           dx: torch.Tensor, dr: torch.Tensor, scratch=None, i=None, di=None, z=None, dz=None, rate=None,
+                           drate=None, dfinal=None, dinit=None, lens=None, stream=None) -> None:
+        """Every gradient of mt_gated_scan from dout and dfinal (the gradient of the last
+        states), with the checkpoints that the forward call wrote; scratch is needed with drate."""
+        batch, length, dim = shape = tuple(x.shape)
+        dt, f32 = x.dtype, torch.float32
+        if (i is None) != (di is None) or (z is None) != (dz is None):
+            raise ValueError("di goes with i, and dz with z")
+        if drate is not None and rate is None:
+            raise ValueError("drate needs rate")
+        need = self.mt_gated_scan_scratch_slots(batch, length, dim) if drate is not None else 0
+        ck = _scratch("checkpoints", checkpoints, self.mt_gated_scan_checkpoint_slots(batch, length, dim))
+        _check(self.lib.mt_gated_scan_grad(_GATED_ARGS.pack(
+            DTYPE_CODE.get(dt, -99), batch, length, dim, 0, batch, *_act("x", x, shape, dt), *_act("r", r, shape, dt),
+            *(_NO_ACT if i is None else _act("i", i, shape, dt)), *(_NO_ACT if z is None else _act("z", z, shape, dt)),
+            _flat("rate", rate, (dim,), f32), 0, 0, _flat("lens", lens, (batch,), torch.int32), *_NO_ACT, ck,
+            _scratch("scratch", scratch, need), *_act("dout", dout, shape, dt), *_act("dx", dx, shape, dt),
+            *_act("dr", dr, shape, dt), *(_NO_ACT if di is None else _act("di", di, shape, dt)),
+            *(_NO_ACT if dz is None else _act("dz", dz, shape, dt)), _flat("drate", drate, (dim,), f32),
+            _flat("dfinal", dfinal, (batch, dim), f32), _flat("dinit", dinit, (batch, dim), f32)), _stream(stream)),
+            "mt_gated_scan_grad")
+
+    def mt_beam_select_scratch_slots(self, batch: int, beams: int, beams_out: int, vocab: int) -> int:
+        return self._slots(self.lib.mt_beam_select_scratch_slots(batch, beams, beams_out, vocab), "mt_beam_select_scratch_slots")
+
+    def mt_beam_select(self, logits: torch.Tensor, tokens: torch.Tensor, parents: torch.Tensor, scores: torch.Tensor,
+                       scratch: torch.Tensor, prior=None, finished=None, finished_out=None, eos: int = -1, slots=None, src=None,
+                       dst=None, stream=None) -> None:
+        """The best continuations of every sequence's beams, logits [batch, beams, vocab]:
+        tokens, parents (int32) and scores (f32) [batch, beams_out], best first, from prior
+        [batch, beams] plus each beam's log-softmax; equal scores by the lowest beam, then
+        token. A beam marked in finished (uint8) goes on with eos alone at its score.
+        slots (int32, [batch, max(beams, beams_out)]) names the beams' rows of state pools and is
+        updated in place; src and dst say which rows to copy then (mt_state_copy), -1 for none."""
+        batch, beams, vocab = shape = tuple(logits.shape)
+        if tokens.dim() != 2 or tokens.shape[0] != batch:
+            raise ValueError(f"tokens must be [{batch}, beams_out]")
+        k = tokens.shape[1]
+        if slots is not None and (src is None or dst is None):
+            raise ValueError("src and dst are needed with slots")
+        i32, u8, f32, out = torch.int32, torch.uint8, torch.float32, (batch, k)
+        need = self.mt_beam_select_scratch_slots(batch, beams, k, vocab)
+        _check(self.lib.mt_beam_select(_BEAM_ARGS.pack(
+            DTYPE_CODE.get(logits.dtype, -99), batch, beams, k, vocab, eos, *_act("logits", logits, shape, logits.dtype),
+            _flat("prior", prior, (batch, beams), f32), _flat("finished", finished, (batch, beams), u8),
+            _flat("tokens", tokens, out, i32), _flat("parents", parents, out, i32), _flat("scores", scores, out, f32),
+            _flat("finished_out", finished_out, out, u8), _flat("slots", slots, (batch, max(beams, k)), i32),
+            _flat("src", src, out, i32), _flat("dst", dst, out, i32), _scratch("scratch", scratch, need)), _stream(stream)),
+            "mt_beam_select")
+
+    def mt_state_copy(self, src: torch.Tensor, dst: torch.Tensor, pools, axis: int = 0, stream=None) -> None:
+        """Row dst[i] of every pool becomes a copy of its row src[i] (int32 of any one shape; a pair with
+        either outside the pool does nothing). `axis` is the pools' axis of slots: 0 for [slots, ...],
+        1 for [layers, slots, ...]; what follows it must be contiguous. No dst may be named
+        twice, nor be another pair's src."""
+        if src.dtype != torch.int32 or dst.dtype != torch.int32 or src.shape != dst.shape:
+            raise ValueError("src and dst must be int32 and of one shape")
+        _contiguous(src=src, dst=dst)
+        if axis not in (0, 1):
+            raise ValueError("axis must be 0 or 1")
+        if isinstance(pools, torch.Tensor):
+            pools = (pools,)
+        blocks = []
+        for t in pools:
+            if t.dim() <= axis:
+                raise ValueError("a pool has fewer axes than that of its slots")
+            row = math.prod(t.shape[axis + 1:])
+            if t.numel() > 0 and not t[(0,) * (axis + 1)].is_contiguous():
+                raise ValueError("a pool's rows must be contiguous")
+            e, s = t.element_size(), t.stride()
+            blocks.append(_POOL.pack(t.data_ptr(), t.shape[axis], row * e, (s[axis] if t.shape[axis] > 1 else row) * e,
+                                     t.shape[0] if axis else 1, (s[0] if axis and t.shape[0] > 1 else row) * e))
+        _check(self.lib.mt_state_copy(src.data_ptr(), dst.data_ptr(), src.numel(), b"".join(blocks), len(blocks),
+                                      _stream(stream)), "mt_state_copy")
+
 
 _default = Library(LIB_PATH)
 lib = _default.lib
@@ -594,6 +727,14 @@ mt_selective_scan_step = _default.mt_selective_scan_step
 mt_selective_scan_grad = _default.mt_selective_scan_grad
 mt_selective_scan_scratch_slots = _default.mt_selective_scan_scratch_slots
 mt_selective_scan_checkpoint_slots = _default.mt_selective_scan_checkpoint_slots
+mt_gated_scan = _default.mt_gated_scan
+mt_gated_scan_step = _default.mt_gated_scan_step
+mt_gated_scan_grad = _default.mt_gated_scan_grad
+mt_gated_scan_scratch_slots = _default.mt_gated_scan_scratch_slots
+mt_gated_scan_checkpoint_slots = _default.mt_gated_scan_checkpoint_slots
+mt_beam_select = _default.mt_beam_select
+mt_beam_select_scratch_slots = _default.mt_beam_select_scratch_slots
+mt_state_copy = _default.mt_state_copy
 
 
 def load_checked() -> Library:

@@ -1,0 +1,111 @@
+// mt_copy.cu -- copies between slots of state pools.
+//
+// Rows of a pool of layers lie far apart, so a CTA takes one pair's chunk of one row and plane, 16 KB
+// of it, and copies it with the widest accesses that the pool's addresses and sizes allow. Only bytes
+// count: each is read once and written once.
+#include "mt_seq.cuh"
+#include "mt_seq.h"
+
+namespace mt {
+
+namespace {
+
+constexpr int kCopyThreads = 256;
+constexpr int kCopyInFlight = 4;                                       // loads of a thread before its stores
+constexpr int64_t kCopyChunk = 16 * kCopyThreads * kCopyInFlight;      // bytes of a CTA
+
+struct CopyPool {
+    char *base;
+    int64_t nslots, row_bytes, row_stride, plane_stride;
+    int64_t first;   // of the grid's first axis: the pools before it
+    int64_t chunks;  // of a row
+    int bytes;       // of an access: 16, 8, 4, 2 or 1
+};
+struct CopyArgs {
+    const int32_t *src, *dst;
+    int64_t pairs;
+    int npools;
+    CopyPool pool[MT_MOST_POOLS];
+};
+
+template <class T> __device__ __forceinline__ void copy_span(const char *from, char *to, int64_t bytes) {
+    const T *f = reinterpret_cast<const T *>(from);
+    T *t = reinterpret_cast<T *>(to);
+    const int n = (int)(bytes / (int64_t)sizeof(T));
+    for (int k0 = threadIdx.x; k0 < n; k0 += kCopyThreads * kCopyInFlight) {
+        T v[kCopyInFlight];
+#pragma unroll
+        for (int k = 0; k < kCopyInFlight; ++k)
+            if (k0 + k * kCopyThreads < n)
+                v[k] = f[k0 + k * kCopyThreads];
+#pragma unroll
+        for (int k = 0; k < kCopyInFlight; ++k)
+            if (k0 + k * kCopyThreads < n)
+                t[k0 + k * kCopyThreads] = v[k];
+    }
+}
+
+__global__ void __launch_bounds__(kCopyThreads) k_state_copy(const __grid_constant__ CopyArgs a) {
+    pdl_prologue();
+    int which = 0;
+    while (which + 1 < a.npools && (int64_t)blockIdx.x >= a.pool[which + 1].first)
+        ++which;
+    const CopyPool &p = a.pool[which];
+    const int64_t at = (int64_t)blockIdx.x - p.first, plane = at / p.chunks, chunk = at - plane * p.chunks;
+    const int64_t begin = chunk * kCopyChunk;
+    const int64_t bytes = p.row_bytes - begin < kCopyChunk ? p.row_bytes - begin : kCopyChunk;
+    char *rows = p.base + plane * p.plane_stride + begin;
+    for (int64_t i = blockIdx.y; i < a.pairs; i += gridDim.y) {
+        const int64_t s = a.src[i], d = a.dst[i];
+        if (s < 0 || s >= p.nslots || d < 0 || d >= p.nslots || s == d)
+            continue;
+        const char *from = rows + s * p.row_stride;
+        char *to = rows + d * p.row_stride;
+        switch (p.bytes) {
+        case 16: copy_span<uint4>(from, to, bytes); break;
+        case 8: copy_span<uint2>(from, to, bytes); break;
+        case 4: copy_span<uint32_t>(from, to, bytes); break;
+        case 2: copy_span<uint16_t>(from, to, bytes); break;
+        default: copy_span<uint8_t>(from, to, bytes);
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t copy_launch(const int32_t *src, const int32_t *dst, int64_t pairs, const mt_pool *pools, int64_t npools,
+                        const Launch &L) {
+    CopyArgs a;
+    a.src = src;
+    a.dst = dst;
+    a.pairs = pairs;
+    a.npools = 0;
+    int64_t blocks = 0;
+    for (int64_t k = 0; k < npools; ++k) {
+        const mt_pool &p = pools[k];
+        if (p.nslots == 0 || p.planes == 0 || p.row_bytes == 0)
+            continue;
+        CopyPool &q = a.pool[a.npools++];
+        q.base = static_cast<char *>(p.base);
+        q.nslots = p.nslots;
+        q.row_bytes = p.row_bytes;
+        q.row_stride = p.row_stride;
+        q.plane_stride = p.planes > 1 ? p.plane_stride : 0;
+        q.first = blocks;
+        q.chunks = (p.row_bytes + kCopyChunk - 1) / kCopyChunk;
+        q.bytes = 16;
+        const uint64_t all = (uint64_t)(uintptr_t)p.base | (uint64_t)q.row_bytes | (uint64_t)q.row_stride | (uint64_t)q.plane_stride;
+        while (all % q.bytes != 0)
+            q.bytes /= 2;
+        blocks += q.chunks * p.planes;
+        if (blocks > INT32_MAX)
+            return cudaErrorInvalidValue;
+    }
+    if (blocks == 0)
+        return cudaSuccess;
+    note_launch();
+    const dim3 grid((unsigned)blocks, (unsigned)(pairs < 65535 ? pairs : 65535));
+    return launch_pdl_2d(k_state_copy, grid, kCopyThreads, L.stream, a);
+}
+
+}  // namespace mt

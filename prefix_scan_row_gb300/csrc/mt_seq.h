@@ -42,4 +42,18 @@ cudaError_t ssm_launch(const mt_ssm_args &a, const Launch &L);
 cudaError_t ssm_grad_launch(const mt_ssm_args &a, const Launch &L);
 cudaError_t ssm_step_launch(const mt_ssm_args &a, const Launch &L);
 
+// ---- gated scan (mt_gated*.cu) ---------------------------------------------------
+constexpr int kGatedTile = 64;  // tokens per checkpoint
+int64_t gated_scratch_slots(int64_t batch, int64_t len, int64_t dim);
+cudaError_t gated_launch(const mt_gated_args &a, const Launch &L);
+cudaError_t gated_step_launch(const mt_gated_args &a, const Launch &L);
+cudaError_t gated_grad_launch(const mt_gated_args &a, const Launch &L);
+
+// ---- beam search's selection (mt_beam.cu) and copies between slots (mt_copy.cu) ----
+constexpr int kBeamsMost = 32;
+int64_t beam_scratch_slots(int64_t batch, int64_t beams, int64_t beams_out, int64_t vocab);
+cudaError_t beam_launch(const mt_beam_args &a, const Launch &L);
+cudaError_t copy_launch(const int32_t *src, const int32_t *dst, int64_t pairs, const mt_pool *pools, int64_t npools,
+                        const Launch &L);
+
 }  // namespace mt

@@ -1,6 +1,6 @@
 // mt_seq_abi.cu -- the exported C ABI of the sequence-model calls
 // (include/mt_scan.h): argument checks, then the launches of mt_embed.cu,
-// mt_conv.cu and mt_ssm.cu.
+// mt_conv.cu, mt_ssm.cu, mt_gated.cu, mt_beam.cu and mt_copy.cu.
 #include <initializer_list>
 
 #include "mt_seq.h"
@@ -101,6 +101,29 @@ int ssm_check(const mt_ssm_args &a, bool tokens) {
     if (!aligned({a.u, a.delta, a.z, a.B, a.C, a.out, a.dout, a.du, a.ddelta, a.dz, a.dB, a.dC}, s) ||
         !aligned({a.A, a.D, a.delta_bias, a.state, a.slots, a.lens, a.checkpoints, a.dA, a.dD, a.ddelta_bias, a.dfinal, a.dinit}, 4) ||
         !aligned({a.scratch}, 16))
+        return MT_ERR_ALIGN;
+    return MT_OK;
+}
+
+int gated_check(const mt_gated_args &a, bool tokens) {
+    const int64_t len = tokens ? a.len : 1;
+    if (a.batch < 0 || len < 0 || a.dim < 0 || a.nslots < 0)
+        return MT_ERR_ARG;
+    const int s = act_size(a.dtype);
+    if (s == 0)
+        return MT_ERR_DTYPE;
+    if (product({a.batch, len, a.dim, 8}) < 0 || product({a.nslots, a.dim, 8}) < 0)
+        return MT_ERR_ARG;
+    if (a.batch == 0 || a.dim == 0)
+        return MT_OK;
+    if (len > 0 && any_null({a.x, a.r}))
+        return MT_ERR_ARG;
+    if (a.slots == nullptr && a.state != nullptr && a.nslots < a.batch)
+        return MT_ERR_ARG;
+    if ((a.slots != nullptr || a.carry_in) && a.state == nullptr)
+        return MT_ERR_ARG;
+    if (!aligned({a.x, a.r, a.i, a.z, a.out, a.dout, a.dx, a.dr, a.di, a.dz}, s) ||
+        !aligned({a.rate, a.state, a.slots, a.lens, a.checkpoints, a.drate, a.dfinal, a.dinit}, 4) || !aligned({a.scratch}, 16))
         return MT_ERR_ALIGN;
     return MT_OK;
 }
@@ -331,4 +354,171 @@ extern "C" int mt_selective_scan_grad(const mt_ssm_args *args, void *stream) {
         !in_device({a.du, a.ddelta, a.dz, a.dB, a.dC, a.dA, a.dD, a.ddelta_bias, a.dfinal, a.dinit}, dev))
         return MT_ERR_MEMORY;
     return done(ssm_grad_launch(a, L));
+}
+
+extern "C" int64_t mt_gated_scan_scratch_slots(int64_t batch, int64_t len, int64_t dim) {
+    if (batch < 0 || len < 0 || dim < 0 || product({batch, len, dim, 16}) < 0 || product({batch, dim, 256}) < 0)
+        return -1;
+    return gated_scratch_slots(batch, len, dim);
+}
+
+extern "C" int64_t mt_gated_scan_checkpoint_slots(int64_t batch, int64_t len, int64_t dim) {
+    if (batch < 0 || len < 0 || dim < 0 || product({batch, len, dim, 16}) < 0)
+        return -1;
+    return (batch * ((len + kGatedTile - 1) / kGatedTile) * dim + 1) / 2;
+}
+
+extern "C" int mt_gated_scan(const mt_gated_args *args, void *stream) {
+    if (args == nullptr)
+        return MT_ERR_ARG;
+    const mt_gated_args &a = *args;
+    const int bad = gated_check(a, true);
+    if (bad != MT_OK || a.batch == 0 || a.dim == 0)
+        return bad;
+    if ((a.len > 0 && a.out == nullptr) || (a.checkpoints != nullptr && a.slots != nullptr))
+        return MT_ERR_ARG;
+    for (const void *p : {(const void *)a.out, (const void *)a.state, (const void *)a.checkpoints})
+        if (among(p, {a.x, a.r, a.i, a.z, a.rate, a.slots, a.lens}))
+            return MT_ERR_ALIAS;
+    if (among(a.out, {a.state, a.checkpoints}) || among(a.state, {a.checkpoints}))
+        return MT_ERR_ALIAS;
+    Launch L;
+    int dev = 0;
+    if (!make_launch(stream, &L, &dev))
+        return MT_ERR_CUDA;
+    if (!in_device({a.x, a.r, a.i, a.z, a.rate, a.state, a.slots, a.lens, a.out, a.checkpoints}, dev))
+        return MT_ERR_MEMORY;
+    return done(gated_launch(a, L));
+}
+
+extern "C" int mt_gated_scan_step(const mt_gated_args *args, void *stream) {
+    if (args == nullptr)
+        return MT_ERR_ARG;
+    const mt_gated_args &a = *args;
+    const int bad = gated_check(a, false);
+    if (bad != MT_OK || a.batch == 0 || a.dim == 0)
+        return bad;
+    if (any_null({a.out, a.state}))
+        return MT_ERR_ARG;
+    if (among(a.out, {a.x, a.r, a.i, a.z, a.rate, a.state, a.slots}) || among(a.state, {a.x, a.r, a.i, a.z, a.rate, a.slots}))
+        return MT_ERR_ALIAS;
+    Launch L;
+    int dev = 0;
+    if (!make_launch(stream, &L, &dev))
+        return MT_ERR_CUDA;
+    if (!in_device({a.x, a.r, a.i, a.z, a.rate, a.state, a.slots, a.out}, dev))
+        return MT_ERR_MEMORY;
+    return done(gated_step_launch(a, L));
+}
+
+extern "C" int mt_gated_scan_grad(const mt_gated_args *args, void *stream) {
+    if (args == nullptr)
+        return MT_ERR_ARG;
+    mt_gated_args a = *args;
+    a.state = nullptr;
+    a.carry_in = 0;
+    const int bad = gated_check(a, true);
+    if (bad != MT_OK || a.dim == 0)
+        return bad;
+    if ((a.drate != nullptr && (a.rate == nullptr || (a.batch > 0 && a.scratch == nullptr))) ||
+        mt_gated_scan_scratch_slots(a.batch, a.len, a.dim) < 0)
+        return MT_ERR_ARG;
+    if (a.batch > 0 && a.len > 0 && (any_null({a.dout, a.checkpoints, a.dx, a.dr}) || (a.i != nullptr && a.di == nullptr) ||
+                                     (a.z != nullptr && a.dz == nullptr)))
+        return MT_ERR_ARG;
+    const void *outs[] = {a.dx, a.dr, a.i != nullptr ? a.di : nullptr, a.z != nullptr ? a.dz : nullptr, a.drate, a.dinit,
+                          a.drate != nullptr ? a.scratch : nullptr};
+    for (size_t k = 0; k < sizeof(outs) / sizeof(*outs); ++k) {
+        if (among(outs[k], {a.x, a.r, a.i, a.z, a.rate, a.lens, a.dout, a.checkpoints, a.dfinal}))
+            return MT_ERR_ALIAS;
+        for (size_t j = 0; j < k; ++j)
+            if (among(outs[k], {outs[j]}))
+                return MT_ERR_ALIAS;
+    }
+    Launch L;
+    int dev = 0;
+    if (!make_launch(stream, &L, &dev))
+        return MT_ERR_CUDA;
+    if (!in_device({a.x, a.r, a.i, a.z, a.rate, a.lens, a.checkpoints, a.dout, a.dfinal}, dev) ||
+        !in_device({outs[0], outs[1], outs[2], outs[3], outs[4], outs[5], outs[6]}, dev))
+        return MT_ERR_MEMORY;
+    return done(gated_grad_launch(a, L));
+}
+
+extern "C" int64_t mt_beam_select_scratch_slots(int64_t batch, int64_t beams, int64_t beams_out, int64_t vocab) {
+    if (batch < 0 || beams < 1 || beams > kBeamsMost || beams_out < 1 || beams_out > kBeamsMost || vocab < 1 ||
+        vocab > INT32_MAX || product({batch, beams, vocab, 8}) < 0)
+        return -1;
+    return beam_scratch_slots(batch, beams, beams_out, vocab);
+}
+
+extern "C" int mt_beam_select(const mt_beam_args *args, void *stream) {
+    if (args == nullptr)
+        return MT_ERR_ARG;
+    const mt_beam_args &a = *args;
+    if (mt_beam_select_scratch_slots(a.batch, a.beams, a.beams_out, a.vocab) < 0 || a.beams_out > a.beams * a.vocab ||
+        a.eos >= a.vocab || (a.finished != nullptr && a.eos < 0))
+        return MT_ERR_ARG;
+    const int s = act_size(a.dtype);
+    if (s == 0)
+        return MT_ERR_DTYPE;
+    if (a.batch == 0)
+        return MT_OK;
+    if (any_null({a.logits, a.tokens, a.parents, a.scores, a.scratch}) || (a.slots != nullptr && any_null({a.src, a.dst})))
+        return MT_ERR_ARG;
+    const bool same = a.beams == a.beams_out;  // then a score may replace its prior, and a mark its beam's
+    const void *outs[] = {a.tokens, a.parents, a.scores, a.finished_out, a.slots, a.slots != nullptr ? a.src : nullptr,
+                          a.slots != nullptr ? a.dst : nullptr, a.scratch};
+    for (size_t k = 0; k < sizeof(outs) / sizeof(*outs); ++k) {
+        if (among(outs[k], {a.logits, same && outs[k] == a.scores ? nullptr : a.prior,
+                            same && outs[k] == a.finished_out ? nullptr : a.finished}))
+            return MT_ERR_ALIAS;
+        for (size_t j = 0; j < k; ++j)
+            if (among(outs[k], {outs[j]}))
+                return MT_ERR_ALIAS;
+    }
+    if (!aligned({a.logits}, s) || !aligned({a.prior, a.tokens, a.parents, a.scores, a.slots, a.src, a.dst}, 4) ||
+        !aligned({a.scratch}, 16))
+        return MT_ERR_ALIGN;
+    Launch L;
+    int dev = 0;
+    if (!make_launch(stream, &L, &dev))
+        return MT_ERR_CUDA;
+    if (!in_device({a.logits, a.prior, a.finished, outs[0], outs[1], outs[2], outs[3], outs[4], outs[5], outs[6], outs[7]}, dev))
+        return MT_ERR_MEMORY;
+    return done(beam_launch(a, L));
+}
+
+extern "C" int mt_state_copy(const int32_t *src, const int32_t *dst, int64_t pairs, const mt_pool *pools, int64_t npools,
+                             void *stream) {
+    if (pairs < 0 || pairs > INT32_MAX || npools < 1 || npools > MT_MOST_POOLS || pools == nullptr)
+        return MT_ERR_ARG;
+    for (int64_t k = 0; k < npools; ++k) {
+        const mt_pool &p = pools[k];
+        if (p.nslots < 0 || p.nslots > INT32_MAX || p.planes < 0 || p.row_bytes < 0 || p.row_stride < p.row_bytes ||
+            (p.planes > 1 && p.plane_stride < p.row_bytes) || product({p.nslots, p.row_stride, 8}) < 0 ||
+            (p.planes > 1 && product({p.planes, p.plane_stride, 8}) < 0))
+            return MT_ERR_ARG;
+        const bool empty = p.nslots == 0 || p.planes == 0 || p.row_bytes == 0;
+        if (!empty && p.base == nullptr)
+            return MT_ERR_ARG;
+        if (pairs > 0 && !empty && among(p.base, {src, dst}))
+            return MT_ERR_ALIAS;
+    }
+    if (pairs == 0)
+        return MT_OK;
+    if (any_null({src, dst}))
+        return MT_ERR_ARG;
+    if (!aligned({src, dst}, 4))
+        return MT_ERR_ALIGN;
+    Launch L;
+    int dev = 0;
+    if (!make_launch(stream, &L, &dev))
+        return MT_ERR_CUDA;
+    if (!in_device({src, dst}, dev))
+        return MT_ERR_MEMORY;
+    for (int64_t k = 0; k < npools; ++k)
+        if (pools[k].nslots > 0 && pools[k].planes > 0 && pools[k].row_bytes > 0 && !in_device({pools[k].base}, dev))
+            return MT_ERR_MEMORY;
+    return done(copy_launch(src, dst, pairs, pools, npools, L));
 }
