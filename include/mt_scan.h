@@ -575,7 +575,7 @@ int64_t mt_selective_scan_checkpoint_slots(int64_t batch, int64_t len, int64_t d
  */
 typedef struct {
     int64_t dtype;                 /* all activations and their gradients: MT_F32, MT_BF16 or MT_F16 */
-    int64_t batch, len, dim;       /* mt_gated_scan_step: len is ignored (one token) */
+    int64_t batch, len, dim;       /* mt_gated_scan_step: len is ignored (one token); len at most 2^31 - 2^16 - 1 */
     int64_t carry_in;              /* nonzero: the state before token 0 is the pool's; zero: it is 0 */
     int64_t nslots;                /* rows of the state pool (batch without slots) */
     const void *x;                 /* [batch, len, dim] */

@@ -1,40 +1,111 @@
-// mt_gated.cu -- launches of the gated scan.
+// mt_gated.cu -- plans and launches of the gated scan, and the join of its parameter's sums.
 #include "mt_gated.cuh"
 
 namespace mt {
 
-int64_t gated_scratch_slots(int64_t batch, int64_t, int64_t dim) { return (batch * dim + 1) / 2; }
-
-template <class S> static cudaError_t forward(const mt_gated_args &p, int64_t tokens, const Launch &L) {
-    const unsigned grid = (unsigned)((p.dim + 127) / 128 * p.batch);
-    note_launch();
-    return p.rate ? launch_pdl(k_gated_plain<S, true>, grid, 128, 0, L.stream, p, tokens)
-                  : launch_pdl(k_gated_plain<S, false>, grid, 128, 0, L.stream, p, tokens);
+// CTAs that share a sequence's tokens: one where sequences and channels give every SM work, and otherwise as many as find
+// place at once, two an SM. A cluster's CTAs wait for one another at every tile, so it pays only then: 4 x 2048 tokens x 4096
+// channels (256 CTAs without clusters), bf16, all gates: 73 us, in clusters of 8 103; 16384 tokens x 2048 (32): 328 and 102.
+// The scratch is sized on the host, so the plan counts GB300's 152 SMs.
+static int gated_ctas(int64_t batch, int64_t len, int64_t dim, int64_t cta_tokens) {
+    const int64_t units = batch * ((dim + kGatedSlab - 1) / kGatedSlab);
+    int n = 1;
+    while (n < 8 && units * n * 2 <= 2 * 152 && n * cta_tokens < len)
+        n *= 2;
+    return n;
 }
-template <class S> static cudaError_t gradient(const mt_gated_args &p, const Launch &L) {
-    const unsigned cols = (unsigned)((p.dim + 127) / 128);
+
+int64_t gated_scratch_slots(int64_t batch, int64_t len, int64_t dim) {
+    return (batch * gated_ctas(batch, len, dim, kGatedWarps * kBwdT) * dim + 1) / 2;
+}
+
+// Sums of parts [rows, dim] over the rows, in order: a warp's lanes share 32 channels, its CTA's warps the rows.
+static __global__ void __launch_bounds__(256) k_gated_rate_join(const float *part, float *drate, int64_t rows, int64_t dim) {
+    __shared__ float sums[8][32];
+    pdl_prologue();
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int64_t d = (int64_t)blockIdx.x * 32 + lane;
+    float s = 0.0f;
+    if (d < dim)
+        for (int64_t k = warp; k < rows; k += 8)
+            s += part[k * dim + d];
+    sums[warp][lane] = s;
+    __syncthreads();
+    if (warp != 0 || d >= dim)
+        return;
+#pragma unroll
+    for (int w = 1; w < 8; ++w)
+        s += sums[w][lane];
+    drate[d] = s;
+}
+
+// b is a token's stride, which the kernels for whole vectors take in 32 bits (in bytes)
+static bool fits(const void *p, int64_t a, int64_t b, int64_t bytes, int64_t values) {
+    return (uintptr_t)p % bytes == 0 && a % values == 0 && b % values == 0 && b > -(1 << 29) && b < 1 << 29;
+}
+// whether `bytes` of every tensor's channels can be moved as one
+static bool all_fit(const mt_gated_args &p, int64_t bytes, bool step, bool grad) {
+    const int64_t v = bytes / (p.dtype == MT_F32 ? 4 : 2), t = step ? 0 : 1;
+    bool fit = p.dim % v == 0 && fits(p.x, p.x_batch, p.x_token * t, bytes, v) && fits(p.r, p.r_batch, p.r_token * t, bytes, v) &&
+               (p.i == nullptr || fits(p.i, p.i_batch, p.i_token * t, bytes, v)) &&
+               (p.z == nullptr || fits(p.z, p.z_batch, p.z_token * t, bytes, v));
+    if (!grad)
+        return fit && fits(p.out, p.out_batch, p.out_token * t, bytes, v);
+    return fit && fits(p.dout, p.dout_batch, p.dout_token, bytes, v) && fits(p.dx, p.dx_batch, p.dx_token, bytes, v) &&
+           fits(p.dr, p.dr_batch, p.dr_token, bytes, v) && (p.i == nullptr || fits(p.di, p.di_batch, p.di_token, bytes, v)) &&
+           (p.z == nullptr || fits(p.dz, p.dz_batch, p.dz_token, bytes, v));
+}
+
+static GatedArgs gated_args(const mt_gated_args &p, int64_t cta_tokens) {
+    GatedArgs g;
+    g.p = p;
+    g.slabs = (int)((p.dim + kGatedSlab - 1) / kGatedSlab);
+    g.ctas = gated_ctas(p.batch, p.len, p.dim, cta_tokens);
+    g.ntiles = (p.len + kGatedTile - 1) / kGatedTile;
+    return g;
+}
+
+#define MT_BY_TYPE(f, ...)                              \
+    switch (p.dtype) {                                  \
+    case MT_F32: return f##_f32(__VA_ARGS__);           \
+    case MT_BF16: return f##_bf16(__VA_ARGS__);         \
+    case MT_F16: return f##_f16(__VA_ARGS__);           \
+    default: return cudaErrorInvalidValue;              \
+    }
+cudaError_t gated_launch(const mt_gated_args &p, const Launch &L) {
+    const GatedArgs g = gated_args(p, kGatedWarps * kFwdT);
+    const bool vec = all_fit(p, 16, false, false);
+    if (p.batch * g.slabs * g.ctas > INT32_MAX)
+        return cudaErrorInvalidValue;
+    MT_BY_TYPE(gated_forward, g, vec, L)
+}
+cudaError_t gated_step_launch(const mt_gated_args &p, const Launch &L) {
+    const GatedArgs g = gated_args(p, kGatedWarps * kFwdT);
+    const bool vec = all_fit(p, p.dtype == MT_F32 ? 8 : 4, true, false);
+    if (p.batch * ((p.dim + 1) / 2) / 128 >= INT32_MAX)
+        return cudaErrorInvalidValue;
+    MT_BY_TYPE(gated_single, g, vec, L)
+}
+static cudaError_t backward(const GatedArgs &g, float *part, const Launch &L) {
+    const mt_gated_args &p = g.p;
+    const bool vec = all_fit(p, 16, false, true);
+    MT_BY_TYPE(gated_backward, g, part, vec, L)
+}
+cudaError_t gated_grad_launch(const mt_gated_args &p, const Launch &L) {
+    const GatedArgs g = gated_args(p, kGatedWarps * kBwdT);
+    float *part = p.drate != nullptr ? static_cast<float *>(p.scratch) : nullptr;
+    if (p.batch * g.slabs * g.ctas > INT32_MAX)
+        return cudaErrorInvalidValue;
     if (p.batch > 0) {
-        note_launch();
-        const cudaError_t e = p.rate ? launch_pdl(k_gated_grad_plain<S, true>, (unsigned)(cols * p.batch), 128, 0, L.stream, p)
-                                     : launch_pdl(k_gated_grad_plain<S, false>, (unsigned)(cols * p.batch), 128, 0, L.stream, p);
-        if (e != cudaSuccess || p.drate == nullptr)
+        const cudaError_t e = backward(g, part, L);
+        if (e != cudaSuccess)
             return e;
     }
     if (p.drate == nullptr)
         return cudaSuccess;
     note_launch();
-    return launch_pdl(k_gated_rate_join, cols, 128, 0, L.stream, (const float *)p.scratch, p.drate, p.batch, p.dim);
+    return launch_pdl(k_gated_rate_join, (unsigned)((p.dim + 31) / 32), 256, 0, L.stream, part, p.drate, p.batch * g.ctas, p.dim);
 }
-#define MT_BY_TYPE(f, ...)                                   \
-    switch (p.dtype) {                                       \
-    case MT_F32: return f<float>(__VA_ARGS__);               \
-    case MT_BF16: return f<__nv_bfloat16>(__VA_ARGS__);      \
-    case MT_F16: return f<__half>(__VA_ARGS__);              \
-    default: return cudaErrorInvalidValue;                   \
-    }
-cudaError_t gated_launch(const mt_gated_args &p, const Launch &L) { MT_BY_TYPE(forward, p, 0, L) }
-cudaError_t gated_step_launch(const mt_gated_args &p, const Launch &L) { MT_BY_TYPE(forward, p, -1, L) }
-cudaError_t gated_grad_launch(const mt_gated_args &p, const Launch &L) { MT_BY_TYPE(gradient, p, L) }
 #undef MT_BY_TYPE
 
 }  // namespace mt

@@ -1,19 +1,42 @@
-// mt_gated.cuh -- the gated scan's mathematics, and its kernels per activation type (mt_gated_*.cu).
+// mt_gated.cuh -- the gated scan's mathematics, and its kernels, instantiated per activation type (mt_gated_*.cu).
 //
 //   s = sigma(r);  a = exp(-rate s), w = sqrt(1 - a^2)  or, without rate,  a = 1 - s, w = s
 //   h_t = a_t h_{t-1} + w_t v_t,  v = sigma(i) x or x,  out = h or h z sigma(z)
 //
 // Gradient, with g_t the gradient by h_t (from out_t, and from h_{t+1} through a_{t+1}):
 //   dh = dout z sigma(z),  g_t = dh_t + a_{t+1} g_{t+1},  dz = dout h sigma(z) (1 + z (1 - sigma(z)))
-//   dx = g w sigma(i),  di = g w v (1 - sigma(i))
+//   dx = g w sigma(i),  di = dx x (1 - sigma(i))
 //   rate: with u = rate s, da/du = -a and dw/du = a^2 / w, so e = g (v a^2 / w - h_{t-1} a) s,
 //         dr = e rate (1 - s), drate = sum of e;  no rate: dr = g (v - h_{t-1}) s (1 - s)
+//
+// Both recurrences are scans with the operator (a, b) o (a', b') = (a a', a' b + b'). Bound: bytes. A
+// token's channel is 4 to 10 bytes at 16-bit storage and 6 to 8 exponentials, reciprocals and roots (30.5 a clock
+// and SM), which together take less than the bytes.
+//
+// So every input is read once: the token axis is cut over the warps of a CTA, and where sequences and channels alone
+// do not fill the GPU over the CTAs of a cluster too. A warp has kT tokens of 64 channels, a lane a pair of channels in
+// a register pair; it makes the decays and inputs of its tokens, and their product and sum as one element of the
+// scan. The elements meet in shared memory, those of a cluster's CTAs in each other's, and each warp then
+// knows its first state and finishes its tokens, whose decays and inputs are still in registers. Nothing is
+// computed or read twice, and no CTA waits for one that may not be resident.
 #pragma once
 
 #include "mt_seq.cuh"
 #include "mt_seq.h"
 
 namespace mt {
+
+constexpr int kGatedSlab = 64;   // channels of a warp
+constexpr int kGatedWarps = 8;   // warps of a CTA
+constexpr int kGatedThreads = 32 * kGatedWarps;
+constexpr int kGatedStages = 2;  // tiles of a warp on their way or in use
+
+struct GatedArgs {
+    mt_gated_args p;
+    int slabs;       // of 64 channels
+    int ctas;        // of a cluster
+    int64_t ntiles;  // checkpoints of a sequence
+};
 
 __device__ __forceinline__ int64_t gated_len(const mt_gated_args &p, int64_t b) {
     const int64_t n = p.lens != nullptr ? (int64_t)p.lens[b] : p.len;
@@ -24,185 +47,758 @@ __device__ __forceinline__ int64_t gated_slot(const mt_gated_args &p, int64_t b)
     return s >= 0 && s < p.nslots ? s : -1;
 }
 
-// sigma(x) and 1 - sigma(x), each to f32's relative precision: e = exp(-|x|) is at most 1, so nothing overflows.
-__device__ __forceinline__ void sigmoid_both(float x, float &s, float &c) {
-    const float e = ex2f(-kLog2e * fabsf(x));
-    const float q = rcpf(1.0f + e);
-    const float eq = e * q;
-    s = x >= 0.0f ? q : eq;
-    c = x >= 0.0f ? eq : q;
+// ---- clusters -----------------------------------------------------------------------------------
+__device__ __forceinline__ unsigned cluster_rank() {
+    unsigned r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// Two pairs to the same place in another CTA's shared memory.
+__device__ __forceinline__ void cluster_put(uint32_t here, unsigned rank, f32x2 a, f32x2 b) {
+    uint32_t there;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(here), "r"(rank));
+    asm volatile("st.shared::cluster.v2.u64 [%0], {%1, %2};" :: "r"(there), "l"(a), "l"(b) : "memory");
 }
 
-// 1 - exp(-u) = u (1 - u/2 (1 - u/3 (...))), Taylor's series of the exponential, for u below 1/2: the first
-// term left out is below 2e-9 of the sum. The decay next to 1 is 1 minus this, so that a long memory's
+// ---- a pair of channels ---------------------------------------------------------------------------
+__device__ __forceinline__ f32x2 less2f(float a, f32x2 b) { return fma2f(b, both(-1.0f), both(a)); }  // a - b
+__device__ __forceinline__ f32x2 max2f(f32x2 a, f32x2 b) {
+    float x, y, v, w;
+    unpack2f(a, x, y);
+    unpack2f(b, v, w);
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(x) : "f"(v));
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(y) : "f"(w));
+    return pack2f(x, y);
+}
+__device__ __forceinline__ f32x2 rsqrt_2f(f32x2 v) {
+    float a, b;
+    unpack2f(v, a, b);
+    asm("rsqrt.approx.ftz.f32 %0, %0;" : "+f"(a));
+    asm("rsqrt.approx.ftz.f32 %0, %0;" : "+f"(b));
+    return pack2f(a, b);
+}
+
+// sigma(x) and 1 - sigma(x), each to f32's relative precision: 1 / (1 + e) and e / (1 + e) with e = exp(-x), which is
+// kept below 2^126 (x above -87.3) so that neither is 0 * inf; the minimum passes NaN on.
+__device__ __forceinline__ f32x2 least_2f(f32x2 v, float most) {
+    float a, b;
+    unpack2f(v, a, b);
+    asm("min.NaN.f32 %0, %0, %1;" : "+f"(a) : "f"(most));
+    asm("min.NaN.f32 %0, %0, %1;" : "+f"(b) : "f"(most));
+    return pack2f(a, b);
+}
+__device__ __forceinline__ void sigmoid_both_2f(f32x2 x, f32x2 &s, f32x2 &c) {
+    const f32x2 e = least_2f(ex2_2f(mul2f(both(-kLog2e), x)), 0x1p126f);
+    s = rcp_2f(add2f(both(1.0f), e));
+    c = mul2f(e, s);
+}
+
+// 1 - exp(-u) = u (1 - u/2! + u^2/3! - ...), Taylor's series of the exponential, for u below 1/4: the first
+// term left out is below 4.9e-8 of the sum. The decay next to 1 is 1 minus this, so that a long memory's
 // decays keep f32's precision and w = sqrt(1 - a^2) its relative one, which 1 - a * a does not.
-__device__ __forceinline__ float one_minus_exp_small(float u) {
-    float p = fmaf(u, -1.0f / 9.0f, 1.0f);
-    p = fmaf(u * p, -1.0f / 8.0f, 1.0f);
-    p = fmaf(u * p, -1.0f / 7.0f, 1.0f);
-    p = fmaf(u * p, -1.0f / 6.0f, 1.0f);
-    p = fmaf(u * p, -1.0f / 5.0f, 1.0f);
-    p = fmaf(u * p, -1.0f / 4.0f, 1.0f);
-    p = fmaf(u * p, -1.0f / 3.0f, 1.0f);
-    p = fmaf(u * p, -1.0f / 2.0f, 1.0f);
-    return u * p;
+constexpr float kNear = 0.25f;
+__device__ __forceinline__ f32x2 one_minus_exp_small_2f(f32x2 u) {
+    f32x2 p = both(-1.0f / 720.0f);
+    p = fma2f(p, u, both(1.0f / 120.0f));
+    p = fma2f(p, u, both(-1.0f / 24.0f));
+    p = fma2f(p, u, both(1.0f / 6.0f));
+    p = fma2f(p, u, both(-0.5f));
+    p = fma2f(p, u, both(1.0f));
+    return mul2f(u, p);
 }
 
-// One token's gate: decay a, weight w, and (rate) 1 / w, 0 where w is.
-template <bool RATE> struct Gate {
-    float s, c, a, w, rw;
-    __device__ __forceinline__ void open(float r, float rate) {
-        sigmoid_both(r, s, c);
-        if constexpr (RATE) {
-            const float u = rate * s;
-            const float small = one_minus_exp_small(u), big = ex2f(-kLog2e * u);
-            const bool near = u < 0.5f;
-            a = near ? 1.0f - small : big;
-            const float d = near ? small : 1.0f - big;
-            const float q = d * (2.0f - d);  // 1 - a^2 = (1 - a) (1 + a)
-            float y;
-            asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(q));
-            rw = q < 1.2e-38f ? 0.0f : y;
-            w = q * rw;
-        } else {
-            a = c;
-            w = s;
-            rw = 0.0f;
-        }
+// With rate: the decay and q = 1 - a^2. w = q / sqrt(q), with q of `least` at least in the root, is 0 where q is.
+constexpr float kLeast = 1.2e-38f;
+__device__ __forceinline__ void decay_2f(f32x2 u, f32x2 &a, f32x2 &q) {
+    const f32x2 small = one_minus_exp_small_2f(u), big = ex2_2f(mul2f(both(-kLog2e), u));
+    const f32x2 far = less2f(1.0f, big), near = less2f(1.0f, small);
+    float u0, u1, s0, s1, b0, b1, f0, f1, n0, n1;
+    unpack2f(u, u0, u1);
+    unpack2f(small, s0, s1);
+    unpack2f(big, b0, b1);
+    unpack2f(far, f0, f1);
+    unpack2f(near, n0, n1);
+    a = pack2f(u0 < kNear ? n0 : b0, u1 < kNear ? n1 : b1);
+    const f32x2 d = pack2f(u0 < kNear ? s0 : f0, u1 < kNear ? s1 : f1);  // 1 - a
+    q = mul2f(d, less2f(2.0f, d));                                     // (1 - a) (1 + a)
+}
+// 1 / sqrt(q), q counting as `least` at least
+__device__ __forceinline__ f32x2 rsqrt_least_2f(f32x2 q, f32x2 least = both(kLeast)) { return rsqrt_2f(max2f(q, least)); }
+// sqrt(q) sigma(i) = q / sqrt(q (1 + e)^2) with e = exp(-i): one root for both. e is kept below 2^60, so sigma(i) is 2^-60 at least.
+__device__ __forceinline__ f32x2 root_sigmoid_2f(f32x2 q, f32x2 i) {
+    const f32x2 n = add2f(both(1.0f), least_2f(ex2_2f(mul2f(both(-kLog2e), i)), 0x1p60f));
+    return mul2f(q, rsqrt_least_2f(mul2f(mul2f(q, n), n)));
+}
+
+// ---- rows of activations --------------------------------------------------------------------------
+template <class S> struct Pair;  // two neighbouring values
+template <> struct Pair<float> {
+    using T = uint2;
+    __device__ __forceinline__ static f32x2 widen(const uint2 &w) { return pack2f(__uint_as_float(w.x), __uint_as_float(w.y)); }
+    __device__ __forceinline__ static uint2 narrow(float a, float b) { return make_uint2(__float_as_uint(a), __float_as_uint(b)); }
+};
+template <> struct Pair<__nv_bfloat16> {
+    using T = uint32_t;
+    __device__ __forceinline__ static f32x2 widen(uint32_t w) {
+        float a, b;
+        Codec<__nv_bfloat16>::two(w, a, b);
+        return pack2f(a, b);
+    }
+    __device__ __forceinline__ static uint32_t narrow(float a, float b) { return Codec<__nv_bfloat16>::pack2(a, b); }
+};
+template <> struct Pair<__half> {
+    using T = uint32_t;
+    __device__ __forceinline__ static f32x2 widen(uint32_t w) {
+        float a, b;
+        Codec<__half>::two(w, a, b);
+        return pack2f(a, b);
+    }
+    __device__ __forceinline__ static uint32_t narrow(float a, float b) { return Codec<__half>::pack2(a, b); }
+};
+
+// A tensor's rows for one sequence and slab. Where VEC, a token's stride in bytes is below 2^31, and a row's
+// address one multiply-add.
+template <class S, bool VEC> struct Rows {
+    S *at;  // token 0, the slab's first channel
+    int64_t token;
+    __device__ __forceinline__ Rows(const void *p, int64_t batch, int64_t token_, int64_t b, int64_t c0)
+        : at(p == nullptr ? nullptr : const_cast<S *>(static_cast<const S *>(p)) + b * batch + c0), token(token_) {}
+    __device__ __forceinline__ S *row(int t) const {
+        if constexpr (VEC)
+            return reinterpret_cast<S *>(reinterpret_cast<char *>(at) + (int64_t)t * (int)((int)token * (int)sizeof(S)));
+        else
+            return at + t * token;
     }
 };
 
-// --- the plain kernels: a thread a channel, token after token ---------------------------------
-template <class S, bool RATE> __global__ void k_gated_plain(mt_gated_args p, int64_t tokens) {
+// T tokens of a tensor in a warp's part of shared memory, 64 channels each. VEC: the rows are 16-byte aligned and
+// whole vectors; otherwise they are copied as the 32-bit words that they touch, and 16-bit rows that begin in
+// the middle of a word are read across words.
+template <class S, int T, bool VEC> struct Tile {
+    static constexpr int kPitch = kGatedSlab * (int)sizeof(S) + (VEC ? 0 : 16);
+    static constexpr int kBytes = T * kPitch;
+    static constexpr int kRow = kGatedSlab * (int)sizeof(S) / 16, kPer = 16 / (int)sizeof(S);  // vectors of a row, values of one
+    // The first n tokens (T at most) from token t0 on, `live` of the slab's channels; `r` from the lane's own vector on where VEC (lane_rows).
+    static __device__ __forceinline__ void copy(uint32_t to, const Rows<S, VEC> &r, int t0, int n, int live, int lane) {
+        if constexpr (VEC) {
+            if (lane % kRow * kPer >= live)
+                return;
+#pragma unroll
+            for (int k = 0; k < T * kRow / 32; ++k) {
+                const int row = k * (32 / kRow) + lane / kRow;
+                if (n >= T || row < n)
+                    cp_async_zfill<16>(to + k * 512 + lane * 16, r.row(t0 + row), true);
+            }
+        } else {
+#pragma unroll 1
+            for (int row = 0; row < (n < T ? n : T); ++row) {
+                const uintptr_t from = (uintptr_t)r.row(t0 + row);
+                const int shift = (int)(from & 3), words = (shift + live * (int)sizeof(S) + 3) / 4;
+                for (int w = lane; w < words; w += 32)
+                    cp_async_zfill<4>(to + row * kPitch + w * 4, (const void *)(from - shift + w * 4), true);
+            }
+        }
+    }
+    // The rows as copy takes them.
+    static __device__ __forceinline__ Rows<S, VEC> lane_rows(Rows<S, VEC> r, int lane) {
+        if constexpr (VEC)
+            if (r.at != nullptr)
+                r.at += lane % kRow * kPer;
+        return r;
+    }
+    // The lane's channels of token t0 + row.
+    static __device__ __forceinline__ f32x2 read(const char *at, const Rows<S, VEC> &r, int t0, int row, int lane) {
+        using P = typename Pair<S>::T;
+        if constexpr (VEC) {
+            return Pair<S>::widen(*reinterpret_cast<const P *>(at + row * kPitch + lane * (int)sizeof(P)));
+        } else if constexpr (sizeof(S) == 4) {
+            const float *f = reinterpret_cast<const float *>(at + row * kPitch) + 2 * lane;
+            return pack2f(f[0], f[1]);
+        } else {
+            const uint32_t *w = reinterpret_cast<const uint32_t *>(at + row * kPitch) + lane;
+            const bool odd = ((uintptr_t)r.row(t0 + row) & 2) != 0;
+            return Pair<S>::widen(odd ? __funnelshift_r(w[0], w[1], 16) : w[0]);
+        }
+    }
+    // Rows from n on hold `v` in every channel.
+    static __device__ __forceinline__ void fill(char *at, int n, S v, int lane) {
+        for (int row = n; row < T; ++row)
+            for (int k = lane; k < kPitch / (int)sizeof(S); k += 32)
+                reinterpret_cast<S *>(at + row * kPitch)[k] = v;
+    }
+};
+
+// a lane's pair, of which the first `live` channels exist (VEC: none or both)
+template <class S, bool VEC> __device__ __forceinline__ void put_pair(S *to, int live, f32x2 v) {
+    float a, b;
+    unpack2f(v, a, b);
+    if constexpr (VEC) {
+        if (live > 0)
+            *reinterpret_cast<typename Pair<S>::T *>(to) = Pair<S>::narrow(a, b);
+    } else {
+        if (live > 0)
+            Codec<S>::store1(to, a);
+        if (live > 1)
+            Codec<S>::store1(to + 1, b);
+    }
+}
+// f32 rows of states and parameters, from the lane's first channel on
+__device__ __forceinline__ f32x2 get_state(const float *p, int live) {
+    return pack2f(live > 0 ? p[0] : 0.0f, live > 1 ? p[1] : 0.0f);
+}
+__device__ __forceinline__ void put_state(float *p, int live, f32x2 v) {
+    float a, b;
+    unpack2f(v, a, b);
+    if (live > 0)
+        p[0] = a;
+    if (live > 1)
+        p[1] = b;
+}
+
+struct alignas(16) Element {  // of the scan
+    f32x2 a, h;
+};
+
+// ---- prompts ----------------------------------------------------------------------------------------
+constexpr int kFwdT = 8;  // tokens of a warp
+
+template <class S, bool VEC> struct FwdShared {
+    static constexpr int kTensors = 4;
+    static constexpr int kTile = Tile<S, kFwdT, VEC>::kBytes;
+    static constexpr int kWarp = kGatedStages * kTensors * kTile;
+    static constexpr int kBytes = kGatedWarps * kWarp;
+};
+
+// IN and Z: the call has an input gate, an output gate (VEC; other rows ask at run time).
+template <class S, bool RATE, bool VEC, bool IN, bool Z>
+__global__ void __launch_bounds__(kGatedThreads, 2) k_gated(const __grid_constant__ GatedArgs g) {
+    using In = Tile<S, kFwdT, VEC>;
+    using Shared = FwdShared<S, VEC>;
+    constexpr int kCtaTokens = kGatedWarps * kFwdT;
+    extern __shared__ __align__(16) char staged[];
+    __shared__ Element of_warps[2][kGatedWarps][32];
+    __shared__ Element of_ctas[2][8][32];
+    if (g.ctas > 1)
+        cluster_arrive();  // waited for below: no CTA writes into one that has not begun
     pdl_prologue();
-    const int64_t cols = (p.dim + blockDim.x - 1) / blockDim.x, b = blockIdx.x / cols;
-    const int64_t d = (blockIdx.x - b * cols) * blockDim.x + threadIdx.x;
-    if (d >= p.dim)
-        return;
-    const bool step = tokens < 0;
+    const mt_gated_args &p = g.p;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int rank = g.ctas > 1 ? (int)cluster_rank() : 0;
+    const int64_t unit = blockIdx.x / g.ctas, b = unit / g.slabs, c0 = (unit - b * g.slabs) * kGatedSlab;
+    const int live = (int)(p.dim - c0 < kGatedSlab ? p.dim - c0 : kGatedSlab), mine = live - 2 * lane;
     const int64_t slot = gated_slot(p, b);
     const bool active = slot >= 0 || p.state == nullptr;
-    const int64_t len = !active ? 0 : step ? 1 : gated_len(p, b), total = step ? 1 : p.len;
-    float h = 0.0f;
-    if (active && p.state != nullptr && (step || p.carry_in))
-        h = p.state[slot * p.dim + d];
-    const float rate = RATE ? p.rate[d] : 0.0f;
-    const S *x = (const S *)p.x + b * p.x_batch + d, *r = (const S *)p.r + b * p.r_batch + d;
-    const S *i = p.i ? (const S *)p.i + b * p.i_batch + d : nullptr, *z = p.z ? (const S *)p.z + b * p.z_batch + d : nullptr;
-    S *out = (S *)p.out + b * p.out_batch + d;
-    const int64_t ntiles = (p.len + kGatedTile - 1) / kGatedTile;
-    for (int64_t t = 0; t < total; ++t) {
-        if (!step && p.checkpoints != nullptr && t % kGatedTile == 0)
-            p.checkpoints[(b * ntiles + t / kGatedTile) * p.dim + d] = h;
-        float y = 0.0f;
-        if (t < len) {
-            Gate<RATE> g;
-            g.open(Codec<S>::load1(r + t * p.r_token), rate);
-            float v = Codec<S>::load1(x + t * p.x_token);
-            if (i) {
-                float s, c;
-                sigmoid_both(Codec<S>::load1(i + t * p.i_token), s, c);
-                v *= s;
-            }
-            h = fmaf(g.a, h, g.w * v);
-            y = h;
-            if (z) {
-                float s, c;
-                const float zz = Codec<S>::load1(z + t * p.z_token);
-                sigmoid_both(zz, s, c);
-                y = h * (zz * s);
-            }
-        }
-        Codec<S>::store1(out + t * p.out_token, y);
-    }
-    if (active && p.state != nullptr)
-        p.state[slot * p.dim + d] = h;
-}
+    const int len = active ? (int)gated_len(p, b) : 0, total = (int)p.len;
+    const Rows<S, VEC> x = In::lane_rows({p.x, p.x_batch, p.x_token, b, c0}, lane), r = In::lane_rows({p.r, p.r_batch, p.r_token, b, c0}, lane),
+                       in = In::lane_rows({p.i, p.i_batch, p.i_token, b, c0}, lane), z = In::lane_rows({p.z, p.z_batch, p.z_token, b, c0}, lane);
+    const Rows<S, VEC> out(p.out, p.out_batch, p.out_token, b, c0 + 2 * lane);
+    const bool has_in = VEC ? IN : in.at != nullptr, has_z = VEC ? Z : z.at != nullptr;
+    const int64_t c = c0 + 2 * lane;
+    const f32x2 rate = RATE ? get_state(p.rate + c, mine) : 0ull;
+    f32x2 carry = 0ull;
+    if (active && p.state != nullptr && p.carry_in)
+        carry = get_state(p.state + slot * p.dim + c, mine);
+    char *own = staged + warp * Shared::kWarp;
+    const uint32_t own_at = (uint32_t)__cvta_generic_to_shared(own);
+    const int step = g.ctas * kCtaTokens, first = rank * kCtaTokens + warp * kFwdT;
 
-template <class S, bool RATE> __global__ void k_gated_grad_plain(mt_gated_args p) {
-    pdl_prologue();
-    const int64_t cols = (p.dim + blockDim.x - 1) / blockDim.x, b = blockIdx.x / cols;
-    const int64_t d = (blockIdx.x - b * cols) * blockDim.x + threadIdx.x;
-    if (d >= p.dim)
-        return;
-    const int64_t len = gated_len(p, b);
-    const int64_t ntiles = (p.len + kGatedTile - 1) / kGatedTile;
-    const float rate = RATE ? p.rate[d] : 0.0f;
-    const S *x = (const S *)p.x + b * p.x_batch + d, *r = (const S *)p.r + b * p.r_batch + d;
-    const S *i = p.i ? (const S *)p.i + b * p.i_batch + d : nullptr, *z = p.z ? (const S *)p.z + b * p.z_batch + d : nullptr;
-    const S *dout = (const S *)p.dout + b * p.dout_batch + d;
-    S *dx = (S *)p.dx + b * p.dx_batch + d, *dr = (S *)p.dr + b * p.dr_batch + d;
-    S *di = (S *)p.di + b * p.di_batch + d, *dz = (S *)p.dz + b * p.dz_batch + d;
-    for (int64_t t = len; t < p.len; ++t) {
-        Codec<S>::store1(dx + t * p.dx_token, 0.0f);
-        Codec<S>::store1(dr + t * p.dr_token, 0.0f);
-        if (i)
-            Codec<S>::store1(di + t * p.di_token, 0.0f);
-        if (z)
-            Codec<S>::store1(dz + t * p.dz_token, 0.0f);
-    }
-    float carry = p.dfinal ? p.dfinal[b * p.dim + d] : 0.0f, drate = 0.0f;
-    for (int64_t tile = (len + kGatedTile - 1) / kGatedTile - 1; tile >= 0; --tile) {
-        float before[kGatedTile];
-        float h = p.checkpoints[(b * ntiles + tile) * p.dim + d];
-        const int64_t t0 = tile * kGatedTile;
-        const int n = (int)(len - t0 < kGatedTile ? len - t0 : kGatedTile);
-        for (int k = 0; k < n; ++k) {
-            Gate<RATE> g;
-            g.open(Codec<S>::load1(r + (t0 + k) * p.r_token), rate);
-            float v = Codec<S>::load1(x + (t0 + k) * p.x_token), s = 1.0f, c;
-            if (i)
-                sigmoid_both(Codec<S>::load1(i + (t0 + k) * p.i_token), s, c);
-            before[k] = h;
-            h = fmaf(g.a, h, g.w * (v * s));
+    auto ask = [&](int t0, int stage) {
+        const int n = len - t0;
+        if (n > 0) {
+            const uint32_t to = own_at + (uint32_t)(stage * (Shared::kTensors * Shared::kTile));
+            In::copy(to, x, t0, n, live, lane);
+            In::copy(to + Shared::kTile, r, t0, n, live, lane);
+            if (has_in)
+                In::copy(to + 2 * Shared::kTile, in, t0, n, live, lane);
+            if (has_z)
+                In::copy(to + 3 * Shared::kTile, z, t0, n, live, lane);
         }
-        for (int k = n - 1; k >= 0; --k) {
-            const int64_t t = t0 + k;
-            Gate<RATE> g;
-            g.open(Codec<S>::load1(r + t * p.r_token), rate);
-            const float xx = Codec<S>::load1(x + t * p.x_token), hp = before[k];
-            float si = 1.0f, ci = 0.0f;
-            if (i)
-                sigmoid_both(Codec<S>::load1(i + t * p.i_token), si, ci);
-            const float v = xx * si, dy = Codec<S>::load1(dout + t * p.dout_token);
-            float gh = dy;
-            if (z) {
-                float s, c;
-                const float zz = Codec<S>::load1(z + t * p.z_token);
-                sigmoid_both(zz, s, c);
-                gh = dy * (zz * s);
-                Codec<S>::store1(dz + t * p.dz_token, dy * fmaf(g.a, hp, g.w * v) * (s * fmaf(zz, c, 1.0f)));
-            }
-            gh += carry;
-            carry = gh * g.a;
-            const float dv = gh * g.w;
-            Codec<S>::store1(dx + t * p.dx_token, dv * si);
-            if (i)
-                Codec<S>::store1(di + t * p.di_token, dv * v * ci);
+        cp_async_commit();
+    };
+    ask(first, 0);
+    ask(first + step, 1);
+    if (g.ctas > 1)
+        cluster_wait();
+
+    int side = 0;
+    for (int base = 0; base < len; base += step, side ^= 1) {
+        const int t0 = base + first, n = len - t0;
+        char *at = own + side * (Shared::kTensors * Shared::kTile);
+        cp_async_wait<kGatedStages - 1>();
+        __syncwarp();
+        if (n < kFwdT) {  // tokens behind the end: a shut gate, which leaves the state
+            const int has = n < 0 ? 0 : n;
+            In::fill(at, has, S(0.0f), lane);
+            In::fill(at + Shared::kTile, has, S(Lim<float>::lo()), lane);
+            In::fill(at + 2 * Shared::kTile, has, S(0.0f), lane);
+            In::fill(at + 3 * Shared::kTile, has, S(0.0f), lane);
+            __syncwarp();
+        }
+        f32x2 a[kFwdT], v[kFwdT], gate[kFwdT];
+        Element e = {both(1.0f), 0ull};
+#pragma unroll
+        for (int k = 0; k < kFwdT; ++k) {
+            const f32x2 rr = In::read(at + Shared::kTile, r, t0, k, lane);
+            f32x2 w;
             if constexpr (RATE) {
-                const float e = gh * (v * (g.a * g.a) * (g.s * g.rw) - hp * g.a * g.s);
-                drate += e;
-                Codec<S>::store1(dr + t * p.dr_token, e * rate * g.c);
+                f32x2 q;
+                decay_2f(mul2f(rate, sigmoid_2f(rr)), a[k], q);
+                w = has_in ? root_sigmoid_2f(q, In::read(at + 2 * Shared::kTile, in, t0, k, lane)) : mul2f(q, rsqrt_least_2f(q));
             } else {
-                Codec<S>::store1(dr + t * p.dr_token, gh * (v - hp) * (g.s * g.c));
+                sigmoid_both_2f(rr, w, a[k]);
+                if (has_in)
+                    w = mul2f(w, sigmoid_2f(In::read(at + 2 * Shared::kTile, in, t0, k, lane)));
             }
+            v[k] = mul2f(w, In::read(at, x, t0, k, lane));
+            if (has_z) {
+                const f32x2 zz = In::read(at + 3 * Shared::kTile, z, t0, k, lane);
+                gate[k] = mul2f(zz, sigmoid_2f(zz));
+            }
+            e.h = fma2f(a[k], e.h, v[k]);
+            e.a = mul2f(e.a, a[k]);
         }
+        __syncwarp();
+        ask(t0 + kGatedStages * step, side);
+        of_warps[side][warp][lane] = e;
+        __syncthreads();
+        f32x2 h = carry;  // before the CTA's first token
+        if (g.ctas == 1) {
+#pragma unroll
+            for (int w = 0; w < kGatedWarps; ++w) {
+                if (w == warp)
+                    h = carry;
+                const Element o = of_warps[side][w][lane];
+                carry = fma2f(o.a, carry, o.h);
+            }
+        } else {
+            // one warp joins the CTA's elements, and tells every CTA of the cluster
+            if (warp == 0) {
+                Element all = {both(1.0f), 0ull};
+#pragma unroll
+                for (int w = 0; w < kGatedWarps; ++w) {
+                    const Element o = of_warps[side][w][lane];
+                    of_warps[side][w][lane] = all;  // of the warps before w
+                    all.h = fma2f(o.a, all.h, o.h);
+                    all.a = mul2f(all.a, o.a);
+                }
+                for (int q = 0; q < g.ctas; ++q)
+                    cluster_put((uint32_t)__cvta_generic_to_shared(&of_ctas[side][rank][lane]), (unsigned)q, all.a, all.h);
+            }
+            cluster_arrive();
+            cluster_wait();
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                if (q == rank)
+                    h = carry;
+                if (q < g.ctas) {
+                    const Element o = of_ctas[side][q][lane];
+                    carry = fma2f(o.a, carry, o.h);
+                }
+            }
+            const Element before = of_warps[side][warp][lane];
+            h = fma2f(before.a, h, before.h);
+        }
+        if (p.checkpoints != nullptr && warp * kFwdT % kGatedTile == 0 && n > 0)
+            put_state(p.checkpoints + (b * g.ntiles + t0 / kGatedTile) * p.dim + c, mine, h);
+        auto finish = [&](bool whole) {
+#pragma unroll
+            for (int k = 0; k < kFwdT; ++k) {
+                h = fma2f(a[k], h, v[k]);
+                f32x2 y = h;
+                if (has_z)
+                    y = mul2f(h, gate[k]);
+                if (whole || k < n)
+                    put_pair<S, VEC>(out.row(t0 + k), mine, y);
+            }
+        };
+        if (n >= kFwdT)
+            finish(true);
+        else
+            finish(false);
     }
-    if (p.dinit != nullptr)
-        p.dinit[b * p.dim + d] = carry;
-    if (RATE && p.drate != nullptr)
-        reinterpret_cast<float *>(p.scratch)[b * p.dim + d] = drate;
+    cp_async_wait<0>();
+    for (int t = len + rank * kGatedWarps + warp; t < total; t += g.ctas * kGatedWarps)
+        put_pair<S, VEC>(out.row(t), mine, 0ull);
+    if (active && p.state != nullptr && rank == 0 && warp == 0)
+        put_state(p.state + slot * p.dim + c, mine, carry);
 }
 
-static __global__ void k_gated_rate_join(const float *part, float *drate, int64_t rows, int64_t dim) {
+// ---- gradients ----------------------------------------------------------------------------------------
+// From the last tokens to the first. A warp's tokens give two elements, the recurrence's from the checkpoint before the
+// CTA's tokens and its adjoint's from behind; with both carries known the states and the gradients by them
+// follow, and what a token's gradients take besides is in registers: four tokens' worth of it.
+constexpr int kBwdT = 4;
+constexpr int kBwdTensors = 5;
+
+template <class S, bool VEC> struct BwdShared {
+    static constexpr int kTile = Tile<S, kBwdT, VEC>::kBytes;
+    static constexpr int kWarp = kGatedStages * kBwdTensors * kTile;
+    static constexpr int kBytes = kGatedWarps * kWarp;
+};
+
+template <class S, bool RATE, bool VEC, bool IN, bool Z>
+__global__ void __launch_bounds__(kGatedThreads, 2) k_gated_grad(const __grid_constant__ GatedArgs g, float *rate_part) {
+    using In = Tile<S, kBwdT, VEC>;
+    using Shared = BwdShared<S, VEC>;
+    constexpr int kCtaTokens = kGatedWarps * kBwdT;
+    static_assert(kCtaTokens == kGatedTile, "a CTA's tokens begin at a checkpoint");
+    extern __shared__ __align__(16) char staged[];
+    __shared__ Element of_warps[2][kGatedWarps][32];
+    __shared__ f32x2 back_of_warps[2][kGatedWarps][32];
+    __shared__ Element behind_warps[kGatedWarps][32];
+    __shared__ Element of_ctas[2][8][32];
+    if (g.ctas > 1)
+        cluster_arrive();  // waited for below: no CTA writes into one that has not begun
     pdl_prologue();
-    const int64_t d = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (d >= dim)
-        return;
-    float s = 0.0f;
-    for (int64_t k = 0; k < rows; ++k)
-        s += part[k * dim + d];
-    drate[d] = s;
+    const mt_gated_args &p = g.p;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int rank = g.ctas > 1 ? (int)cluster_rank() : 0;
+    const int64_t unit = blockIdx.x / g.ctas, b = unit / g.slabs, c0 = (unit - b * g.slabs) * kGatedSlab;
+    const int live = (int)(p.dim - c0 < kGatedSlab ? p.dim - c0 : kGatedSlab), mine = live - 2 * lane;
+    const int len = (int)gated_len(p, b), total = (int)p.len;
+    const Rows<S, VEC> x = In::lane_rows({p.x, p.x_batch, p.x_token, b, c0}, lane), r = In::lane_rows({p.r, p.r_batch, p.r_token, b, c0}, lane),
+                       in = In::lane_rows({p.i, p.i_batch, p.i_token, b, c0}, lane), z = In::lane_rows({p.z, p.z_batch, p.z_token, b, c0}, lane),
+                       dout = In::lane_rows({p.dout, p.dout_batch, p.dout_token, b, c0}, lane);
+    const int64_t c = c0 + 2 * lane;
+    const Rows<S, VEC> dx(p.dx, p.dx_batch, p.dx_token, b, c), dr(p.dr, p.dr_batch, p.dr_token, b, c), di(p.di, p.di_batch, p.di_token, b, c),
+        dz(p.dz, p.dz_batch, p.dz_token, b, c);
+    const bool has_in = VEC ? IN : in.at != nullptr, has_z = VEC ? Z : z.at != nullptr;
+    const f32x2 rate = RATE ? get_state(p.rate + c, mine) : 0ull;
+    f32x2 carry = p.dfinal != nullptr ? get_state(p.dfinal + b * p.dim + c, mine) : 0ull;
+    f32x2 rate_sum = 0ull, least = 0ull;
+    if (RATE) {  // without any decay 1 / w counts as 0: 1 / sqrt(inf)
+        float r0, r1;
+        unpack2f(rate, r0, r1);
+        least = pack2f(r0 == 0.0f ? Lim<float>::hi() : kLeast, r1 == 0.0f ? Lim<float>::hi() : kLeast);
+    }
+    char *own = staged + warp * Shared::kWarp;
+    const uint32_t own_at = (uint32_t)__cvta_generic_to_shared(own);
+    const int step = g.ctas * kCtaTokens, first = rank * kCtaTokens + warp * kBwdT;
+
+    auto ask = [&](int base, int stage) {
+        const int t0 = base + first, n = len - t0;
+        if (base >= 0 && n > 0) {
+            const uint32_t to = own_at + (uint32_t)(stage * (kBwdTensors * Shared::kTile));
+            In::copy(to, x, t0, n, live, lane);
+            In::copy(to + Shared::kTile, r, t0, n, live, lane);
+            if (has_in)
+                In::copy(to + 2 * Shared::kTile, in, t0, n, live, lane);
+            if (has_z)
+                In::copy(to + 3 * Shared::kTile, z, t0, n, live, lane);
+            In::copy(to + 4 * Shared::kTile, dout, t0, n, live, lane);
+        }
+        cp_async_commit();
+    };
+    const int last = len > 0 ? (len - 1) / step * step : -1;  // where the last CTAs' tokens begin
+    ask(last, 0);
+    ask(last - step, 1);
+    if (g.ctas > 1)
+        cluster_wait();
+
+    int side = 0;
+    for (int base = last; base >= 0; base -= step, side ^= 1) {
+        const int t0 = base + first, n = len - t0;
+        char *at = own + side * (kBwdTensors * Shared::kTile);
+        f32x2 h = 0ull;  // before the CTA's first token
+        if (t0 - warp * kBwdT < len)
+            h = get_state(p.checkpoints + (b * g.ntiles + t0 / kGatedTile) * p.dim + c, mine);
+        cp_async_wait<kGatedStages - 1>();
+        __syncwarp();
+        if (n < kBwdT) {  // tokens behind the end: a shut gate, which passes states and gradients by them
+            const int has = n < 0 ? 0 : n;
+            In::fill(at, has, S(0.0f), lane);
+            In::fill(at + Shared::kTile, has, S(Lim<float>::lo()), lane);
+            In::fill(at + 2 * Shared::kTile, has, S(0.0f), lane);
+            In::fill(at + 3 * Shared::kTile, has, S(0.0f), lane);
+            In::fill(at + 4 * Shared::kTile, has, S(0.0f), lane);
+            __syncwarp();
+        }
+        // per token: decay, w v (later the state before it), dh; w sigma(i), x (1 - sigma(i)), dz / h; and of
+        // e = g as (m - h_{t-1}), with as = a s and m = v a / w (without rate 1 and v), those and dr / e
+        f32x2 a[kBwdT], v[kBwdT], dh[kBwdT], to_x[kBwdT], to_i[kBwdT], to_z[kBwdT], as[kBwdT], m[kBwdT], to_r[kBwdT];
+        Element e = {both(1.0f), 0ull};
+#pragma unroll
+        for (int k = 0; k < kBwdT; ++k) {
+            f32x2 s, cs, w, rw = 0ull;
+            sigmoid_both_2f(In::read(at + Shared::kTile, r, t0, k, lane), s, cs);
+            if constexpr (RATE) {
+                f32x2 q;
+                decay_2f(mul2f(rate, s), a[k], q);
+                rw = rsqrt_least_2f(q, least);
+                w = mul2f(q, rw);
+            } else {
+                a[k] = cs;
+                w = s;
+            }
+            const f32x2 xx = In::read(at, x, t0, k, lane), dy = In::read(at + 4 * Shared::kTile, dout, t0, k, lane);
+            f32x2 vv = xx;
+            to_x[k] = w;
+            to_i[k] = 0ull;
+            if (has_in) {
+                f32x2 si, ci;
+                sigmoid_both_2f(In::read(at + 2 * Shared::kTile, in, t0, k, lane), si, ci);
+                vv = mul2f(xx, si);
+                to_x[k] = mul2f(w, si);
+                to_i[k] = mul2f(xx, ci);
+            }
+            dh[k] = dy;
+            to_z[k] = 0ull;
+            if (has_z) {
+                f32x2 sz, cz;
+                const f32x2 zz = In::read(at + 3 * Shared::kTile, z, t0, k, lane);
+                sigmoid_both_2f(zz, sz, cz);
+                dh[k] = mul2f(dy, mul2f(zz, sz));
+                to_z[k] = mul2f(dy, mul2f(sz, fma2f(zz, cz, both(1.0f))));
+            }
+            v[k] = mul2f(w, vv);
+            if constexpr (RATE) {
+                as[k] = mul2f(a[k], s);
+                m[k] = mul2f(vv, mul2f(a[k], rw));
+                to_r[k] = mul2f(rate, cs);
+            } else {
+                m[k] = vv;
+                to_r[k] = mul2f(s, cs);
+            }
+            e.h = fma2f(a[k], e.h, v[k]);
+            e.a = mul2f(e.a, a[k]);
+        }
+        f32x2 back = 0ull;
+#pragma unroll
+        for (int k = kBwdT - 1; k >= 0; --k)
+            back = mul2f(a[k], add2f(dh[k], back));
+        __syncwarp();
+        ask(base - kGatedStages * step, side);
+        of_warps[side][warp][lane] = e;
+        back_of_warps[side][warp][lane] = back;
+        __syncthreads();
+        // the state before this warp's tokens
+        for (int w = 0; w < warp; ++w) {
+            const Element o = of_warps[side][w][lane];
+            h = fma2f(o.a, h, o.h);
+        }
+        f32x2 gh = carry;  // by the state after the CTA's last token
+        if (g.ctas == 1) {
+#pragma unroll
+            for (int w = kGatedWarps - 1; w >= 0; --w) {
+                if (w == warp)
+                    gh = carry;
+                carry = fma2f(of_warps[side][w][lane].a, carry, back_of_warps[side][w][lane]);
+            }
+        } else {
+            // one warp joins the CTA's elements of the adjoint, and tells every CTA of the cluster
+            if (warp == 0) {
+                Element all = {both(1.0f), 0ull};
+#pragma unroll
+                for (int w = kGatedWarps - 1; w >= 0; --w) {
+                    const f32x2 oa = of_warps[side][w][lane].a, ob = back_of_warps[side][w][lane];
+                    behind_warps[w][lane] = all;
+                    all.h = fma2f(oa, all.h, ob);
+                    all.a = mul2f(all.a, oa);
+                }
+                for (int q = 0; q < g.ctas; ++q)
+                    cluster_put((uint32_t)__cvta_generic_to_shared(&of_ctas[side][rank][lane]), (unsigned)q, all.a, all.h);
+            }
+            cluster_arrive();
+            cluster_wait();
+#pragma unroll
+            for (int q = 7; q >= 0; --q) {
+                if (q == rank)
+                    gh = carry;
+                if (q < g.ctas) {
+                    const Element o = of_ctas[side][q][lane];
+                    carry = fma2f(o.a, carry, o.h);
+                }
+            }
+            const Element behind = behind_warps[warp][lane];
+            gh = fma2f(behind.a, gh, behind.h);
+        }
+#pragma unroll
+        for (int k = 0; k < kBwdT; ++k) {
+            const f32x2 now = fma2f(a[k], h, v[k]);
+            v[k] = h;
+            to_z[k] = mul2f(to_z[k], now);
+            h = now;
+        }
+        auto finish = [&](bool whole) {
+#pragma unroll
+            for (int k = kBwdT - 1; k >= 0; --k) {
+                const f32x2 gt = add2f(dh[k], gh);
+                gh = mul2f(gt, a[k]);
+                f32x2 to = mul2f(gt, fma2f(v[k], both(-1.0f), m[k]));
+                if (RATE)
+                    to = mul2f(to, as[k]);
+                const f32x2 gx = mul2f(gt, to_x[k]);
+                if (whole || k < n) {
+                    if (RATE)
+                        rate_sum = add2f(rate_sum, to);
+                    put_pair<S, VEC>(dx.row(t0 + k), mine, gx);
+                    put_pair<S, VEC>(dr.row(t0 + k), mine, mul2f(to, to_r[k]));
+                    if (has_in)
+                        put_pair<S, VEC>(di.row(t0 + k), mine, mul2f(gx, to_i[k]));
+                    if (has_z)
+                        put_pair<S, VEC>(dz.row(t0 + k), mine, to_z[k]);
+                }
+            }
+        };
+        if (n >= kBwdT)
+            finish(true);
+        else
+            finish(false);
+    }
+    cp_async_wait<0>();
+    for (int t = len + rank * kGatedWarps + warp; t < total; t += g.ctas * kGatedWarps) {
+        put_pair<S, VEC>(dx.row(t), mine, 0ull);
+        put_pair<S, VEC>(dr.row(t), mine, 0ull);
+        if (has_in)
+            put_pair<S, VEC>(di.row(t), mine, 0ull);
+        if (has_z)
+            put_pair<S, VEC>(dz.row(t), mine, 0ull);
+    }
+    if (p.dinit != nullptr && rank == 0 && warp == 0)
+        put_state(p.dinit + b * p.dim + c, mine, carry);
+    if (RATE && rate_part != nullptr) {
+        __syncthreads();  // the loop's last reads of back_of_warps
+        back_of_warps[0][warp][lane] = rate_sum;
+        __syncthreads();
+        if (warp == 0) {
+            f32x2 s = 0ull;
+#pragma unroll
+            for (int w = 0; w < kGatedWarps; ++w)
+                s = add2f(s, back_of_warps[0][w][lane]);
+            put_state(rate_part + (b * g.ctas + rank) * p.dim + c, mine, s);
+        }
+    }
 }
+
+// ---- single tokens ----------------------------------------------------------------------------------
+// A thread a pair of channels of one sequence.
+template <class S, bool RATE, bool VEC> __global__ void __launch_bounds__(128) k_gated_step(const __grid_constant__ GatedArgs g) {
+    pdl_prologue();
+    const mt_gated_args &p = g.p;
+    const int64_t pairs = (p.dim + 1) / 2, at = (int64_t)blockIdx.x * 128 + threadIdx.x, b = at / pairs;
+    if (b >= p.batch)
+        return;
+    const int64_t c = (at - b * pairs) * 2;
+    const int live = (int)(p.dim - c < 2 ? p.dim - c : 2);
+    const int64_t slot = gated_slot(p, b);
+    S *out = static_cast<S *>(p.out) + b * p.out_batch + c;
+    if (slot < 0) {
+        put_pair<S, VEC>(out, live, 0ull);
+        return;
+    }
+    auto get = [&](const void *q, int64_t batch) {
+        const S *s = static_cast<const S *>(q) + b * batch + c;
+        if constexpr (VEC)
+            return Pair<S>::widen(*reinterpret_cast<const typename Pair<S>::T *>(s));
+        else
+            return pack2f(Codec<S>::load1(s), live > 1 ? Codec<S>::load1(s + 1) : 0.0f);
+    };
+    float *state = p.state + slot * p.dim + c;
+    const f32x2 r = get(p.r, p.r_batch), x = get(p.x, p.x_batch), i = p.i != nullptr ? get(p.i, p.i_batch) : 0ull,
+                z = p.z != nullptr ? get(p.z, p.z_batch) : 0ull, h = get_state(state, live);
+    f32x2 a, w;
+    if constexpr (RATE) {
+        f32x2 q;
+        decay_2f(mul2f(get_state(p.rate + c, live), sigmoid_2f(r)), a, q);
+        w = p.i != nullptr ? root_sigmoid_2f(q, i) : mul2f(q, rsqrt_least_2f(q));
+    } else {
+        sigmoid_both_2f(r, w, a);
+        if (p.i != nullptr)
+            w = mul2f(w, sigmoid_2f(i));
+    }
+    const f32x2 now = fma2f(a, h, mul2f(w, x));
+    put_state(state, live, now);
+    put_pair<S, VEC>(out, live, p.z != nullptr ? mul2f(now, mul2f(z, sigmoid_2f(z))) : now);
+}
+
+// ---- launches ---------------------------------------------------------------------------------------
+template <class... KArgs, class... Args>
+static cudaError_t launch_cluster(void (*kernel)(KArgs...), int64_t grid, unsigned block, int smem, int cluster, cudaStream_t stream,
+                                  Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
+
+// The dynamic shared memory of a kernel is allowed once per device.
+template <class F> static cudaError_t allow_shared(F kernel, int bytes, PerDevice &done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || dev >= kMaxDevices || done.get(dev) != 0)
+        return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess)
+        done.set(dev, 1);
+    return e;
+}
+
+template <class S, bool RATE, bool VEC, bool IN, bool Z> static cudaError_t gated_forward_of(const GatedArgs &g, const Launch &L) {
+    static PerDevice ready;
+    constexpr int smem = FwdShared<S, VEC>::kBytes;
+    const cudaError_t e = allow_shared(k_gated<S, RATE, VEC, IN, Z>, smem, ready);
+    if (e != cudaSuccess)
+        return e;
+    note_launch();
+    return launch_cluster(k_gated<S, RATE, VEC, IN, Z>, g.p.batch * g.slabs * g.ctas, kGatedThreads, smem, g.ctas, L.stream, g);
+}
+template <class S, bool RATE, bool VEC, bool IN, bool Z>
+static cudaError_t gated_backward_of(const GatedArgs &g, float *part, const Launch &L) {
+    static PerDevice ready;
+    constexpr int smem = BwdShared<S, VEC>::kBytes;
+    const cudaError_t e = allow_shared(k_gated_grad<S, RATE, VEC, IN, Z>, smem, ready);
+    if (e != cudaSuccess)
+        return e;
+    note_launch();
+    return launch_cluster(k_gated_grad<S, RATE, VEC, IN, Z>, g.p.batch * g.slabs * g.ctas, kGatedThreads, smem, g.ctas, L.stream, g, part);
+}
+#define MT_GATED_GATES(f, ...)                                                                                             \
+    if constexpr (!VEC)                                                                                                    \
+        return f<S, RATE, false, false, false>(__VA_ARGS__);                                                               \
+    else if (g.p.i != nullptr)                                                                                             \
+        return g.p.z != nullptr ? f<S, RATE, true, true, true>(__VA_ARGS__) : f<S, RATE, true, true, false>(__VA_ARGS__);  \
+    else                                                                                                                   \
+        return g.p.z != nullptr ? f<S, RATE, true, false, true>(__VA_ARGS__) : f<S, RATE, true, false, false>(__VA_ARGS__);
+template <class S, bool RATE, bool VEC> static cudaError_t gated_forward(const GatedArgs &g, const Launch &L) {
+    MT_GATED_GATES(gated_forward_of, g, L)
+}
+template <class S, bool RATE, bool VEC> static cudaError_t gated_backward(const GatedArgs &g, float *part, const Launch &L) {
+    MT_GATED_GATES(gated_backward_of, g, part, L)
+}
+template <class S, bool RATE, bool VEC> static cudaError_t gated_single(const GatedArgs &g, const Launch &L) {
+    const int64_t threads = g.p.batch * ((g.p.dim + 1) / 2);
+    note_launch();
+    return launch_cluster(k_gated_step<S, RATE, VEC>, (threads + 127) / 128, 128, 0, 1, L.stream, g);
+}
+
+#define MT_GATED_BY(f, ...)                                                                              \
+    (g.p.rate != nullptr ? (vec ? f<S, true, true>(__VA_ARGS__) : f<S, true, false>(__VA_ARGS__))        \
+                         : (vec ? f<S, false, true>(__VA_ARGS__) : f<S, false, false>(__VA_ARGS__)))
+#define MT_GATED_TYPE(name, T)                                                                           \
+    using S = T;                                                                                         \
+    cudaError_t gated_forward_##name(const GatedArgs &g, bool vec, const Launch &L) { return MT_GATED_BY(gated_forward, g, L); }   \
+    cudaError_t gated_backward_##name(const GatedArgs &g, float *part, bool vec, const Launch &L) { return MT_GATED_BY(gated_backward, g, part, L); } \
+    cudaError_t gated_single_##name(const GatedArgs &g, bool vec, const Launch &L) { return MT_GATED_BY(gated_single, g, L); }
+
+#define MT_GATED_DECL(name)                                                                  \
+    cudaError_t gated_forward_##name(const GatedArgs &g, bool vec, const Launch &L);         \
+    cudaError_t gated_backward_##name(const GatedArgs &g, float *part, bool vec, const Launch &L); \
+    cudaError_t gated_single_##name(const GatedArgs &g, bool vec, const Launch &L);
+MT_GATED_DECL(f32)
+MT_GATED_DECL(bf16)
+MT_GATED_DECL(f16)
+#undef MT_GATED_DECL
 
 }  // namespace mt

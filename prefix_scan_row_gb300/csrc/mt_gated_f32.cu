@@ -1,0 +1,6 @@
+// mt_gated_f32.cu -- the gated scan's kernels for f32 activations.
+#include "mt_gated.cuh"
+
+namespace mt {
+MT_GATED_TYPE(f32, float)
+}  // namespace mt

@@ -43,7 +43,8 @@ cudaError_t ssm_grad_launch(const mt_ssm_args &a, const Launch &L);
 cudaError_t ssm_step_launch(const mt_ssm_args &a, const Launch &L);
 
 // ---- gated scan (mt_gated*.cu) ---------------------------------------------------
-constexpr int kGatedTile = 64;  // tokens per checkpoint
+constexpr int kGatedTile = 32;  // tokens per checkpoint
+constexpr int64_t kGatedMost = INT32_MAX - 65536;  // tokens of a sequence: they are counted in 32 bits
 int64_t gated_scratch_slots(int64_t batch, int64_t len, int64_t dim);
 cudaError_t gated_launch(const mt_gated_args &a, const Launch &L);
 cudaError_t gated_step_launch(const mt_gated_args &a, const Launch &L);

@@ -107,7 +107,7 @@ int ssm_check(const mt_ssm_args &a, bool tokens) {
 
 int gated_check(const mt_gated_args &a, bool tokens) {
     const int64_t len = tokens ? a.len : 1;
-    if (a.batch < 0 || len < 0 || a.dim < 0 || a.nslots < 0)
+    if (a.batch < 0 || len < 0 || len > kGatedMost || a.dim < 0 || a.nslots < 0)
         return MT_ERR_ARG;
     const int s = act_size(a.dtype);
     if (s == 0)
@@ -357,13 +357,13 @@ extern "C" int mt_selective_scan_grad(const mt_ssm_args *args, void *stream) {
 }
 
 extern "C" int64_t mt_gated_scan_scratch_slots(int64_t batch, int64_t len, int64_t dim) {
-    if (batch < 0 || len < 0 || dim < 0 || product({batch, len, dim, 16}) < 0 || product({batch, dim, 256}) < 0)
+    if (batch < 0 || len < 0 || len > kGatedMost || dim < 0 || product({batch, len, dim, 16}) < 0 || product({batch, dim, 256}) < 0)
         return -1;
     return gated_scratch_slots(batch, len, dim);
 }
 
 extern "C" int64_t mt_gated_scan_checkpoint_slots(int64_t batch, int64_t len, int64_t dim) {
-    if (batch < 0 || len < 0 || dim < 0 || product({batch, len, dim, 16}) < 0)
+    if (batch < 0 || len < 0 || len > kGatedMost || dim < 0 || product({batch, len, dim, 16}) < 0)
         return -1;
     return (batch * ((len + kGatedTile - 1) / kGatedTile) * dim + 1) / 2;
 }

@@ -8,7 +8,7 @@ kernel groups three factors or terms otherwise, or joins spans of tokens), and t
   good to 2^-22; a reciprocal to 2^-23. So sigma(r) = 1 / (1 + exp(-|r|)) or exp(-|r|) / (1 + exp(-|r|)) and
   1 - sigma(r) are each good to ((2 |r| + 8) U + 2^-21) of themselves (8 U for the sum, the products around
   the reciprocal, and a reciprocal shared by three gates; 2^-21 for the exponential, the reciprocal, and the other gates').
-* 1 - exp(-u) below u = 1/2 by its series: 4 U of itself; above, from exp(-u), good to (2 u + 2) U + 2^-22 of
+* 1 - exp(-u) below u = 1/4 by its series: 4 U of itself (one for the terms left out); above, from exp(-u), good to (2 u + 2) U + 2^-22 of
   itself. An error of u moves exp(-u) by u times its relative error, 1 - exp(-u) by at most that.
 * 1 / sqrt(q): 2^-22, and half of q's error.
 """
@@ -77,7 +77,7 @@ class GatedCase:
         else:
             u = Ball(self.rate) * s
             a, d = torch.exp(-u.v), -torch.expm1(-u.v)
-            low, high = u.v < 0.51, u.v > 0.49
+            low, high = u.v < 0.26, u.v > 0.24
             far = a * ((2 * u.v + 2) * U + 2.0 ** -22)
             ea = a * u.e + torch.where(low, 4 * U * d + U, 0.0) + torch.where(high, far, 0.0)
             rel = torch.where(u.v > 0, u.e / u.v.clamp(min=1e-300), torch.zeros((), dtype=F64))
