@@ -667,7 +667,7 @@ typedef struct {
  * of one beam by their logits; they are rounded once, at the store.
  *
  * Logits: NaN counts as -inf (a token that may not come next), +inf as the
- * largest finite f32. A beam whose logits are all -inf, or whose prior is -inf or
+ * largest finite value of their type. A beam whose logits are all -inf, or whose prior is -inf or
  * NaN, has no continuation: all its scores are -inf, and only fill places that
  * no others take. +inf as a prior counts as the largest finite f32.
  * A finished beam has one continuation, (k, eos), with the beam's prior as its score; its logits

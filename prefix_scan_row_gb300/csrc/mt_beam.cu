@@ -14,20 +14,23 @@ namespace mt {
 namespace {
 
 constexpr int kBeamThreads = 256;
-constexpr int64_t kBeamChunk = 8192;  // logits of a CTA
+constexpr int kBeamWarps = kBeamThreads / 32;
+constexpr int kBeamGroup = 4;                              // lanes whose logits share one maximum
+constexpr int kBeamGroups = kBeamThreads / kBeamGroup;     // of a CTA
+constexpr int kBeamKept = 1024;                            // logits that may reach the threshold
 
-// Logits as unsigned numbers in the order of their values; NaN as -inf, +inf as the largest finite value, -0 as 0.
-__device__ __forceinline__ float tidy(float x) {
-    x = x == x ? x : Lim<float>::lo();
-    return fminf(x, 3.402823466e38f) + 0.0f;
-}
+// Values as unsigned numbers in their order, -0 below 0; not for NaN, whose sign is anything.
 __device__ __forceinline__ uint32_t order_of(float x) {
     const uint32_t u = __float_as_uint(x);
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 __device__ __forceinline__ float value_of(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k); }
-// Larger values first, of equal ones the lower token.
-__device__ __forceinline__ uint64_t key_of(float x, uint32_t token) { return (uint64_t)order_of(x) << 32 | (uint32_t)~token; }
+constexpr uint32_t kOrderLow = 0x007fffffu;   // of -inf
+constexpr uint32_t kOrderHigh = 0xff800000u;  // of +inf
+// NaN as -inf, +inf as the largest finite value.
+__device__ __forceinline__ float tidy(float x, float most) { return x == x ? fminf(x, most) : Lim<float>::lo(); }
+// Larger values first, of equal ones the lower token; 0 and -0 are equal.
+__device__ __forceinline__ uint64_t key_of(float x, uint32_t token) { return (uint64_t)order_of(x + 0.0f) << 32 | (uint32_t)~token; }
 
 __device__ __forceinline__ uint32_t redux_max(uint32_t v) { return __reduce_max_sync(kFull, v); }
 // The largest of a warp's keys.
@@ -37,63 +40,281 @@ __device__ __forceinline__ uint64_t warp_max(uint64_t key) {
     return (uint64_t)hi << 32 | lo;
 }
 
-// A chunk's place in the scratch: sum and largest value, then beams_out keys.
+// A 16-byte vector of logits.
+template <class S> struct Logits;
+template <> struct Logits<float> {
+    static constexpr int E = 4;
+    static __device__ __forceinline__ float most() { return 3.402823466e38f; }
+    static __device__ __forceinline__ uint4 none() { return make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u); }
+    static __device__ __forceinline__ float larger(float m, float x) {
+        asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(x));
+        return m;
+    }
+    using Most = float;
+    static __device__ __forceinline__ Most low() { return Lim<float>::lo(); }
+    static __device__ __forceinline__ Most max_of(Most m, const uint4 &w) {
+        return larger(larger(larger(larger(m, __uint_as_float(w.x)), __uint_as_float(w.y)), __uint_as_float(w.z)), __uint_as_float(w.w));
+    }
+    static __device__ __forceinline__ float widen(Most m) { return m; }
+};
+template <class S, uint32_t LOW, uint32_t HIGH> struct LogitsOf16 {
+    static constexpr int E = 8;
+    static __device__ __forceinline__ float most() {
+        float a, b;
+        Codec<S>::two(HIGH, a, b);
+        return a;
+    }
+    static __device__ __forceinline__ uint4 none() { return make_uint4(LOW, LOW, LOW, LOW); }
+    using Most = uint32_t;  // two maxima
+    static __device__ __forceinline__ Most low() { return LOW; }
+    static __device__ __forceinline__ uint32_t larger(uint32_t m, uint32_t x);
+    static __device__ __forceinline__ Most max_of(Most m, const uint4 &w) { return larger(larger(m, larger(w.x, w.y)), larger(w.z, w.w)); }
+    static __device__ __forceinline__ float widen(Most m) {
+        float a, b;
+        Codec<S>::two(m, a, b);
+        return Logits<float>::larger(a, b);
+    }
+};
+template <> __device__ __forceinline__ uint32_t LogitsOf16<__nv_bfloat16, 0xff80ff80u, 0x7f7f7f7fu>::larger(uint32_t m, uint32_t x) {
+    asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(x));
+    return m;
+}
+template <> __device__ __forceinline__ uint32_t LogitsOf16<__half, 0xfc00fc00u, 0x7bff7bffu>::larger(uint32_t m, uint32_t x) {
+    asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(m) : "r"(x));
+    return m;
+}
+template <> struct Logits<__nv_bfloat16> : LogitsOf16<__nv_bfloat16, 0xff80ff80u, 0x7f7f7f7fu> {};
+template <> struct Logits<__half> : LogitsOf16<__half, 0xfc00fc00u, 0x7bff7bffu> {};
+
+// A chunk's place in the scratch: sum (in units of 2^-40) and largest value, then beams_out keys, 0 for none.
 struct BeamPlan {
+    int per_thread;  // logits of a thread: 64 or 16
     int64_t chunks;  // of a beam's logits
     int64_t slots;   // of a chunk
 };
-BeamPlan beam_plan(int64_t beams_out, int64_t vocab) { return {(vocab + kBeamChunk - 1) / kBeamChunk, beams_out + 2}; }
+// A CTA's chunk: large, so that what follows the reading costs little beside it, where there are many CTAs all the same.
+BeamPlan beam_plan(int64_t rows, int64_t beams_out, int64_t vocab) {
+    BeamPlan p;
+    auto chunks = [&](int per_thread) { return (vocab + per_thread * kBeamThreads - 1) / (per_thread * kBeamThreads); };
+    p.per_thread = rows * chunks(64) >= 2 * 152 ? 64 : 16;
+    p.chunks = chunks(p.per_thread);
+    p.slots = beams_out + 2;
+    return p;
+}
 
-template <class S> __global__ void __launch_bounds__(kBeamThreads) k_beam_chunk(mt_beam_args a, BeamPlan plan) {
-    __shared__ uint64_t best[kBeamThreads / 32];
-    __shared__ double part[kBeamThreads / 32];
+// Rows that are not made of aligned vectors: a chunk's n logits to the same places of shared memory, from the 32-bit words
+// that they touch. Which thread has which token does not depend on a row's address, so that equal rows have equal sums.
+template <class S, int PER> __device__ __forceinline__ void stage_words(uint32_t *to, const S *x, int n) {
+    constexpr int kWords = PER * kBeamThreads * (int)sizeof(S) / 4;
+    const uint32_t low = Logits<S>::none().x;
+    if constexpr (sizeof(S) == 4) {
+        const uint32_t at = (uint32_t)__cvta_generic_to_shared(to);
+        for (int i = threadIdx.x; i < kWords; i += kBeamThreads) {
+            if (i < n)
+                cp_async_zfill<4>(at + i * 4, x + i, true);
+            else
+                to[i] = low;
+        }
+        cp_async_commit();
+        cp_async_wait<0>();
+    } else {
+        const bool odd = ((uintptr_t)x & 2) != 0;
+        const uint32_t *words = reinterpret_cast<const uint32_t *>((uintptr_t)x & ~(uintptr_t)3);
+#pragma unroll 8
+        for (int i = threadIdx.x; i < kWords; i += kBeamThreads) {
+            const uint32_t w0 = 2 * i < n ? words[i] : low;
+            const uint32_t w1 = odd && 2 * i + 1 < n ? words[i + 1] : low;
+            uint32_t w = odd ? __funnelshift_r(w0, w1, 16) : w0;
+            if (2 * i + 1 >= n)
+                w = (w & 0xffffu) | (low & 0xffff0000u);
+            to[i] = 2 * i < n ? w : low;
+        }
+    }
+    __syncthreads();
+}
+
+// A thread's logits stay in its own places of shared memory, where they are copied to and read from three times: for
+// their maxima, for the sum, and (few threads) for those that reach the threshold. VEC: rows are made of aligned vectors.
+template <class S, int PER, bool VEC> __global__ void __launch_bounds__(kBeamThreads) k_beam_chunk(const __grid_constant__ mt_beam_args a, BeamPlan plan) {
+    using L = Logits<S>;
+    constexpr int E = L::E, V = PER / E;  // values of a vector, vectors of a thread
+    __shared__ __align__(16) uint32_t group_max[kBeamGroups];
+    __shared__ uint32_t threshold, top_order, count;
+    __shared__ uint32_t sum_low[kBeamWarps], sum_high[kBeamWarps];
+    __shared__ uint64_t kept[kBeamKept];
+    extern __shared__ __align__(16) uint4 staged[];
     pdl_prologue();
-    const int64_t row = blockIdx.x / plan.chunks, chunk = blockIdx.x - row * plan.chunks, b = row / a.beams, k = row - b * a.beams;
+    const int64_t row = blockIdx.x / plan.chunks, chunk = blockIdx.x - row * plan.chunks, b = row / a.beams, beam = row - b * a.beams;
     if (a.finished != nullptr && a.finished[row] != 0)
         return;
-    const int64_t first = chunk * kBeamChunk;
-    const int n = (int)(a.vocab - first < kBeamChunk ? a.vocab - first : kBeamChunk);
-    const S *x = static_cast<const S *>(a.logits) + b * a.logits_batch + k * a.logits_beam + first;
-    uint64_t *mine = static_cast<uint64_t *>(a.scratch) + (row * plan.chunks + chunk) * plan.slots;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    uint64_t last = ~0ull;
-    float top = 0.0f;
-    for (int j = 0; j < a.beams_out && j < n; ++j) {
-        uint64_t m = 0;
-        for (int t = threadIdx.x; t < n; t += kBeamThreads) {
-            const uint64_t key = key_of(tidy(Codec<S>::load1(x + t)), (uint32_t)(first + t));
-            if (key < last && key > m)
-                m = key;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, K = (int)a.beams_out;
+    const S *x = static_cast<const S *>(a.logits) + b * a.logits_batch + beam * a.logits_beam;
+    // vector j of the thread: tokens first + j * 2048 (or 1024) and on
+    const int64_t first = chunk * (kBeamThreads * PER) + threadIdx.x * E;
+    uint4 *own = staged + threadIdx.x;  // vector j: own[j * kBeamThreads]
+    if constexpr (VEC) {
+        const uint32_t own_at = (uint32_t)__cvta_generic_to_shared(own);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int64_t at = first + j * (kBeamThreads * E);
+            if (at < a.vocab)
+                cp_async_zfill<16>(own_at + j * (kBeamThreads * 16), x + at, true);
+            else
+                own[j * kBeamThreads] = L::none();
         }
-        m = warp_max(m);
-        if (lane == 0)
-            best[warp] = m;
-        __syncthreads();
-        last = best[0];
-        for (int w = 1; w < kBeamThreads / 32; ++w)
-            last = best[w] > last ? best[w] : last;
-        __syncthreads();
-        if (j == 0)
-            top = value_of((uint32_t)(last >> 32));
-        if (threadIdx.x == 0)
-            mine[2 + j] = last;
+        cp_async_commit();
+        cp_async_wait<0>();
+    } else {
+        const int64_t begin = chunk * (kBeamThreads * PER), left = a.vocab - begin;
+        stage_words<S, PER>(reinterpret_cast<uint32_t *>(staged), x + begin, left < kBeamThreads * PER ? (int)left : kBeamThreads * PER);
     }
-    for (int j = n + threadIdx.x; j < a.beams_out; j += kBeamThreads)
-        mine[2 + j] = 0;
-    double sum = 0.0;
-    if (top != Lim<float>::lo())
-        for (int t = threadIdx.x; t < n; t += kBeamThreads)
-            sum += (double)ex2f(kLog2e * (tidy(Codec<S>::load1(x + t)) - top));
-    for (int o = 16; o > 0; o /= 2)
-        sum += __shfl_xor_sync(kFull, sum, o);
-    if (lane == 0)
-        part[warp] = sum;
+    uint32_t mine;  // the thread's largest value
+    for (bool again = false;; again = true) {
+        typename L::Most most = L::low();
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            most = L::max_of(most, own[j * kBeamThreads]);
+        const float widest = L::widen(most);
+        mine = widest == widest ? order_of(widest + 0.0f) : ~0u;
+        uint32_t m = mine;
+        m = max(m, __shfl_xor_sync(kFull, m, 1));
+        m = max(m, __shfl_xor_sync(kFull, m, 2));
+        if (lane % kBeamGroup == 0)
+            group_max[threadIdx.x / kBeamGroup] = m;
+        if (threadIdx.x == 0)
+            count = 0;
+        __syncthreads();
+        // the beams_out-th largest of the groups' maxima, which so many logits reach: four lanes count what is before one
+        {
+            const int g = threadIdx.x / kBeamGroup, part = lane % kBeamGroup * (kBeamGroups / kBeamGroup);
+            int before = 0;
+#pragma unroll
+            for (int q = 0; q < kBeamGroups / kBeamGroup; q += 4) {
+                const uint4 o = *reinterpret_cast<const uint4 *>(&group_max[part + q]);
+                before += o.x > m || (o.x == m && part + q < g);
+                before += o.y > m || (o.y == m && part + q + 1 < g);
+                before += o.z > m || (o.z == m && part + q + 2 < g);
+                before += o.w > m || (o.w == m && part + q + 3 < g);
+            }
+            before += __shfl_xor_sync(kFull, before, 1);
+            before += __shfl_xor_sync(kFull, before, 2);
+            if (lane % kBeamGroup == 0 && before == K - 1)
+                threshold = m;
+            if (lane % kBeamGroup == 0 && before == 0)
+                top_order = m;
+        }
+        __syncthreads();
+        if (again || top_order < kOrderHigh)
+            break;
+        // an infinity or NaN among them: made finite, and once more
+#pragma unroll 1
+        for (int j = 0; j < V; ++j) {
+            float f[E];
+            Codec<S>::unpack(own[j * kBeamThreads], f);
+#pragma unroll
+            for (int q = 0; q < E; ++q)
+                f[q] = tidy(f[q], L::most());
+            own[j * kBeamThreads] = Codec<S>::pack(f);
+        }
+    }
+    uint64_t *out = static_cast<uint64_t *>(a.scratch) + (row * plan.chunks + chunk) * plan.slots;
+    const uint32_t top = top_order;
+    if (top <= kOrderLow) {  // nothing here may come next
+        if (threadIdx.x < plan.slots)
+            out[threadIdx.x] = threadIdx.x == 1 ? __float_as_uint(Lim<float>::lo()) : 0;
+        return;
+    }
+    // the logits that reach the threshold
+    const uint32_t least = threshold > kOrderLow ? threshold : kOrderLow + 1;
+    if (mine >= least) {
+#pragma unroll 1
+        for (int j = 0; j < V; ++j) {
+            float f[E];
+            Codec<S>::unpack(own[j * kBeamThreads], f);
+#pragma unroll
+            for (int q = 0; q < E; ++q) {
+                const uint64_t key = key_of(f[q], (uint32_t)(first + j * (kBeamThreads * E) + q));
+                if ((uint32_t)(key >> 32) >= least) {
+                    const uint32_t n = atomicAdd(&count, 1u);
+                    if (n < kBeamKept)
+                        kept[n] = key;
+                }
+            }
+        }
+    }
+    // sum of exp(x - top): f32 in the thread, then whole numbers, whose sum has no order
+    {
+        const f32x2 less = both(-value_of(top));
+        f32x2 s0 = 0ull, s1 = 0ull;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            float f[E];
+            Codec<S>::unpack(own[j * kBeamThreads], f);
+#pragma unroll
+            for (int q = 0; q < E; q += 4) {
+                s0 = add2f(s0, ex2_2f(mul2f(add2f(pack2f(f[q], f[q + 1]), less), both(kLog2e))));
+                s1 = add2f(s1, ex2_2f(mul2f(add2f(pack2f(f[q + 2], f[q + 3]), less), both(kLog2e))));
+            }
+        }
+        float p, r;
+        unpack2f(add2f(s0, s1), p, r);
+        const float s = p + r;
+        const uint32_t high = (uint32_t)(s * 0x1p20f), low = (uint32_t)((s * 0x1p20f - (float)high) * 0x1p20f);
+        const uint32_t low_all = __reduce_add_sync(kFull, low), high_all = __reduce_add_sync(kFull, high);
+        if (lane == 0) {
+            sum_low[warp] = low_all;
+            sum_high[warp] = high_all;
+        }
+    }
     __syncthreads();
+    const int n = (int)count;
+    if (n <= kBeamKept) {
+        for (int t = threadIdx.x; t < n; t += kBeamThreads) {
+            const uint64_t key = kept[t];
+            int before = 0;
+            for (int q = 0; q < n; ++q)
+                before += kept[q] > key;
+            if (before < K)
+                out[2 + before] = key;
+        }
+        for (int t = n + threadIdx.x; t < K; t += kBeamThreads)
+            out[2 + t] = 0;
+    } else {
+        // more equal values than there is place for: the largest key below the last one, beams_out times
+        uint64_t last = ~0ull;
+        for (int t = 0; t < K; ++t) {
+            uint64_t m = 0;
+#pragma unroll 1
+            for (int j = 0; j < V; ++j) {
+                float f[E];
+                Codec<S>::unpack(own[j * kBeamThreads], f);
+#pragma unroll
+                for (int q = 0; q < E; ++q) {
+                    const uint64_t key = key_of(f[q], (uint32_t)(first + j * (kBeamThreads * E) + q));
+                    if ((uint32_t)(key >> 32) >= least && key < last && key > m)
+                        m = key;
+                }
+            }
+            m = warp_max(m);
+            __syncthreads();
+            if (lane == 0)
+                kept[warp] = m;
+            __syncthreads();
+            last = kept[0];
+#pragma unroll
+            for (int q = 1; q < kBeamWarps; ++q)
+                last = kept[q] > last ? kept[q] : last;
+            if (threadIdx.x == 0)
+                out[2 + t] = last;
+        }
+    }
     if (threadIdx.x == 0) {
-        for (int w = 1; w < kBeamThreads / 32; ++w)
-            sum += part[w];
-        mine[0] = (uint64_t)__double_as_longlong(sum);
-        mine[1] = __float_as_uint(top);
+        uint64_t sum = 0;
+#pragma unroll
+        for (int q = 0; q < kBeamWarps; ++q)
+            sum += (uint64_t)sum_low[q] + ((uint64_t)sum_high[q] << 20);
+        out[0] = sum;
+        out[1] = __float_as_uint(value_of(top));
     }
 }
 
@@ -104,60 +325,72 @@ __device__ __forceinline__ uint64_t order_of(double x) {
 }
 __device__ __forceinline__ double score_of(uint64_t k) { return __longlong_as_double((long long)(k >> 63 ? k & ~(1ull << 63) : ~k)); }
 
-__global__ void __launch_bounds__(kBeamThreads) k_beam_join(mt_beam_args a, BeamPlan plan) {
+// The 32 largest of two lists that a warp holds in falling order, a key a lane.
+__device__ __forceinline__ uint64_t join_lists(uint64_t p, uint64_t q, int lane) {
+    const uint64_t o = __shfl_sync(kFull, q, 31 - lane);
+    p = o > p ? o : p;  // rising, then falling: sorted by halves
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) {
+        const uint64_t r = __shfl_xor_sync(kFull, p, d);
+        p = ((lane & d) == 0) == (r > p) ? r : p;
+    }
+    return p;
+}
+
+__global__ void __launch_bounds__(kBeamThreads) k_beam_join(const __grid_constant__ mt_beam_args a, BeamPlan plan) {
     __shared__ uint64_t score[kBeamsMost][kBeamsMost];  // of each beam's first continuations, in order
     __shared__ int32_t token[kBeamsMost][kBeamsMost];
     pdl_prologue();
     const int64_t b = blockIdx.x;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int K = (int)a.beams_out, n = (int)(a.vocab < K ? a.vocab : K);  // continuations of a beam that can matter
-    for (int k = warp; k < a.beams; k += kBeamThreads / 32) {
+    for (int k = warp; k < a.beams; k += kBeamWarps) {
         const int64_t row = b * a.beams + k;
-        float prior = a.prior != nullptr ? a.prior[row] : 0.0f;
-        prior = tidy(prior);
+        const float prior = a.prior != nullptr ? tidy(a.prior[row], 3.402823466e38f) : 0.0f;
         const bool done = a.finished != nullptr && a.finished[row] != 0;
         const uint64_t *mine = static_cast<const uint64_t *>(a.scratch) + row * plan.chunks * plan.slots;
         float top = Lim<float>::lo();
         double sum = 0.0;
-        if (!done) {
+        uint64_t key = 0;
+        if (!done && prior != Lim<float>::lo()) {
             for (int64_t c = lane; c < plan.chunks; c += 32)
                 top = fmaxf(top, __uint_as_float((uint32_t)mine[c * plan.slots + 1]));
             top = value_of(redux_max(order_of(top)));
-            for (int64_t c = lane; c < plan.chunks; c += 32) {
-                const float m = __uint_as_float((uint32_t)mine[c * plan.slots + 1]);
-                if (m != Lim<float>::lo())
-                    sum += __longlong_as_double((long long)mine[c * plan.slots]) * exp((double)m - (double)top);
-            }
-            for (int o = 16; o > 0; o /= 2)
-                sum += __shfl_xor_sync(kFull, sum, o);
-        }
-        if (done || prior == Lim<float>::lo() || top == Lim<float>::lo()) {
-            // no logits count: the end with the prior's score (done), and tokens in order that may not come next
-            if (lane < n) {
-                const bool end = done && lane == 0;
-                token[k][lane] = !done ? lane : end ? (int)a.eos : lane - 1 < a.eos ? lane - 1 : lane;
-                score[k][lane] = order_of(end ? (double)prior : (double)Lim<float>::lo());
-            }
-        } else {
-            const double less = log(sum);
-            uint64_t last = ~0ull;
-            for (int j = 0; j < n; ++j) {
-                uint64_t m = 0;
-                for (int64_t c = lane; c < plan.chunks; c += 32)
-                    for (int q = 0; q < K; ++q) {
-                        const uint64_t key = mine[c * plan.slots + 2 + q];
-                        if (key < last) {
-                            m = key > m ? key : m;
-                            break;
-                        }
-                    }
-                last = warp_max(m);
-                if (lane == 0) {
-                    const double x = (double)value_of((uint32_t)(last >> 32)) - (double)top;
-                    token[k][j] = (int32_t)~(uint32_t)last;
-                    score[k][j] = order_of((double)prior + (x - less));
+            if (top != Lim<float>::lo()) {
+                for (int64_t c = lane; c < plan.chunks; c += 32) {
+                    const float m = __uint_as_float((uint32_t)mine[c * plan.slots + 1]);
+                    if (m != Lim<float>::lo())
+                        sum += (double)mine[c * plan.slots] * 0x1p-40 * exp((double)m - (double)top);
                 }
+                for (int o = 16; o > 0; o /= 2)
+                    sum += __shfl_xor_sync(kFull, sum, o);
+#pragma unroll 2
+                for (int64_t c = 0; c < plan.chunks; ++c)
+                    key = join_lists(key, lane < K ? mine[c * plan.slots + 2 + lane] : 0, lane);
             }
+        }
+        const int has = __popc(__ballot_sync(kFull, key != 0));  // logits that may come next, as far as they matter
+        int32_t tok = (int32_t)~(uint32_t)key;
+        double s = Lim<double>::lo();
+        if (key != 0)
+            s = (double)prior + ((double)value_of((uint32_t)(key >> 32)) - (double)top - log(sum));
+        if (done && prior != Lim<float>::lo()) {  // the end with the beam's score, then the other tokens in order
+            tok = lane == 0 ? (int)a.eos : lane - 1 < a.eos ? lane - 1 : lane;
+            if (lane == 0)
+                s = (double)prior;
+        } else if (has < n) {
+            // all that may come next is in the list: behind it the tokens that may not, in order
+            int next = 0;
+            for (int j = has; j < n; ++j, ++next) {
+                while (__any_sync(kFull, lane < has && tok == next))
+                    ++next;
+                if (lane == j)
+                    tok = next;
+            }
+        }
+        if (lane < n) {
+            token[k][lane] = tok;
+            score[k][lane] = order_of(s);
         }
     }
     __syncthreads();
@@ -202,8 +435,10 @@ __global__ void __launch_bounds__(kBeamThreads) k_beam_join(mt_beam_args a, Beam
     const uint32_t moving = __ballot_sync(kFull, lane < group && !stays);
     const int32_t old = __shfl_sync(kFull, slot, parent);
     // the lanes that move, and those behind the beams, take the free slots in order
-    const int rank = __popc(moving & ((1u << lane) - 1));
-    const int32_t fresh = __shfl_sync(kFull, slot, __fns(free, 0, rank + 1) & 31);
+    if (free >> lane & 1u)
+        token[0][__popc(free & ((1u << lane) - 1))] = slot;
+    __syncwarp();
+    const int32_t fresh = token[0][__popc(moving & ((1u << lane) - 1)) & 31];
     if (lane < group)
         a.slots[b * group + lane] = stays ? old : fresh;
     if (out) {
@@ -212,13 +447,24 @@ __global__ void __launch_bounds__(kBeamThreads) k_beam_join(mt_beam_args a, Beam
     }
 }
 
+template <class S, int PER, bool VEC> cudaError_t launch_chunks(const mt_beam_args &a, const BeamPlan &plan, unsigned blocks, const Launch &L) {
+    static PerDevice ready;
+    constexpr int smem = kBeamThreads * PER * (int)sizeof(S);
+    const cudaError_t e = allow_shared(k_beam_chunk<S, PER, VEC>, smem, ready);
+    if (e != cudaSuccess)
+        return e;
+    note_launch();
+    return launch_pdl(k_beam_chunk<S, PER, VEC>, blocks, kBeamThreads, smem, L.stream, a, plan);
+}
 template <class S> cudaError_t launch(const mt_beam_args &a, const Launch &L) {
-    const BeamPlan plan = beam_plan(a.beams_out, a.vocab);
-    const int64_t blocks = a.batch * a.beams * plan.chunks;
+    const BeamPlan plan = beam_plan(a.batch * a.beams, a.beams_out, a.vocab);
+    const int64_t blocks = a.batch * a.beams * plan.chunks, vector = Logits<S>::E;
     if (blocks > INT32_MAX)
         return cudaErrorInvalidValue;
-    note_launch();
-    const cudaError_t e = launch_pdl(k_beam_chunk<S>, (unsigned)blocks, kBeamThreads, 0, L.stream, a, plan);
+    const bool vec = (uintptr_t)a.logits % 16 == 0 && a.vocab % vector == 0 && a.logits_batch % vector == 0 && a.logits_beam % vector == 0;
+    const unsigned n = (unsigned)blocks;
+    const cudaError_t e = plan.per_thread == 64 ? (vec ? launch_chunks<S, 64, true>(a, plan, n, L) : launch_chunks<S, 64, false>(a, plan, n, L))
+                                                : (vec ? launch_chunks<S, 16, true>(a, plan, n, L) : launch_chunks<S, 16, false>(a, plan, n, L));
     if (e != cudaSuccess)
         return e;
     note_launch();
@@ -228,7 +474,7 @@ template <class S> cudaError_t launch(const mt_beam_args &a, const Launch &L) {
 }  // namespace
 
 int64_t beam_scratch_slots(int64_t batch, int64_t beams, int64_t beams_out, int64_t vocab) {
-    const BeamPlan plan = beam_plan(beams_out, vocab);
+    const BeamPlan plan = beam_plan(batch * beams, beams_out, vocab);
     return batch * beams * plan.chunks * plan.slots;
 }
 

@@ -733,18 +733,6 @@ static cudaError_t launch_cluster(void (*kernel)(KArgs...), int64_t grid, unsign
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
-// The dynamic shared memory of a kernel is allowed once per device.
-template <class F> static cudaError_t allow_shared(F kernel, int bytes, PerDevice &done) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess || dev >= kMaxDevices || done.get(dev) != 0)
-        return e;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess)
-        done.set(dev, 1);
-    return e;
-}
-
 template <class S, bool RATE, bool VEC, bool IN, bool Z> static cudaError_t gated_forward_of(const GatedArgs &g, const Launch &L) {
     static PerDevice ready;
     constexpr int smem = FwdShared<S, VEC>::kBytes;

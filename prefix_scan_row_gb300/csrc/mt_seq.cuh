@@ -29,6 +29,18 @@ static cudaError_t launch_pdl_2d(void (*kernel)(KArgs...), dim3 grid, unsigned b
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
+// The dynamic shared memory of a kernel is allowed once per device.
+template <class F> static cudaError_t allow_shared(F kernel, int bytes, PerDevice &done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || dev >= kMaxDevices || done.get(dev) != 0)
+        return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess)
+        done.set(dev, 1);
+    return e;
+}
+
 // ---- four neighbouring values -------------------------------------------------
 // as one vector access when `vec` (then p is aligned to four values) and all four
 // are `live`, otherwise value by value; those that do not exist load as 0.

@@ -163,9 +163,9 @@ def beam_select(logits, k_out, prior=None, finished=None, eos=-1, slots=None):
     with slots their new row and the copies."""
     b, k, v = logits.shape
     x = logits.detach().cpu().to(F64)
-    x = torch.where(x.isnan(), float("-inf"), x).clamp(max=3.4028234663852886e38)
+    x = torch.where(x.isnan(), float("-inf"), x).clamp(max=torch.finfo(logits.dtype).max)
     prior = torch.zeros(b, k, dtype=F64) if prior is None else prior.cpu().to(F64)
-    prior = torch.where(prior.isnan(), float("-inf"), prior).clamp(max=3.4028234663852886e38)
+    prior = torch.where(prior.isnan(), float("-inf"), prior).clamp(max=torch.finfo(torch.float32).max)
     ended = torch.zeros(b, k, dtype=torch.bool) if finished is None else finished.cpu() != 0
     r = dict(tokens=[], parents=[], scores=[], finished=[], slots=[], src=[], dst=[])
     for n in range(b):
