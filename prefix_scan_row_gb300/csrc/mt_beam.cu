@@ -133,8 +133,37 @@ template <class S, int PER> __device__ __forceinline__ void stage_words(uint32_t
     __syncthreads();
 }
 
+// Thread t's logits from `least` on, as keys; their number goes on beyond the places that there are.
+template <class S, int PER>
+__device__ __forceinline__ void keep_reached(const uint4 *staged, int t, int lane, uint32_t begin, uint32_t least, uint64_t *kept, uint32_t &count) {
+    constexpr int E = Logits<S>::E, kWords = PER / E * 4;  // 32-bit words of a thread
+#pragma unroll
+    for (int i = 0; i < kWords; i += 32) {
+        const int word = i + lane;
+        if (word < kWords) {
+            const int j = word / 4, q = word % 4 * (E / 4);
+            const uint32_t w = reinterpret_cast<const uint32_t *>(staged + j * kBeamThreads + t)[word % 4];
+            float f[2];
+            if constexpr (E == 8)
+                Codec<S>::two(w, f[0], f[1]);
+            else
+                f[0] = __uint_as_float(w);
+            const uint32_t token = begin + (uint32_t)(j * (kBeamThreads * E) + t * E + q);
+#pragma unroll
+            for (int k = 0; k < E / 4; ++k) {
+                const uint64_t key = key_of(f[k], token + k);
+                if ((uint32_t)(key >> 32) >= least) {
+                    const uint32_t n = atomicAdd(&count, 1u);
+                    if (n < kBeamKept)
+                        kept[n] = key;
+                }
+            }
+        }
+    }
+}
+
 // A thread's logits stay in its own places of shared memory, where they are copied to and read from three times: for
-// their maxima, for the sum, and (few threads) for those that reach the threshold. VEC: rows are made of aligned vectors.
+// their maxima, for the sum, and (of few threads) for those that reach the threshold. VEC: rows are made of aligned vectors.
 template <class S, int PER, bool VEC> __global__ void __launch_bounds__(kBeamThreads) k_beam_chunk(const __grid_constant__ mt_beam_args a, BeamPlan plan) {
     using L = Logits<S>;
     constexpr int E = L::E, V = PER / E;  // values of a vector, vectors of a thread
@@ -144,7 +173,8 @@ template <class S, int PER, bool VEC> __global__ void __launch_bounds__(kBeamThr
     __shared__ uint64_t kept[kBeamKept];
     extern __shared__ __align__(16) uint4 staged[];
     pdl_prologue();
-    const int64_t row = blockIdx.x / plan.chunks, chunk = blockIdx.x - row * plan.chunks, b = row / a.beams, beam = row - b * a.beams;
+    const uint32_t chunks = (uint32_t)plan.chunks, beams = (uint32_t)a.beams;
+    const int64_t row = blockIdx.x / chunks, chunk = blockIdx.x % chunks, b = (uint32_t)row / beams, beam = (uint32_t)row % beams;
     if (a.finished != nullptr && a.finished[row] != 0)
         return;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, K = (int)a.beams_out;
@@ -164,6 +194,7 @@ template <class S, int PER, bool VEC> __global__ void __launch_bounds__(kBeamThr
         }
         cp_async_commit();
         cp_async_wait<0>();
+        __syncwarp();
     } else {
         const int64_t begin = chunk * (kBeamThreads * PER), left = a.vocab - begin;
         stage_words<S, PER>(reinterpret_cast<uint32_t *>(staged), x + begin, left < kBeamThreads * PER ? (int)left : kBeamThreads * PER);
@@ -224,24 +255,10 @@ template <class S, int PER, bool VEC> __global__ void __launch_bounds__(kBeamThr
             out[threadIdx.x] = threadIdx.x == 1 ? __float_as_uint(Lim<float>::lo()) : 0;
         return;
     }
-    // the logits that reach the threshold
+    // the logits that reach the threshold: few lanes have one, and the warp goes through each of theirs together
     const uint32_t least = threshold > kOrderLow ? threshold : kOrderLow + 1;
-    if (mine >= least) {
-#pragma unroll 1
-        for (int j = 0; j < V; ++j) {
-            float f[E];
-            Codec<S>::unpack(own[j * kBeamThreads], f);
-#pragma unroll
-            for (int q = 0; q < E; ++q) {
-                const uint64_t key = key_of(f[q], (uint32_t)(first + j * (kBeamThreads * E) + q));
-                if ((uint32_t)(key >> 32) >= least) {
-                    const uint32_t n = atomicAdd(&count, 1u);
-                    if (n < kBeamKept)
-                        kept[n] = key;
-                }
-            }
-        }
-    }
+    for (uint32_t lanes = __ballot_sync(kFull, mine >= least); lanes != 0; lanes &= lanes - 1)
+        keep_reached<S, PER>(staged, warp * 32 + __ffs(lanes) - 1, lane, (uint32_t)(chunk * (kBeamThreads * PER)), least, kept, count);
     // sum of exp(x - top): f32 in the thread, then whole numbers, whose sum has no order
     {
         const f32x2 less = both(-value_of(top));
@@ -267,7 +284,51 @@ template <class S, int PER, bool VEC> __global__ void __launch_bounds__(kBeamThr
         }
     }
     __syncthreads();
-    const int n = (int)count;
+    int n = (int)count;
+    if (n > kBeamKept) {
+        // More equal values than there is place for (a mask of a finite value, for instance): those above the threshold,
+        // and of those at it the first beams_out, vector after vector.
+        __syncthreads();
+        if (threadIdx.x == 0)
+            count = 0;
+        __syncthreads();
+        for (uint32_t lanes = __ballot_sync(kFull, mine > least); lanes != 0; lanes &= lanes - 1)
+            keep_reached<S, PER>(staged, warp * 32 + __ffs(lanes) - 1, lane, (uint32_t)(chunk * (kBeamThreads * PER)), least + 1, kept, count);
+        __syncthreads();
+        n = (int)count;  // places behind those take the equal ones
+        int had = 0;
+#pragma unroll 1
+        for (int j = 0; j < V && had < K && n + K <= kBeamKept; ++j) {
+            float f[E];
+            Codec<S>::unpack(own[j * kBeamThreads], f);
+            uint32_t equal = 0;
+#pragma unroll
+            for (int q = 0; q < E; ++q)
+                equal |= order_of(f[q] + 0.0f) == least ? 1u << q : 0u;
+            int before = __popc(equal), all = before;
+#pragma unroll
+            for (int d = 1; d < 32; d *= 2) {
+                const int o = __shfl_up_sync(kFull, before, d);
+                before += lane >= d ? o : 0;
+            }
+            if (lane == 31)
+                group_max[j % 2 * kBeamWarps + warp] = (uint32_t)before;
+            before += had - all;
+            __syncthreads();
+#pragma unroll
+            for (int q = 0; q < kBeamWarps; ++q) {
+                const int o = (int)group_max[j % 2 * kBeamWarps + q];
+                before += q < warp ? o : 0;
+                had += o;
+            }
+            for (; equal != 0 && before < K; equal &= equal - 1, ++before) {
+                const int q = __ffs(equal) - 1;
+                kept[n + before] = (uint64_t)least << 32 | (uint32_t)~(uint32_t)(first + j * (kBeamThreads * E) + q);
+            }
+        }
+        n = n + K <= kBeamKept ? n + (had < K ? had : K) : kBeamKept + 1;
+        __syncthreads();
+    }
     if (n <= kBeamKept) {
         for (int t = threadIdx.x; t < n; t += kBeamThreads) {
             const uint64_t key = kept[t];
@@ -280,7 +341,7 @@ template <class S, int PER, bool VEC> __global__ void __launch_bounds__(kBeamThr
         for (int t = n + threadIdx.x; t < K; t += kBeamThreads)
             out[2 + t] = 0;
     } else {
-        // more equal values than there is place for: the largest key below the last one, beams_out times
+        // too many in too few places: the largest key below the last one, beams_out times
         uint64_t last = ~0ull;
         for (int t = 0; t < K; ++t) {
             uint64_t m = 0;
@@ -337,36 +398,50 @@ __device__ __forceinline__ uint64_t join_lists(uint64_t p, uint64_t q, int lane)
     return p;
 }
 
-__global__ void __launch_bounds__(kBeamThreads) k_beam_join(const __grid_constant__ mt_beam_args a, BeamPlan plan) {
+// A warp a beam.
+constexpr int kJoinAhead = 8;  // lists on their way
+__global__ void __launch_bounds__(32 * kBeamsMost) k_beam_join(const __grid_constant__ mt_beam_args a, BeamPlan plan) {
     __shared__ uint64_t score[kBeamsMost][kBeamsMost];  // of each beam's first continuations, in order
     __shared__ int32_t token[kBeamsMost][kBeamsMost];
     pdl_prologue();
     const int64_t b = blockIdx.x;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, k = warp, chunks = (int)plan.chunks;
     const int K = (int)a.beams_out, n = (int)(a.vocab < K ? a.vocab : K);  // continuations of a beam that can matter
-    for (int k = warp; k < a.beams; k += kBeamWarps) {
+    {
         const int64_t row = b * a.beams + k;
+        const uint64_t *mine = static_cast<const uint64_t *>(a.scratch) + row * plan.chunks * plan.slots;
         const float prior = a.prior != nullptr ? tidy(a.prior[row], 3.402823466e38f) : 0.0f;
         const bool done = a.finished != nullptr && a.finished[row] != 0;
-        const uint64_t *mine = static_cast<const uint64_t *>(a.scratch) + row * plan.chunks * plan.slots;
         float top = Lim<float>::lo();
         double sum = 0.0;
         uint64_t key = 0;
         if (!done && prior != Lim<float>::lo()) {
-            for (int64_t c = lane; c < plan.chunks; c += 32)
+            uint64_t list[kJoinAhead];
+#pragma unroll
+            for (int q = 0; q < kJoinAhead; ++q)
+                list[q] = q < chunks && lane < K ? mine[q * plan.slots + 2 + lane] : 0;
+            for (int c = lane; c < chunks; c += 32)
                 top = fmaxf(top, __uint_as_float((uint32_t)mine[c * plan.slots + 1]));
             top = value_of(redux_max(order_of(top)));
             if (top != Lim<float>::lo()) {
-                for (int64_t c = lane; c < plan.chunks; c += 32) {
+                for (int c = lane; c < chunks; c += 32) {
                     const float m = __uint_as_float((uint32_t)mine[c * plan.slots + 1]);
                     if (m != Lim<float>::lo())
                         sum += (double)mine[c * plan.slots] * 0x1p-40 * exp((double)m - (double)top);
                 }
                 for (int o = 16; o > 0; o /= 2)
-                    sum += __shfl_xor_sync(kFull, sum, o);
-#pragma unroll 2
-                for (int64_t c = 0; c < plan.chunks; ++c)
-                    key = join_lists(key, lane < K ? mine[c * plan.slots + 2 + lane] : 0, lane);
+                    if (chunks > o)
+                        sum += __shfl_xor_sync(kFull, sum, o);
+                sum = __shfl_sync(kFull, sum, 0);
+                for (int c0 = 0; c0 < chunks; c0 += kJoinAhead) {
+#pragma unroll
+                    for (int q = 0; q < kJoinAhead; ++q)
+                        if (c0 + q < chunks) {
+                            key = c0 + q == 0 ? list[q] : join_lists(key, list[q], lane);
+                            const int c = c0 + q + kJoinAhead;
+                            list[q] = c < chunks && lane < K ? mine[c * plan.slots + 2 + lane] : 0;
+                        }
+                }
             }
         }
         const int has = __popc(__ballot_sync(kFull, key != 0));  // logits that may come next, as far as they matter
@@ -397,22 +472,22 @@ __global__ void __launch_bounds__(kBeamThreads) k_beam_join(const __grid_constan
     if (warp != 0)
         return;
     // beams side by side, each with its best continuation that is left; of equal scores the lowest beam's
-    int at = 0, parent = 0, tok = 0;
-    float best = 0.0f;
+    int at = 0, parent = 0, place = 0;
+    uint64_t best = 0;
     for (int j = 0; j < K; ++j) {
         const bool has = lane < a.beams && at < n;
         const uint64_t s = has ? score[lane][at] : 0ull;  // 0 is below every score's number
         const uint64_t m = warp_max(s);
         const int from = __ffs(__ballot_sync(kFull, has && s == m)) - 1;
+        const int its = __shfl_sync(kFull, at, from);
         if (lane == j) {
-            best = (float)score_of(m);
+            best = m;
             parent = from;
+            place = its;
         }
-        const int t = token[from][__shfl_sync(kFull, at, from)];
-        if (lane == j)
-            tok = t;
         at += lane == from;
     }
+    const int tok = token[parent][place];
     const bool out = lane < K;
     const int64_t to = b * K + lane;
     const bool done = a.finished != nullptr && out && a.finished[b * a.beams + parent] != 0;
@@ -422,7 +497,7 @@ __global__ void __launch_bounds__(kBeamThreads) k_beam_join(const __grid_constan
     if (out) {
         a.tokens[to] = tok;
         a.parents[to] = parent;
-        a.scores[to] = best;
+        a.scores[to] = (float)score_of(best);
         if (a.finished_out != nullptr)
             a.finished_out[to] = done || tok == a.eos;
     }
@@ -468,7 +543,7 @@ template <class S> cudaError_t launch(const mt_beam_args &a, const Launch &L) {
     if (e != cudaSuccess)
         return e;
     note_launch();
-    return launch_pdl(k_beam_join, (unsigned)a.batch, kBeamThreads, 0, L.stream, a, plan);
+    return launch_pdl(k_beam_join, (unsigned)a.batch, (unsigned)(32 * a.beams), 0, L.stream, a, plan);
 }
 
 }  // namespace
