@@ -15,9 +15,7 @@ namespace {
 
 constexpr int kBeamThreads = 256;
 constexpr int kBeamWarps = kBeamThreads / 32;
-constexpr int kBeamGroup = 4;                              // lanes whose logits share one maximum
-constexpr int kBeamGroups = kBeamThreads / kBeamGroup;     // of a CTA
-constexpr int kBeamKept = 1024;                            // logits that may reach the threshold
+constexpr int kBeamKept = 1024;  // logits of a chunk that may reach the threshold
 
 // Values as unsigned numbers in their order, -0 below 0; not for NaN, whose sign is anything.
 __device__ __forceinline__ uint32_t order_of(float x) {
@@ -27,6 +25,10 @@ __device__ __forceinline__ uint32_t order_of(float x) {
 __device__ __forceinline__ float value_of(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k); }
 constexpr uint32_t kOrderLow = 0x007fffffu;   // of -inf
 constexpr uint32_t kOrderHigh = 0xff800000u;  // of +inf
+// The power of two that a chunk's sum is relative to: below 2^23 from 0 where its largest value is below 2^22; others' sums
+// are relative to exp of that value; and a chunk with no sum.
+constexpr float kFarTop = 4194304.0f;
+constexpr int kNoPower = 1 << 30, kLeastPower = -(1 << 30);
 // NaN as -inf, +inf as the largest finite value.
 __device__ __forceinline__ float tidy(float x, float most) { return x == x ? fminf(x, most) : Lim<float>::lo(); }
 // Larger values first, of equal ones the lower token; 0 and -0 are equal.
@@ -86,7 +88,7 @@ template <> __device__ __forceinline__ uint32_t LogitsOf16<__half, 0xfc00fc00u, 
 template <> struct Logits<__nv_bfloat16> : LogitsOf16<__nv_bfloat16, 0xff80ff80u, 0x7f7f7f7fu> {};
 template <> struct Logits<__half> : LogitsOf16<__half, 0xfc00fc00u, 0x7bff7bffu> {};
 
-// A chunk's place in the scratch: sum (in units of 2^-40) and largest value, then beams_out keys, 0 for none.
+// A chunk's place in the scratch: sum (in units of 2^-40), largest value and power, then beams_out keys, 0 for none.
 struct BeamPlan {
     int per_thread;  // logits of a thread: 64 or 16
     int64_t chunks;  // of a beam's logits
@@ -102,34 +104,67 @@ BeamPlan beam_plan(int64_t rows, int64_t beams_out, int64_t vocab) {
     return p;
 }
 
-// Rows that are not made of aligned vectors: a chunk's n logits to the same places of shared memory, from the 32-bit words
-// that they touch. Which thread has which token does not depend on a row's address, so that equal rows have equal sums.
-template <class S, int PER> __device__ __forceinline__ void stage_words(uint32_t *to, const S *x, int n) {
-    constexpr int kWords = PER * kBeamThreads * (int)sizeof(S) / 4;
-    const uint32_t low = Logits<S>::none().x;
-    if constexpr (sizeof(S) == 4) {
-        const uint32_t at = (uint32_t)__cvta_generic_to_shared(to);
-        for (int i = threadIdx.x; i < kWords; i += kBeamThreads) {
-            if (i < n)
-                cp_async_zfill<4>(at + i * 4, x + i, true);
-            else
-                to[i] = low;
+// Rows that are not made of aligned vectors: the thread's vectors, tokens begin + j * 2048 (or 1024) on, from the aligned
+// ones that they touch (each holds a logit of the row at least). Which thread has which token does not depend on a row's address,
+// so that equal rows have equal sums.
+template <class S, int V, int WORDS> __device__ __forceinline__ void stage_shifted(uint4 *own, const S *x, int64_t begin, int64_t vocab) {
+    constexpr int E = Logits<S>::E;
+    const uintptr_t end = (uintptr_t)(x + vocab);
+    const int half = (int)((uintptr_t)x & 2) * 8;
+#pragma unroll 4
+    for (int j = 0; j < V; ++j) {
+        const int64_t at = begin + j * (kBeamThreads * E);
+        uint4 w = Logits<S>::none();
+        if (at < vocab) {
+            const uintptr_t from = (uintptr_t)(x + at) & ~(uintptr_t)15;
+            const uint4 p = *reinterpret_cast<const uint4 *>(from);
+            const uint4 q = from + 16 < end ? *reinterpret_cast<const uint4 *>(from + 16) : w;
+            const uint32_t o[9] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w, 0};
+            w = make_uint4(__funnelshift_r(o[WORDS], o[WORDS + 1], half), __funnelshift_r(o[WORDS + 1], o[WORDS + 2], half),
+                           __funnelshift_r(o[WORDS + 2], o[WORDS + 3], half), __funnelshift_r(o[WORDS + 3], o[WORDS + 4], half));
+            if (at + E > vocab) {
+                uint4 none = Logits<S>::none();
+                S *s = reinterpret_cast<S *>(&w);
+#pragma unroll
+                for (int k = 0; k < E; ++k)
+                    if (at + k >= vocab)
+                        s[k] = reinterpret_cast<S *>(&none)[k];
+            }
         }
-        cp_async_commit();
-        cp_async_wait<0>();
-    } else {
-        const bool odd = ((uintptr_t)x & 2) != 0;
-        const uint32_t *words = reinterpret_cast<const uint32_t *>((uintptr_t)x & ~(uintptr_t)3);
-#pragma unroll 8
-        for (int i = threadIdx.x; i < kWords; i += kBeamThreads) {
-            const uint32_t w0 = 2 * i < n ? words[i] : low;
-            const uint32_t w1 = odd && 2 * i + 1 < n ? words[i + 1] : low;
-            uint32_t w = odd ? __funnelshift_r(w0, w1, 16) : w0;
-            if (2 * i + 1 >= n)
-                w = (w & 0xffffu) | (low & 0xffff0000u);
-            to[i] = 2 * i < n ? w : low;
-        }
+        own[j * kBeamThreads] = w;
     }
+}
+
+// A value that beams_out logits of the CTA reach at least: of the maxima of every LANES threads the beams_out-th largest.
+// And the largest. LANES threads count together what is before their group's maximum. Few logits reach it: of 16384
+// independent ones about 22 for 16 of 32 groups, and 44 for 32 of 64 (130 for 32 of 32).
+template <int LANES>
+__device__ __forceinline__ void find_threshold(uint32_t mine, int K, uint32_t *group_max, uint32_t &threshold, uint32_t &top_order) {
+    constexpr int kGroups = kBeamThreads / LANES, kPart = kGroups / LANES;
+    const int lane = threadIdx.x % 32, g = threadIdx.x / LANES, part = lane % LANES * kPart;
+    uint32_t m = mine;
+#pragma unroll
+    for (int d = 1; d < LANES; d *= 2)
+        m = max(m, __shfl_xor_sync(kFull, m, d));
+    if (lane % LANES == 0)
+        group_max[g] = m;
+    __syncthreads();
+    int before = 0;
+#pragma unroll
+    for (int q = 0; q < kPart; q += 4) {
+        const uint4 o = *reinterpret_cast<const uint4 *>(&group_max[part + q]);
+        before += o.x > m || (o.x == m && part + q < g);
+        before += o.y > m || (o.y == m && part + q + 1 < g);
+        before += o.z > m || (o.z == m && part + q + 2 < g);
+        before += o.w > m || (o.w == m && part + q + 3 < g);
+    }
+#pragma unroll
+    for (int d = 1; d < LANES; d *= 2)
+        before += __shfl_xor_sync(kFull, before, d);
+    if (lane % LANES == 0 && before == K - 1)
+        threshold = m;
+    if (lane % LANES == 0 && before == 0)
+        top_order = m;
     __syncthreads();
 }
 
@@ -167,7 +202,7 @@ __device__ __forceinline__ void keep_reached(const uint4 *staged, int t, int lan
 template <class S, int PER, bool VEC> __global__ void __launch_bounds__(kBeamThreads) k_beam_chunk(const __grid_constant__ mt_beam_args a, BeamPlan plan) {
     using L = Logits<S>;
     constexpr int E = L::E, V = PER / E;  // values of a vector, vectors of a thread
-    __shared__ __align__(16) uint32_t group_max[kBeamGroups];
+    __shared__ __align__(16) uint32_t group_max[kBeamThreads / 4];
     __shared__ uint32_t threshold, top_order, count;
     __shared__ uint32_t sum_low[kBeamWarps], sum_high[kBeamWarps];
     __shared__ uint64_t kept[kBeamKept];
@@ -184,21 +219,32 @@ template <class S, int PER, bool VEC> __global__ void __launch_bounds__(kBeamThr
     uint4 *own = staged + threadIdx.x;  // vector j: own[j * kBeamThreads]
     if constexpr (VEC) {
         const uint32_t own_at = (uint32_t)__cvta_generic_to_shared(own);
+        const S *from = x + first;
+        if ((chunk + 1) * (kBeamThreads * PER) <= a.vocab) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const int64_t at = first + j * (kBeamThreads * E);
-            if (at < a.vocab)
-                cp_async_zfill<16>(own_at + j * (kBeamThreads * 16), x + at, true);
-            else
-                own[j * kBeamThreads] = L::none();
+            for (int j = 0; j < V; ++j)
+                cp_async_zfill<16>(own_at + j * (kBeamThreads * 16), from + j * (kBeamThreads * E), true);
+        } else {
+            const int left = (int)(a.vocab - first < INT32_MAX ? a.vocab - first : INT32_MAX);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                if (j * (kBeamThreads * E) < left)
+                    cp_async_zfill<16>(own_at + j * (kBeamThreads * 16), from + j * (kBeamThreads * E), true);
+                else
+                    own[j * kBeamThreads] = L::none();
+            }
         }
         cp_async_commit();
         cp_async_wait<0>();
-        __syncwarp();
     } else {
-        const int64_t begin = chunk * (kBeamThreads * PER), left = a.vocab - begin;
-        stage_words<S, PER>(reinterpret_cast<uint32_t *>(staged), x + begin, left < kBeamThreads * PER ? (int)left : kBeamThreads * PER);
+        switch ((uintptr_t)x % 16 / 4) {
+        case 0: stage_shifted<S, V, 0>(own, x, first, a.vocab); break;
+        case 1: stage_shifted<S, V, 1>(own, x, first, a.vocab); break;
+        case 2: stage_shifted<S, V, 2>(own, x, first, a.vocab); break;
+        default: stage_shifted<S, V, 3>(own, x, first, a.vocab);
+        }
     }
+    __syncwarp();
     uint32_t mine;  // the thread's largest value
     for (bool again = false;; again = true) {
         typename L::Most most = L::low();
@@ -207,34 +253,12 @@ template <class S, int PER, bool VEC> __global__ void __launch_bounds__(kBeamThr
             most = L::max_of(most, own[j * kBeamThreads]);
         const float widest = L::widen(most);
         mine = widest == widest ? order_of(widest + 0.0f) : ~0u;
-        uint32_t m = mine;
-        m = max(m, __shfl_xor_sync(kFull, m, 1));
-        m = max(m, __shfl_xor_sync(kFull, m, 2));
-        if (lane % kBeamGroup == 0)
-            group_max[threadIdx.x / kBeamGroup] = m;
         if (threadIdx.x == 0)
             count = 0;
-        __syncthreads();
-        // the beams_out-th largest of the groups' maxima, which so many logits reach: four lanes count what is before one
-        {
-            const int g = threadIdx.x / kBeamGroup, part = lane % kBeamGroup * (kBeamGroups / kBeamGroup);
-            int before = 0;
-#pragma unroll
-            for (int q = 0; q < kBeamGroups / kBeamGroup; q += 4) {
-                const uint4 o = *reinterpret_cast<const uint4 *>(&group_max[part + q]);
-                before += o.x > m || (o.x == m && part + q < g);
-                before += o.y > m || (o.y == m && part + q + 1 < g);
-                before += o.z > m || (o.z == m && part + q + 2 < g);
-                before += o.w > m || (o.w == m && part + q + 3 < g);
-            }
-            before += __shfl_xor_sync(kFull, before, 1);
-            before += __shfl_xor_sync(kFull, before, 2);
-            if (lane % kBeamGroup == 0 && before == K - 1)
-                threshold = m;
-            if (lane % kBeamGroup == 0 && before == 0)
-                top_order = m;
-        }
-        __syncthreads();
+        if (K <= 16)
+            find_threshold<8>(mine, K, group_max, threshold, top_order);
+        else
+            find_threshold<4>(mine, K, group_max, threshold, top_order);
         if (again || top_order < kOrderHigh)
             break;
         // an infinity or NaN among them: made finite, and once more
@@ -252,27 +276,37 @@ template <class S, int PER, bool VEC> __global__ void __launch_bounds__(kBeamThr
     const uint32_t top = top_order;
     if (top <= kOrderLow) {  // nothing here may come next
         if (threadIdx.x < plan.slots)
-            out[threadIdx.x] = threadIdx.x == 1 ? __float_as_uint(Lim<float>::lo()) : 0;
+            out[threadIdx.x] = threadIdx.x == 1 ? __float_as_uint(Lim<float>::lo()) | (uint64_t)(uint32_t)kLeastPower << 32 : 0;
         return;
     }
     // the logits that reach the threshold: few lanes have one, and the warp goes through each of theirs together
     const uint32_t least = threshold > kOrderLow ? threshold : kOrderLow + 1;
     for (uint32_t lanes = __ballot_sync(kFull, mine >= least); lanes != 0; lanes &= lanes - 1)
         keep_reached<S, PER>(staged, warp * 32 + __ffs(lanes) - 1, lane, (uint32_t)(chunk * (kBeamThreads * PER)), least, kept, count);
-    // sum of exp(x - top): f32 in the thread, then whole numbers, whose sum has no order
+    // Sum of exp(x - top): f32 in the thread, then whole numbers, whose sum has no order. Where top is not too far out, of
+    // 2^(log2(e) x - k) with the whole number k next to log2(e) top: one multiply-add, rounded once, makes the
+    // exponent, and sums of chunks differ by powers of two.
+    const bool by_power = fabsf(value_of(top)) < kFarTop;
+    const float power = rintf(kLog2e * value_of(top));
     {
-        const f32x2 less = both(-value_of(top));
         f32x2 s0 = 0ull, s1 = 0ull;
+        auto add = [&](auto term) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            float f[E];
-            Codec<S>::unpack(own[j * kBeamThreads], f);
+            for (int j = 0; j < V; ++j) {
+                float f[E];
+                Codec<S>::unpack(own[j * kBeamThreads], f);
 #pragma unroll
-            for (int q = 0; q < E; q += 4) {
-                s0 = add2f(s0, ex2_2f(mul2f(add2f(pack2f(f[q], f[q + 1]), less), both(kLog2e))));
-                s1 = add2f(s1, ex2_2f(mul2f(add2f(pack2f(f[q + 2], f[q + 3]), less), both(kLog2e))));
+                for (int q = 0; q < E; q += 4) {
+                    s0 = add2f(s0, ex2_2f(term(pack2f(f[q], f[q + 1]))));
+                    s1 = add2f(s1, ex2_2f(term(pack2f(f[q + 2], f[q + 3]))));
+                }
             }
-        }
+        };
+        const f32x2 scale = both(kLog2e), less = both(by_power ? -power : -value_of(top));
+        if (by_power)
+            add([&](f32x2 v) { return fma2f(v, scale, less); });
+        else
+            add([&](f32x2 v) { return mul2f(add2f(v, less), scale); });
         float p, r;
         unpack2f(add2f(s0, s1), p, r);
         const float s = p + r;
@@ -375,7 +409,7 @@ template <class S, int PER, bool VEC> __global__ void __launch_bounds__(kBeamThr
         for (int q = 0; q < kBeamWarps; ++q)
             sum += (uint64_t)sum_low[q] + ((uint64_t)sum_high[q] << 20);
         out[0] = sum;
-        out[1] = __float_as_uint(value_of(top));
+        out[1] = __float_as_uint(value_of(top)) | (uint64_t)(uint32_t)(by_power ? (int)power : kNoPower) << 32;
     }
 }
 
@@ -398,57 +432,111 @@ __device__ __forceinline__ uint64_t join_lists(uint64_t p, uint64_t q, int lane)
     return p;
 }
 
-// A warp a beam.
+// The logarithm of a beam's sum relative to its largest value: `sum` in units of 2^-30 relative to 2^power, or (kNoPower)
+// a double relative to exp(top). The terms' exponents are x log2(e) with log2(e) as f32, so top's is taken the same.
+__device__ __forceinline__ double log_of_sum(uint64_t sum, int power, float top) {
+    if (power == kNoPower)
+        return log(__longlong_as_double((long long)sum));
+    return log((double)sum * 0x1p-30) + ((double)power - (double)top * (double)kLog2e) * 0.693147180559945309417;
+}
+
+// A warp a beam, and one more for the logarithms of all (64-bit arithmetic is slow here: a warp's instruction takes 16 clocks of
+// the SM, so a lane makes each beam's, not a warp).
 constexpr int kJoinAhead = 8;  // lists on their way
 __global__ void __launch_bounds__(32 * kBeamsMost) k_beam_join(const __grid_constant__ mt_beam_args a, BeamPlan plan) {
     __shared__ uint64_t score[kBeamsMost][kBeamsMost];  // of each beam's first continuations, in order
     __shared__ int32_t token[kBeamsMost][kBeamsMost];
+    __shared__ uint64_t sums[kBeamsMost];
+    __shared__ int powers[kBeamsMost];
+    __shared__ float tops[kBeamsMost];
+    __shared__ double less[kBeamsMost];  // the logarithms
     pdl_prologue();
     const int64_t b = blockIdx.x;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, k = warp, chunks = (int)plan.chunks;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, k = warp, chunks = (int)plan.chunks, beams = (int)a.beams;
     const int K = (int)a.beams_out, n = (int)(a.vocab < K ? a.vocab : K);  // continuations of a beam that can matter
-    {
-        const int64_t row = b * a.beams + k;
-        const uint64_t *mine = static_cast<const uint64_t *>(a.scratch) + row * plan.chunks * plan.slots;
-        const float prior = a.prior != nullptr ? tidy(a.prior[row], 3.402823466e38f) : 0.0f;
-        const bool done = a.finished != nullptr && a.finished[row] != 0;
+    const int64_t row = b * a.beams + (k < beams ? k : 0);
+    const uint64_t *mine = static_cast<const uint64_t *>(a.scratch) + row * plan.chunks * plan.slots;
+    const float prior = a.prior != nullptr ? tidy(a.prior[row], 3.402823466e38f) : 0.0f;
+    const bool done = a.finished != nullptr && a.finished[row] != 0;
+    const bool reads = k < beams && !done && prior != Lim<float>::lo();
+    uint64_t list[kJoinAhead];
+    if (reads) {
+#pragma unroll
+        for (int q = 0; q < kJoinAhead; ++q)
+            list[q] = q < chunks && lane < K ? mine[q * plan.slots + 2 + lane] : 0;
         float top = Lim<float>::lo();
-        double sum = 0.0;
-        uint64_t key = 0;
-        if (!done && prior != Lim<float>::lo()) {
-            uint64_t list[kJoinAhead];
-#pragma unroll
-            for (int q = 0; q < kJoinAhead; ++q)
-                list[q] = q < chunks && lane < K ? mine[q * plan.slots + 2 + lane] : 0;
-            for (int c = lane; c < chunks; c += 32)
-                top = fmaxf(top, __uint_as_float((uint32_t)mine[c * plan.slots + 1]));
-            top = value_of(redux_max(order_of(top)));
-            if (top != Lim<float>::lo()) {
-                for (int c = lane; c < chunks; c += 32) {
-                    const float m = __uint_as_float((uint32_t)mine[c * plan.slots + 1]);
-                    if (m != Lim<float>::lo())
-                        sum += (double)mine[c * plan.slots] * 0x1p-40 * exp((double)m - (double)top);
-                }
-                for (int o = 16; o > 0; o /= 2)
-                    if (chunks > o)
-                        sum += __shfl_xor_sync(kFull, sum, o);
-                sum = __shfl_sync(kFull, sum, 0);
-                for (int c0 = 0; c0 < chunks; c0 += kJoinAhead) {
-#pragma unroll
-                    for (int q = 0; q < kJoinAhead; ++q)
-                        if (c0 + q < chunks) {
-                            key = c0 + q == 0 ? list[q] : join_lists(key, list[q], lane);
-                            const int c = c0 + q + kJoinAhead;
-                            list[q] = c < chunks && lane < K ? mine[c * plan.slots + 2 + lane] : 0;
-                        }
-                }
+        int power = kLeastPower;
+        uint64_t sum = 0;
+        if (chunks <= 32) {
+            if (lane < chunks) {
+                sum = mine[lane * plan.slots];
+                const uint64_t o = mine[lane * plan.slots + 1];
+                top = __uint_as_float((uint32_t)o);
+                power = (int)(uint32_t)(o >> 32);
+            }
+        } else {
+            for (int c = lane; c < chunks; c += 32) {
+                const uint64_t o = mine[c * plan.slots + 1];
+                top = fmaxf(top, __uint_as_float((uint32_t)o));
+                power = max(power, (int)(uint32_t)(o >> 32));
             }
         }
+        const int own_power = power;
+        top = value_of(redux_max(order_of(top)));
+        power = __reduce_max_sync(kFull, power);
+        if (power == kNoPower) {  // far out: sums in 64 bits, relative to the largest value
+            double all = 0.0;
+            for (int c = lane; c < chunks; c += 32) {
+                const uint64_t o = mine[c * plan.slots + 1];
+                const double m = (double)__uint_as_float((uint32_t)o), s = (double)mine[c * plan.slots] * 0x1p-40;
+                const int p = (int)(uint32_t)(o >> 32);
+                if (p != kLeastPower)
+                    all += s * exp(m - (double)top + (p == kNoPower ? 0.0 : ((double)p - m * (double)kLog2e) * 0.693147180559945309417));
+            }
+            for (int o = 16; o > 0; o /= 2)
+                all += __shfl_xor_sync(kFull, all, o);
+            sum = (uint64_t)__double_as_longlong(all);
+        } else {
+            if (chunks <= 32) {
+                sum = sum >> 10 >> min(power - own_power, 53);
+            } else {
+                for (int c = lane; c < chunks; c += 32)
+                    sum += mine[c * plan.slots] >> 10 >> min(power - (int)(uint32_t)(mine[c * plan.slots + 1] >> 32), 53);
+            }
+            for (int o = 16; o > 0; o /= 2)
+                sum += __shfl_xor_sync(kFull, sum, o);
+        }
+        if (lane == 0) {
+            sums[k] = sum;
+            powers[k] = power;
+            tops[k] = top;
+        }
+    } else if (k < beams && lane == 0) {
+        powers[k] = kLeastPower;
+    }
+    __syncthreads();
+    const int logs = blockDim.x / 32 - 1;  // the warp of the logarithms, a beam's own too where there are 32
+    if (warp == logs && lane < beams)
+        less[lane] = powers[lane] == kLeastPower ? 0.0 : log_of_sum(sums[lane], powers[lane], tops[lane]);
+    uint64_t key = 0;
+    if (reads && powers[k] != kLeastPower) {
+        for (int c0 = 0; c0 < chunks; c0 += kJoinAhead) {
+#pragma unroll
+            for (int q = 0; q < kJoinAhead; ++q)
+                if (c0 + q < chunks) {
+                    key = c0 + q == 0 ? list[q] : join_lists(key, list[q], lane);
+                    const int c = c0 + q + kJoinAhead;
+                    list[q] = c < chunks && lane < K ? mine[c * plan.slots + 2 + lane] : 0;
+                }
+        }
+    }
+    __syncthreads();
+    if (k < beams) {
         const int has = __popc(__ballot_sync(kFull, key != 0));  // logits that may come next, as far as they matter
         int32_t tok = (int32_t)~(uint32_t)key;
         double s = Lim<double>::lo();
         if (key != 0)
-            s = (double)prior + ((double)value_of((uint32_t)(key >> 32)) - (double)top - log(sum));
+            s = (double)prior + (((double)value_of((uint32_t)(key >> 32)) - (double)tops[k]) - less[k]);
         if (done && prior != Lim<float>::lo()) {  // the end with the beam's score, then the other tokens in order
             tok = lane == 0 ? (int)a.eos : lane - 1 < a.eos ? lane - 1 : lane;
             if (lane == 0)
@@ -490,7 +578,7 @@ __global__ void __launch_bounds__(32 * kBeamsMost) k_beam_join(const __grid_cons
     const int tok = token[parent][place];
     const bool out = lane < K;
     const int64_t to = b * K + lane;
-    const bool done = a.finished != nullptr && out && a.finished[b * a.beams + parent] != 0;
+    const bool ended = a.finished != nullptr && out && a.finished[b * a.beams + parent] != 0;
     const int group = (int)(a.beams > K ? a.beams : K);
     const int32_t slot = a.slots != nullptr && lane < group ? a.slots[b * group + lane] : 0;
     __syncwarp();
@@ -499,7 +587,7 @@ __global__ void __launch_bounds__(32 * kBeamsMost) k_beam_join(const __grid_cons
         a.parents[to] = parent;
         a.scores[to] = (float)score_of(best);
         if (a.finished_out != nullptr)
-            a.finished_out[to] = done || tok == a.eos;
+            a.finished_out[to] = ended || tok == a.eos;
     }
     if (a.slots == nullptr)
         return;
@@ -543,7 +631,7 @@ template <class S> cudaError_t launch(const mt_beam_args &a, const Launch &L) {
     if (e != cudaSuccess)
         return e;
     note_launch();
-    return launch_pdl(k_beam_join, (unsigned)a.batch, (unsigned)(32 * a.beams), 0, L.stream, a, plan);
+    return launch_pdl(k_beam_join, (unsigned)a.batch, (unsigned)(32 * (a.beams < kBeamsMost ? a.beams + 1 : kBeamsMost)), 0, L.stream, a, plan);
 }
 
 }  // namespace
