@@ -663,8 +663,8 @@ typedef struct {
  *   prior[k] + logits[k, v] - log(sum over v' of exp(logits[k, v']))
  * the beams_out best ones, best first; equal scores by the lowest k, then the
  * lowest v. parents[j] = k, tokens[j] = v, scores[j] the score. All arrays but
- * logits are contiguous. Scores of different beams are compared in 64 bits, those
- * of one beam by their logits; they are rounded once, at the store.
+ * logits are contiguous. Scores are made and compared as pairs of f32 (48 bits),
+ * and rounded once, at the store.
  *
  * Logits: NaN counts as -inf (a token that may not come next), +inf as the
  * largest finite value of their type. A beam whose logits are all -inf, or whose prior is -inf or

@@ -1,11 +1,15 @@
 // mt_beam.cu -- a beam search's selection over beams and vocabulary.
 //
-// Two kernels. The first gives every CTA a chunk of one beam's logits: its largest value, the sum of
-// exp(x - largest), and its beams_out first tokens in order. The second has a CTA a sequence: it joins the
-// chunks of each beam, then the beams, and gives out the slots.
+// Two kernels. In the first every warp reads a span of one beam's logits, a group of 1024 (f32: 512) after the other, and leaves the
+// sum of their exponentials and each group's largest value: one pass at the speed of memory, with no word between warps.
+// The second has a CTA a sequence: it joins the sums, and keeps the beams_out best groups, by the score of their largest logit and,
+// where those are equal, by their place. That loses nothing: a logit that is among the beams_out first cannot be in a group that
+// as many groups are before, since each of those holds a logit before it. So only beams_out groups are read
+// again, and the few logits in them that reach the last one's score are ranked. Where there are many such logits (equal ones, or
+// high ones beside each other), the same step over the groups' vectors, and then over theirs, leaves few.
 //
-// Within a beam the order of the scores is the order of the logits, so only joining beams needs scores; they are
-// made and compared in 64 bits there, a few hundred of them. What bounds the whole is reading the logits once.
+#include <initializer_list>
+
 #include "mt_seq.cuh"
 #include "mt_seq.h"
 
@@ -13,9 +17,11 @@ namespace mt {
 
 namespace {
 
-constexpr int kBeamThreads = 256;
-constexpr int kBeamWarps = kBeamThreads / 32;
-constexpr int kBeamKept = 1024;  // logits of a chunk that may reach the threshold
+constexpr int kBeamThreads = 256;  // of the first kernel
+constexpr int kJoinThreads = 512, kJoinWarps = kJoinThreads / 32;
+constexpr int kBatch = 4;        // vectors of a lane in a group
+constexpr int kMostBatches = 8;  // groups of a warp
+constexpr int kGroupVectors = 32 * kBatch;
 
 // Values as unsigned numbers in their order, -0 below 0; not for NaN, whose sign is anything.
 __device__ __forceinline__ uint32_t order_of(float x) {
@@ -23,24 +29,30 @@ __device__ __forceinline__ uint32_t order_of(float x) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 __device__ __forceinline__ float value_of(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k); }
-constexpr uint32_t kOrderLow = 0x007fffffu;   // of -inf
-constexpr uint32_t kOrderHigh = 0xff800000u;  // of +inf
-// The power of two that a chunk's sum is relative to: below 2^23 from 0 where its largest value is below 2^22; others' sums
-// are relative to exp of that value; and a chunk with no sum.
-constexpr float kFarTop = 4194304.0f;
-constexpr int kNoPower = 1 << 30, kLeastPower = -(1 << 30);
+constexpr uint32_t kOrderLow = 0x007fffffu;  // of -inf
+// A score is a pair of f32, the value rounded and what that leaves: 48 bits, by f32 additions (f64 ones take a
+// warp 16 clocks of the SM each here, and a few thousand scores are made). As a number in their order; 0 is below all of them.
+__device__ __forceinline__ uint64_t order_of(float high, float low) { return (uint64_t)order_of(high + 0.0f) << 32 | order_of(low + 0.0f); }
+__device__ __forceinline__ float score_of(uint64_t k) { return value_of((uint32_t)(k >> 32)); }
+// a + b and its rounding error (Knuth's sum)
+__device__ __forceinline__ float two_sum(float a, float b, float &error) {
+    const float s = a + b, t = s - a;
+    error = (a - (s - t)) + (b - t);
+    return s;
+}
+// (x - top) + (high + low)
+__device__ __forceinline__ uint64_t score_order(float x, float top, float high, float low) {
+    float e0, e1;
+    const float d = two_sum(x, -top, e0), s = two_sum(d, high, e1), rest = e1 + (e0 + low), sum = s + rest;
+    return fabsf(s) < Lim<float>::hi() ? order_of(sum, rest - (sum - s)) : order_of(s, 0.0f);
+}
 // NaN as -inf, +inf as the largest finite value.
 __device__ __forceinline__ float tidy(float x, float most) { return x == x ? fminf(x, most) : Lim<float>::lo(); }
-// Larger values first, of equal ones the lower token; 0 and -0 are equal.
-__device__ __forceinline__ uint64_t key_of(float x, uint32_t token) { return (uint64_t)order_of(x + 0.0f) << 32 | (uint32_t)~token; }
 
-__device__ __forceinline__ uint32_t redux_max(uint32_t v) { return __reduce_max_sync(kFull, v); }
-// The largest of a warp's keys.
-__device__ __forceinline__ uint64_t warp_max(uint64_t key) {
-    const uint32_t hi = redux_max((uint32_t)(key >> 32));
-    const uint32_t lo = redux_max((uint32_t)(key >> 32) == hi ? (uint32_t)key : 0u);
-    return (uint64_t)hi << 32 | lo;
-}
+// The power of two that a span's sum is relative to: below 2^23 from 0 where its largest value is below 2^22; others' sums
+// are relative to exp of that value; and a span with no sum.
+constexpr float kFarTop = 4194304.0f;
+constexpr int kNoPower = 1 << 30, kLeastPower = -(1 << 30);
 
 // A 16-byte vector of logits.
 template <class S> struct Logits;
@@ -88,348 +100,193 @@ template <> __device__ __forceinline__ uint32_t LogitsOf16<__half, 0xfc00fc00u, 
 template <> struct Logits<__nv_bfloat16> : LogitsOf16<__nv_bfloat16, 0xff80ff80u, 0x7f7f7f7fu> {};
 template <> struct Logits<__half> : LogitsOf16<__half, 0xfc00fc00u, 0x7bff7bffu> {};
 
-// A chunk's place in the scratch: sum (in units of 2^-40), largest value and power, then beams_out keys, 0 for none.
+// In the scratch: a span's sum (in units of 2^-40), its largest value and power; then the groups' largest values, as numbers in order.
 struct BeamPlan {
-    int per_thread;  // logits of a thread: 64 or 16
-    int64_t chunks;  // of a beam's logits
-    int64_t slots;   // of a chunk
+    int batches;    // groups of a span
+    int64_t spans;  // of a beam's logits
 };
-// A CTA's chunk: large, so that what follows the reading costs little beside it, where there are many CTAs all the same.
-BeamPlan beam_plan(int64_t rows, int64_t beams_out, int64_t vocab) {
+// Spans as long as leave enough warps.
+constexpr int64_t kEnoughSpans = 152 * 32 * 2;
+BeamPlan beam_plan(int64_t rows, int64_t vocab, int64_t size) {
     BeamPlan p;
-    auto chunks = [&](int per_thread) { return (vocab + per_thread * kBeamThreads - 1) / (per_thread * kBeamThreads); };
-    p.per_thread = rows * chunks(64) >= 2 * 152 ? 64 : 16;
-    p.chunks = chunks(p.per_thread);
-    p.slots = beams_out + 2;
-    return p;
+    for (p.batches = kMostBatches;; p.batches /= 2) {
+        const int64_t bytes = (int64_t)p.batches * kGroupVectors * 16;
+        p.spans = (vocab * size + bytes - 1) / bytes;
+        if (p.batches == 1 || rows * p.spans >= kEnoughSpans)
+            return p;
+    }
 }
 
-// Rows that are not made of aligned vectors: the thread's vectors, tokens begin + j * 2048 (or 1024) on, from the aligned
-// ones that they touch (each holds a logit of the row at least). Which thread has which token does not depend on a row's address,
+// The vector of logits from token `at` on, -inf behind the row. WORDS < 0: rows are made of aligned vectors. Otherwise the row begins
+// WORDS words (and, `half` 16, another 16 bits) behind an aligned vector, and the values come from the two aligned ones that they lie
+// in, each of which holds a logit of the row at least. Which thread has which token does not depend on a row's address,
 // so that equal rows have equal sums.
-template <class S, int V, int WORDS> __device__ __forceinline__ void stage_shifted(uint4 *own, const S *x, int64_t begin, int64_t vocab) {
+template <class S, int WORDS> __device__ __forceinline__ uint4 load_logits(const S *x, int64_t at, int64_t vocab, int half) {
     constexpr int E = Logits<S>::E;
-    const uintptr_t end = (uintptr_t)(x + vocab);
-    const int half = (int)((uintptr_t)x & 2) * 8;
-#pragma unroll 4
-    for (int j = 0; j < V; ++j) {
-        const int64_t at = begin + j * (kBeamThreads * E);
-        uint4 w = Logits<S>::none();
-        if (at < vocab) {
-            const uintptr_t from = (uintptr_t)(x + at) & ~(uintptr_t)15;
-            const uint4 p = *reinterpret_cast<const uint4 *>(from);
-            const uint4 q = from + 16 < end ? *reinterpret_cast<const uint4 *>(from + 16) : w;
-            const uint32_t o[9] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w, 0};
-            w = make_uint4(__funnelshift_r(o[WORDS], o[WORDS + 1], half), __funnelshift_r(o[WORDS + 1], o[WORDS + 2], half),
-                           __funnelshift_r(o[WORDS + 2], o[WORDS + 3], half), __funnelshift_r(o[WORDS + 3], o[WORDS + 4], half));
-            if (at + E > vocab) {
-                uint4 none = Logits<S>::none();
-                S *s = reinterpret_cast<S *>(&w);
-#pragma unroll
-                for (int k = 0; k < E; ++k)
-                    if (at + k >= vocab)
-                        s[k] = reinterpret_cast<S *>(&none)[k];
-            }
-        }
-        own[j * kBeamThreads] = w;
-    }
-}
-
-// A value that beams_out logits of the CTA reach at least: of the maxima of every LANES threads the beams_out-th largest.
-// And the largest. LANES threads count together what is before their group's maximum. Few logits reach it: of 16384
-// independent ones about 22 for 16 of 32 groups, and 44 for 32 of 64 (130 for 32 of 32).
-template <int LANES>
-__device__ __forceinline__ void find_threshold(uint32_t mine, int K, uint32_t *group_max, uint32_t &threshold, uint32_t &top_order) {
-    constexpr int kGroups = kBeamThreads / LANES, kPart = kGroups / LANES;
-    const int lane = threadIdx.x % 32, g = threadIdx.x / LANES, part = lane % LANES * kPart;
-    uint32_t m = mine;
-#pragma unroll
-    for (int d = 1; d < LANES; d *= 2)
-        m = max(m, __shfl_xor_sync(kFull, m, d));
-    if (lane % LANES == 0)
-        group_max[g] = m;
-    __syncthreads();
-    int before = 0;
-#pragma unroll
-    for (int q = 0; q < kPart; q += 4) {
-        const uint4 o = *reinterpret_cast<const uint4 *>(&group_max[part + q]);
-        before += o.x > m || (o.x == m && part + q < g);
-        before += o.y > m || (o.y == m && part + q + 1 < g);
-        before += o.z > m || (o.z == m && part + q + 2 < g);
-        before += o.w > m || (o.w == m && part + q + 3 < g);
-    }
-#pragma unroll
-    for (int d = 1; d < LANES; d *= 2)
-        before += __shfl_xor_sync(kFull, before, d);
-    if (lane % LANES == 0 && before == K - 1)
-        threshold = m;
-    if (lane % LANES == 0 && before == 0)
-        top_order = m;
-    __syncthreads();
-}
-
-// Thread t's logits from `least` on, as keys; their number goes on beyond the places that there are.
-template <class S, int PER>
-__device__ __forceinline__ void keep_reached(const uint4 *staged, int t, int lane, uint32_t begin, uint32_t least, uint64_t *kept, uint32_t &count) {
-    constexpr int E = Logits<S>::E, kWords = PER / E * 4;  // 32-bit words of a thread
-#pragma unroll
-    for (int i = 0; i < kWords; i += 32) {
-        const int word = i + lane;
-        if (word < kWords) {
-            const int j = word / 4, q = word % 4 * (E / 4);
-            const uint32_t w = reinterpret_cast<const uint32_t *>(staged + j * kBeamThreads + t)[word % 4];
-            float f[2];
-            if constexpr (E == 8)
-                Codec<S>::two(w, f[0], f[1]);
-            else
-                f[0] = __uint_as_float(w);
-            const uint32_t token = begin + (uint32_t)(j * (kBeamThreads * E) + t * E + q);
-#pragma unroll
-            for (int k = 0; k < E / 4; ++k) {
-                const uint64_t key = key_of(f[k], token + k);
-                if ((uint32_t)(key >> 32) >= least) {
-                    const uint32_t n = atomicAdd(&count, 1u);
-                    if (n < kBeamKept)
-                        kept[n] = key;
-                }
-            }
-        }
-    }
-}
-
-// A thread's logits stay in its own places of shared memory, where they are copied to and read from three times: for
-// their maxima, for the sum, and (of few threads) for those that reach the threshold. VEC: rows are made of aligned vectors.
-template <class S, int PER, bool VEC> __global__ void __launch_bounds__(kBeamThreads) k_beam_chunk(const __grid_constant__ mt_beam_args a, BeamPlan plan) {
-    using L = Logits<S>;
-    constexpr int E = L::E, V = PER / E;  // values of a vector, vectors of a thread
-    __shared__ __align__(16) uint32_t group_max[kBeamThreads / 4];
-    __shared__ uint32_t threshold, top_order, count;
-    __shared__ uint32_t sum_low[kBeamWarps], sum_high[kBeamWarps];
-    __shared__ uint64_t kept[kBeamKept];
-    extern __shared__ __align__(16) uint4 staged[];
-    pdl_prologue();
-    const uint32_t chunks = (uint32_t)plan.chunks, beams = (uint32_t)a.beams;
-    const int64_t row = blockIdx.x / chunks, chunk = blockIdx.x % chunks, b = (uint32_t)row / beams, beam = (uint32_t)row % beams;
-    if (a.finished != nullptr && a.finished[row] != 0)
-        return;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, K = (int)a.beams_out;
-    const S *x = static_cast<const S *>(a.logits) + b * a.logits_batch + beam * a.logits_beam;
-    // vector j of the thread: tokens first + j * 2048 (or 1024) and on
-    const int64_t first = chunk * (kBeamThreads * PER) + threadIdx.x * E;
-    uint4 *own = staged + threadIdx.x;  // vector j: own[j * kBeamThreads]
-    if constexpr (VEC) {
-        const uint32_t own_at = (uint32_t)__cvta_generic_to_shared(own);
-        const S *from = x + first;
-        if ((chunk + 1) * (kBeamThreads * PER) <= a.vocab) {
-#pragma unroll
-            for (int j = 0; j < V; ++j)
-                cp_async_zfill<16>(own_at + j * (kBeamThreads * 16), from + j * (kBeamThreads * E), true);
-        } else {
-            const int left = (int)(a.vocab - first < INT32_MAX ? a.vocab - first : INT32_MAX);
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                if (j * (kBeamThreads * E) < left)
-                    cp_async_zfill<16>(own_at + j * (kBeamThreads * 16), from + j * (kBeamThreads * E), true);
-                else
-                    own[j * kBeamThreads] = L::none();
-            }
-        }
-        cp_async_commit();
-        cp_async_wait<0>();
+    uint4 w = Logits<S>::none();
+    if (at >= vocab)
+        return w;
+    if constexpr (WORDS < 0) {
+        return ld_stream(reinterpret_cast<const uint4 *>(x + at));
     } else {
-        switch ((uintptr_t)x % 16 / 4) {
-        case 0: stage_shifted<S, V, 0>(own, x, first, a.vocab); break;
-        case 1: stage_shifted<S, V, 1>(own, x, first, a.vocab); break;
-        case 2: stage_shifted<S, V, 2>(own, x, first, a.vocab); break;
-        default: stage_shifted<S, V, 3>(own, x, first, a.vocab);
+        const uintptr_t from = (uintptr_t)(x + at) & ~(uintptr_t)15;
+        const uint4 p = *reinterpret_cast<const uint4 *>(from);
+        const uint4 q = from + 16 < (uintptr_t)(x + vocab) ? *reinterpret_cast<const uint4 *>(from + 16) : w;
+        const uint32_t o[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
+        w = make_uint4(__funnelshift_r(o[WORDS], o[WORDS + 1], half), __funnelshift_r(o[WORDS + 1], o[WORDS + 2], half),
+                       __funnelshift_r(o[WORDS + 2], o[WORDS + 3], half), __funnelshift_r(o[WORDS + 3], o[WORDS + 4], half));
+        if (at + E > vocab) {
+            uint4 none = Logits<S>::none();
+            S *s = reinterpret_cast<S *>(&w);
+#pragma unroll
+            for (int k = 0; k < E; ++k)
+                if (at + k >= vocab)
+                    s[k] = reinterpret_cast<S *>(&none)[k];
         }
+        return w;
     }
-    __syncwarp();
-    uint32_t mine;  // the thread's largest value
-    for (bool again = false;; again = true) {
+}
+// A lane's part of a span: its largest value, and the sum of 2^(log2(e) x - k) with k the whole number next to log2(e) times
+// the largest (kept between -+kMostPower). One multiply-add, rounded once, makes an exponent, and a larger k scales the sum by
+// a power of two. (A sum relative to exp of the largest would take a subtraction for each logit.)
+constexpr float kMostPower = 8388608.0f;
+__device__ __forceinline__ float power_of(float top) { return fminf(fmaxf(rintf(kLog2e * top), -kMostPower), kMostPower); }
+template <class S> struct Part {
+    using L = Logits<S>;
+    float top, power;
+    f32x2 s0, s1;
+    __device__ __forceinline__ void begin() {
+        top = Lim<float>::lo();
+        power = -kMostPower;
+        s0 = s1 = 0ull;
+    }
+    __device__ __forceinline__ float largest(const uint4 (&w)[kBatch]) const {
         typename L::Most most = L::low();
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-            most = L::max_of(most, own[j * kBeamThreads]);
-        const float widest = L::widen(most);
-        mine = widest == widest ? order_of(widest + 0.0f) : ~0u;
-        if (threadIdx.x == 0)
-            count = 0;
-        if (K <= 16)
-            find_threshold<8>(mine, K, group_max, threshold, top_order);
-        else
-            find_threshold<4>(mine, K, group_max, threshold, top_order);
-        if (again || top_order < kOrderHigh)
-            break;
-        // an infinity or NaN among them: made finite, and once more
-#pragma unroll 1
-        for (int j = 0; j < V; ++j) {
-            float f[E];
-            Codec<S>::unpack(own[j * kBeamThreads], f);
+        for (int j = 0; j < kBatch; ++j)
+            most = L::max_of(most, w[j]);
+        return L::widen(most);
+    }
+    // returns the batch's largest value
+    __device__ __forceinline__ float add(uint4 (&w)[kBatch]) {
+        float m = largest(w);
+        if (!(m < Lim<float>::hi())) {  // an infinity or NaN among them: made finite
 #pragma unroll
-            for (int q = 0; q < E; ++q)
-                f[q] = tidy(f[q], L::most());
-            own[j * kBeamThreads] = Codec<S>::pack(f);
+            for (int j = 0; j < kBatch; ++j) {
+                float f[L::E];
+                Codec<S>::unpack(w[j], f);
+#pragma unroll
+                for (int q = 0; q < L::E; ++q)
+                    f[q] = tidy(f[q], L::most());
+                w[j] = Codec<S>::pack(f);
+            }
+            m = largest(w);
+        }
+        top = fmaxf(top, m);
+        const float p = power_of(top);
+        const f32x2 scale = both(ex2f(power - p)), less = both(-p);
+        power = p;
+        s0 = mul2f(s0, scale);
+        s1 = mul2f(s1, scale);
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            float f[L::E];
+            Codec<S>::unpack(w[j], f);
+#pragma unroll
+            for (int q = 0; q < L::E; q += 4) {
+                s0 = add2f(s0, ex2_2f(fma2f(pack2f(f[q], f[q + 1]), both(kLog2e), less)));
+                s1 = add2f(s1, ex2_2f(fma2f(pack2f(f[q + 2], f[q + 3]), both(kLog2e), less)));
+            }
+        }
+        return m;
+    }
+    __device__ __forceinline__ float sum() const {
+        float a, b;
+        unpack2f(add2f(s0, s1), a, b);
+        return a + b;
+    }
+};
+// The span from token `begin` on, `lane_at` the lane's place in a row of vectors; the next batch is on its way while one is worked
+// on. Lane t gets group t's largest value.
+template <class S, int WORDS>
+__device__ __forceinline__ uint32_t read_span(Part<S> &part, const S *x, int64_t begin, int64_t vocab, int batches, int lane, int half) {
+    constexpr int E = Logits<S>::E;
+    const int64_t first = begin + lane * E;
+    uint32_t mine = kOrderLow;
+    uint4 w[2][kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j)
+        w[0][j] = load_logits<S, WORDS>(x, first + j * (32 * E), vocab, half);
+#pragma unroll 1
+    for (int t = 0; t < batches; t += 2) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            if (t + u < batches) {
+                if (t + u + 1 < batches) {
+#pragma unroll
+                    for (int j = 0; j < kBatch; ++j)
+                        w[1 - u][j] = load_logits<S, WORDS>(x, first + ((t + u + 1) * kBatch + j) * (32 * E), vocab, half);
+                }
+                const uint32_t m = __reduce_max_sync(kFull, order_of(part.add(w[u]) + 0.0f));
+                mine = lane == t + u ? m : mine;
+            }
         }
     }
-    uint64_t *out = static_cast<uint64_t *>(a.scratch) + (row * plan.chunks + chunk) * plan.slots;
-    const uint32_t top = top_order;
-    if (top <= kOrderLow) {  // nothing here may come next
-        if (threadIdx.x < plan.slots)
-            out[threadIdx.x] = threadIdx.x == 1 ? __float_as_uint(Lim<float>::lo()) | (uint64_t)(uint32_t)kLeastPower << 32 : 0;
+    return mine;
+}
+
+// VEC: rows are made of aligned vectors.
+template <class S, bool VEC> __global__ void __launch_bounds__(kBeamThreads) k_beam_read(const __grid_constant__ mt_beam_args a, BeamPlan plan) {
+    constexpr int E = Logits<S>::E;
+    pdl_prologue();
+    const int lane = threadIdx.x % 32;
+    const int64_t id = (int64_t)blockIdx.x * (kBeamThreads / 32) + threadIdx.x / 32, rows = a.batch * a.beams;
+    const int64_t row = id / plan.spans, span = id - row * plan.spans, b = row / a.beams, beam = row - b * a.beams;
+    if (row >= rows || (a.finished != nullptr && a.finished[row] != 0))
         return;
-    }
-    // the logits that reach the threshold: few lanes have one, and the warp goes through each of theirs together
-    const uint32_t least = threshold > kOrderLow ? threshold : kOrderLow + 1;
-    for (uint32_t lanes = __ballot_sync(kFull, mine >= least); lanes != 0; lanes &= lanes - 1)
-        keep_reached<S, PER>(staged, warp * 32 + __ffs(lanes) - 1, lane, (uint32_t)(chunk * (kBeamThreads * PER)), least, kept, count);
-    // Sum of exp(x - top): f32 in the thread, then whole numbers, whose sum has no order. Where top is not too far out, of
-    // 2^(log2(e) x - k) with the whole number k next to log2(e) top: one multiply-add, rounded once, makes the
-    // exponent, and sums of chunks differ by powers of two.
-    const bool by_power = fabsf(value_of(top)) < kFarTop;
-    const float power = rintf(kLog2e * value_of(top));
-    {
-        f32x2 s0 = 0ull, s1 = 0ull;
-        auto add = [&](auto term) {
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                float f[E];
-                Codec<S>::unpack(own[j * kBeamThreads], f);
-#pragma unroll
-                for (int q = 0; q < E; q += 4) {
-                    s0 = add2f(s0, ex2_2f(term(pack2f(f[q], f[q + 1]))));
-                    s1 = add2f(s1, ex2_2f(term(pack2f(f[q + 2], f[q + 3]))));
-                }
-            }
-        };
-        const f32x2 scale = both(kLog2e), less = both(by_power ? -power : -value_of(top));
-        if (by_power)
-            add([&](f32x2 v) { return fma2f(v, scale, less); });
-        else
-            add([&](f32x2 v) { return mul2f(add2f(v, less), scale); });
-        float p, r;
-        unpack2f(add2f(s0, s1), p, r);
-        const float s = p + r;
-        const uint32_t high = (uint32_t)(s * 0x1p20f), low = (uint32_t)((s * 0x1p20f - (float)high) * 0x1p20f);
-        const uint32_t low_all = __reduce_add_sync(kFull, low), high_all = __reduce_add_sync(kFull, high);
-        if (lane == 0) {
-            sum_low[warp] = low_all;
-            sum_high[warp] = high_all;
+    const S *x = static_cast<const S *>(a.logits) + b * a.logits_batch + beam * a.logits_beam;
+    const int64_t begin = span * plan.batches * (kGroupVectors * E);
+    Part<S> part;
+    part.begin();
+    uint32_t mine;
+    if constexpr (VEC) {
+        mine = read_span<S, -1>(part, x, begin, a.vocab, plan.batches, lane, 0);
+    } else {
+        const int half = (int)((uintptr_t)x & 2) * 8;
+        switch ((uintptr_t)x % 16 / 4) {
+        case 0: mine = read_span<S, 0>(part, x, begin, a.vocab, plan.batches, lane, half); break;
+        case 1: mine = read_span<S, 1>(part, x, begin, a.vocab, plan.batches, lane, half); break;
+        case 2: mine = read_span<S, 2>(part, x, begin, a.vocab, plan.batches, lane, half); break;
+        default: mine = read_span<S, 3>(part, x, begin, a.vocab, plan.batches, lane, half);
         }
     }
-    __syncthreads();
-    int n = (int)count;
-    if (n > kBeamKept) {
-        // More equal values than there is place for (a mask of a finite value, for instance): those above the threshold,
-        // and of those at it the first beams_out, vector after vector.
-        __syncthreads();
-        if (threadIdx.x == 0)
-            count = 0;
-        __syncthreads();
-        for (uint32_t lanes = __ballot_sync(kFull, mine > least); lanes != 0; lanes &= lanes - 1)
-            keep_reached<S, PER>(staged, warp * 32 + __ffs(lanes) - 1, lane, (uint32_t)(chunk * (kBeamThreads * PER)), least + 1, kept, count);
-        __syncthreads();
-        n = (int)count;  // places behind those take the equal ones
-        int had = 0;
+    const float top = value_of(__reduce_max_sync(kFull, mine)), power = power_of(top);
+    const bool by_power = fabsf(top) < kFarTop;
+    float s = part.sum() * ex2f(part.power - power);
+    if (!by_power && top != Lim<float>::lo()) {  // far out, where log2(e) x is no longer exact enough: relative to exp(top)
+        s = 0.0f;
 #pragma unroll 1
-        for (int j = 0; j < V && had < K && n + K <= kBeamKept; ++j) {
-            float f[E];
-            Codec<S>::unpack(own[j * kBeamThreads], f);
-            uint32_t equal = 0;
+        for (int i = 0; i < plan.batches * kBatch; ++i) {
+            const int64_t at = begin + (i * 32 + lane) * E;
+            float t = 0.0f;
 #pragma unroll
             for (int q = 0; q < E; ++q)
-                equal |= order_of(f[q] + 0.0f) == least ? 1u << q : 0u;
-            int before = __popc(equal), all = before;
-#pragma unroll
-            for (int d = 1; d < 32; d *= 2) {
-                const int o = __shfl_up_sync(kFull, before, d);
-                before += lane >= d ? o : 0;
-            }
-            if (lane == 31)
-                group_max[j % 2 * kBeamWarps + warp] = (uint32_t)before;
-            before += had - all;
-            __syncthreads();
-#pragma unroll
-            for (int q = 0; q < kBeamWarps; ++q) {
-                const int o = (int)group_max[j % 2 * kBeamWarps + q];
-                before += q < warp ? o : 0;
-                had += o;
-            }
-            for (; equal != 0 && before < K; equal &= equal - 1, ++before) {
-                const int q = __ffs(equal) - 1;
-                kept[n + before] = (uint64_t)least << 32 | (uint32_t)~(uint32_t)(first + j * (kBeamThreads * E) + q);
-            }
-        }
-        n = n + K <= kBeamKept ? n + (had < K ? had : K) : kBeamKept + 1;
-        __syncthreads();
-    }
-    if (n <= kBeamKept) {
-        for (int t = threadIdx.x; t < n; t += kBeamThreads) {
-            const uint64_t key = kept[t];
-            int before = 0;
-            for (int q = 0; q < n; ++q)
-                before += kept[q] > key;
-            if (before < K)
-                out[2 + before] = key;
-        }
-        for (int t = n + threadIdx.x; t < K; t += kBeamThreads)
-            out[2 + t] = 0;
-    } else {
-        // too many in too few places: the largest key below the last one, beams_out times
-        uint64_t last = ~0ull;
-        for (int t = 0; t < K; ++t) {
-            uint64_t m = 0;
-#pragma unroll 1
-            for (int j = 0; j < V; ++j) {
-                float f[E];
-                Codec<S>::unpack(own[j * kBeamThreads], f);
-#pragma unroll
-                for (int q = 0; q < E; ++q) {
-                    const uint64_t key = key_of(f[q], (uint32_t)(first + j * (kBeamThreads * E) + q));
-                    if ((uint32_t)(key >> 32) >= least && key < last && key > m)
-                        m = key;
-                }
-            }
-            m = warp_max(m);
-            __syncthreads();
-            if (lane == 0)
-                kept[warp] = m;
-            __syncthreads();
-            last = kept[0];
-#pragma unroll
-            for (int q = 1; q < kBeamWarps; ++q)
-                last = kept[q] > last ? kept[q] : last;
-            if (threadIdx.x == 0)
-                out[2 + t] = last;
+                if (at + q < a.vocab)
+                    t += ex2f(kLog2e * (tidy(Codec<S>::load1(x + at + q), Logits<S>::most()) - top));
+            s += t;
         }
     }
-    if (threadIdx.x == 0) {
-        uint64_t sum = 0;
-#pragma unroll
-        for (int q = 0; q < kBeamWarps; ++q)
-            sum += (uint64_t)sum_low[q] + ((uint64_t)sum_high[q] << 20);
-        out[0] = sum;
-        out[1] = __float_as_uint(value_of(top)) | (uint64_t)(uint32_t)(by_power ? (int)power : kNoPower) << 32;
+    // the lanes' sums as whole numbers, whose sum has no order
+    const uint32_t high = (uint32_t)(s * 0x1p18f), low = (uint32_t)((s * 0x1p18f - (float)high) * 0x1p22f);
+    const uint32_t low_all = __reduce_add_sync(kFull, low), high_all = __reduce_add_sync(kFull, high);
+    uint64_t *stat = static_cast<uint64_t *>(a.scratch) + 2 * id;
+    uint32_t *groups = reinterpret_cast<uint32_t *>(static_cast<uint64_t *>(a.scratch) + 2 * rows * plan.spans) + id * plan.batches;
+    if (lane == 0) {
+        stat[0] = top == Lim<float>::lo() ? 0 : (uint64_t)low_all + ((uint64_t)high_all << 22);
+        stat[1] = __float_as_uint(top) | (uint64_t)(uint32_t)(top == Lim<float>::lo() ? kLeastPower : by_power ? (int)power : kNoPower) << 32;
     }
-}
-
-// 64-bit scores as unsigned numbers in the order of their values.
-__device__ __forceinline__ uint64_t order_of(double x) {
-    const uint64_t u = (uint64_t)__double_as_longlong(x);
-    return u >> 63 ? ~u : u | 1ull << 63;
-}
-__device__ __forceinline__ double score_of(uint64_t k) { return __longlong_as_double((long long)(k >> 63 ? k & ~(1ull << 63) : ~k)); }
-
-// The 32 largest of two lists that a warp holds in falling order, a key a lane.
-__device__ __forceinline__ uint64_t join_lists(uint64_t p, uint64_t q, int lane) {
-    const uint64_t o = __shfl_sync(kFull, q, 31 - lane);
-    p = o > p ? o : p;  // rising, then falling: sorted by halves
-#pragma unroll
-    for (int d = 16; d > 0; d /= 2) {
-        const uint64_t r = __shfl_xor_sync(kFull, p, d);
-        p = ((lane & d) == 0) == (r > p) ? r : p;
-    }
-    return p;
+    if (lane < plan.batches)
+        groups[lane] = mine;
 }
 
 // The logarithm of a beam's sum relative to its largest value: `sum` in units of 2^-30 relative to 2^power, or (kNoPower)
@@ -440,154 +297,303 @@ __device__ __forceinline__ double log_of_sum(uint64_t sum, int power, float top)
     return log((double)sum * 0x1p-30) + ((double)power - (double)top * (double)kLog2e) * 0.693147180559945309417;
 }
 
-// A warp a beam, and one more for the logarithms of all (64-bit arithmetic is slow here: a warp's instruction takes 16 clocks of
-// the SM, so a lane makes each beam's, not a warp).
-constexpr int kJoinAhead = 8;  // lists on their way
-__global__ void __launch_bounds__(32 * kBeamsMost) k_beam_join(const __grid_constant__ mt_beam_args a, BeamPlan plan) {
-    __shared__ uint64_t score[kBeamsMost][kBeamsMost];  // of each beam's first continuations, in order
-    __shared__ int32_t token[kBeamsMost][kBeamsMost];
+// A block of logits, or one, as it is chosen: by its score's number, then by the lower place. Score 0 is none.
+struct Choice {
+    uint64_t score, place;
+    __device__ __forceinline__ bool before(const Choice &o) const { return score > o.score || (score == o.score && place < o.place); }
+};
+constexpr int kChosen = 1024;  // that may reach the threshold
+constexpr int kPart = kJoinThreads / 32;  // threads that share a first choice, and that rank one
+struct ChooseShared {
+    Choice best[32], kept[kChosen], list[kBeamsMost];
+    Choice threshold;
+    int count;
+};
+__device__ __forceinline__ Choice first_of(Choice c, int lanes) {
+    for (int d = 1; d < lanes; d *= 2) {
+        const Choice o = {__shfl_xor_sync(kFull, c.score, d), __shfl_xor_sync(kFull, c.place, d)};
+        c = o.before(c) ? o : c;
+    }
+    return c;
+}
+// How many of n choices are before c, counted by the kPart threads that hold the same c.
+__device__ __forceinline__ int rank_of(const Choice &c, const Choice *of, int n) {
+    int before = 0;
+    for (int q = threadIdx.x % kPart; q < n; q += kPart)
+        before += of[q].before(c);
+#pragma unroll
+    for (int d = 1; d < kPart; d *= 2)
+        before += __shfl_xor_sync(kFull, before, d);
+    return before;
+}
+__device__ __forceinline__ void keep(ChooseShared &s, const Choice &c) {
+    const int at = atomicAdd(&s.count, 1);
+    if (at < kChosen)
+        s.kept[at] = c;
+}
+// The K first of the kept ones to s.list. A barrier before and one after.
+__device__ __forceinline__ void rank_kept(ChooseShared &s, int count, int K) {
+    for (int t0 = 0; t0 < count; t0 += 32) {
+        const int t = t0 + threadIdx.x / kPart;
+        const Choice c = t < count ? s.kept[t] : Choice{0, ~0ull};
+        const int before = rank_of(c, s.kept, count);
+        if (t < count && before < K && threadIdx.x % kPart == 0)
+            s.list[before] = c;
+    }
+}
+// The K first of get(0) .. get(n - 1), in order, in s.list; returns how many there are (K at most). A threshold that K of them
+// reach at least is the K-th of the first ones of 32 parts of the CTA; few others reach it, and where that is not so (in one
+// part, more than there is place for) they are taken one after the other. A barrier before it; ends with one.
+template <class F> __device__ __forceinline__ int choose(int64_t n, int K, ChooseShared &s, F get) {
+    const int tid = threadIdx.x, lane = tid % 32;
+    Choice mine = {0, ~0ull};
+    for (int64_t i = tid; i < n; i += kJoinThreads) {
+        const Choice c = get(i);
+        if (c.before(mine))
+            mine = c;
+    }
+    if (mine.score == 0)
+        mine.place = ~(uint64_t)tid;  // no two are equal
+    const Choice top = first_of(mine, kPart);
+    if (tid % kPart == 0)
+        s.best[tid / kPart] = top;
+    if (tid == 0)
+        s.count = 0;
+    __syncthreads();
+    if (rank_of(top, s.best, 32) == K - 1 && tid % kPart == 0)
+        s.threshold = top;
+    __syncthreads();
+    const Choice least = s.threshold;
+    if (mine.score != 0 && !least.before(mine))
+        for (int64_t i = tid; i < n; i += kJoinThreads) {
+            const Choice c = get(i);
+            if (c.score != 0 && !least.before(c))
+                keep(s, c);
+        }
+    __syncthreads();
+    const int count = s.count;
+    if (count <= kChosen) {
+        rank_kept(s, count, K);
+    } else {
+        Choice last = {~0ull, 0};
+        for (int t = 0; t < K; ++t) {
+            mine = {0, ~0ull};
+            for (int64_t i = tid; i < n; i += kJoinThreads) {
+                const Choice c = get(i);
+                if (last.before(c) && c.before(mine))
+                    mine = c;
+            }
+            mine = first_of(mine, 32);
+            if (lane == 0)
+                s.best[tid / 32] = mine;
+            __syncthreads();
+            last = first_of(s.best[lane % kJoinWarps], kJoinWarps);
+            if (tid == 0)
+                s.list[t] = last;
+            __syncthreads();
+        }
+    }
+    __syncthreads();
+    return count < K ? count : K;
+}
+
+template <class S, bool VEC> __global__ void __launch_bounds__(kJoinThreads) k_beam_join(const __grid_constant__ mt_beam_args a, BeamPlan plan) {
+    constexpr int E = Logits<S>::E;
+    __shared__ ChooseShared s;
     __shared__ uint64_t sums[kBeamsMost];
     __shared__ int powers[kBeamsMost];
-    __shared__ float tops[kBeamsMost];
-    __shared__ double less[kBeamsMost];  // the logarithms
+    __shared__ float priors[kBeamsMost], tops[kBeamsMost];
+    __shared__ float highs[kBeamsMost], lows[kBeamsMost];  // the scores of the beams' largest logits
+    __shared__ float cuts[kBeamsMost];
+    __shared__ uint64_t blocks[kBeamsMost];
+    __shared__ int32_t spare[kBeamsMost];
+    __shared__ uint32_t ended;  // beams that go on with their end alone
     pdl_prologue();
     const int64_t b = blockIdx.x;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, k = warp, chunks = (int)plan.chunks, beams = (int)a.beams;
-    const int K = (int)a.beams_out, n = (int)(a.vocab < K ? a.vocab : K);  // continuations of a beam that can matter
-    const int64_t row = b * a.beams + (k < beams ? k : 0);
-    const uint64_t *mine = static_cast<const uint64_t *>(a.scratch) + row * plan.chunks * plan.slots;
-    const float prior = a.prior != nullptr ? tidy(a.prior[row], 3.402823466e38f) : 0.0f;
-    const bool done = a.finished != nullptr && a.finished[row] != 0;
-    const bool reads = k < beams && !done && prior != Lim<float>::lo();
-    uint64_t list[kJoinAhead];
-    if (reads) {
-#pragma unroll
-        for (int q = 0; q < kJoinAhead; ++q)
-            list[q] = q < chunks && lane < K ? mine[q * plan.slots + 2 + lane] : 0;
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, beams = (int)a.beams, K = (int)a.beams_out;
+    const int spans = (int)plan.spans;
+    const uint64_t *stats = static_cast<const uint64_t *>(a.scratch) + 2 * b * beams * plan.spans;
+    const uint32_t *groups =
+        reinterpret_cast<const uint32_t *>(static_cast<const uint64_t *>(a.scratch) + 2 * a.batch * beams * plan.spans) + b * beams * plan.spans * plan.batches;
+    if (tid == 0)
+        ended = 0;
+    __syncthreads();
+    for (int k = warp; k < beams; k += kJoinWarps) {
+        const float prior = a.prior != nullptr ? tidy(a.prior[b * beams + k], 3.402823466e38f) : 0.0f;
+        const bool done = a.finished != nullptr && a.finished[b * beams + k] != 0;
+        const bool reads = !done && prior != Lim<float>::lo();
         float top = Lim<float>::lo();
         int power = kLeastPower;
         uint64_t sum = 0;
-        if (chunks <= 32) {
-            if (lane < chunks) {
-                sum = mine[lane * plan.slots];
-                const uint64_t o = mine[lane * plan.slots + 1];
-                top = __uint_as_float((uint32_t)o);
-                power = (int)(uint32_t)(o >> 32);
-            }
-        } else {
-            for (int c = lane; c < chunks; c += 32) {
-                const uint64_t o = mine[c * plan.slots + 1];
+        if (reads) {
+            const ulonglong2 *mine = reinterpret_cast<const ulonglong2 *>(stats) + (int64_t)k * spans;
+            const ulonglong2 one = lane < spans ? mine[lane] : make_ulonglong2(0, (uint64_t)(uint32_t)kLeastPower << 32 | 0xff800000u);
+            top = __uint_as_float((uint32_t)one.y);
+            power = (int)(uint32_t)(one.y >> 32);
+            const int own_power = power;
+            for (int c = lane + 32; c < spans; c += 32) {
+                const uint64_t o = mine[c].y;
                 top = fmaxf(top, __uint_as_float((uint32_t)o));
                 power = max(power, (int)(uint32_t)(o >> 32));
             }
-        }
-        const int own_power = power;
-        top = value_of(redux_max(order_of(top)));
-        power = __reduce_max_sync(kFull, power);
-        if (power == kNoPower) {  // far out: sums in 64 bits, relative to the largest value
-            double all = 0.0;
-            for (int c = lane; c < chunks; c += 32) {
-                const uint64_t o = mine[c * plan.slots + 1];
-                const double m = (double)__uint_as_float((uint32_t)o), s = (double)mine[c * plan.slots] * 0x1p-40;
-                const int p = (int)(uint32_t)(o >> 32);
-                if (p != kLeastPower)
-                    all += s * exp(m - (double)top + (p == kNoPower ? 0.0 : ((double)p - m * (double)kLog2e) * 0.693147180559945309417));
-            }
-            for (int o = 16; o > 0; o /= 2)
-                all += __shfl_xor_sync(kFull, all, o);
-            sum = (uint64_t)__double_as_longlong(all);
-        } else {
-            if (chunks <= 32) {
-                sum = sum >> 10 >> min(power - own_power, 53);
+            top = value_of(__reduce_max_sync(kFull, order_of(top)));
+            power = __reduce_max_sync(kFull, power);
+            if (power == kNoPower) {  // far out: sums in 64 bits, relative to the largest value
+                double all = 0.0;
+                for (int c = lane; c < spans; c += 32) {
+                    const ulonglong2 o = mine[c];
+                    const double m = (double)__uint_as_float((uint32_t)o.y);
+                    const int p = (int)(uint32_t)(o.y >> 32);
+                    if (p != kLeastPower)
+                        all += (double)o.x * 0x1p-40 * exp(m - (double)top + (p == kNoPower ? 0.0 : ((double)p - m * (double)kLog2e) * 0.693147180559945309417));
+                }
+                for (int o = 16; o > 0; o /= 2)
+                    all += __shfl_xor_sync(kFull, all, o);
+                sum = (uint64_t)__double_as_longlong(all);
             } else {
-                for (int c = lane; c < chunks; c += 32)
-                    sum += mine[c * plan.slots] >> 10 >> min(power - (int)(uint32_t)(mine[c * plan.slots + 1] >> 32), 53);
+                sum = one.x >> 10 >> min(power - own_power, 53);
+                for (int c = lane + 32; c < spans; c += 32)
+                    sum += mine[c].x >> 10 >> min(power - (int)(uint32_t)(mine[c].y >> 32), 53);
+                for (int o = 16; o > 0; o /= 2)
+                    sum += __shfl_xor_sync(kFull, sum, o);
             }
-            for (int o = 16; o > 0; o /= 2)
-                sum += __shfl_xor_sync(kFull, sum, o);
         }
         if (lane == 0) {
             sums[k] = sum;
             powers[k] = power;
             tops[k] = top;
+            priors[k] = prior;
+            if (done && prior != Lim<float>::lo())
+                atomicOr(&ended, 1u << k);
         }
-    } else if (k < beams && lane == 0) {
-        powers[k] = kLeastPower;
     }
     __syncthreads();
-    const int logs = blockDim.x / 32 - 1;  // the warp of the logarithms, a beam's own too where there are 32
-    if (warp == logs && lane < beams)
-        less[lane] = powers[lane] == kLeastPower ? 0.0 : log_of_sum(sums[lane], powers[lane], tops[lane]);
-    uint64_t key = 0;
-    if (reads && powers[k] != kLeastPower) {
-        for (int c0 = 0; c0 < chunks; c0 += kJoinAhead) {
+    // a lane makes each beam's logarithm, in 64 bits, not a warp
+    if (warp == 0 && lane < beams && powers[lane] != kLeastPower) {
+        const double best = (double)priors[lane] - log_of_sum(sums[lane], powers[lane], tops[lane]);
+        highs[lane] = (float)best;
+        lows[lane] = (float)(best - (double)(float)best);
+    }
+    __syncthreads();
+    auto score = [&](int k, float x) { return score_order(x, tops[k], highs[k], lows[k]); };
+    // places: the beam, and the group, vector or token in its row
+    const int per_beam = spans * plan.batches;
+    int n = choose((int64_t)beams * per_beam, K, s, [&](int64_t i) {
+        const int k = (int)i / per_beam, g = (int)i - k * per_beam;
+        Choice c = {0, (uint64_t)k << 32 | (uint32_t)g};
+        if (powers[k] != kLeastPower) {
+            const uint32_t o = groups[i];
+            if (o > kOrderLow)
+                c.score = score(k, value_of(o));
+        }
+        return c;
+    });
+    if (tid < n)
+        blocks[tid] = s.list[tid].place;
+    // What a logit has to reach for the last group's score, a little less for the roundings: the others' scores are not made.
+    if (tid < beams) {
+        const float last = score_of(s.list[K - 1].score), at = last - highs[tid];
+        cuts[tid] = n < K ? Lim<float>::lo() : tops[tid] + at - 1e-6f * (fabsf(at) + fabsf(last) + fabsf(highs[tid]) + fabsf(tops[tid]));
+    }
+    auto row_of = [&](int k) { return static_cast<const S *>(a.logits) + b * a.logits_batch + k * a.logits_beam; };
+    auto logit = [&](const S *x, int64_t at) { return tidy(Codec<S>::load1(x + at), Logits<S>::most()); };
+    auto choice = [&](int k, float x, uint32_t at) {
+        return Choice{x == Lim<float>::lo() || x < cuts[k] ? 0 : score(k, x + 0.0f), (uint64_t)k << 32 | at};
+    };
+    if (tid == 0)
+        s.count = 0;
+    __syncthreads();
+    // The logits of these groups that reach it, with the ends of beams that are finished: hardly more than beams_out.
+    for (int i = tid; i < n * kGroupVectors; i += kJoinThreads) {
+        const uint64_t block = blocks[i / kGroupVectors];
+        const int k = (int)(block >> 32);
+        const int64_t at = ((int64_t)(uint32_t)block * kGroupVectors + i % kGroupVectors) * E;
+        const S *x = row_of(k);
+        if (at >= a.vocab)
+            continue;
+        float f[E];
+        if constexpr (VEC) {
+            Codec<S>::unpack(*reinterpret_cast<const uint4 *>(x + at), f);
+        } else {
 #pragma unroll
-            for (int q = 0; q < kJoinAhead; ++q)
-                if (c0 + q < chunks) {
-                    key = c0 + q == 0 ? list[q] : join_lists(key, list[q], lane);
-                    const int c = c0 + q + kJoinAhead;
-                    list[q] = c < chunks && lane < K ? mine[c * plan.slots + 2 + lane] : 0;
-                }
+            for (int q = 0; q < E; ++q)
+                f[q] = at + q < a.vocab ? Codec<S>::load1(x + at + q) : Lim<float>::lo();
+        }
+        const float cut = cuts[k];
+#pragma unroll
+        for (int q = 0; q < E; ++q) {
+            if (f[q] < cut || f[q] == Lim<float>::lo())
+                continue;
+            const Choice c = choice(k, tidy(f[q], Logits<S>::most()), (uint32_t)(at + q));
+            if (c.score != 0)
+                keep(s, c);
         }
     }
+    if (tid < beams && (ended >> tid & 1u))
+        keep(s, {order_of(priors[tid], 0.0f), (uint64_t)tid << 32 | (uint32_t)a.eos});
     __syncthreads();
-    if (k < beams) {
-        const int has = __popc(__ballot_sync(kFull, key != 0));  // logits that may come next, as far as they matter
-        int32_t tok = (int32_t)~(uint32_t)key;
-        double s = Lim<double>::lo();
-        if (key != 0)
-            s = (double)prior + (((double)value_of((uint32_t)(key >> 32)) - (double)tops[k]) - less[k]);
-        if (done && prior != Lim<float>::lo()) {  // the end with the beam's score, then the other tokens in order
-            tok = lane == 0 ? (int)a.eos : lane - 1 < a.eos ? lane - 1 : lane;
-            if (lane == 0)
-                s = (double)prior;
-        } else if (has < n) {
-            // all that may come next is in the list: behind it the tokens that may not, in order
-            int next = 0;
-            for (int j = has; j < n; ++j, ++next) {
-                while (__any_sync(kFull, lane < has && tok == next))
-                    ++next;
-                if (lane == j)
-                    tok = next;
+    const int count = s.count;
+    if (count <= kChosen) {
+        rank_kept(s, count, K);
+        n = count < K ? count : K;
+        __syncthreads();
+    } else {
+        // Or there are many: of the groups' vectors the first ones, and of their logits.
+        n = choose((int64_t)n * kGroupVectors, K, s, [&](int64_t i) {
+            const uint64_t block = blocks[i / kGroupVectors];
+            const int k = (int)(block >> 32);
+            const uint32_t v = (uint32_t)block * kGroupVectors + (uint32_t)(i % kGroupVectors);
+            const int64_t at = (int64_t)v * E;
+            const S *x = row_of(k);
+            float m = Lim<float>::lo();
+#pragma unroll
+            for (int q = 0; q < E; ++q)
+                if (at + q < a.vocab)
+                    m = fmaxf(m, logit(x, at + q));
+            return choice(k, m, v);
+        });
+        if (tid < n)
+            blocks[tid] = s.list[tid].place;
+        __syncthreads();
+        const int logits = n * E;
+        n = choose((int64_t)logits + beams, K, s, [&](int64_t i) {
+            if (i >= logits) {
+                const int k = (int)i - logits;
+                return Choice{ended >> k & 1u ? order_of(priors[k], 0.0f) : 0, (uint64_t)k << 32 | (uint32_t)a.eos};
             }
-        }
-        if (lane < n) {
-            token[k][lane] = tok;
-            score[k][lane] = order_of(s);
-        }
+            const uint64_t block = blocks[i / E];
+            const int k = (int)(block >> 32);
+            const int64_t at = (int64_t)(uint32_t)block * E + i % E;
+            return choice(k, at < a.vocab ? logit(row_of(k), at) : Lim<float>::lo(), (uint32_t)at);
+        });
     }
-    __syncthreads();
     if (warp != 0)
         return;
-    // beams side by side, each with its best continuation that is left; of equal scores the lowest beam's
-    int at = 0, parent = 0, place = 0;
-    uint64_t best = 0;
-    for (int j = 0; j < K; ++j) {
-        const bool has = lane < a.beams && at < n;
-        const uint64_t s = has ? score[lane][at] : 0ull;  // 0 is below every score's number
-        const uint64_t m = warp_max(s);
-        const int from = __ffs(__ballot_sync(kFull, has && s == m)) - 1;
-        const int its = __shfl_sync(kFull, at, from);
-        if (lane == j) {
-            best = m;
-            parent = from;
-            place = its;
+    const Choice chosen = lane < n ? s.list[lane] : Choice{order_of(Lim<float>::lo(), 0.0f), 0};
+    int parent = (int)(chosen.place >> 32), tok = (int)(uint32_t)chosen.place;
+    if (n < K) {  // behind all that may come next what may not, in order
+        int64_t next = 0;
+        for (int j = n; j < K; ++j, ++next) {
+            while (__any_sync(kFull, lane < n && parent * a.vocab + tok == next))
+                ++next;
+            if (lane == j) {
+                parent = (int)(next / a.vocab);
+                tok = (int)(next % a.vocab);
+            }
         }
-        at += lane == from;
     }
-    const int tok = token[parent][place];
     const bool out = lane < K;
     const int64_t to = b * K + lane;
-    const bool ended = a.finished != nullptr && out && a.finished[b * a.beams + parent] != 0;
+    const bool was = a.finished != nullptr && out && a.finished[b * a.beams + parent] != 0;
     const int group = (int)(a.beams > K ? a.beams : K);
     const int32_t slot = a.slots != nullptr && lane < group ? a.slots[b * group + lane] : 0;
     __syncwarp();
     if (out) {
         a.tokens[to] = tok;
         a.parents[to] = parent;
-        a.scores[to] = (float)score_of(best);
+        a.scores[to] = score_of(chosen.score);
         if (a.finished_out != nullptr)
-            a.finished_out[to] = ended || tok == a.eos;
+            a.finished_out[to] = was || tok == a.eos;
     }
     if (a.slots == nullptr)
         return;
@@ -599,9 +605,9 @@ __global__ void __launch_bounds__(32 * kBeamsMost) k_beam_join(const __grid_cons
     const int32_t old = __shfl_sync(kFull, slot, parent);
     // the lanes that move, and those behind the beams, take the free slots in order
     if (free >> lane & 1u)
-        token[0][__popc(free & ((1u << lane) - 1))] = slot;
+        spare[__popc(free & ((1u << lane) - 1))] = slot;
     __syncwarp();
-    const int32_t fresh = token[0][__popc(moving & ((1u << lane) - 1)) & 31];
+    const int32_t fresh = spare[__popc(moving & ((1u << lane) - 1)) & 31];
     if (lane < group)
         a.slots[b * group + lane] = stays ? old : fresh;
     if (out) {
@@ -610,35 +616,32 @@ __global__ void __launch_bounds__(32 * kBeamsMost) k_beam_join(const __grid_cons
     }
 }
 
-template <class S, int PER, bool VEC> cudaError_t launch_chunks(const mt_beam_args &a, const BeamPlan &plan, unsigned blocks, const Launch &L) {
-    static PerDevice ready;
-    constexpr int smem = kBeamThreads * PER * (int)sizeof(S);
-    const cudaError_t e = allow_shared(k_beam_chunk<S, PER, VEC>, smem, ready);
-    if (e != cudaSuccess)
-        return e;
-    note_launch();
-    return launch_pdl(k_beam_chunk<S, PER, VEC>, blocks, kBeamThreads, smem, L.stream, a, plan);
-}
 template <class S> cudaError_t launch(const mt_beam_args &a, const Launch &L) {
-    const BeamPlan plan = beam_plan(a.batch * a.beams, a.beams_out, a.vocab);
-    const int64_t blocks = a.batch * a.beams * plan.chunks, vector = Logits<S>::E;
-    if (blocks > INT32_MAX)
+    const BeamPlan plan = beam_plan(a.batch * a.beams, a.vocab, sizeof(S));
+    const int64_t vector = Logits<S>::E, warps = kBeamThreads / 32, blocks = (a.batch * a.beams * plan.spans + warps - 1) / warps;
+    if (blocks > INT32_MAX || a.batch > INT32_MAX)
         return cudaErrorInvalidValue;
     const bool vec = (uintptr_t)a.logits % 16 == 0 && a.vocab % vector == 0 && a.logits_batch % vector == 0 && a.logits_beam % vector == 0;
-    const unsigned n = (unsigned)blocks;
-    const cudaError_t e = plan.per_thread == 64 ? (vec ? launch_chunks<S, 64, true>(a, plan, n, L) : launch_chunks<S, 64, false>(a, plan, n, L))
-                                                : (vec ? launch_chunks<S, 16, true>(a, plan, n, L) : launch_chunks<S, 16, false>(a, plan, n, L));
+    note_launch();
+    const cudaError_t e = vec ? launch_pdl(k_beam_read<S, true>, (unsigned)blocks, kBeamThreads, 0, L.stream, a, plan)
+                              : launch_pdl(k_beam_read<S, false>, (unsigned)blocks, kBeamThreads, 0, L.stream, a, plan);
     if (e != cudaSuccess)
         return e;
     note_launch();
-    return launch_pdl(k_beam_join, (unsigned)a.batch, (unsigned)(32 * (a.beams < kBeamsMost ? a.beams + 1 : kBeamsMost)), 0, L.stream, a, plan);
+    return vec ? launch_pdl(k_beam_join<S, true>, (unsigned)a.batch, kJoinThreads, 0, L.stream, a, plan)
+               : launch_pdl(k_beam_join<S, false>, (unsigned)a.batch, kJoinThreads, 0, L.stream, a, plan);
 }
 
 }  // namespace
 
-int64_t beam_scratch_slots(int64_t batch, int64_t beams, int64_t beams_out, int64_t vocab) {
-    const BeamPlan plan = beam_plan(batch * beams, beams_out, vocab);
-    return batch * beams * plan.chunks * plan.slots;
+int64_t beam_scratch_slots(int64_t batch, int64_t beams, int64_t, int64_t vocab) {
+    int64_t most = 0;  // of the types
+    for (const int64_t size : {2, 4}) {
+        const BeamPlan plan = beam_plan(batch * beams, vocab, size);
+        const int64_t slots = batch * beams * plan.spans * 2 + (batch * beams * plan.spans * plan.batches + 1) / 2;
+        most = slots > most ? slots : most;
+    }
+    return most;
 }
 
 cudaError_t beam_launch(const mt_beam_args &a, const Launch &L) {
