@@ -213,22 +213,34 @@ __device__ __forceinline__ uint32_t read_span(Part<S> &part, const S *x, int64_t
     constexpr int E = Logits<S>::E;
     const int64_t first = begin + lane * E;
     uint32_t mine = kOrderLow;
-    uint4 w[2][kBatch];
-#pragma unroll
-    for (int j = 0; j < kBatch; ++j)
-        w[0][j] = load_logits<S, WORDS>(x, first + j * (32 * E), vocab, half);
+    if constexpr (WORDS >= 0) {  // a vector comes from two, which would have to be there before they are one: no batch ahead, more warps
 #pragma unroll 1
-    for (int t = 0; t < batches; t += 2) {
+        for (int t = 0; t < batches; ++t) {
+            uint4 w[kBatch];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            if (t + u < batches) {
-                if (t + u + 1 < batches) {
+            for (int j = 0; j < kBatch; ++j)
+                w[j] = load_logits<S, WORDS>(x, first + (t * kBatch + j) * (32 * E), vocab, half);
+            const uint32_t m = __reduce_max_sync(kFull, order_of(part.add(w) + 0.0f));
+            mine = lane == t ? m : mine;
+        }
+    } else {
+        uint4 w[2][kBatch];
 #pragma unroll
-                    for (int j = 0; j < kBatch; ++j)
-                        w[1 - u][j] = load_logits<S, WORDS>(x, first + ((t + u + 1) * kBatch + j) * (32 * E), vocab, half);
+        for (int j = 0; j < kBatch; ++j)
+            w[0][j] = load_logits<S, WORDS>(x, first + j * (32 * E), vocab, half);
+#pragma unroll 1
+        for (int t = 0; t < batches; t += 2) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                if (t + u < batches) {
+                    if (t + u + 1 < batches) {
+#pragma unroll
+                        for (int j = 0; j < kBatch; ++j)
+                            w[1 - u][j] = load_logits<S, WORDS>(x, first + ((t + u + 1) * kBatch + j) * (32 * E), vocab, half);
+                    }
+                    const uint32_t m = __reduce_max_sync(kFull, order_of(part.add(w[u]) + 0.0f));
+                    mine = lane == t + u ? m : mine;
                 }
-                const uint32_t m = __reduce_max_sync(kFull, order_of(part.add(w[u]) + 0.0f));
-                mine = lane == t + u ? m : mine;
             }
         }
     }
@@ -303,6 +315,7 @@ struct Choice {
     __device__ __forceinline__ bool before(const Choice &o) const { return score > o.score || (score == o.score && place < o.place); }
 };
 constexpr int kChosen = 1024;  // that may reach the threshold
+constexpr int kAhead = 4;                 // vectors of a thread on their way
 constexpr int kPart = kJoinThreads / 32;  // threads that share a first choice, and that rank one
 struct ChooseShared {
     Choice best[32], kept[kChosen], list[kBeamsMost];
@@ -347,6 +360,7 @@ __device__ __forceinline__ void rank_kept(ChooseShared &s, int count, int K) {
 template <class F> __device__ __forceinline__ int choose(int64_t n, int K, ChooseShared &s, F get) {
     const int tid = threadIdx.x, lane = tid % 32;
     Choice mine = {0, ~0ull};
+#pragma unroll 4
     for (int64_t i = tid; i < n; i += kJoinThreads) {
         const Choice c = get(i);
         if (c.before(mine))
@@ -407,7 +421,7 @@ template <class S, bool VEC> __global__ void __launch_bounds__(kJoinThreads) k_b
     __shared__ float cuts[kBeamsMost];
     __shared__ uint64_t blocks[kBeamsMost];
     __shared__ int32_t spare[kBeamsMost];
-    __shared__ uint32_t ended;  // beams that go on with their end alone
+    __shared__ uint32_t finished, ended;  // finished beams, and those of them that go on
     pdl_prologue();
     const int64_t b = blockIdx.x;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, beams = (int)a.beams, K = (int)a.beams_out;
@@ -416,9 +430,13 @@ template <class S, bool VEC> __global__ void __launch_bounds__(kJoinThreads) k_b
     const uint32_t *groups =
         reinterpret_cast<const uint32_t *>(static_cast<const uint64_t *>(a.scratch) + 2 * a.batch * beams * plan.spans) + b * beams * plan.spans * plan.batches;
     if (tid == 0)
-        ended = 0;
+        finished = ended = 0;
+    const int group = beams > K ? beams : K;
+    const int32_t slot = a.slots != nullptr && tid < group ? a.slots[b * group + tid] : 0;
     __syncthreads();
     for (int k = warp; k < beams; k += kJoinWarps) {
+        const ulonglong2 *mine = reinterpret_cast<const ulonglong2 *>(stats) + (int64_t)k * spans;
+        const ulonglong2 one = lane < spans ? mine[lane] : make_ulonglong2(0, (uint64_t)(uint32_t)kLeastPower << 32 | 0xff800000u);
         const float prior = a.prior != nullptr ? tidy(a.prior[b * beams + k], 3.402823466e38f) : 0.0f;
         const bool done = a.finished != nullptr && a.finished[b * beams + k] != 0;
         const bool reads = !done && prior != Lim<float>::lo();
@@ -426,8 +444,6 @@ template <class S, bool VEC> __global__ void __launch_bounds__(kJoinThreads) k_b
         int power = kLeastPower;
         uint64_t sum = 0;
         if (reads) {
-            const ulonglong2 *mine = reinterpret_cast<const ulonglong2 *>(stats) + (int64_t)k * spans;
-            const ulonglong2 one = lane < spans ? mine[lane] : make_ulonglong2(0, (uint64_t)(uint32_t)kLeastPower << 32 | 0xff800000u);
             top = __uint_as_float((uint32_t)one.y);
             power = (int)(uint32_t)(one.y >> 32);
             const int own_power = power;
@@ -463,6 +479,8 @@ template <class S, bool VEC> __global__ void __launch_bounds__(kJoinThreads) k_b
             powers[k] = power;
             tops[k] = top;
             priors[k] = prior;
+            if (done)
+                atomicOr(&finished, 1u << k);
             if (done && prior != Lim<float>::lo())
                 atomicOr(&ended, 1u << k);
         }
@@ -480,13 +498,8 @@ template <class S, bool VEC> __global__ void __launch_bounds__(kJoinThreads) k_b
     const int per_beam = spans * plan.batches;
     int n = choose((int64_t)beams * per_beam, K, s, [&](int64_t i) {
         const int k = (int)i / per_beam, g = (int)i - k * per_beam;
-        Choice c = {0, (uint64_t)k << 32 | (uint32_t)g};
-        if (powers[k] != kLeastPower) {
-            const uint32_t o = groups[i];
-            if (o > kOrderLow)
-                c.score = score(k, value_of(o));
-        }
-        return c;
+        const uint32_t o = groups[i];  // of a beam that was not read it is not looked at
+        return Choice{powers[k] != kLeastPower && o > kOrderLow ? score(k, value_of(o)) : 0, (uint64_t)k << 32 | (uint32_t)g};
     });
     if (tid < n)
         blocks[tid] = s.list[tid].place;
@@ -504,29 +517,38 @@ template <class S, bool VEC> __global__ void __launch_bounds__(kJoinThreads) k_b
         s.count = 0;
     __syncthreads();
     // The logits of these groups that reach it, with the ends of beams that are finished: hardly more than beams_out.
-    for (int i = tid; i < n * kGroupVectors; i += kJoinThreads) {
-        const uint64_t block = blocks[i / kGroupVectors];
-        const int k = (int)(block >> 32);
-        const int64_t at = ((int64_t)(uint32_t)block * kGroupVectors + i % kGroupVectors) * E;
-        const S *x = row_of(k);
-        if (at >= a.vocab)
-            continue;
-        float f[E];
-        if constexpr (VEC) {
-            Codec<S>::unpack(*reinterpret_cast<const uint4 *>(x + at), f);
-        } else {
+    for (int i0 = tid; i0 < n * kGroupVectors; i0 += kJoinThreads * kAhead) {
+        float f[kAhead][E];
+        int64_t at[kAhead];
+        int k[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int i = i0 + u * kJoinThreads;
+            const uint64_t block = i < n * kGroupVectors ? blocks[i / kGroupVectors] : 0;
+            k[u] = (int)(block >> 32);
+            at[u] = i < n * kGroupVectors ? ((int64_t)(uint32_t)block * kGroupVectors + i % kGroupVectors) * E : a.vocab;
+            const S *x = row_of(k[u]) + at[u];
+            if (VEC && at[u] < a.vocab) {
+                Codec<S>::unpack(*reinterpret_cast<const uint4 *>(x), f[u]);
+            } else {
+#pragma unroll
+                for (int q = 0; q < E; ++q)
+                    f[u][q] = at[u] + q < a.vocab ? Codec<S>::load1(x + q) : Lim<float>::lo();
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const float cut = cuts[k[u]];
+            uint32_t reach = 0;
 #pragma unroll
             for (int q = 0; q < E; ++q)
-                f[q] = at + q < a.vocab ? Codec<S>::load1(x + at + q) : Lim<float>::lo();
-        }
-        const float cut = cuts[k];
-#pragma unroll
-        for (int q = 0; q < E; ++q) {
-            if (f[q] < cut || f[q] == Lim<float>::lo())
-                continue;
-            const Choice c = choice(k, tidy(f[q], Logits<S>::most()), (uint32_t)(at + q));
-            if (c.score != 0)
-                keep(s, c);
+                reach |= !(f[u][q] < cut) && f[u][q] != Lim<float>::lo() ? 1u << q : 0u;
+            for (; reach != 0; reach &= reach - 1) {
+                const int q = __ffs(reach) - 1;
+                const Choice c = choice(k[u], logit(row_of(k[u]), at[u] + q), (uint32_t)(at[u] + q));
+                if (c.score != 0)
+                    keep(s, c);
+            }
         }
     }
     if (tid < beams && (ended >> tid & 1u))
@@ -584,16 +606,12 @@ template <class S, bool VEC> __global__ void __launch_bounds__(kJoinThreads) k_b
     }
     const bool out = lane < K;
     const int64_t to = b * K + lane;
-    const bool was = a.finished != nullptr && out && a.finished[b * a.beams + parent] != 0;
-    const int group = (int)(a.beams > K ? a.beams : K);
-    const int32_t slot = a.slots != nullptr && lane < group ? a.slots[b * group + lane] : 0;
-    __syncwarp();
     if (out) {
         a.tokens[to] = tok;
         a.parents[to] = parent;
         a.scores[to] = score_of(chosen.score);
         if (a.finished_out != nullptr)
-            a.finished_out[to] = was || tok == a.eos;
+            a.finished_out[to] = (finished >> parent & 1u) != 0 || tok == a.eos;
     }
     if (a.slots == nullptr)
         return;
