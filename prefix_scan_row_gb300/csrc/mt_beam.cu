@@ -301,12 +301,59 @@ template <class S, bool VEC> __global__ void __launch_bounds__(kBeamThreads) k_b
         groups[lane] = mine;
 }
 
-// The logarithm of a beam's sum relative to its largest value: `sum` in units of 2^-30 relative to 2^power, or (kNoPower)
-// a double relative to exp(top). The terms' exponents are x log2(e) with log2(e) as f32, so top's is taken the same.
-__device__ __forceinline__ double log_of_sum(uint64_t sum, int power, float top) {
-    if (power == kNoPower)
-        return log(__longlong_as_double((long long)sum));
-    return log((double)sum * 0x1p-30) + ((double)power - (double)top * (double)kLog2e) * 0.693147180559945309417;
+// Logarithms of c = 1 - j / 128, j below 64, as f32 pairs: the series of 2 atanh((c - 1) / (c + 1)), summed by the compiler.
+struct LogTable {
+    float high[64], low[64];
+    constexpr LogTable() : high(), low() {
+        for (int j = 0; j < 64; ++j) {
+            const double c = 1.0 - j / 128.0, r = (c - 1.0) / (c + 1.0);
+            double sum = 0.0, power = r;
+            for (int k = 1; k < 60; k += 2) {
+                sum += power / k;
+                power *= r * r;
+            }
+            high[j] = (float)(2.0 * sum);
+            low[j] = (float)(2.0 * sum - (double)(float)(2.0 * sum));
+        }
+    }
+};
+__constant__ LogTable kLogTable = LogTable();
+
+// The score of a beam's largest logit, as a pair: prior - log(sum of exp(x - top)), with `sum` in units of 2^-30 relative to 2^power
+// (the terms' exponents are x log2(e) with log2(e) as f32, so top's is taken the same), or (kNoPower) a double.
+// In f32 pairs, good to 2e-9 (64-bit arithmetic's latency made 1.7 of the join's 7.7 us): with c of 7 bits next to 1 / m,
+// log(2^e m) = e log(2) - log(c) + log(c m), whose last argument is within 1/128 of 1.
+__device__ __forceinline__ void best_score(float prior, uint64_t sum, int power, float top, float &high, float &low) {
+    if (power == kNoPower) {
+        const double s = (double)prior - log(__longlong_as_double((long long)sum));
+        high = (float)s;
+        low = (float)(s - (double)high);
+        return;
+    }
+    const int e = 63 - __clzll((long long)sum);
+    const uint64_t bits = sum << (63 - e);  // m = bits / 2^63
+    const float m_high = (float)(uint32_t)(bits >> 40) * 0x1p-23f, m_low = (float)(uint32_t)(bits >> 16 & 0xffffffu) * 0x1p-47f;
+    const int j = 128 - (int)rintf(128.0f * rcpf(m_high));  // 0 to 64
+    const int at = j < 63 ? j : 63;
+    const float c = 1.0f - (float)at * 0.0078125f, p = m_high * c, z = (p - 1.0f) + fmaf(m_high, c, -p) + m_low * c;
+    float log1 = fmaf(z, 1.0f / 7.0f, -1.0f / 6.0f);  // log(1 + z) - z
+    log1 = fmaf(log1, z, 0.2f);
+    log1 = fmaf(log1, z, -0.25f);
+    log1 = fmaf(log1, z, 1.0f / 3.0f);
+    log1 = fmaf(log1, z, -0.5f) * z * z;
+    // (power - log2(e) top) log(2), exactly but for its last rounding; and e log(2), whose first part has few bits
+    const float t = kLog2e * top, d = (float)power - t, d_low = -fmaf(kLog2e, top, -t);
+    const float w = d * kLn2, w_low = fmaf(d, kLn2, -w) + (d * -1.90465421e-9f + d_low * kLn2);
+    const float f = (float)(e - 30), e_high = f * 0.693359375f, e_low = f * -2.12194440e-4f;
+    float r0, r1, r2, r3, s = two_sum(prior, -e_high, r0);
+    s = two_sum(s, kLogTable.high[at], r1);
+    s = two_sum(s, -z, r2);
+    s = two_sum(s, -w, r3);
+    const float rest = (r0 + r1) + (r2 + r3) + ((kLogTable.low[at] - e_low) - (log1 + w_low));
+    high = s + rest;
+    low = rest - (high - s);
+    if (!(fabsf(s) < Lim<float>::hi()))
+        low = 0.0f;
 }
 
 // A block of logits, or one, as it is chosen: by its score's number, then by the lower place. Score 0 is none.
@@ -378,12 +425,16 @@ template <class F> __device__ __forceinline__ int choose(int64_t n, int K, Choos
         s.threshold = top;
     __syncthreads();
     const Choice least = s.threshold;
-    if (mine.score != 0 && !least.before(mine))
+    if (n <= kJoinThreads) {  // a thread had one
+        if (mine.score != 0 && !least.before(mine))
+            keep(s, mine);
+    } else if (mine.score != 0 && !least.before(mine)) {
         for (int64_t i = tid; i < n; i += kJoinThreads) {
             const Choice c = get(i);
             if (c.score != 0 && !least.before(c))
                 keep(s, c);
         }
+    }
     __syncthreads();
     const int count = s.count;
     if (count <= kChosen) {
@@ -436,7 +487,11 @@ template <class S, bool VEC> __global__ void __launch_bounds__(kJoinThreads) k_b
     __syncthreads();
     for (int k = warp; k < beams; k += kJoinWarps) {
         const ulonglong2 *mine = reinterpret_cast<const ulonglong2 *>(stats) + (int64_t)k * spans;
-        const ulonglong2 one = lane < spans ? mine[lane] : make_ulonglong2(0, (uint64_t)(uint32_t)kLeastPower << 32 | 0xff800000u);
+        const ulonglong2 none = make_ulonglong2(0, (uint64_t)(uint32_t)kLeastPower << 32 | 0xff800000u);
+        ulonglong2 own[kAhead];  // those of the first spans, on their way before it is known whether they count
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            own[u] = lane + 32 * u < spans ? mine[lane + 32 * u] : none;
         const float prior = a.prior != nullptr ? tidy(a.prior[b * beams + k], 3.402823466e38f) : 0.0f;
         const bool done = a.finished != nullptr && a.finished[b * beams + k] != 0;
         const bool reads = !done && prior != Lim<float>::lo();
@@ -444,32 +499,34 @@ template <class S, bool VEC> __global__ void __launch_bounds__(kJoinThreads) k_b
         int power = kLeastPower;
         uint64_t sum = 0;
         if (reads) {
-            top = __uint_as_float((uint32_t)one.y);
-            power = (int)(uint32_t)(one.y >> 32);
-            const int own_power = power;
-            for (int c = lane + 32; c < spans; c += 32) {
-                const uint64_t o = mine[c].y;
-                top = fmaxf(top, __uint_as_float((uint32_t)o));
-                power = max(power, (int)(uint32_t)(o >> 32));
-            }
+            auto top_of = [](const ulonglong2 &o) { return __uint_as_float((uint32_t)o.y); };
+            auto power_in = [](const ulonglong2 &o) { return (int)(uint32_t)(o.y >> 32); };
+            auto each = [&](auto f) {
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u)
+                    f(own[u]);
+                for (int c = lane + 32 * kAhead; c < spans; c += 32)
+                    f(mine[c]);
+            };
+            each([&](const ulonglong2 &o) {
+                top = fmaxf(top, top_of(o));
+                power = max(power, power_in(o));
+            });
             top = value_of(__reduce_max_sync(kFull, order_of(top)));
             power = __reduce_max_sync(kFull, power);
             if (power == kNoPower) {  // far out: sums in 64 bits, relative to the largest value
                 double all = 0.0;
-                for (int c = lane; c < spans; c += 32) {
-                    const ulonglong2 o = mine[c];
-                    const double m = (double)__uint_as_float((uint32_t)o.y);
-                    const int p = (int)(uint32_t)(o.y >> 32);
+                each([&](const ulonglong2 &o) {
+                    const double m = (double)top_of(o);
+                    const int p = power_in(o);
                     if (p != kLeastPower)
                         all += (double)o.x * 0x1p-40 * exp(m - (double)top + (p == kNoPower ? 0.0 : ((double)p - m * (double)kLog2e) * 0.693147180559945309417));
-                }
+                });
                 for (int o = 16; o > 0; o /= 2)
                     all += __shfl_xor_sync(kFull, all, o);
                 sum = (uint64_t)__double_as_longlong(all);
             } else {
-                sum = one.x >> 10 >> min(power - own_power, 53);
-                for (int c = lane + 32; c < spans; c += 32)
-                    sum += mine[c].x >> 10 >> min(power - (int)(uint32_t)(mine[c].y >> 32), 53);
+                each([&](const ulonglong2 &o) { sum += o.x >> 10 >> min(power - power_in(o), 53); });
                 for (int o = 16; o > 0; o /= 2)
                     sum += __shfl_xor_sync(kFull, sum, o);
             }
@@ -486,12 +543,9 @@ template <class S, bool VEC> __global__ void __launch_bounds__(kJoinThreads) k_b
         }
     }
     __syncthreads();
-    // a lane makes each beam's logarithm, in 64 bits, not a warp
-    if (warp == 0 && lane < beams && powers[lane] != kLeastPower) {
-        const double best = (double)priors[lane] - log_of_sum(sums[lane], powers[lane], tops[lane]);
-        highs[lane] = (float)best;
-        lows[lane] = (float)(best - (double)(float)best);
-    }
+    // a lane makes each beam's logarithm
+    if (warp == 0 && lane < beams && powers[lane] != kLeastPower)
+        best_score(priors[lane], sums[lane], powers[lane], tops[lane], highs[lane], lows[lane]);
     __syncthreads();
     auto score = [&](int k, float x) { return score_order(x, tops[k], highs[k], lows[k]); };
     // places: the beam, and the group, vector or token in its row
@@ -545,7 +599,11 @@ template <class S, bool VEC> __global__ void __launch_bounds__(kJoinThreads) k_b
                 reach |= !(f[u][q] < cut) && f[u][q] != Lim<float>::lo() ? 1u << q : 0u;
             for (; reach != 0; reach &= reach - 1) {
                 const int q = __ffs(reach) - 1;
-                const Choice c = choice(k[u], logit(row_of(k[u]), at[u] + q), (uint32_t)(at[u] + q));
+                float x = f[u][0];
+#pragma unroll
+                for (int o = 1; o < E; ++o)
+                    x = q == o ? f[u][o] : x;
+                const Choice c = choice(k[u], tidy(x, Logits<S>::most()), (uint32_t)(at[u] + q));
                 if (c.score != 0)
                     keep(s, c);
             }
