@@ -6,6 +6,7 @@
 
 #include "mt_internal.h"
 #include "mt_scan.h"
+#include "mt_seq.h"
 
 namespace mt {
 
@@ -414,9 +415,10 @@ extern "C" int mt_scan_status(void *stream) {
     if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess)
         return MT_ERR_CUDA;
     int worst = MT_OK;
-    cudaError_t (*takers[9])(int *) = {rows_take_error,   rows_minmax_take_error, rows_mul_take_error,
-                                       scan1d_take_error, scan1d_ext_take_error,  select_take_error,
-                                       rbk_take_error,    noalloc_take_error,     reduce_take_error};
+    cudaError_t (*takers[])(int *) = {
+        rows_take_error,      rows_minmax_take_error, rows_mul_take_error,   scan1d_take_error,         scan1d_ext_take_error,
+        select_take_error,    rbk_take_error,         noalloc_take_error,    reduce_take_error,         gated_f32_take_error,
+        gated_bf16_take_error, gated_f16_take_error,  gated_grad_f32_take_error, gated_grad_bf16_take_error, gated_grad_f16_take_error};
     for (auto take : takers) {
         int code = 0;
         if (take(&code) != cudaSuccess)

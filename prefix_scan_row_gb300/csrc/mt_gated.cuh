@@ -18,7 +18,7 @@
 // a register pair; it makes the decays and inputs of its tokens, and their product and sum as one element of the
 // scan. The elements meet in shared memory, those of a cluster's CTAs in each other's, and each warp then
 // knows its first state and finishes its tokens, whose decays and inputs are still in registers. Nothing is
-// computed or read twice, and no CTA waits for one that may not be resident.
+// computed or read twice. A cluster's CTAs are resident together, so their waits for one another end.
 #pragma once
 
 #include "mt_seq.cuh"
@@ -55,11 +55,19 @@ __device__ __forceinline__ unsigned cluster_rank() {
 }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-// Two pairs to the same place in another CTA's shared memory.
-__device__ __forceinline__ void cluster_put(uint32_t here, unsigned rank, f32x2 a, f32x2 b) {
-    uint32_t there;
+// Two pairs to the same place in another CTA's shared memory, counted by the barrier at the same place there: data and
+// signal go one way together, where stores and a barrier of the cluster go there, back, and there again.
+__device__ __forceinline__ void cluster_send(uint32_t here, uint32_t bar_here, unsigned rank, f32x2 a, f32x2 b) {
+    uint32_t there, bar;
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(here), "r"(rank));
-    asm volatile("st.shared::cluster.v2.u64 [%0], {%1, %2};" :: "r"(there), "l"(a), "l"(b) : "memory");
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(bar) : "r"(bar_here), "r"(rank));
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b64 [%0], {%1, %2}, [%3];"
+                 :: "r"(there), "l"(a), "l"(b), "r"(bar) : "memory");
+}
+// Until all CTAs' elements are here; a wait that gives up is reported as the look-back's are.
+__device__ __forceinline__ void cluster_await(uint64_t *bar, uint32_t parity) {
+    if (!mbar_wait(bar, parity, kCopyWaitLimit))
+        atomicCAS(&g_mt_err, 0, kErrTimeout);
 }
 
 // ---- a pair of channels ---------------------------------------------------------------------------
@@ -126,10 +134,10 @@ __device__ __forceinline__ void decay_2f(f32x2 u, f32x2 &a, f32x2 &q) {
 }
 // 1 / sqrt(q), q counting as `least` at least
 __device__ __forceinline__ f32x2 rsqrt_least_2f(f32x2 q, f32x2 least = both(kLeast)) { return rsqrt_2f(max2f(q, least)); }
-// sqrt(q) sigma(i) = q / sqrt(q (1 + e)^2) with e = exp(-i): one root for both. e is kept below 2^60, so sigma(i) is 2^-60 at least.
+// sqrt(q) sigma(i) = q / sqrt(q (1 + e)^2) with e = exp(-i): one root for both; 0 where (1 + e)^2 is out of range (i below -44).
 __device__ __forceinline__ f32x2 root_sigmoid_2f(f32x2 q, f32x2 i) {
-    const f32x2 n = add2f(both(1.0f), least_2f(ex2_2f(mul2f(both(-kLog2e), i)), 0x1p60f));
-    return mul2f(q, rsqrt_least_2f(mul2f(mul2f(q, n), n)));
+    const f32x2 n = add2f(both(1.0f), ex2_2f(mul2f(both(-kLog2e), i)));
+    return mul2f(q, rsqrt_2f(mul2f(mul2f(max2f(q, both(kLeast)), n), n)));
 }
 
 // ---- rows of activations --------------------------------------------------------------------------
@@ -271,8 +279,8 @@ template <class S, bool VEC> struct FwdShared {
     static constexpr int kBytes = kGatedWarps * kWarp;
 };
 
-// IN and Z: the call has an input gate, an output gate (VEC; other rows ask at run time).
-template <class S, bool RATE, bool VEC, bool IN, bool Z>
+// IN and Z: the call has an input gate, an output gate; CLUSTER: CTAs share the tokens (VEC; other rows ask at run time).
+template <class S, bool RATE, bool VEC, bool IN, bool Z, bool CLUSTER>
 __global__ void __launch_bounds__(kGatedThreads, 2) k_gated(const __grid_constant__ GatedArgs g) {
     using In = Tile<S, kFwdT, VEC>;
     using Shared = FwdShared<S, VEC>;
@@ -280,13 +288,21 @@ __global__ void __launch_bounds__(kGatedThreads, 2) k_gated(const __grid_constan
     extern __shared__ __align__(16) char staged[];
     __shared__ Element of_warps[2][kGatedWarps][32];
     __shared__ Element of_ctas[2][8][32];
-    if (g.ctas > 1)
-        cluster_arrive();  // waited for below: no CTA writes into one that has not begun
+    __shared__ __align__(8) uint64_t arrived[2];  // of_ctas is complete
+    const int ctas = VEC && !CLUSTER ? 1 : g.ctas;
+    if (ctas > 1) {
+        if (threadIdx.x == 0) {
+            mbar_init(&arrived[0], 1);
+            mbar_init(&arrived[1], 1);
+            fence_mbar_init();
+        }
+        cluster_arrive();  // waited for below: no CTA sends to one that has not begun
+    }
     pdl_prologue();
     const mt_gated_args &p = g.p;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int rank = g.ctas > 1 ? (int)cluster_rank() : 0;
-    const int64_t unit = blockIdx.x / g.ctas, b = unit / g.slabs, c0 = (unit - b * g.slabs) * kGatedSlab;
+    const int rank = ctas > 1 ? (int)cluster_rank() : 0;
+    const int64_t unit = blockIdx.x / ctas, b = unit / g.slabs, c0 = (unit - b * g.slabs) * kGatedSlab;
     const int live = (int)(p.dim - c0 < kGatedSlab ? p.dim - c0 : kGatedSlab), mine = live - 2 * lane;
     const int64_t slot = gated_slot(p, b);
     const bool active = slot >= 0 || p.state == nullptr;
@@ -302,7 +318,7 @@ __global__ void __launch_bounds__(kGatedThreads, 2) k_gated(const __grid_constan
         carry = get_state(p.state + slot * p.dim + c, mine);
     char *own = staged + warp * Shared::kWarp;
     const uint32_t own_at = (uint32_t)__cvta_generic_to_shared(own);
-    const int step = g.ctas * kCtaTokens, first = rank * kCtaTokens + warp * kFwdT;
+    const int step = ctas * kCtaTokens, first = rank * kCtaTokens + warp * kFwdT;
 
     auto ask = [&](int t0, int stage) {
         const int n = len - t0;
@@ -319,10 +335,11 @@ __global__ void __launch_bounds__(kGatedThreads, 2) k_gated(const __grid_constan
     };
     ask(first, 0);
     ask(first + step, 1);
-    if (g.ctas > 1)
+    if (ctas > 1)
         cluster_wait();
 
     int side = 0;
+    uint32_t parity = 0;  // of the barriers' phases, each of which serves every other tile
     for (int base = 0; base < len; base += step, side ^= 1) {
         const int t0 = base + first, n = len - t0;
         char *at = own + side * (Shared::kTensors * Shared::kTile);
@@ -364,7 +381,7 @@ __global__ void __launch_bounds__(kGatedThreads, 2) k_gated(const __grid_constan
         of_warps[side][warp][lane] = e;
         __syncthreads();
         f32x2 h = carry;  // before the CTA's first token
-        if (g.ctas == 1) {
+        if (ctas == 1) {
 #pragma unroll
             for (int w = 0; w < kGatedWarps; ++w) {
                 if (w == warp)
@@ -383,16 +400,19 @@ __global__ void __launch_bounds__(kGatedThreads, 2) k_gated(const __grid_constan
                     all.h = fma2f(o.a, all.h, o.h);
                     all.a = mul2f(all.a, o.a);
                 }
-                for (int q = 0; q < g.ctas; ++q)
-                    cluster_put((uint32_t)__cvta_generic_to_shared(&of_ctas[side][rank][lane]), (unsigned)q, all.a, all.h);
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive_expect_tx(&arrived[side], (uint32_t)ctas * 32 * (uint32_t)sizeof(Element));
+                for (int q = 0; q < ctas; ++q)
+                    cluster_send(smem_addr(&of_ctas[side][rank][lane]), smem_addr(&arrived[side]), (unsigned)q, all.a, all.h);
             }
-            cluster_arrive();
-            cluster_wait();
+            cluster_await(&arrived[side], parity);
+            parity ^= (uint32_t)side;
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
                 if (q == rank)
                     h = carry;
-                if (q < g.ctas) {
+                if (q < ctas) {
                     const Element o = of_ctas[side][q][lane];
                     carry = fma2f(o.a, carry, o.h);
                 }
@@ -419,15 +439,19 @@ __global__ void __launch_bounds__(kGatedThreads, 2) k_gated(const __grid_constan
             finish(false);
     }
     cp_async_wait<0>();
-    for (int t = len + rank * kGatedWarps + warp; t < total; t += g.ctas * kGatedWarps)
+    if (ctas > 1) {  // no CTA ends that another might still send to
+        cluster_arrive();
+        cluster_wait();
+    }
+    for (int t = len + rank * kGatedWarps + warp; t < total; t += ctas * kGatedWarps)
         put_pair<S, VEC>(out.row(t), mine, 0ull);
     if (active && p.state != nullptr && rank == 0 && warp == 0)
         put_state(p.state + slot * p.dim + c, mine, carry);
 }
 
 // ---- gradients ----------------------------------------------------------------------------------------
-// From the last tokens to the first. A warp's tokens give two elements, the recurrence's from the checkpoint before the
-// CTA's tokens and its adjoint's from behind; with both carries known the states and the gradients by them
+// From the last tokens to the first. A warp's tokens give two elements, the recurrence's from the checkpoint before
+// them and its adjoint's from behind; with both carries known the states and the gradients by them
 // follow, and what a token's gradients take besides is in registers: four tokens' worth of it.
 constexpr int kBwdT = 4;
 constexpr int kBwdTensors = 5;
@@ -438,24 +462,32 @@ template <class S, bool VEC> struct BwdShared {
     static constexpr int kBytes = kGatedWarps * kWarp;
 };
 
-template <class S, bool RATE, bool VEC, bool IN, bool Z>
+template <class S, bool RATE, bool VEC, bool IN, bool Z, bool CLUSTER>
 __global__ void __launch_bounds__(kGatedThreads, 2) k_gated_grad(const __grid_constant__ GatedArgs g, float *rate_part) {
     using In = Tile<S, kBwdT, VEC>;
     using Shared = BwdShared<S, VEC>;
     constexpr int kCtaTokens = kGatedWarps * kBwdT;
-    static_assert(kCtaTokens == kGatedTile, "a CTA's tokens begin at a checkpoint");
+    constexpr int kMarkWarps = kGatedTile / kBwdT;  // that share a checkpoint
+    static_assert(kCtaTokens % kGatedTile == 0 && kGatedTile % kBwdT == 0, "a CTA's tokens begin at a checkpoint");
     extern __shared__ __align__(16) char staged[];
     __shared__ Element of_warps[2][kGatedWarps][32];
-    __shared__ f32x2 back_of_warps[2][kGatedWarps][32];
-    __shared__ Element behind_warps[kGatedWarps][32];
+    __shared__ Element back_of_warps[2][kGatedWarps][32];  // the adjoint's
     __shared__ Element of_ctas[2][8][32];
-    if (g.ctas > 1)
-        cluster_arrive();  // waited for below: no CTA writes into one that has not begun
+    __shared__ __align__(8) uint64_t arrived[2];  // of_ctas is complete
+    const int ctas = VEC && !CLUSTER ? 1 : g.ctas;
+    if (ctas > 1) {
+        if (threadIdx.x == 0) {
+            mbar_init(&arrived[0], 1);
+            mbar_init(&arrived[1], 1);
+            fence_mbar_init();
+        }
+        cluster_arrive();  // waited for below: no CTA sends to one that has not begun
+    }
     pdl_prologue();
     const mt_gated_args &p = g.p;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int rank = g.ctas > 1 ? (int)cluster_rank() : 0;
-    const int64_t unit = blockIdx.x / g.ctas, b = unit / g.slabs, c0 = (unit - b * g.slabs) * kGatedSlab;
+    const int rank = ctas > 1 ? (int)cluster_rank() : 0;
+    const int64_t unit = blockIdx.x / ctas, b = unit / g.slabs, c0 = (unit - b * g.slabs) * kGatedSlab;
     const int live = (int)(p.dim - c0 < kGatedSlab ? p.dim - c0 : kGatedSlab), mine = live - 2 * lane;
     const int len = (int)gated_len(p, b), total = (int)p.len;
     const Rows<S, VEC> x = In::lane_rows({p.x, p.x_batch, p.x_token, b, c0}, lane), r = In::lane_rows({p.r, p.r_batch, p.r_token, b, c0}, lane),
@@ -475,7 +507,7 @@ __global__ void __launch_bounds__(kGatedThreads, 2) k_gated_grad(const __grid_co
     }
     char *own = staged + warp * Shared::kWarp;
     const uint32_t own_at = (uint32_t)__cvta_generic_to_shared(own);
-    const int step = g.ctas * kCtaTokens, first = rank * kCtaTokens + warp * kBwdT;
+    const int step = ctas * kCtaTokens, first = rank * kCtaTokens + warp * kBwdT;
 
     auto ask = [&](int base, int stage) {
         const int t0 = base + first, n = len - t0;
@@ -494,15 +526,16 @@ __global__ void __launch_bounds__(kGatedThreads, 2) k_gated_grad(const __grid_co
     const int last = len > 0 ? (len - 1) / step * step : -1;  // where the last CTAs' tokens begin
     ask(last, 0);
     ask(last - step, 1);
-    if (g.ctas > 1)
+    if (ctas > 1)
         cluster_wait();
 
     int side = 0;
+    uint32_t parity = 0;  // of the barriers' phases, each of which serves every other tile
     for (int base = last; base >= 0; base -= step, side ^= 1) {
         const int t0 = base + first, n = len - t0;
         char *at = own + side * (kBwdTensors * Shared::kTile);
-        f32x2 h = 0ull;  // before the CTA's first token
-        if (t0 - warp * kBwdT < len)
+        f32x2 h = 0ull;  // before the first token of the checkpoint's warps
+        if (t0 / kGatedTile * kGatedTile < len)
             h = get_state(p.checkpoints + (b * g.ntiles + t0 / kGatedTile) * p.dim + c, mine);
         cp_async_wait<kGatedStages - 1>();
         __syncwarp();
@@ -571,20 +604,21 @@ __global__ void __launch_bounds__(kGatedThreads, 2) k_gated_grad(const __grid_co
         __syncwarp();
         ask(base - kGatedStages * step, side);
         of_warps[side][warp][lane] = e;
-        back_of_warps[side][warp][lane] = back;
+        back_of_warps[side][warp][lane] = {e.a, back};
         __syncthreads();
         // the state before this warp's tokens
-        for (int w = 0; w < warp; ++w) {
+        for (int w = warp / kMarkWarps * kMarkWarps; w < warp; ++w) {
             const Element o = of_warps[side][w][lane];
             h = fma2f(o.a, h, o.h);
         }
         f32x2 gh = carry;  // by the state after the CTA's last token
-        if (g.ctas == 1) {
+        if (ctas == 1) {
 #pragma unroll
             for (int w = kGatedWarps - 1; w >= 0; --w) {
                 if (w == warp)
                     gh = carry;
-                carry = fma2f(of_warps[side][w][lane].a, carry, back_of_warps[side][w][lane]);
+                const Element o = back_of_warps[side][w][lane];
+                carry = fma2f(o.a, carry, o.h);
             }
         } else {
             // one warp joins the CTA's elements of the adjoint, and tells every CTA of the cluster
@@ -592,26 +626,29 @@ __global__ void __launch_bounds__(kGatedThreads, 2) k_gated_grad(const __grid_co
                 Element all = {both(1.0f), 0ull};
 #pragma unroll
                 for (int w = kGatedWarps - 1; w >= 0; --w) {
-                    const f32x2 oa = of_warps[side][w][lane].a, ob = back_of_warps[side][w][lane];
-                    behind_warps[w][lane] = all;
-                    all.h = fma2f(oa, all.h, ob);
-                    all.a = mul2f(all.a, oa);
+                    const Element o = back_of_warps[side][w][lane];
+                    back_of_warps[side][w][lane] = all;  // of the warps behind w
+                    all.h = fma2f(o.a, all.h, o.h);
+                    all.a = mul2f(all.a, o.a);
                 }
-                for (int q = 0; q < g.ctas; ++q)
-                    cluster_put((uint32_t)__cvta_generic_to_shared(&of_ctas[side][rank][lane]), (unsigned)q, all.a, all.h);
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive_expect_tx(&arrived[side], (uint32_t)ctas * 32 * (uint32_t)sizeof(Element));
+                for (int q = 0; q < ctas; ++q)
+                    cluster_send(smem_addr(&of_ctas[side][rank][lane]), smem_addr(&arrived[side]), (unsigned)q, all.a, all.h);
             }
-            cluster_arrive();
-            cluster_wait();
+            cluster_await(&arrived[side], parity);
+            parity ^= (uint32_t)side;
 #pragma unroll
             for (int q = 7; q >= 0; --q) {
                 if (q == rank)
                     gh = carry;
-                if (q < g.ctas) {
+                if (q < ctas) {
                     const Element o = of_ctas[side][q][lane];
                     carry = fma2f(o.a, carry, o.h);
                 }
             }
-            const Element behind = behind_warps[warp][lane];
+            const Element behind = back_of_warps[side][warp][lane];
             gh = fma2f(behind.a, gh, behind.h);
         }
 #pragma unroll
@@ -648,7 +685,11 @@ __global__ void __launch_bounds__(kGatedThreads, 2) k_gated_grad(const __grid_co
             finish(false);
     }
     cp_async_wait<0>();
-    for (int t = len + rank * kGatedWarps + warp; t < total; t += g.ctas * kGatedWarps) {
+    if (ctas > 1) {  // no CTA ends that another might still send to
+        cluster_arrive();
+        cluster_wait();
+    }
+    for (int t = len + rank * kGatedWarps + warp; t < total; t += ctas * kGatedWarps) {
         put_pair<S, VEC>(dx.row(t), mine, 0ull);
         put_pair<S, VEC>(dr.row(t), mine, 0ull);
         if (has_in)
@@ -660,14 +701,14 @@ __global__ void __launch_bounds__(kGatedThreads, 2) k_gated_grad(const __grid_co
         put_state(p.dinit + b * p.dim + c, mine, carry);
     if (RATE && rate_part != nullptr) {
         __syncthreads();  // the loop's last reads of back_of_warps
-        back_of_warps[0][warp][lane] = rate_sum;
+        back_of_warps[0][warp][lane].h = rate_sum;
         __syncthreads();
         if (warp == 0) {
             f32x2 s = 0ull;
 #pragma unroll
             for (int w = 0; w < kGatedWarps; ++w)
-                s = add2f(s, back_of_warps[0][w][lane]);
-            put_state(rate_part + (b * g.ctas + rank) * p.dim + c, mine, s);
+                s = add2f(s, back_of_warps[0][w][lane].h);
+            put_state(rate_part + (b * ctas + rank) * p.dim + c, mine, s);
         }
     }
 }
@@ -733,32 +774,33 @@ static cudaError_t launch_cluster(void (*kernel)(KArgs...), int64_t grid, unsign
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
-template <class S, bool RATE, bool VEC, bool IN, bool Z> static cudaError_t gated_forward_of(const GatedArgs &g, const Launch &L) {
+template <class S, bool RATE, bool VEC, bool IN, bool Z, bool CLUSTER> static cudaError_t gated_forward_of(const GatedArgs &g, const Launch &L) {
     static PerDevice ready;
     constexpr int smem = FwdShared<S, VEC>::kBytes;
-    const cudaError_t e = allow_shared(k_gated<S, RATE, VEC, IN, Z>, smem, ready);
+    const cudaError_t e = allow_shared(k_gated<S, RATE, VEC, IN, Z, CLUSTER>, smem, ready);
     if (e != cudaSuccess)
         return e;
     note_launch();
-    return launch_cluster(k_gated<S, RATE, VEC, IN, Z>, g.p.batch * g.slabs * g.ctas, kGatedThreads, smem, g.ctas, L.stream, g);
+    return launch_cluster(k_gated<S, RATE, VEC, IN, Z, CLUSTER>, g.p.batch * g.slabs * g.ctas, kGatedThreads, smem, g.ctas, L.stream, g);
 }
-template <class S, bool RATE, bool VEC, bool IN, bool Z>
+template <class S, bool RATE, bool VEC, bool IN, bool Z, bool CLUSTER>
 static cudaError_t gated_backward_of(const GatedArgs &g, float *part, const Launch &L) {
     static PerDevice ready;
     constexpr int smem = BwdShared<S, VEC>::kBytes;
-    const cudaError_t e = allow_shared(k_gated_grad<S, RATE, VEC, IN, Z>, smem, ready);
+    const cudaError_t e = allow_shared(k_gated_grad<S, RATE, VEC, IN, Z, CLUSTER>, smem, ready);
     if (e != cudaSuccess)
         return e;
     note_launch();
-    return launch_cluster(k_gated_grad<S, RATE, VEC, IN, Z>, g.p.batch * g.slabs * g.ctas, kGatedThreads, smem, g.ctas, L.stream, g, part);
+    return launch_cluster(k_gated_grad<S, RATE, VEC, IN, Z, CLUSTER>, g.p.batch * g.slabs * g.ctas, kGatedThreads, smem, g.ctas, L.stream, g, part);
 }
-#define MT_GATED_GATES(f, ...)                                                                                             \
-    if constexpr (!VEC)                                                                                                    \
-        return f<S, RATE, false, false, false>(__VA_ARGS__);                                                               \
-    else if (g.p.i != nullptr)                                                                                             \
-        return g.p.z != nullptr ? f<S, RATE, true, true, true>(__VA_ARGS__) : f<S, RATE, true, true, false>(__VA_ARGS__);  \
-    else                                                                                                                   \
-        return g.p.z != nullptr ? f<S, RATE, true, false, true>(__VA_ARGS__) : f<S, RATE, true, false, false>(__VA_ARGS__);
+#define MT_GATED_CLUSTER(f, IN, Z, ...) (g.ctas > 1 ? f<S, RATE, true, IN, Z, true>(__VA_ARGS__) : f<S, RATE, true, IN, Z, false>(__VA_ARGS__))
+#define MT_GATED_GATES(f, ...)                                                                                      \
+    if constexpr (!VEC)                                                                                             \
+        return f<S, RATE, false, false, false, false>(__VA_ARGS__);                                                 \
+    else if (g.p.i != nullptr)                                                                                      \
+        return g.p.z != nullptr ? MT_GATED_CLUSTER(f, true, true, __VA_ARGS__) : MT_GATED_CLUSTER(f, true, false, __VA_ARGS__);   \
+    else                                                                                                            \
+        return g.p.z != nullptr ? MT_GATED_CLUSTER(f, false, true, __VA_ARGS__) : MT_GATED_CLUSTER(f, false, false, __VA_ARGS__);
 template <class S, bool RATE, bool VEC> static cudaError_t gated_forward(const GatedArgs &g, const Launch &L) {
     MT_GATED_GATES(gated_forward_of, g, L)
 }
@@ -774,11 +816,22 @@ template <class S, bool RATE, bool VEC> static cudaError_t gated_single(const Ga
 #define MT_GATED_BY(f, ...)                                                                              \
     (g.p.rate != nullptr ? (vec ? f<S, true, true>(__VA_ARGS__) : f<S, true, false>(__VA_ARGS__))        \
                          : (vec ? f<S, false, true>(__VA_ARGS__) : f<S, false, false>(__VA_ARGS__)))
-#define MT_GATED_TYPE(name, T)                                                                           \
-    using S = T;                                                                                         \
-    cudaError_t gated_forward_##name(const GatedArgs &g, bool vec, const Launch &L) { return MT_GATED_BY(gated_forward, g, L); }   \
+#define MT_GATED_TYPE(name, T)                                                                                                      \
+    using S = T;                                                                                                                    \
+    cudaError_t gated_forward_##name(const GatedArgs &g, bool vec, const Launch &L) { return MT_GATED_BY(gated_forward, g, L); }    \
+    cudaError_t gated_single_##name(const GatedArgs &g, bool vec, const Launch &L) { return MT_GATED_BY(gated_single, g, L); }      \
+    cudaError_t gated_##name##_take_error(int *code) { return gated_take_error_word(code); }
+#define MT_GATED_GRAD_TYPE(name, T)                                                                                                 \
+    using S = T;                                                                                                                    \
     cudaError_t gated_backward_##name(const GatedArgs &g, float *part, bool vec, const Launch &L) { return MT_GATED_BY(gated_backward, g, part, L); } \
-    cudaError_t gated_single_##name(const GatedArgs &g, bool vec, const Launch &L) { return MT_GATED_BY(gated_single, g, L); }
+    cudaError_t gated_grad_##name##_take_error(int *code) { return gated_take_error_word(code); }
+
+// Reads and clears this translation unit's device error word.
+static cudaError_t gated_take_error_word(int *code) {
+    const int zero = 0;
+    const cudaError_t e = cudaMemcpyFromSymbol(code, g_mt_err, sizeof(int));
+    return e != cudaSuccess ? e : cudaMemcpyToSymbol(g_mt_err, &zero, sizeof(int));
+}
 
 #define MT_GATED_DECL(name)                                                                  \
     cudaError_t gated_forward_##name(const GatedArgs &g, bool vec, const Launch &L);         \

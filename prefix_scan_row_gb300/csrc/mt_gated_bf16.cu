@@ -1,4 +1,4 @@
-// mt_gated_bf16.cu -- the gated scan's kernels for bf16 activations.
+// mt_gated_bf16.cu -- the gated scan's kernels for bf16 activations: prompts and single tokens.
 #include "mt_gated.cuh"
 
 namespace mt {

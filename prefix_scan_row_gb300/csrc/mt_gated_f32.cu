@@ -1,4 +1,4 @@
-// mt_gated_f32.cu -- the gated scan's kernels for f32 activations.
+// mt_gated_f32.cu -- the gated scan's kernels for f32 activations: prompts and single tokens.
 #include "mt_gated.cuh"
 
 namespace mt {

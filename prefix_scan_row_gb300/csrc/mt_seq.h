@@ -43,12 +43,18 @@ cudaError_t ssm_grad_launch(const mt_ssm_args &a, const Launch &L);
 cudaError_t ssm_step_launch(const mt_ssm_args &a, const Launch &L);
 
 // ---- gated scan (mt_gated*.cu) ---------------------------------------------------
-constexpr int kGatedTile = 32;  // tokens per checkpoint
+constexpr int kGatedTile = 16;  // tokens per checkpoint
 constexpr int64_t kGatedMost = INT32_MAX - 65536;  // tokens of a sequence: they are counted in 32 bits
 int64_t gated_scratch_slots(int64_t batch, int64_t len, int64_t dim);
 cudaError_t gated_launch(const mt_gated_args &a, const Launch &L);
 cudaError_t gated_step_launch(const mt_gated_args &a, const Launch &L);
 cudaError_t gated_grad_launch(const mt_gated_args &a, const Launch &L);
+cudaError_t gated_f32_take_error(int *code);  // of each translation unit's error word
+cudaError_t gated_bf16_take_error(int *code);
+cudaError_t gated_f16_take_error(int *code);
+cudaError_t gated_grad_f32_take_error(int *code);
+cudaError_t gated_grad_bf16_take_error(int *code);
+cudaError_t gated_grad_f16_take_error(int *code);
 
 // ---- beam search's selection (mt_beam.cu) and copies between slots (mt_copy.cu) ----
 constexpr int kBeamsMost = 32;
