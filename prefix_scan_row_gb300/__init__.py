@@ -684,14 +684,16 @@ class Library:
             pools = (pools,)
         blocks = []
         for t in pools:
-            if t.dim() <= axis:
+            shape, stride, e, row = t.shape, t.stride(), t.element_size(), 1
+            if len(shape) <= axis:
                 raise ValueError("a pool has fewer axes than that of its slots")
-            row = math.prod(t.shape[axis + 1:])
-            if t.numel() > 0 and not t[(0,) * (axis + 1)].is_contiguous():
-                raise ValueError("a pool's rows must be contiguous")
-            e, s = t.element_size(), t.stride()
-            blocks.append(_POOL.pack(t.data_ptr(), t.shape[axis], row * e, (s[axis] if t.shape[axis] > 1 else row) * e,
-                                     t.shape[0] if axis else 1, (s[0] if axis and t.shape[0] > 1 else row) * e))
+            for d in range(len(shape) - 1, axis, -1):
+                if stride[d] != row and shape[d] > 1:
+                    raise ValueError("a pool's rows must be contiguous")
+                row *= shape[d]
+            slots = shape[axis]
+            blocks.append(_POOL.pack(t.data_ptr(), slots, row * e, (stride[axis] if slots > 1 else row) * e,
+                                     shape[0] if axis else 1, (stride[0] if axis and shape[0] > 1 else row) * e))
         _check(self.lib.mt_state_copy(src.data_ptr(), dst.data_ptr(), src.numel(), b"".join(blocks), len(blocks),
                                       _stream(stream)), "mt_state_copy")
 

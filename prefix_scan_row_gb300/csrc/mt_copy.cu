@@ -1,8 +1,9 @@
 // mt_copy.cu -- copies between slots of state pools.
 //
-// Rows of a pool of layers lie far apart, so a CTA takes one pair's chunk of one row and plane, 16 KB
-// of it, and copies it with the widest accesses that the pool's addresses and sizes allow. Only bytes
-// count: each is read once and written once.
+// Rows of a pool of layers lie far apart, so a CTA takes one chunk of a row and plane, 16 KB, with the widest accesses that the
+// pool's addresses and sizes allow. Where there are many pairs it takes that chunk of up to 32 of them, since most pairs of
+// a beam search copy nothing and a CTA for each costs more than the rest of its work. Only bytes count: each is read
+// once and written once.
 #include "mt_seq.cuh"
 #include "mt_seq.h"
 
@@ -14,6 +15,8 @@ constexpr int kCopyThreads = 256;
 constexpr int kCopyInFlight = 4;                                       // loads of a thread before its stores
 constexpr int64_t kCopyChunk = 16 * kCopyThreads * kCopyInFlight;      // bytes of a CTA
 
+constexpr int64_t kEnoughCtas = 152 * 8 * 4;
+
 struct CopyPool {
     char *base;
     int64_t nslots, row_bytes, row_stride, plane_stride;
@@ -24,7 +27,7 @@ struct CopyPool {
 struct CopyArgs {
     const int32_t *src, *dst;
     int64_t pairs;
-    int npools;
+    int npools, per_cta;  // pairs of a CTA
     CopyPool pool[MT_MOST_POOLS];
 };
 
@@ -55,18 +58,24 @@ __global__ void __launch_bounds__(kCopyThreads) k_state_copy(const __grid_consta
     const int64_t begin = chunk * kCopyChunk;
     const int64_t bytes = p.row_bytes - begin < kCopyChunk ? p.row_bytes - begin : kCopyChunk;
     char *rows = p.base + plane * p.plane_stride + begin;
-    for (int64_t i = blockIdx.y; i < a.pairs; i += gridDim.y) {
-        const int64_t s = a.src[i], d = a.dst[i];
-        if (s < 0 || s >= p.nslots || d < 0 || d >= p.nslots || s == d)
-            continue;
-        const char *from = rows + s * p.row_stride;
-        char *to = rows + d * p.row_stride;
-        switch (p.bytes) {
-        case 16: copy_span<uint4>(from, to, bytes); break;
-        case 8: copy_span<uint2>(from, to, bytes); break;
-        case 4: copy_span<uint32_t>(from, to, bytes); break;
-        case 2: copy_span<uint16_t>(from, to, bytes); break;
-        default: copy_span<uint8_t>(from, to, bytes);
+    const int lane = threadIdx.x % 32;
+    for (int64_t i0 = (int64_t)blockIdx.y * a.per_cta; i0 < a.pairs; i0 += (int64_t)gridDim.y * a.per_cta) {
+        int32_t s = -1, d = -1;
+        if (lane < a.per_cta && i0 + lane < a.pairs) {
+            s = a.src[i0 + lane];
+            d = a.dst[i0 + lane];
+        }
+        for (uint32_t left = __ballot_sync(kFull, s >= 0 && s < p.nslots && d >= 0 && d < p.nslots && s != d); left != 0; left &= left - 1) {
+            const int q = __ffs(left) - 1;
+            const char *from = rows + (int64_t)__shfl_sync(kFull, s, q) * p.row_stride;
+            char *to = rows + (int64_t)__shfl_sync(kFull, d, q) * p.row_stride;
+            switch (p.bytes) {
+            case 16: copy_span<uint4>(from, to, bytes); break;
+            case 8: copy_span<uint2>(from, to, bytes); break;
+            case 4: copy_span<uint32_t>(from, to, bytes); break;
+            case 2: copy_span<uint16_t>(from, to, bytes); break;
+            default: copy_span<uint8_t>(from, to, bytes);
+            }
         }
     }
 }
@@ -103,8 +112,12 @@ cudaError_t copy_launch(const int32_t *src, const int32_t *dst, int64_t pairs, c
     }
     if (blocks == 0)
         return cudaSuccess;
+    a.per_cta = 1;
+    while (a.per_cta < 32 && blocks * ((pairs + a.per_cta - 1) / a.per_cta) > kEnoughCtas)
+        a.per_cta *= 2;
+    const int64_t rows = (pairs + a.per_cta - 1) / a.per_cta;
     note_launch();
-    const dim3 grid((unsigned)blocks, (unsigned)(pairs < 65535 ? pairs : 65535));
+    const dim3 grid((unsigned)blocks, (unsigned)(rows < 65535 ? rows : 65535));
     return launch_pdl_2d(k_state_copy, grid, kCopyThreads, L.stream, a);
 }
 

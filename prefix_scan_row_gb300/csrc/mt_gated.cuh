@@ -28,7 +28,10 @@ namespace mt {
 
 constexpr int kGatedSlab = 64;   // channels of a warp
 constexpr int kGatedWarps = 8;   // warps of a CTA
-constexpr int kGatedThreads = 32 * kGatedWarps;
+// and where 16-bit calls have more CTAs than three an SM, so that a smaller one's end leaves less idle. Both, us, all gates, 4096 channels, prompt
+// and gradient, by sequences x tokens (CTAs): 4 x 2048 (256) 73 and 140, 73 and 151; 6 x 2048 (384) 110 and 213, 125 and
+// 199; 8 x 2048 (512) 140 and 271, 127 and 253; 16 x 1024 (1024) 125 and 240, 111 and 224. f32: 8 x 2048 211 and 403, 246 and 444.
+constexpr int kGatedFewWarps = 4;
 constexpr int kGatedStages = 2;  // tiles of a warp on their way or in use
 
 struct GatedArgs {
@@ -272,21 +275,22 @@ struct alignas(16) Element {  // of the scan
 // ---- prompts ----------------------------------------------------------------------------------------
 constexpr int kFwdT = 8;  // tokens of a warp
 
-template <class S, bool VEC> struct FwdShared {
+template <class S, bool VEC, int W> struct FwdShared {
     static constexpr int kTensors = 4;
     static constexpr int kTile = Tile<S, kFwdT, VEC>::kBytes;
     static constexpr int kWarp = kGatedStages * kTensors * kTile;
-    static constexpr int kBytes = kGatedWarps * kWarp;
+    static constexpr int kBytes = W * kWarp;
 };
 
 // IN and Z: the call has an input gate, an output gate; CLUSTER: CTAs share the tokens (VEC; other rows ask at run time).
-template <class S, bool RATE, bool VEC, bool IN, bool Z, bool CLUSTER>
-__global__ void __launch_bounds__(kGatedThreads, 2) k_gated(const __grid_constant__ GatedArgs g) {
+// W: warps of the CTA.
+template <class S, bool RATE, bool VEC, bool IN, bool Z, bool CLUSTER, int W>
+__global__ void __launch_bounds__(32 * W, 16 / W) k_gated(const __grid_constant__ GatedArgs g) {
     using In = Tile<S, kFwdT, VEC>;
-    using Shared = FwdShared<S, VEC>;
-    constexpr int kCtaTokens = kGatedWarps * kFwdT;
+    using Shared = FwdShared<S, VEC, W>;
+    constexpr int kCtaTokens = W * kFwdT;
     extern __shared__ __align__(16) char staged[];
-    __shared__ Element of_warps[2][kGatedWarps][32];
+    __shared__ Element of_warps[2][W][32];
     __shared__ Element of_ctas[2][8][32];
     __shared__ __align__(8) uint64_t arrived[2];  // of_ctas is complete
     const int ctas = VEC && !CLUSTER ? 1 : g.ctas;
@@ -383,7 +387,7 @@ __global__ void __launch_bounds__(kGatedThreads, 2) k_gated(const __grid_constan
         f32x2 h = carry;  // before the CTA's first token
         if (ctas == 1) {
 #pragma unroll
-            for (int w = 0; w < kGatedWarps; ++w) {
+            for (int w = 0; w < W; ++w) {
                 if (w == warp)
                     h = carry;
                 const Element o = of_warps[side][w][lane];
@@ -394,7 +398,7 @@ __global__ void __launch_bounds__(kGatedThreads, 2) k_gated(const __grid_constan
             if (warp == 0) {
                 Element all = {both(1.0f), 0ull};
 #pragma unroll
-                for (int w = 0; w < kGatedWarps; ++w) {
+                for (int w = 0; w < W; ++w) {
                     const Element o = of_warps[side][w][lane];
                     of_warps[side][w][lane] = all;  // of the warps before w
                     all.h = fma2f(o.a, all.h, o.h);
@@ -443,7 +447,7 @@ __global__ void __launch_bounds__(kGatedThreads, 2) k_gated(const __grid_constan
         cluster_arrive();
         cluster_wait();
     }
-    for (int t = len + rank * kGatedWarps + warp; t < total; t += ctas * kGatedWarps)
+    for (int t = len + rank * W + warp; t < total; t += ctas * W)
         put_pair<S, VEC>(out.row(t), mine, 0ull);
     if (active && p.state != nullptr && rank == 0 && warp == 0)
         put_state(p.state + slot * p.dim + c, mine, carry);
@@ -456,22 +460,22 @@ __global__ void __launch_bounds__(kGatedThreads, 2) k_gated(const __grid_constan
 constexpr int kBwdT = 4;
 constexpr int kBwdTensors = 5;
 
-template <class S, bool VEC> struct BwdShared {
+template <class S, bool VEC, int W> struct BwdShared {
     static constexpr int kTile = Tile<S, kBwdT, VEC>::kBytes;
     static constexpr int kWarp = kGatedStages * kBwdTensors * kTile;
-    static constexpr int kBytes = kGatedWarps * kWarp;
+    static constexpr int kBytes = W * kWarp;
 };
 
-template <class S, bool RATE, bool VEC, bool IN, bool Z, bool CLUSTER>
-__global__ void __launch_bounds__(kGatedThreads, 2) k_gated_grad(const __grid_constant__ GatedArgs g, float *rate_part) {
+template <class S, bool RATE, bool VEC, bool IN, bool Z, bool CLUSTER, int W>
+__global__ void __launch_bounds__(32 * W, 16 / W) k_gated_grad(const __grid_constant__ GatedArgs g, float *rate_part) {
     using In = Tile<S, kBwdT, VEC>;
-    using Shared = BwdShared<S, VEC>;
-    constexpr int kCtaTokens = kGatedWarps * kBwdT;
+    using Shared = BwdShared<S, VEC, W>;
+    constexpr int kCtaTokens = W * kBwdT;
     constexpr int kMarkWarps = kGatedTile / kBwdT;  // that share a checkpoint
     static_assert(kCtaTokens % kGatedTile == 0 && kGatedTile % kBwdT == 0, "a CTA's tokens begin at a checkpoint");
     extern __shared__ __align__(16) char staged[];
-    __shared__ Element of_warps[2][kGatedWarps][32];
-    __shared__ Element back_of_warps[2][kGatedWarps][32];  // the adjoint's
+    __shared__ Element of_warps[2][W][32];
+    __shared__ Element back_of_warps[2][W][32];  // the adjoint's
     __shared__ Element of_ctas[2][8][32];
     __shared__ __align__(8) uint64_t arrived[2];  // of_ctas is complete
     const int ctas = VEC && !CLUSTER ? 1 : g.ctas;
@@ -614,7 +618,7 @@ __global__ void __launch_bounds__(kGatedThreads, 2) k_gated_grad(const __grid_co
         f32x2 gh = carry;  // by the state after the CTA's last token
         if (ctas == 1) {
 #pragma unroll
-            for (int w = kGatedWarps - 1; w >= 0; --w) {
+            for (int w = W - 1; w >= 0; --w) {
                 if (w == warp)
                     gh = carry;
                 const Element o = back_of_warps[side][w][lane];
@@ -625,7 +629,7 @@ __global__ void __launch_bounds__(kGatedThreads, 2) k_gated_grad(const __grid_co
             if (warp == 0) {
                 Element all = {both(1.0f), 0ull};
 #pragma unroll
-                for (int w = kGatedWarps - 1; w >= 0; --w) {
+                for (int w = W - 1; w >= 0; --w) {
                     const Element o = back_of_warps[side][w][lane];
                     back_of_warps[side][w][lane] = all;  // of the warps behind w
                     all.h = fma2f(o.a, all.h, o.h);
@@ -689,7 +693,7 @@ __global__ void __launch_bounds__(kGatedThreads, 2) k_gated_grad(const __grid_co
         cluster_arrive();
         cluster_wait();
     }
-    for (int t = len + rank * kGatedWarps + warp; t < total; t += ctas * kGatedWarps) {
+    for (int t = len + rank * W + warp; t < total; t += ctas * W) {
         put_pair<S, VEC>(dx.row(t), mine, 0ull);
         put_pair<S, VEC>(dr.row(t), mine, 0ull);
         if (has_in)
@@ -706,7 +710,7 @@ __global__ void __launch_bounds__(kGatedThreads, 2) k_gated_grad(const __grid_co
         if (warp == 0) {
             f32x2 s = 0ull;
 #pragma unroll
-            for (int w = 0; w < kGatedWarps; ++w)
+            for (int w = 0; w < W; ++w)
                 s = add2f(s, back_of_warps[0][w][lane].h);
             put_state(rate_part + (b * ctas + rank) * p.dim + c, mine, s);
         }
@@ -774,33 +778,47 @@ static cudaError_t launch_cluster(void (*kernel)(KArgs...), int64_t grid, unsign
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
-template <class S, bool RATE, bool VEC, bool IN, bool Z, bool CLUSTER> static cudaError_t gated_forward_of(const GatedArgs &g, const Launch &L) {
+template <class S, bool RATE, bool VEC, bool IN, bool Z, bool CLUSTER, int W> static cudaError_t gated_forward_of(const GatedArgs &g, const Launch &L) {
     static PerDevice ready;
-    constexpr int smem = FwdShared<S, VEC>::kBytes;
-    const cudaError_t e = allow_shared(k_gated<S, RATE, VEC, IN, Z, CLUSTER>, smem, ready);
+    constexpr int smem = FwdShared<S, VEC, W>::kBytes;
+    const cudaError_t e = allow_shared(k_gated<S, RATE, VEC, IN, Z, CLUSTER, W>, smem, ready);
     if (e != cudaSuccess)
         return e;
     note_launch();
-    return launch_cluster(k_gated<S, RATE, VEC, IN, Z, CLUSTER>, g.p.batch * g.slabs * g.ctas, kGatedThreads, smem, g.ctas, L.stream, g);
+    return launch_cluster(k_gated<S, RATE, VEC, IN, Z, CLUSTER, W>, g.p.batch * g.slabs * g.ctas, 32 * W, smem, g.ctas, L.stream, g);
 }
-template <class S, bool RATE, bool VEC, bool IN, bool Z, bool CLUSTER>
+template <class S, bool RATE, bool VEC, bool IN, bool Z, bool CLUSTER, int W>
 static cudaError_t gated_backward_of(const GatedArgs &g, float *part, const Launch &L) {
     static PerDevice ready;
-    constexpr int smem = BwdShared<S, VEC>::kBytes;
-    const cudaError_t e = allow_shared(k_gated_grad<S, RATE, VEC, IN, Z, CLUSTER>, smem, ready);
+    constexpr int smem = BwdShared<S, VEC, W>::kBytes;
+    const cudaError_t e = allow_shared(k_gated_grad<S, RATE, VEC, IN, Z, CLUSTER, W>, smem, ready);
     if (e != cudaSuccess)
         return e;
     note_launch();
-    return launch_cluster(k_gated_grad<S, RATE, VEC, IN, Z, CLUSTER>, g.p.batch * g.slabs * g.ctas, kGatedThreads, smem, g.ctas, L.stream, g, part);
+    return launch_cluster(k_gated_grad<S, RATE, VEC, IN, Z, CLUSTER, W>, g.p.batch * g.slabs * g.ctas, 32 * W, smem, g.ctas, L.stream, g, part);
 }
-#define MT_GATED_CLUSTER(f, IN, Z, ...) (g.ctas > 1 ? f<S, RATE, true, IN, Z, true>(__VA_ARGS__) : f<S, RATE, true, IN, Z, false>(__VA_ARGS__))
+// The kernel of a call's gates and warps.
+#define MT_GATED_WARPS(f, IN, Z, ...)                                                                               \
+    {                                                                                                               \
+        if (g.ctas > 1)                                                                                             \
+            return f<S, RATE, true, IN, Z, true, kGatedWarps>(__VA_ARGS__);                                         \
+        if constexpr (sizeof(S) == 2)                                                                               \
+            if (g.p.batch * g.slabs > 3 * 152)                                                                      \
+                return f<S, RATE, true, IN, Z, false, kGatedFewWarps>(__VA_ARGS__);                                 \
+        return f<S, RATE, true, IN, Z, false, kGatedWarps>(__VA_ARGS__);                                            \
+    }
 #define MT_GATED_GATES(f, ...)                                                                                      \
-    if constexpr (!VEC)                                                                                             \
-        return f<S, RATE, false, false, false, false>(__VA_ARGS__);                                                 \
-    else if (g.p.i != nullptr)                                                                                      \
-        return g.p.z != nullptr ? MT_GATED_CLUSTER(f, true, true, __VA_ARGS__) : MT_GATED_CLUSTER(f, true, false, __VA_ARGS__);   \
-    else                                                                                                            \
-        return g.p.z != nullptr ? MT_GATED_CLUSTER(f, false, true, __VA_ARGS__) : MT_GATED_CLUSTER(f, false, false, __VA_ARGS__);
+    if constexpr (!VEC) {                                                                                           \
+        return f<S, RATE, false, false, false, false, kGatedWarps>(__VA_ARGS__);                                    \
+    } else if (g.p.i != nullptr) {                                                                                  \
+        if (g.p.z != nullptr)                                                                                       \
+            MT_GATED_WARPS(f, true, true, __VA_ARGS__)                                                              \
+        MT_GATED_WARPS(f, true, false, __VA_ARGS__)                                                                 \
+    } else {                                                                                                        \
+        if (g.p.z != nullptr)                                                                                       \
+            MT_GATED_WARPS(f, false, true, __VA_ARGS__)                                                             \
+        MT_GATED_WARPS(f, false, false, __VA_ARGS__)                                                                \
+    }
 template <class S, bool RATE, bool VEC> static cudaError_t gated_forward(const GatedArgs &g, const Launch &L) {
     MT_GATED_GATES(gated_forward_of, g, L)
 }
