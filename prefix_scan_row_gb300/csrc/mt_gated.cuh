@@ -176,6 +176,10 @@ template <class S, bool VEC> struct Rows {
     int64_t token;
     __device__ __forceinline__ Rows(const void *p, int64_t batch, int64_t token_, int64_t b, int64_t c0)
         : at(p == nullptr ? nullptr : const_cast<S *>(static_cast<const S *>(p)) + b * batch + c0), token(token_) {}
+    // bits by which row t begins behind a 32-bit word, t of a tile whose first token is even
+    __device__ __forceinline__ int shift(int t) const {
+        return sizeof(S) == 4 ? 0 : (int)(((uintptr_t)at ^ (uintptr_t)(t % 2 * token * 2)) & 2) * 8;
+    }
     __device__ __forceinline__ S *row(int t) const {
         if constexpr (VEC)
             return reinterpret_cast<S *>(reinterpret_cast<char *>(at) + (int64_t)t * (int)((int)token * (int)sizeof(S)));
@@ -203,12 +207,19 @@ template <class S, int T, bool VEC> struct Tile {
                     cp_async_zfill<16>(to + k * 512 + lane * 16, r.row(t0 + row), true);
             }
         } else {
-#pragma unroll 1
-            for (int row = 0; row < (n < T ? n : T); ++row) {
-                const uintptr_t from = (uintptr_t)r.row(t0 + row);
-                const int shift = (int)(from & 3), words = (shift + live * (int)sizeof(S) + 3) / 4;
-                for (int w = lane; w < words; w += 32)
-                    cp_async_zfill<4>(to + row * kPitch + w * 4, (const void *)(from - shift + w * 4), true);
+const char *from = reinterpret_cast<const char *>(r.row(t0));
+            const int64_t token = r.token * (int64_t)sizeof(S);
+#pragma unroll
+            for (int row = 0; row < T; ++row, from += token) {
+                if (row >= n)
+                    continue;
+                const int shift = r.shift(row) / 8, words = (shift + live * (int)sizeof(S) + 3) / 4;
+#pragma unroll
+                for (int w = 0; w < kGatedSlab * (int)sizeof(S) / 4; w += 32)
+                    if (w + lane < words)
+                        cp_async_zfill<4>(to + row * kPitch + (w + lane) * 4, from - shift + (w + lane) * 4, true);
+                if (sizeof(S) == 2 && lane == 0 && words > 32)
+                    cp_async_zfill<4>(to + row * kPitch + 128, from - shift + 128, true);
             }
         }
     }
@@ -219,8 +230,8 @@ template <class S, int T, bool VEC> struct Tile {
                 r.at += lane % kRow * kPer;
         return r;
     }
-    // The lane's channels of token t0 + row.
-    static __device__ __forceinline__ f32x2 read(const char *at, const Rows<S, VEC> &r, int t0, int row, int lane) {
+    // The lane's channels of the tile's row.
+    static __device__ __forceinline__ f32x2 read(const char *at, const Rows<S, VEC> &r, int row, int lane) {
         using P = typename Pair<S>::T;
         if constexpr (VEC) {
             return Pair<S>::widen(*reinterpret_cast<const P *>(at + row * kPitch + lane * (int)sizeof(P)));
@@ -229,8 +240,7 @@ template <class S, int T, bool VEC> struct Tile {
             return pack2f(f[0], f[1]);
         } else {
             const uint32_t *w = reinterpret_cast<const uint32_t *>(at + row * kPitch) + lane;
-            const bool odd = ((uintptr_t)r.row(t0 + row) & 2) != 0;
-            return Pair<S>::widen(odd ? __funnelshift_r(w[0], w[1], 16) : w[0]);
+            return Pair<S>::widen(__funnelshift_r(w[0], w[1], r.shift(row)));
         }
     }
     // Rows from n on hold `v` in every channel.
@@ -282,7 +292,7 @@ template <class S, bool VEC, int W> struct FwdShared {
     static constexpr int kBytes = W * kWarp;
 };
 
-// IN and Z: the call has an input gate, an output gate; CLUSTER: CTAs share the tokens (VEC; other rows ask at run time).
+// IN and Z: the call has an input gate, an output gate; CLUSTER: CTAs share the tokens (or, where not VEC, may).
 // W: warps of the CTA.
 template <class S, bool RATE, bool VEC, bool IN, bool Z, bool CLUSTER, int W>
 __global__ void __launch_bounds__(32 * W, 16 / W) k_gated(const __grid_constant__ GatedArgs g) {
@@ -293,7 +303,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) k_gated(const __grid_constant_
     __shared__ Element of_warps[2][W][32];
     __shared__ Element of_ctas[2][8][32];
     __shared__ __align__(8) uint64_t arrived[2];  // of_ctas is complete
-    const int ctas = VEC && !CLUSTER ? 1 : g.ctas;
+    const int ctas = CLUSTER ? g.ctas : 1;
     if (ctas > 1) {
         if (threadIdx.x == 0) {
             mbar_init(&arrived[0], 1);
@@ -314,7 +324,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) k_gated(const __grid_constant_
     const Rows<S, VEC> x = In::lane_rows({p.x, p.x_batch, p.x_token, b, c0}, lane), r = In::lane_rows({p.r, p.r_batch, p.r_token, b, c0}, lane),
                        in = In::lane_rows({p.i, p.i_batch, p.i_token, b, c0}, lane), z = In::lane_rows({p.z, p.z_batch, p.z_token, b, c0}, lane);
     const Rows<S, VEC> out(p.out, p.out_batch, p.out_token, b, c0 + 2 * lane);
-    const bool has_in = VEC ? IN : in.at != nullptr, has_z = VEC ? Z : z.at != nullptr;
+    constexpr bool has_in = IN, has_z = Z;
     const int64_t c = c0 + 2 * lane;
     const f32x2 rate = RATE ? get_state(p.rate + c, mine) : 0ull;
     f32x2 carry = 0ull;
@@ -361,20 +371,20 @@ __global__ void __launch_bounds__(32 * W, 16 / W) k_gated(const __grid_constant_
         Element e = {both(1.0f), 0ull};
 #pragma unroll
         for (int k = 0; k < kFwdT; ++k) {
-            const f32x2 rr = In::read(at + Shared::kTile, r, t0, k, lane);
+            const f32x2 rr = In::read(at + Shared::kTile, r, k, lane);
             f32x2 w;
             if constexpr (RATE) {
                 f32x2 q;
                 decay_2f(mul2f(rate, sigmoid_2f(rr)), a[k], q);
-                w = has_in ? root_sigmoid_2f(q, In::read(at + 2 * Shared::kTile, in, t0, k, lane)) : mul2f(q, rsqrt_least_2f(q));
+                w = has_in ? root_sigmoid_2f(q, In::read(at + 2 * Shared::kTile, in, k, lane)) : mul2f(q, rsqrt_least_2f(q));
             } else {
                 sigmoid_both_2f(rr, w, a[k]);
                 if (has_in)
-                    w = mul2f(w, sigmoid_2f(In::read(at + 2 * Shared::kTile, in, t0, k, lane)));
+                    w = mul2f(w, sigmoid_2f(In::read(at + 2 * Shared::kTile, in, k, lane)));
             }
-            v[k] = mul2f(w, In::read(at, x, t0, k, lane));
+            v[k] = mul2f(w, In::read(at, x, k, lane));
             if (has_z) {
-                const f32x2 zz = In::read(at + 3 * Shared::kTile, z, t0, k, lane);
+                const f32x2 zz = In::read(at + 3 * Shared::kTile, z, k, lane);
                 gate[k] = mul2f(zz, sigmoid_2f(zz));
             }
             e.h = fma2f(a[k], e.h, v[k]);
@@ -478,7 +488,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) k_gated_grad(const __grid_cons
     __shared__ Element back_of_warps[2][W][32];  // the adjoint's
     __shared__ Element of_ctas[2][8][32];
     __shared__ __align__(8) uint64_t arrived[2];  // of_ctas is complete
-    const int ctas = VEC && !CLUSTER ? 1 : g.ctas;
+    const int ctas = CLUSTER ? g.ctas : 1;
     if (ctas > 1) {
         if (threadIdx.x == 0) {
             mbar_init(&arrived[0], 1);
@@ -500,7 +510,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) k_gated_grad(const __grid_cons
     const int64_t c = c0 + 2 * lane;
     const Rows<S, VEC> dx(p.dx, p.dx_batch, p.dx_token, b, c), dr(p.dr, p.dr_batch, p.dr_token, b, c), di(p.di, p.di_batch, p.di_token, b, c),
         dz(p.dz, p.dz_batch, p.dz_token, b, c);
-    const bool has_in = VEC ? IN : in.at != nullptr, has_z = VEC ? Z : z.at != nullptr;
+    constexpr bool has_in = IN, has_z = Z;
     const f32x2 rate = RATE ? get_state(p.rate + c, mine) : 0ull;
     f32x2 carry = p.dfinal != nullptr ? get_state(p.dfinal + b * p.dim + c, mine) : 0ull;
     f32x2 rate_sum = 0ull, least = 0ull;
@@ -559,7 +569,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) k_gated_grad(const __grid_cons
 #pragma unroll
         for (int k = 0; k < kBwdT; ++k) {
             f32x2 s, cs, w, rw = 0ull;
-            sigmoid_both_2f(In::read(at + Shared::kTile, r, t0, k, lane), s, cs);
+            sigmoid_both_2f(In::read(at + Shared::kTile, r, k, lane), s, cs);
             if constexpr (RATE) {
                 f32x2 q;
                 decay_2f(mul2f(rate, s), a[k], q);
@@ -569,13 +579,13 @@ __global__ void __launch_bounds__(32 * W, 16 / W) k_gated_grad(const __grid_cons
                 a[k] = cs;
                 w = s;
             }
-            const f32x2 xx = In::read(at, x, t0, k, lane), dy = In::read(at + 4 * Shared::kTile, dout, t0, k, lane);
+            const f32x2 xx = In::read(at, x, k, lane), dy = In::read(at + 4 * Shared::kTile, dout, k, lane);
             f32x2 vv = xx;
             to_x[k] = w;
             to_i[k] = 0ull;
             if (has_in) {
                 f32x2 si, ci;
-                sigmoid_both_2f(In::read(at + 2 * Shared::kTile, in, t0, k, lane), si, ci);
+                sigmoid_both_2f(In::read(at + 2 * Shared::kTile, in, k, lane), si, ci);
                 vv = mul2f(xx, si);
                 to_x[k] = mul2f(w, si);
                 to_i[k] = mul2f(xx, ci);
@@ -584,7 +594,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) k_gated_grad(const __grid_cons
             to_z[k] = 0ull;
             if (has_z) {
                 f32x2 sz, cz;
-                const f32x2 zz = In::read(at + 3 * Shared::kTile, z, t0, k, lane);
+                const f32x2 zz = In::read(at + 3 * Shared::kTile, z, k, lane);
                 sigmoid_both_2f(zz, sz, cz);
                 dh[k] = mul2f(dy, mul2f(zz, sz));
                 to_z[k] = mul2f(dy, mul2f(sz, fma2f(zz, cz, both(1.0f))));
@@ -800,6 +810,8 @@ static cudaError_t gated_backward_of(const GatedArgs &g, float *part, const Laun
 // The kernel of a call's gates and warps.
 #define MT_GATED_WARPS(f, IN, Z, ...)                                                                               \
     {                                                                                                               \
+        if constexpr (!VEC)                                                                                         \
+            return f<S, RATE, false, IN, Z, true, kGatedWarps>(__VA_ARGS__);                                        \
         if (g.ctas > 1)                                                                                             \
             return f<S, RATE, true, IN, Z, true, kGatedWarps>(__VA_ARGS__);                                         \
         if constexpr (sizeof(S) == 2)                                                                               \
@@ -808,9 +820,7 @@ static cudaError_t gated_backward_of(const GatedArgs &g, float *part, const Laun
         return f<S, RATE, true, IN, Z, false, kGatedWarps>(__VA_ARGS__);                                            \
     }
 #define MT_GATED_GATES(f, ...)                                                                                      \
-    if constexpr (!VEC) {                                                                                           \
-        return f<S, RATE, false, false, false, false, kGatedWarps>(__VA_ARGS__);                                    \
-    } else if (g.p.i != nullptr) {                                                                                  \
+    if (g.p.i != nullptr) {                                                                                  \
         if (g.p.z != nullptr)                                                                                       \
             MT_GATED_WARPS(f, true, true, __VA_ARGS__)                                                              \
         MT_GATED_WARPS(f, true, false, __VA_ARGS__)                                                                 \
