@@ -38,6 +38,7 @@ struct GatedArgs {
     mt_gated_args p;
     int slabs;       // of 64 channels
     int ctas;        // of a cluster
+    bool pairs;      // of every output, two neighbouring channels are aligned as one
     int64_t ntiles;  // checkpoints of a sequence
 };
 
@@ -252,10 +253,11 @@ const char *from = reinterpret_cast<const char *>(r.row(t0));
 };
 
 // a lane's pair, of which the first `live` channels exist (VEC: none or both)
-template <class S, bool VEC> __device__ __forceinline__ void put_pair(S *to, int live, f32x2 v) {
+// `pairs`: where not VEC, pairs are aligned all the same.
+template <class S, bool VEC> __device__ __forceinline__ void put_pair(S *to, int live, f32x2 v, bool pairs) {
     float a, b;
     unpack2f(v, a, b);
-    if constexpr (VEC) {
+    if (VEC || (pairs && live > 1)) {
         if (live > 0)
             *reinterpret_cast<typename Pair<S>::T *>(to) = Pair<S>::narrow(a, b);
     } else {
@@ -444,7 +446,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) k_gated(const __grid_constant_
                 if (has_z)
                     y = mul2f(h, gate[k]);
                 if (whole || k < n)
-                    put_pair<S, VEC>(out.row(t0 + k), mine, y);
+                    put_pair<S, VEC>(out.row(t0 + k), mine, y, g.pairs);
             }
         };
         if (n >= kFwdT)
@@ -458,7 +460,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) k_gated(const __grid_constant_
         cluster_wait();
     }
     for (int t = len + rank * W + warp; t < total; t += ctas * W)
-        put_pair<S, VEC>(out.row(t), mine, 0ull);
+        put_pair<S, VEC>(out.row(t), mine, 0ull, g.pairs);
     if (active && p.state != nullptr && rank == 0 && warp == 0)
         put_state(p.state + slot * p.dim + c, mine, carry);
 }
@@ -684,12 +686,12 @@ __global__ void __launch_bounds__(32 * W, 16 / W) k_gated_grad(const __grid_cons
                 if (whole || k < n) {
                     if (RATE)
                         rate_sum = add2f(rate_sum, to);
-                    put_pair<S, VEC>(dx.row(t0 + k), mine, gx);
-                    put_pair<S, VEC>(dr.row(t0 + k), mine, mul2f(to, to_r[k]));
+                    put_pair<S, VEC>(dx.row(t0 + k), mine, gx, g.pairs);
+                    put_pair<S, VEC>(dr.row(t0 + k), mine, mul2f(to, to_r[k]), g.pairs);
                     if (has_in)
-                        put_pair<S, VEC>(di.row(t0 + k), mine, mul2f(gx, to_i[k]));
+                        put_pair<S, VEC>(di.row(t0 + k), mine, mul2f(gx, to_i[k]), g.pairs);
                     if (has_z)
-                        put_pair<S, VEC>(dz.row(t0 + k), mine, to_z[k]);
+                        put_pair<S, VEC>(dz.row(t0 + k), mine, to_z[k], g.pairs);
                 }
             }
         };
@@ -704,12 +706,12 @@ __global__ void __launch_bounds__(32 * W, 16 / W) k_gated_grad(const __grid_cons
         cluster_wait();
     }
     for (int t = len + rank * W + warp; t < total; t += ctas * W) {
-        put_pair<S, VEC>(dx.row(t), mine, 0ull);
-        put_pair<S, VEC>(dr.row(t), mine, 0ull);
+        put_pair<S, VEC>(dx.row(t), mine, 0ull, g.pairs);
+        put_pair<S, VEC>(dr.row(t), mine, 0ull, g.pairs);
         if (has_in)
-            put_pair<S, VEC>(di.row(t), mine, 0ull);
+            put_pair<S, VEC>(di.row(t), mine, 0ull, g.pairs);
         if (has_z)
-            put_pair<S, VEC>(dz.row(t), mine, 0ull);
+            put_pair<S, VEC>(dz.row(t), mine, 0ull, g.pairs);
     }
     if (p.dinit != nullptr && rank == 0 && warp == 0)
         put_state(p.dinit + b * p.dim + c, mine, carry);
@@ -740,7 +742,7 @@ template <class S, bool RATE, bool VEC> __global__ void __launch_bounds__(128) k
     const int64_t slot = gated_slot(p, b);
     S *out = static_cast<S *>(p.out) + b * p.out_batch + c;
     if (slot < 0) {
-        put_pair<S, VEC>(out, live, 0ull);
+        put_pair<S, VEC>(out, live, 0ull, false);
         return;
     }
     auto get = [&](const void *q, int64_t batch) {
@@ -765,7 +767,7 @@ template <class S, bool RATE, bool VEC> __global__ void __launch_bounds__(128) k
     }
     const f32x2 now = fma2f(a, h, mul2f(w, x));
     put_state(state, live, now);
-    put_pair<S, VEC>(out, live, p.z != nullptr ? mul2f(now, mul2f(z, sigmoid_2f(z))) : now);
+    put_pair<S, VEC>(out, live, p.z != nullptr ? mul2f(now, mul2f(z, sigmoid_2f(z))) : now, false);
 }
 
 // ---- launches ---------------------------------------------------------------------------------------
