@@ -21,6 +21,8 @@
 // computed or read twice. A cluster's CTAs are resident together, so their waits for one another end.
 #pragma once
 
+#include <initializer_list>
+
 #include "mt_seq.cuh"
 #include "mt_seq.h"
 
@@ -177,9 +179,13 @@ template <class S, bool VEC> struct Rows {
     int64_t token;
     __device__ __forceinline__ Rows(const void *p, int64_t batch, int64_t token_, int64_t b, int64_t c0)
         : at(p == nullptr ? nullptr : const_cast<S *>(static_cast<const S *>(p)) + b * batch + c0), token(token_) {}
-    // bits by which row t begins behind a 32-bit word, t of a tile whose first token is even
-    __device__ __forceinline__ int shift(int t) const {
-        return sizeof(S) == 4 ? 0 : (int)(((uintptr_t)at ^ (uintptr_t)(t % 2 * token * 2)) & 2) * 8;
+    // of a tile: where its first row begins in a 16-byte vector, and what a token adds to that
+    int low = 0, token_low = 0;
+    __device__ __forceinline__ void begin_tile(int t0) {
+        if constexpr (!VEC && sizeof(S) == 2) {
+            low = (int)((uintptr_t)row(t0) & 15);
+            token_low = (int)(token * (int64_t)sizeof(S) & 15);
+        }
     }
     __device__ __forceinline__ S *row(int t) const {
         if constexpr (VEC)
@@ -190,8 +196,9 @@ template <class S, bool VEC> struct Rows {
 };
 
 // T tokens of a tensor in a warp's part of shared memory, 64 channels each. VEC: the rows are 16-byte aligned and
-// whole vectors; otherwise they are copied as the 32-bit words that they touch, and 16-bit rows that begin in
-// the middle of a word are read across words.
+// whole vectors; otherwise f32 rows are copied value by value, and 16-bit ones as the aligned vectors that they touch (each holds a
+// channel of the row) and read from where they begin in the first, across words where that is in the middle of one.
+// 4 x 2048 tokens x 4095 channels, bf16, all gates: 129 and 304 us for prompt and gradient (4096: 73 and 140); as 32-bit words 154 and 332.
 template <class S, int T, bool VEC> struct Tile {
     static constexpr int kPitch = kGatedSlab * (int)sizeof(S) + (VEC ? 0 : 16);
     static constexpr int kBytes = T * kPitch;
@@ -207,20 +214,19 @@ template <class S, int T, bool VEC> struct Tile {
                 if (n >= T || row < n)
                     cp_async_zfill<16>(to + k * 512 + lane * 16, r.row(t0 + row), true);
             }
+        } else if constexpr (sizeof(S) == 4) {
+#pragma unroll
+            for (int k = 0; k < 2 * T; ++k)
+                if (k / 2 < n && k % 2 * 32 + lane < live)
+                    cp_async_zfill<4>(to + k / 2 * kPitch + (k % 2 * 32 + lane) * 4, r.row(t0 + k / 2) + k % 2 * 32 + lane, true);
         } else {
-const char *from = reinterpret_cast<const char *>(r.row(t0));
-            const int64_t token = r.token * (int64_t)sizeof(S);
+            constexpr int kVectors = kPitch / 16;  // that a row can touch
 #pragma unroll
-            for (int row = 0; row < T; ++row, from += token) {
-                if (row >= n)
-                    continue;
-                const int shift = r.shift(row) / 8, words = (shift + live * (int)sizeof(S) + 3) / 4;
-#pragma unroll
-                for (int w = 0; w < kGatedSlab * (int)sizeof(S) / 4; w += 32)
-                    if (w + lane < words)
-                        cp_async_zfill<4>(to + row * kPitch + (w + lane) * 4, from - shift + (w + lane) * 4, true);
-                if (sizeof(S) == 2 && lane == 0 && words > 32)
-                    cp_async_zfill<4>(to + row * kPitch + 128, from - shift + 128, true);
+            for (int k = 0; k < (T * kVectors + 31) / 32; ++k) {
+                const int q = k * 32 + lane, row = q / kVectors, col = q % kVectors;
+                const uintptr_t from = (uintptr_t)r.row(t0 + row);
+                if (row < n && row < T && col * 16 < (int)(from & 15) + live * (int)sizeof(S))
+                    cp_async_zfill<16>(to + row * kPitch + col * 16, (const void *)((from & ~(uintptr_t)15) + col * 16), true);
             }
         }
     }
@@ -240,8 +246,9 @@ const char *from = reinterpret_cast<const char *>(r.row(t0));
             const float *f = reinterpret_cast<const float *>(at + row * kPitch) + 2 * lane;
             return pack2f(f[0], f[1]);
         } else {
-            const uint32_t *w = reinterpret_cast<const uint32_t *>(at + row * kPitch) + lane;
-            return Pair<S>::widen(__funnelshift_r(w[0], w[1], r.shift(row)));
+            const int shift = (r.low + row * r.token_low) & 15;
+            const uint32_t *w = reinterpret_cast<const uint32_t *>(at + row * kPitch + (shift & ~3)) + lane;
+            return Pair<S>::widen(__funnelshift_r(w[0], w[1], (shift & 2) * 8));
         }
     }
     // Rows from n on hold `v` in every channel.
@@ -323,7 +330,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) k_gated(const __grid_constant_
     const int64_t slot = gated_slot(p, b);
     const bool active = slot >= 0 || p.state == nullptr;
     const int len = active ? (int)gated_len(p, b) : 0, total = (int)p.len;
-    const Rows<S, VEC> x = In::lane_rows({p.x, p.x_batch, p.x_token, b, c0}, lane), r = In::lane_rows({p.r, p.r_batch, p.r_token, b, c0}, lane),
+    Rows<S, VEC> x = In::lane_rows({p.x, p.x_batch, p.x_token, b, c0}, lane), r = In::lane_rows({p.r, p.r_batch, p.r_token, b, c0}, lane),
                        in = In::lane_rows({p.i, p.i_batch, p.i_token, b, c0}, lane), z = In::lane_rows({p.z, p.z_batch, p.z_token, b, c0}, lane);
     const Rows<S, VEC> out(p.out, p.out_batch, p.out_token, b, c0 + 2 * lane);
     constexpr bool has_in = IN, has_z = Z;
@@ -369,6 +376,8 @@ __global__ void __launch_bounds__(32 * W, 16 / W) k_gated(const __grid_constant_
             In::fill(at + 3 * Shared::kTile, has, S(0.0f), lane);
             __syncwarp();
         }
+        for (Rows<S, VEC> *rows : {&x, &r, &in, &z})
+            rows->begin_tile(t0);
         f32x2 a[kFwdT], v[kFwdT], gate[kFwdT];
         Element e = {both(1.0f), 0ull};
 #pragma unroll
@@ -506,7 +515,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) k_gated_grad(const __grid_cons
     const int64_t unit = blockIdx.x / ctas, b = unit / g.slabs, c0 = (unit - b * g.slabs) * kGatedSlab;
     const int live = (int)(p.dim - c0 < kGatedSlab ? p.dim - c0 : kGatedSlab), mine = live - 2 * lane;
     const int len = (int)gated_len(p, b), total = (int)p.len;
-    const Rows<S, VEC> x = In::lane_rows({p.x, p.x_batch, p.x_token, b, c0}, lane), r = In::lane_rows({p.r, p.r_batch, p.r_token, b, c0}, lane),
+    Rows<S, VEC> x = In::lane_rows({p.x, p.x_batch, p.x_token, b, c0}, lane), r = In::lane_rows({p.r, p.r_batch, p.r_token, b, c0}, lane),
                        in = In::lane_rows({p.i, p.i_batch, p.i_token, b, c0}, lane), z = In::lane_rows({p.z, p.z_batch, p.z_token, b, c0}, lane),
                        dout = In::lane_rows({p.dout, p.dout_batch, p.dout_token, b, c0}, lane);
     const int64_t c = c0 + 2 * lane;
@@ -564,6 +573,8 @@ __global__ void __launch_bounds__(32 * W, 16 / W) k_gated_grad(const __grid_cons
             In::fill(at + 4 * Shared::kTile, has, S(0.0f), lane);
             __syncwarp();
         }
+        for (Rows<S, VEC> *rows : {&x, &r, &in, &z, &dout})
+            rows->begin_tile(t0);
         // per token: decay, w v (later the state before it), dh; w sigma(i), x (1 - sigma(i)), dz / h; and of
         // e = g as (m - h_{t-1}), with as = a s and m = v a / w (without rate 1 and v), those and dr / e
         f32x2 a[kBwdT], v[kBwdT], dh[kBwdT], to_x[kBwdT], to_i[kBwdT], to_z[kBwdT], as[kBwdT], m[kBwdT], to_r[kBwdT];
