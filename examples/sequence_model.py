@@ -5,7 +5,8 @@ a few steps, then used as it would be served (prompts, then single tokens).
            -> selective scan with gate -> projection -> + -> logits (the embedding's table, transposed)
 
 Forward and backward of the embedding, the convolution and the scan are the
-library's calls; the projections are torch matrix products. Run it on a GB300:
+library's calls, and so are a beam search's selection and the copies of states
+that follow its beams; the projections are torch matrix products. Run it on a GB300:
 
     python examples/sequence_model.py
 """
@@ -45,21 +46,22 @@ class SequenceModel:
     def _cast(self):
         return {k: v.to(self.dtype) if k in ("table", "into", "select", "out") else v for k, v in self.w.items()}
 
-    def _mix(self, c, e, conv_state=None, scan_state=None, carry=False, lens=None, checkpoints=None):
+    def _mix(self, c, e, conv_state=None, scan_state=None, carry=False, lens=None, checkpoints=None, slots=None):
         """The token mixer on embedded prompts [batch, len, dim]; everything the backward pass needs."""
         b, t, _ = e.shape
         d, n = self.inner, self.nstate
         xz = e @ c["into"]
         x, z = xz[..., :d], xz[..., d:]  # halves of one projection's rows, used where they lie
         v = torch.empty(b, t, d, dtype=self.dtype, device="cuda")
-        mt.mt_causal_conv(x, c["conv"], v, bias=c["conv_bias"], state=conv_state, carry_in=carry, lens=lens)
+        mt.mt_causal_conv(x, c["conv"], v, bias=c["conv_bias"], state=conv_state, carry_in=carry, lens=lens, slots=slots)
         p = v @ c["select"]
         delta, B, C = p[..., :d], p[..., d:d + n].unsqueeze(2), p[..., d + n:].unsqueeze(2)
         A = -torch.exp(c["A_log"])
         y = torch.empty(b, t, d, dtype=self.dtype, device="cuda")
-        slots = mt.mt_selective_scan_scratch_slots(b, t, d, n)
-        mt.mt_selective_scan(v, delta, A, B, C, y, self._slots("scan", slots) if slots else None, D=c["D"], z=z,
-                             delta_bias=c["delta_bias"], state=scan_state, carry_in=carry, lens=lens, checkpoints=checkpoints)
+        need = mt.mt_selective_scan_scratch_slots(b, t, d, n)
+        mt.mt_selective_scan(v, delta, A, B, C, y, self._slots("scan", need) if need else None, D=c["D"], z=z,
+                             delta_bias=c["delta_bias"], state=scan_state, carry_in=carry, lens=lens, checkpoints=checkpoints,
+                             slots=slots)
         return dict(x=x, z=z, v=v, delta=delta, B=B, C=C, A=A, y=y)
 
     def train_step(self, tokens, lr=0.003):
@@ -114,32 +116,59 @@ class SequenceModel:
             self.w[k] = self.w[k] - lr * (m1 / (1 - 0.9 ** self.steps)) / ((m2 / (1 - 0.99 ** self.steps)).sqrt() + 1e-8)
         return float(loss)
 
-    def prompt(self, tokens, lens, states):
-        """Logits after the last live token of each prompt [batch, len]; `states` are left at it."""
+    def prompt(self, tokens, lens, states, slots=None):
+        """Logits after the last live token of each prompt [batch, len]; `states` are left at it, in the rows `slots`."""
         c = self._cast()
         e = torch.empty(*tokens.shape, self.dim, dtype=self.dtype, device="cuda")
         mt.mt_embed(tokens, c["table"], e, scale=math.sqrt(self.dim))
-        m = self._mix(c, e, states[0], states[1], lens=lens)
+        m = self._mix(c, e, states[0], states[1], lens=lens, slots=slots)
         hidden = e + m["y"] @ c["out"]
         last = hidden[torch.arange(len(tokens), device="cuda"), lens.long() - 1]
         return (last @ c["table"].t()).float()
 
-    def token(self, tokens, states):
-        """Logits after one more token [batch] of each sequence."""
+    def token(self, tokens, states, slots=None):
+        """Logits after one more token [batch] of each sequence, whose states are the rows `slots`."""
         c, b, d, n = self._cast(), len(tokens), self.inner, self.nstate
         new = lambda *s: torch.empty(*s, dtype=self.dtype, device="cuda")  # noqa: E731
         e, v, y = new(b, self.dim), new(b, d), new(b, d)
         mt.mt_embed(tokens, c["table"], e, scale=math.sqrt(self.dim))
         xz = e @ c["into"]
-        mt.mt_causal_conv_step(xz[:, :d], c["conv"], states[0], v, bias=c["conv_bias"])
+        mt.mt_causal_conv_step(xz[:, :d], c["conv"], states[0], v, bias=c["conv_bias"], slots=slots)
         p = v @ c["select"]
         mt.mt_selective_scan_step(v, p[:, :d], -torch.exp(c["A_log"]), p[:, d:d + n].unsqueeze(1), p[:, d + n:].unsqueeze(1),
-                                  states[1], y, D=c["D"], z=xz[:, d:], delta_bias=c["delta_bias"])
+                                  states[1], y, D=c["D"], z=xz[:, d:], delta_bias=c["delta_bias"], slots=slots)
         return ((e + y @ c["out"]) @ c["table"].t()).float()
 
     def new_states(self, batch):
         return (torch.empty(batch, self.width - 1, self.inner, dtype=self.dtype, device="cuda"),
                 torch.empty(batch, self.inner, self.nstate, device="cuda"))
+
+    def search(self, prompts, lens, beams, steps, eos=-1):
+        """Beam search after each prompt: the tokens [batch, beams, steps] of the best continuations, best first, and their
+        scores (sums of log-probabilities). A continuation ends with eos, which is repeated behind it."""
+        b, vocab = len(prompts), self.vocab
+        states = self.new_states(b * beams)  # pools of a row for every beam
+        new = lambda dtype, *s: torch.empty(b, beams, *s, dtype=dtype, device="cuda")  # noqa: E731
+        tokens, parents, src, dst = (new(torch.int32) for _ in range(4))
+        scores, finished = new(torch.float32), new(torch.uint8)
+        slots = torch.arange(b * beams, dtype=torch.int32, device="cuda").view(b, beams)
+        scratch = self._slots("beams", max(mt.mt_beam_select_scratch_slots(b, k, beams, vocab) for k in (1, beams)))
+        logits = self.prompt(prompts, lens, states, slots=slots[:, 0].contiguous())
+        path = []
+        for t in range(steps):
+            more = dict(prior=scores, finished=finished if eos >= 0 else None) if t else {}  # scores and marks are updated in place
+            mt.mt_beam_select(logits.view(b, -1, vocab), tokens, parents, scores, scratch, finished_out=finished, eos=eos, slots=slots,
+                              src=src, dst=dst, **more)
+            mt.mt_state_copy(src, dst, states)  # at first every beam is a copy of the prompt's
+            path.append((tokens.clone(), parents.long()))
+            if t + 1 < steps:
+                logits = self.token(tokens.view(-1), states, slots=slots.view(-1))
+        out = new(torch.int32, steps)
+        at = torch.arange(beams, device="cuda").expand(b, beams)
+        for t in reversed(range(steps)):  # from each beam back to the prompt
+            out[:, :, t] = path[t][0].gather(1, at)
+            at = path[t][1].gather(1, at)
+        return out, scores
 
 
 def counting(batch, length, vocab, seed):
@@ -161,6 +190,8 @@ def main(steps=60, vocab=64, batch=16, length=65):
         tokens = logits.argmax(-1).to(torch.int32)
         logits = model.token(tokens, states)
     print("next tokens after 8 more:", logits.argmax(-1).tolist())
+    tokens, scores = model.search(prompts, lens, beams=4, steps=8)
+    print("best of 4 beams:", tokens[:, 0].tolist(), "scores", [round(v, 3) for v in scores[:, 0].tolist()])
     return losses
 
 
