@@ -248,7 +248,7 @@ __device__ __forceinline__ uint32_t read_span(Part<S> &part, const S *x, int64_t
 }
 
 // VEC: rows are made of aligned vectors.
-template <class S, bool VEC> __global__ void __launch_bounds__(kBeamThreads) k_beam_read(const __grid_constant__ mt_beam_args a, BeamPlan plan) {
+template <class S, bool VEC> __global__ void __launch_bounds__(kBeamThreads, 5) k_beam_read(const __grid_constant__ mt_beam_args a, BeamPlan plan) {
     constexpr int E = Logits<S>::E;
     pdl_prologue();
     const int lane = threadIdx.x % 32;
