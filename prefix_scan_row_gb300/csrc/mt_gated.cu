@@ -16,7 +16,7 @@ static int gated_ctas(int64_t batch, int64_t len, int64_t dim, int64_t cta_token
 }
 
 int64_t gated_scratch_slots(int64_t batch, int64_t len, int64_t dim) {
-    return (batch * gated_ctas(batch, len, dim, kGatedWarps * kBwdT) * dim + 1) / 2;
+    return (batch * gated_ctas(batch, len, dim, kBwdWarps * kBwdT) * dim + 1) / 2;
 }
 
 // Sums of parts [rows, dim] over the rows, in order: a warp's lanes share 32 channels, its CTA's warps the rows.
@@ -96,7 +96,7 @@ static cudaError_t backward(const GatedArgs &g, float *part, const Launch &L) {
     MT_BY_TYPE(gated_backward, g, part, vec, L)
 }
 cudaError_t gated_grad_launch(const mt_gated_args &p, const Launch &L) {
-    const GatedArgs g = gated_args(p, kGatedWarps * kBwdT, true);
+    const GatedArgs g = gated_args(p, kBwdWarps * kBwdT, true);
     float *part = p.drate != nullptr ? static_cast<float *>(p.scratch) : nullptr;
     if (p.batch * g.slabs * g.ctas > INT32_MAX)
         return cudaErrorInvalidValue;

@@ -22,6 +22,7 @@
 #pragma once
 
 #include <initializer_list>
+#include <type_traits>
 
 #include "mt_seq.cuh"
 #include "mt_seq.h"
@@ -29,10 +30,10 @@
 namespace mt {
 
 constexpr int kGatedSlab = 64;   // channels of a warp
-constexpr int kGatedWarps = 8;   // warps of a CTA
-// and where 16-bit calls have more CTAs than three an SM, so that a smaller one's end leaves less idle. Both, us, all gates, 4096 channels, prompt
-// and gradient, by sequences x tokens (CTAs): 4 x 2048 (256) 73 and 140, 73 and 151; 6 x 2048 (384) 110 and 213, 125 and
-// 199; 8 x 2048 (512) 140 and 271, 127 and 253; 16 x 1024 (1024) 125 and 240, 111 and 224. f32: 8 x 2048 211 and 403, 246 and 444.
+constexpr int kGatedWarps = 8;   // warps of a prompt's CTA
+// and where 16-bit calls have more CTAs than three an SM, so that a smaller one's end leaves less idle. Both, us, all gates,
+// 4096 channels, bf16, by sequences x tokens (CTAs): 4 x 2048 (256) 73, 73; 6 x 2048 (384) 110, 125; 8 x 2048 (512)
+// 140, 127; 16 x 1024 (1024) 125, 111. f32: 8 x 2048 211, 246.
 constexpr int kGatedFewWarps = 4;
 constexpr int kGatedStages = 2;  // tiles of a warp on their way or in use
 
@@ -477,20 +478,24 @@ __global__ void __launch_bounds__(32 * W, 16 / W) k_gated(const __grid_constant_
 // ---- gradients ----------------------------------------------------------------------------------------
 // From the last tokens to the first. A warp's tokens give two elements, the recurrence's from the checkpoint before
 // them and its adjoint's from behind; with both carries known the states and the gradients by them
-// follow, and what a token's gradients take besides is in registers: four tokens' worth of it.
-constexpr int kBwdT = 4;
+// follow, and what a token's gradients take besides is in registers: eight tokens' worth of it, in all that a thread can
+// have. So an SM holds eight such warps, in two CTAs. Twice the warps of four tokens, which take the carries' work twice as
+// often, against these, us, all gates, 4096 channels, bf16: 4 x 2048 tokens 140 and 121, 8 x 2048 253 and 237; no output gate 4 x 4096 254 and 198.
+constexpr int kBwdT = 8;
+constexpr int kBwdWarps = 4;
 constexpr int kBwdTensors = 5;
 
-template <class S, bool VEC, int W> struct BwdShared {
+template <class S, bool VEC> struct BwdShared {
     static constexpr int kTile = Tile<S, kBwdT, VEC>::kBytes;
     static constexpr int kWarp = kGatedStages * kBwdTensors * kTile;
-    static constexpr int kBytes = W * kWarp;
+    static constexpr int kBytes = kBwdWarps * kWarp;
 };
 
-template <class S, bool RATE, bool VEC, bool IN, bool Z, bool CLUSTER, int W>
-__global__ void __launch_bounds__(32 * W, 16 / W) k_gated_grad(const __grid_constant__ GatedArgs g, float *rate_part) {
+template <class S, bool RATE, bool VEC, bool IN, bool Z, bool CLUSTER>
+__global__ void __launch_bounds__(32 * kBwdWarps, 2) k_gated_grad(const __grid_constant__ GatedArgs g, float *rate_part) {
     using In = Tile<S, kBwdT, VEC>;
-    using Shared = BwdShared<S, VEC, W>;
+    using Shared = BwdShared<S, VEC>;
+    constexpr int W = kBwdWarps;
     constexpr int kCtaTokens = W * kBwdT;
     constexpr int kMarkWarps = kGatedTile / kBwdT;  // that share a checkpoint
     static_assert(kCtaTokens % kGatedTile == 0 && kGatedTile % kBwdT == 0, "a CTA's tokens begin at a checkpoint");
@@ -810,43 +815,41 @@ template <class S, bool RATE, bool VEC, bool IN, bool Z, bool CLUSTER, int W> st
     note_launch();
     return launch_cluster(k_gated<S, RATE, VEC, IN, Z, CLUSTER, W>, g.p.batch * g.slabs * g.ctas, 32 * W, smem, g.ctas, L.stream, g);
 }
-template <class S, bool RATE, bool VEC, bool IN, bool Z, bool CLUSTER, int W>
+template <class S, bool RATE, bool VEC, bool IN, bool Z, bool CLUSTER>
 static cudaError_t gated_backward_of(const GatedArgs &g, float *part, const Launch &L) {
     static PerDevice ready;
-    constexpr int smem = BwdShared<S, VEC, W>::kBytes;
-    const cudaError_t e = allow_shared(k_gated_grad<S, RATE, VEC, IN, Z, CLUSTER, W>, smem, ready);
+    constexpr int smem = BwdShared<S, VEC>::kBytes;
+    const cudaError_t e = allow_shared(k_gated_grad<S, RATE, VEC, IN, Z, CLUSTER>, smem, ready);
     if (e != cudaSuccess)
         return e;
     note_launch();
-    return launch_cluster(k_gated_grad<S, RATE, VEC, IN, Z, CLUSTER, W>, g.p.batch * g.slabs * g.ctas, 32 * W, smem, g.ctas, L.stream, g, part);
+    return launch_cluster(k_gated_grad<S, RATE, VEC, IN, Z, CLUSTER>, g.p.batch * g.slabs * g.ctas, 32 * kBwdWarps, smem, g.ctas, L.stream, g, part);
 }
-// The kernel of a call's gates and warps.
-#define MT_GATED_WARPS(f, IN, Z, ...)                                                                               \
-    {                                                                                                               \
-        if constexpr (!VEC)                                                                                         \
-            return f<S, RATE, false, IN, Z, true, kGatedWarps>(__VA_ARGS__);                                        \
-        if (g.ctas > 1)                                                                                             \
-            return f<S, RATE, true, IN, Z, true, kGatedWarps>(__VA_ARGS__);                                         \
-        if constexpr (sizeof(S) == 2)                                                                               \
-            if (g.p.batch * g.slabs > 3 * 152)                                                                      \
-                return f<S, RATE, true, IN, Z, false, kGatedFewWarps>(__VA_ARGS__);                                 \
-        return f<S, RATE, true, IN, Z, false, kGatedWarps>(__VA_ARGS__);                                            \
-    }
-#define MT_GATED_GATES(f, ...)                                                                                      \
-    if (g.p.i != nullptr) {                                                                                  \
-        if (g.p.z != nullptr)                                                                                       \
-            MT_GATED_WARPS(f, true, true, __VA_ARGS__)                                                              \
-        MT_GATED_WARPS(f, true, false, __VA_ARGS__)                                                                 \
-    } else {                                                                                                        \
-        if (g.p.z != nullptr)                                                                                       \
-            MT_GATED_WARPS(f, false, true, __VA_ARGS__)                                                             \
-        MT_GATED_WARPS(f, false, false, __VA_ARGS__)                                                                \
-    }
+// The kernel of a call's gates: f(std::bool_constant of the input gate, of the output gate).
+template <class F> static cudaError_t by_gates(const mt_gated_args &p, F f) {
+    if (p.i != nullptr)
+        return p.z != nullptr ? f(std::true_type(), std::true_type()) : f(std::true_type(), std::false_type());
+    return p.z != nullptr ? f(std::false_type(), std::true_type()) : f(std::false_type(), std::false_type());
+}
 template <class S, bool RATE, bool VEC> static cudaError_t gated_forward(const GatedArgs &g, const Launch &L) {
-    MT_GATED_GATES(gated_forward_of, g, L)
+    return by_gates(g.p, [&](auto in, auto z) {
+        if constexpr (!VEC)
+            return gated_forward_of<S, RATE, false, in(), z(), true, kGatedWarps>(g, L);
+        else if (g.ctas > 1)
+            return gated_forward_of<S, RATE, true, in(), z(), true, kGatedWarps>(g, L);
+        else if (sizeof(S) == 2 && g.p.batch * g.slabs > 3 * 152)
+            return gated_forward_of<S, RATE, true, in(), z(), false, sizeof(S) == 2 ? kGatedFewWarps : kGatedWarps>(g, L);
+        else
+            return gated_forward_of<S, RATE, true, in(), z(), false, kGatedWarps>(g, L);
+    });
 }
 template <class S, bool RATE, bool VEC> static cudaError_t gated_backward(const GatedArgs &g, float *part, const Launch &L) {
-    MT_GATED_GATES(gated_backward_of, g, part, L)
+    return by_gates(g.p, [&](auto in, auto z) {
+        if constexpr (VEC)
+            if (g.ctas == 1)
+                return gated_backward_of<S, RATE, true, in(), z(), false>(g, part, L);
+        return gated_backward_of<S, RATE, VEC, in(), z(), true>(g, part, L);
+    });
 }
 template <class S, bool RATE, bool VEC> static cudaError_t gated_single(const GatedArgs &g, const Launch &L) {
     const int64_t threads = g.p.batch * ((g.p.dim + 1) / 2);
