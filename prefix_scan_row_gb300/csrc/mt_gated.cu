@@ -77,7 +77,7 @@ static GatedArgs gated_args(const mt_gated_args &p, int64_t cta_tokens, bool gra
     default: return cudaErrorInvalidValue;              \
     }
 cudaError_t gated_launch(const mt_gated_args &p, const Launch &L) {
-    const GatedArgs g = gated_args(p, kGatedWarps * kFwdT, false);
+    const GatedArgs g = gated_args(p, gated_cluster_warps(p.dtype == MT_F32 ? 4 : 2) * kFwdT, false);
     const bool vec = all_fit(p, 16, false, false);
     if (p.batch * g.slabs * g.ctas > INT32_MAX)
         return cudaErrorInvalidValue;

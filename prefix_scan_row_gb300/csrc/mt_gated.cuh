@@ -35,6 +35,9 @@ constexpr int kGatedWarps = 8;   // warps of a prompt's CTA
 // 4096 channels, bf16, by sequences x tokens (CTAs): 4 x 2048 (256) 73, 73; 6 x 2048 (384) 110, 125; 8 x 2048 (512)
 // 140, 127; 16 x 1024 (1024) 125, 111. f32: 8 x 2048 211, 246.
 constexpr int kGatedFewWarps = 4;
+// and of a cluster, of values of so many bytes: f32's tiles leave no place for two CTAs of eight warps in an SM, and a cluster's
+// CTAs have to be resident together. f32, us, with four and with eight: 16384 x 2048 135, 221; 4096 x 4096 68, 76; 4 x 333 x 1024 11, 17.
+constexpr int gated_cluster_warps(int bytes) { return bytes == 4 ? kGatedFewWarps : kGatedWarps; }
 constexpr int kGatedStages = 2;  // tiles of a warp on their way or in use
 
 struct GatedArgs {
@@ -183,7 +186,7 @@ template <class S, bool VEC> struct Rows {
     // of a tile: where its first row begins in a 16-byte vector, and what a token adds to that
     int low = 0, token_low = 0;
     __device__ __forceinline__ void begin_tile(int t0) {
-        if constexpr (!VEC && sizeof(S) == 2) {
+        if constexpr (!VEC) {
             low = (int)((uintptr_t)row(t0) & 15);
             token_low = (int)(token * (int64_t)sizeof(S) & 15);
         }
@@ -197,10 +200,11 @@ template <class S, bool VEC> struct Rows {
 };
 
 // T tokens of a tensor in a warp's part of shared memory, 64 channels each. VEC: the rows are 16-byte aligned and
-// whole vectors; otherwise f32 rows are copied value by value, and 16-bit ones as the aligned vectors that they touch (each holds a
-// channel of the row) and read from where they begin in the first, across words where that is in the middle of one.
-// 4 x 2048 tokens x 4095 channels, bf16, all gates: 129 and 304 us for prompt and gradient (4096: 73 and 140); as 32-bit words 154 and 332.
-template <class S, int T, bool VEC> struct Tile {
+// whole vectors. Otherwise rows are copied as the aligned vectors that they touch (each holds a channel of the row) and read from
+// where they begin in the first, 16-bit ones across words where that is in the middle of one; or, WORDS, f32 value by value.
+// 4 x 2048 tokens x 4095 channels, all gates, us: bf16 prompt 129 and gradient 286 (as 32-bit words 154 and 332; of 4096
+// channels 73 and 121); f32 prompt by words 189, by vectors 208, gradient 398 and 320.
+template <class S, int T, bool VEC, bool WORDS = false> struct Tile {
     static constexpr int kPitch = kGatedSlab * (int)sizeof(S) + (VEC ? 0 : 16);
     static constexpr int kBytes = T * kPitch;
     static constexpr int kRow = kGatedSlab * (int)sizeof(S) / 16, kPer = 16 / (int)sizeof(S);  // vectors of a row, values of one
@@ -215,7 +219,7 @@ template <class S, int T, bool VEC> struct Tile {
                 if (n >= T || row < n)
                     cp_async_zfill<16>(to + k * 512 + lane * 16, r.row(t0 + row), true);
             }
-        } else if constexpr (sizeof(S) == 4) {
+        } else if constexpr (WORDS) {
 #pragma unroll
             for (int k = 0; k < 2 * T; ++k)
                 if (k / 2 < n && k % 2 * 32 + lane < live)
@@ -241,13 +245,13 @@ template <class S, int T, bool VEC> struct Tile {
     // The lane's channels of the tile's row.
     static __device__ __forceinline__ f32x2 read(const char *at, const Rows<S, VEC> &r, int row, int lane) {
         using P = typename Pair<S>::T;
-        if constexpr (VEC) {
+        if constexpr (VEC)
             return Pair<S>::widen(*reinterpret_cast<const P *>(at + row * kPitch + lane * (int)sizeof(P)));
-        } else if constexpr (sizeof(S) == 4) {
-            const float *f = reinterpret_cast<const float *>(at + row * kPitch) + 2 * lane;
+        const int shift = WORDS ? 0 : (r.low + row * r.token_low) & 15;
+        if constexpr (sizeof(S) == 4) {
+            const float *f = reinterpret_cast<const float *>(at + row * kPitch + shift) + 2 * lane;
             return pack2f(f[0], f[1]);
         } else {
-            const int shift = (r.low + row * r.token_low) & 15;
             const uint32_t *w = reinterpret_cast<const uint32_t *>(at + row * kPitch + (shift & ~3)) + lane;
             return Pair<S>::widen(__funnelshift_r(w[0], w[1], (shift & 2) * 8));
         }
@@ -295,9 +299,11 @@ struct alignas(16) Element {  // of the scan
 // ---- prompts ----------------------------------------------------------------------------------------
 constexpr int kFwdT = 8;  // tokens of a warp
 
+template <class S, bool VEC> using FwdTile = Tile<S, kFwdT, VEC, sizeof(S) == 4>;
+
 template <class S, bool VEC, int W> struct FwdShared {
     static constexpr int kTensors = 4;
-    static constexpr int kTile = Tile<S, kFwdT, VEC>::kBytes;
+    static constexpr int kTile = FwdTile<S, VEC>::kBytes;
     static constexpr int kWarp = kGatedStages * kTensors * kTile;
     static constexpr int kBytes = W * kWarp;
 };
@@ -306,7 +312,7 @@ template <class S, bool VEC, int W> struct FwdShared {
 // W: warps of the CTA.
 template <class S, bool RATE, bool VEC, bool IN, bool Z, bool CLUSTER, int W>
 __global__ void __launch_bounds__(32 * W, 16 / W) k_gated(const __grid_constant__ GatedArgs g) {
-    using In = Tile<S, kFwdT, VEC>;
+    using In = FwdTile<S, VEC>;
     using Shared = FwdShared<S, VEC, W>;
     constexpr int kCtaTokens = W * kFwdT;
     extern __shared__ __align__(16) char staged[];
@@ -834,9 +840,9 @@ template <class F> static cudaError_t by_gates(const mt_gated_args &p, F f) {
 template <class S, bool RATE, bool VEC> static cudaError_t gated_forward(const GatedArgs &g, const Launch &L) {
     return by_gates(g.p, [&](auto in, auto z) {
         if constexpr (!VEC)
-            return gated_forward_of<S, RATE, false, in(), z(), true, kGatedWarps>(g, L);
+            return gated_forward_of<S, RATE, false, in(), z(), true, gated_cluster_warps(sizeof(S))>(g, L);
         else if (g.ctas > 1)
-            return gated_forward_of<S, RATE, true, in(), z(), true, kGatedWarps>(g, L);
+            return gated_forward_of<S, RATE, true, in(), z(), true, gated_cluster_warps(sizeof(S))>(g, L);
         else if (sizeof(S) == 2 && g.p.batch * g.slabs > 3 * 152)
             return gated_forward_of<S, RATE, true, in(), z(), false, sizeof(S) == 2 ? kGatedFewWarps : kGatedWarps>(g, L);
         else
