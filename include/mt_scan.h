@@ -301,7 +301,7 @@ int64_t mt_scan_rows_scratch_slots(int64_t rows, int64_t n, int dtype);
 /*
  * mt_scan_status -- synchronise `stream`, then read and clear the device
  * error word of every kernel of the library on the current device.
- * Returns MT_OK, MT_ERR_LOOKBACK_TIMEOUT (a look-back wait gave up and the
+ * Returns MT_OK, MT_ERR_LOOKBACK_TIMEOUT (a look-back or cluster wait gave up and the
  * results of the calls since the last check are not valid), MT_ERR_BOUNDS
  * (only from the bounds-checked build of the library, libmtscan_checked.so:
  * a kernel computed an address outside the buffer it was writing or the
@@ -375,11 +375,13 @@ int mt_scan_rows_noalloc(const void *inp, void *out, int64_t rows, int64_t n, in
 /* ------------------------------------------------------------------------
  * Operators of sequence models: the embedding lookup, the short causal
  * convolution, the selective state space scan and the gated scan, forward, backward and for
- * single tokens; a beam search's selection, and copies between slots of state pools. They follow the rules above: caller-owned device memory,
- * work enqueued on `stream` only, host-checkable mistakes refused before any
- * launch, f32 arithmetic with one rounding at each store. Every sum has a
- * fixed order, so a call gives the same bits each time. No call waits
- * between CTAs.
+ * single tokens; a beam search's selection, and copies between slots of state
+ * pools. They follow the rules above: caller-owned device memory, work enqueued
+ * on `stream` only, host-checkable mistakes refused before any launch, f32
+ * arithmetic with one rounding at each store. Every sum has a fixed order, so a
+ * call gives the same bits each time. No call waits between CTAs, but for the
+ * gated scan's, whose CTAs of one cluster wait for one another; those waits are
+ * bounded, and one that gave up is reported by mt_scan_status.
  *
  * Activations are [batch, len, dim] with the channels contiguous and any
  * strides (in elements) of the other two axes, so they may be parts of wider
@@ -586,7 +588,7 @@ typedef struct {
     int64_t i_batch, i_token;
     const void *z;                 /* [batch, len, dim], optional: the gate of the output */
     int64_t z_batch, z_token;
-    const float *rate;             /* [dim], optional, 0 or more */
+    const float *rate;             /* [dim], optional, 0 to 2^100 */
     float *state;                  /* [nslots, dim] contiguous */
     const int32_t *slots, *lens;   /* optional */
     void *out;                     /* [batch, len, dim] */

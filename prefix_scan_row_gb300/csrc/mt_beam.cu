@@ -8,6 +8,10 @@
 // again, and the few logits in them that reach the last one's score are ranked. Where there are many such logits (equal ones, or
 // high ones beside each other), the same step over the groups' vectors, and then over theirs, leaves few.
 //
+// Bound: the first kernel by bytes, f32, and by its instructions, 16-bit (an exponential a logit; issue 63 %, XU 38 %); the second
+// by its chain of loads, barriers and comparisons, 8 to 10 us. Both together, us in a CUDA graph (share of the measured copy rate, 6798 GB/s):
+// 64 x 16 x 131072 logits f32 91 (87 %), bf16 55 (71 %); 64 x 8 x 32768 bf16 16.8 (29 %); 1 x 4 x 32768 f32 7.9. Rows that are not
+// aligned take two loads for a vector: 64 x 16 x 131071 bf16 84 (47 %). All logits equal, 64 x 16 x 131072 bf16: 102.
 #include <initializer_list>
 
 #include "mt_seq.cuh"
@@ -105,7 +109,8 @@ struct BeamPlan {
     int batches;    // groups of a span
     int64_t spans;  // of a beam's logits
 };
-// Spans as long as leave enough warps.
+// Spans as long as leave enough warps, us by the warps asked for, 152 x 8, 152 x 64 and 152 x 256: 64 x 8 x 32768 bf16 19.1, 16.8, 16.6;
+// 64 x 16 x 131071 bf16 83.9, 83.7, 90.7; 5 x 7 x 100003 f16 13.8, 13.3, 13.2.
 constexpr int64_t kEnoughSpans = 152 * 32 * 2;
 BeamPlan beam_plan(int64_t rows, int64_t vocab, int64_t size) {
     BeamPlan p;
@@ -247,7 +252,7 @@ __device__ __forceinline__ uint32_t read_span(Part<S> &part, const S *x, int64_t
     return mine;
 }
 
-// VEC: rows are made of aligned vectors.
+// VEC: rows are made of aligned vectors. Five CTAs an SM (48 registers): 64 x 16 x 131071 bf16 84 us, with four 98.
 template <class S, bool VEC> __global__ void __launch_bounds__(kBeamThreads, 5) k_beam_read(const __grid_constant__ mt_beam_args a, BeamPlan plan) {
     constexpr int E = Logits<S>::E;
     pdl_prologue();
@@ -301,6 +306,10 @@ template <class S, bool VEC> __global__ void __launch_bounds__(kBeamThreads, 5) 
         groups[lane] = mine;
 }
 
+// log(2) as a pair, and as one whose first part has 9 bits, so that a small whole number times it is exact
+constexpr double kLn2Double = 0.693147180559945309417;
+constexpr float kLn2Low = (float)(kLn2Double - (double)kLn2), kLn2Few = 355.0f / 512.0f, kLn2FewLow = (float)(kLn2Double - (double)kLn2Few);
+
 // Logarithms of c = 1 - j / 128, j below 64, as f32 pairs: the series of 2 atanh((c - 1) / (c + 1)), summed by the compiler.
 struct LogTable {
     float high[64], low[64];
@@ -343,8 +352,8 @@ __device__ __forceinline__ void best_score(float prior, uint64_t sum, int power,
     log1 = fmaf(log1, z, -0.5f) * z * z;
     // (power - log2(e) top) log(2), exactly but for its last rounding; and e log(2), whose first part has few bits
     const float t = kLog2e * top, d = (float)power - t, d_low = -fmaf(kLog2e, top, -t);
-    const float w = d * kLn2, w_low = fmaf(d, kLn2, -w) + (d * -1.90465421e-9f + d_low * kLn2);
-    const float f = (float)(e - 30), e_high = f * 0.693359375f, e_low = f * -2.12194440e-4f;
+    const float w = d * kLn2, w_low = fmaf(d, kLn2, -w) + (d * kLn2Low + d_low * kLn2);
+    const float f = (float)(e - 30), e_high = f * kLn2Few, e_low = f * kLn2FewLow;
     float r0, r1, r2, r3, s = two_sum(prior, -e_high, r0);
     s = two_sum(s, kLogTable.high[at], r1);
     s = two_sum(s, -z, r2);
@@ -520,7 +529,7 @@ template <class S, bool VEC> __global__ void __launch_bounds__(kJoinThreads) k_b
                     const double m = (double)top_of(o);
                     const int p = power_in(o);
                     if (p != kLeastPower)
-                        all += (double)o.x * 0x1p-40 * exp(m - (double)top + (p == kNoPower ? 0.0 : ((double)p - m * (double)kLog2e) * 0.693147180559945309417));
+                        all += (double)o.x * 0x1p-40 * exp(m - (double)top + (p == kNoPower ? 0.0 : ((double)p - m * (double)kLog2e) * kLn2Double));
                 });
                 for (int o = 16; o > 0; o /= 2)
                     all += __shfl_xor_sync(kFull, all, o);

@@ -3,7 +3,8 @@
 // Rows of a pool of layers lie far apart, so a CTA takes one chunk of a row and plane, 16 KB, with the widest accesses that the
 // pool's addresses and sizes allow. Where there are many pairs it takes that chunk of up to 32 of them, since most pairs of
 // a beam search copy nothing and a CTA for each costs more than the rest of its work. Only bytes count: each is read
-// once and written once.
+// once and written once. 64 sequences of 8 beams, 192 copies of 287 KB in each of 4 layers: 66 us in a CUDA graph, 98 % of the measured
+// copy rate (6798 GB/s); one sequence of 4 beams, one layer: 2.0.
 #include "mt_seq.cuh"
 #include "mt_seq.h"
 
@@ -14,7 +15,8 @@ namespace {
 constexpr int kCopyThreads = 256;
 constexpr int kCopyInFlight = 4;                                       // loads of a thread before its stores
 constexpr int64_t kCopyChunk = 16 * kCopyThreads * kCopyInFlight;      // bytes of a CTA
-
+// More CTAs than these take more pairs each. us, by one pair a CTA, this rule, and one wave of CTAs (152 x 8): 64 x 8 beams x 4 layers, 3 of
+// 8 beams copied 83.9, 66.0, 69.6; 7 of 8 106, 91, 98; one layer 22.7, 17.9, 15.1; 8 x 4 beams x 4 layers 6.4, 6.4, 5.9.
 constexpr int64_t kEnoughCtas = 152 * 8 * 4;
 
 struct CopyPool {

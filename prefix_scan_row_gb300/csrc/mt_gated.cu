@@ -4,8 +4,9 @@
 namespace mt {
 
 // CTAs that share a sequence's tokens: one where sequences and channels give every SM work, and otherwise as many as find
-// place at once, two an SM. A cluster's CTAs wait for one another at every tile, so it pays only then: 4 x 2048 tokens x 4096
-// channels (256 CTAs without clusters), bf16, all gates: 73 us, in clusters of 8 103; 16384 tokens x 2048 (32): 328 and 102.
+// place at once, two an SM. A cluster's CTAs wait for one another at every tile, so it pays only then. bf16, all gates, prompt, us, in
+// clusters of 1, 2, 4 and 8 CTAs: 4 x 2048 tokens x 4096 channels (256 CTAs without clusters) 73, 89, 86, 101; 16384 tokens x
+// 2048 (32) 339, 224, 117, 98.
 // The scratch is sized on the host, so the plan counts GB300's 152 SMs.
 static int gated_ctas(int64_t batch, int64_t len, int64_t dim, int64_t cta_tokens) {
     const int64_t units = batch * ((dim + kGatedSlab - 1) / kGatedSlab);
@@ -61,7 +62,9 @@ static GatedArgs gated_args(const mt_gated_args &p, int64_t cta_tokens, bool gra
     g.p = p;
     g.slabs = (int)((p.dim + kGatedSlab - 1) / kGatedSlab);
     g.ctas = gated_ctas(p.batch, p.len, p.dim, cta_tokens);
-    auto even = [&](const void *q, int64_t batch, int64_t token) { return q == nullptr || ((uintptr_t)q % (p.dtype == MT_F32 ? 8 : 4) == 0 && batch % 2 == 0 && token % 2 == 0); };
+    auto even = [&](const void *q, int64_t batch, int64_t token) {
+        return q == nullptr || ((uintptr_t)q % (p.dtype == MT_F32 ? 8 : 4) == 0 && batch % 2 == 0 && token % 2 == 0);
+    };
     g.pairs = grad ? even(p.dx, p.dx_batch, p.dx_token) && even(p.dr, p.dr_batch, p.dr_token) && (p.i == nullptr || even(p.di, p.di_batch, p.di_token)) &&
                          (p.z == nullptr || even(p.dz, p.dz_batch, p.dz_token))
                    : even(p.out, p.out_batch, p.out_token);

@@ -9,9 +9,9 @@
 //   rate: with u = rate s, da/du = -a and dw/du = a^2 / w, so e = g (v a^2 / w - h_{t-1} a) s,
 //         dr = e rate (1 - s), drate = sum of e;  no rate: dr = g (v - h_{t-1}) s (1 - s)
 //
-// Both recurrences are scans with the operator (a, b) o (a', b') = (a a', a' b + b'). Bound: bytes. A
-// token's channel is 4 to 10 bytes at 16-bit storage and 6 to 8 exponentials, reciprocals and roots (30.5 a clock
-// and SM), which together take less than the bytes.
+// Both recurrences are scans with the operator (a, b) o (a', b') = (a a', a' b + b'). The floor is bytes: a
+// token's channel is 6 to 8 of them at 16-bit storage (gradient 10 to 18), and its 5 to 8 exponentials,
+// reciprocals and roots, at 30.5 a clock and SM, take less.
 //
 // So every input is read once: the token axis is cut over the warps of a CTA, and where sequences and channels alone
 // do not fill the GPU over the CTAs of a cluster too. A warp has kT tokens of 64 channels, a lane a pair of channels in
@@ -19,6 +19,12 @@
 // scan. The elements meet in shared memory, those of a cluster's CTAs in each other's, and each warp then
 // knows its first state and finishes its tokens, whose decays and inputs are still in registers. Nothing is
 // computed or read twice. A cluster's CTAs are resident together, so their waits for one another end.
+//
+// Measured, all gates, us (share of the measured copy rate, 6798 GB/s): 16 x 1024 tokens x 4096 channels bf16, prompt 112
+// (88 %), gradient 222 (80 %); 4 x 2048 x 4096 bf16 74 (67 %) and 121 (73 %): 256 CTAs leave some SMs two and others one, and
+// the schedulers, the exponentials' unit and the multiply-adds' are each 25 to 57 % busy (86 instructions for a pair's token in
+// the prompt, 132 in the gradient); 16384 x 2048 bf16 98 (50 %) and 158 (56 %): the same, and clusters' waits; 8 x 2048 x 4096
+// f32 212 (93 %) and 414 (86 %).
 #pragma once
 
 #include <initializer_list>
@@ -264,8 +270,8 @@ template <class S, int T, bool VEC, bool WORDS = false> struct Tile {
     }
 };
 
-// a lane's pair, of which the first `live` channels exist (VEC: none or both)
-// `pairs`: where not VEC, pairs are aligned all the same.
+// A lane's pair, of which the first `live` channels exist (VEC: none or both). `pairs`: where not VEC, pairs are aligned all
+// the same and leave as one: 4 x 2048 tokens x 4098 channels, bf16, gradient, us: 309, one by one 333.
 template <class S, bool VEC> __device__ __forceinline__ void put_pair(S *to, int live, f32x2 v, bool pairs) {
     float a, b;
     unpack2f(v, a, b);
@@ -297,7 +303,9 @@ struct alignas(16) Element {  // of the scan
 };
 
 // ---- prompts ----------------------------------------------------------------------------------------
-constexpr int kFwdT = 8;  // tokens of a warp
+// Tokens of a warp. 4 x 2048 x 4096, bf16, all gates, us, eight warps a CTA: 4 tokens 115 (three CTAs an SM), 8 74, 16 77 (one). Four warps
+// of 16 take 69 there, but 8 x 2048 134 (of 8: 127), and 4 x 4096 without output gate 147 (114).
+constexpr int kFwdT = 8;
 
 template <class S, bool VEC> using FwdTile = Tile<S, kFwdT, VEC, sizeof(S) == 4>;
 
@@ -873,7 +881,9 @@ template <class S, bool RATE, bool VEC> static cudaError_t gated_single(const Ga
     cudaError_t gated_##name##_take_error(int *code) { return gated_take_error_word(code); }
 #define MT_GATED_GRAD_TYPE(name, T)                                                                                                 \
     using S = T;                                                                                                                    \
-    cudaError_t gated_backward_##name(const GatedArgs &g, float *part, bool vec, const Launch &L) { return MT_GATED_BY(gated_backward, g, part, L); } \
+    cudaError_t gated_backward_##name(const GatedArgs &g, float *part, bool vec, const Launch &L) {                                 \
+        return MT_GATED_BY(gated_backward, g, part, L);                                                                             \
+    }                                                                                                                               \
     cudaError_t gated_grad_##name##_take_error(int *code) { return gated_take_error_word(code); }
 
 // Reads and clears this translation unit's device error word.
