@@ -6,14 +6,18 @@ namespace mt {
 // CTAs that share a sequence's tokens: one where sequences and channels give every SM work, and otherwise as many as find
 // place at once, two an SM. A cluster's CTAs wait for one another at every tile, so it pays only then. bf16, all gates, prompt, us, in
 // clusters of 1, 2, 4 and 8 CTAs: 4 x 2048 tokens x 4096 channels (256 CTAs without clusters) 73, 89, 86, 101; 16384 tokens x
-// 2048 (32) 339, 224, 117, 98.
-// The scratch is sized on the host, so the plan counts GB300's 152 SMs.
+// 2048 (32) 339, 224, 117, 98. Of the sizes with the same number of tiles the smallest.
+// The scratch is sized on the host, so the plan counts GB300's 152 SMs, and by the cluster's size the CTAs that were found to run
+// at once: clusters lie within a group of SMs, so not all places can be taken (with 266 CTAs in 38 clusters of 7 a prompt of 2048 tokens takes as
+// long as with 252, its gradient 41 us for 30; 288 in 48 of 6 33 and 51 us for 23 and 32).
 static int gated_ctas(int64_t batch, int64_t len, int64_t dim, int64_t cta_tokens) {
-    const int64_t units = batch * ((dim + kGatedSlab - 1) / kGatedSlab);
-    int n = 1;
-    while (n < 8 && units * n * 2 <= 2 * 152 && n * cta_tokens < len)
-        n *= 2;
-    return n;
+    constexpr int kPlaces[] = {0, 304, 304, 276, 276, 264, 264, 252, 264};
+    const int64_t units = batch * ((dim + kGatedSlab - 1) / kGatedSlab), tiles = (len + cta_tokens - 1) / cta_tokens;
+    int64_t n = 8;
+    while (n > 1 && (units * n > kPlaces[n] || n > tiles))
+        --n;
+    const int64_t rounds = (tiles + n - 1) / n;
+    return rounds > 0 ? (int)((tiles + rounds - 1) / rounds) : 1;
 }
 
 int64_t gated_scratch_slots(int64_t batch, int64_t len, int64_t dim) {
@@ -86,8 +90,10 @@ cudaError_t gated_launch(const mt_gated_args &p, const Launch &L) {
         return cudaErrorInvalidValue;
     MT_BY_TYPE(gated_forward, g, vec, L)
 }
-cudaError_t gated_step_launch(const mt_gated_args &p, const Launch &L) {
-    const GatedArgs g = gated_args(p, kGatedWarps * kFwdT, false);
+cudaError_t gated_step_launch(const mt_gated_args &a, const Launch &L) {
+    mt_gated_args p = a;
+    p.len = 1;
+    const GatedArgs g = gated_args(p, kFwdT, false);
     const bool vec = all_fit(p, p.dtype == MT_F32 ? 8 : 4, true, false);
     if (p.batch * ((p.dim + 1) / 2) / 128 >= INT32_MAX)
         return cudaErrorInvalidValue;

@@ -309,19 +309,21 @@ constexpr int kFwdT = 8;
 
 template <class S, bool VEC> using FwdTile = Tile<S, kFwdT, VEC, sizeof(S) == 4>;
 
-template <class S, bool VEC, int W> struct FwdShared {
-    static constexpr int kTensors = 4;
+// With room for all four tensors, used or not: with less a cluster's f32 CTAs go three an SM, and unevenly (2 x 2048 x 4096, no
+// output gate, 72 us for 57).
+template <class S, bool VEC> struct FwdShared {
     static constexpr int kTile = FwdTile<S, VEC>::kBytes;
-    static constexpr int kWarp = kGatedStages * kTensors * kTile;
-    static constexpr int kBytes = W * kWarp;
+    static constexpr int kIn = 2 * kTile, kZ = 3 * kTile;  // behind x and r
+    static constexpr int kStage = 4 * kTile;
+    static constexpr int kWarp = kGatedStages * kStage;
 };
 
 // IN and Z: the call has an input gate, an output gate; CLUSTER: CTAs share the tokens (or, where not VEC, may).
-// W: warps of the CTA.
+// W: warps of the CTA; fewer where these have all tokens.
 template <class S, bool RATE, bool VEC, bool IN, bool Z, bool CLUSTER, int W>
 __global__ void __launch_bounds__(32 * W, 16 / W) k_gated(const __grid_constant__ GatedArgs g) {
     using In = FwdTile<S, VEC>;
-    using Shared = FwdShared<S, VEC, W>;
+    using Shared = FwdShared<S, VEC>;
     constexpr int kCtaTokens = W * kFwdT;
     extern __shared__ __align__(16) char staged[];
     __shared__ Element of_warps[2][W][32];
@@ -338,7 +340,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) k_gated(const __grid_constant_
     }
     pdl_prologue();
     const mt_gated_args &p = g.p;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int warps = blockDim.x / 32, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int rank = ctas > 1 ? (int)cluster_rank() : 0;
     const int64_t unit = blockIdx.x / ctas, b = unit / g.slabs, c0 = (unit - b * g.slabs) * kGatedSlab;
     const int live = (int)(p.dim - c0 < kGatedSlab ? p.dim - c0 : kGatedSlab), mine = live - 2 * lane;
@@ -361,16 +363,18 @@ __global__ void __launch_bounds__(32 * W, 16 / W) k_gated(const __grid_constant_
     auto ask = [&](int t0, int stage) {
         const int n = len - t0;
         if (n > 0) {
-            const uint32_t to = own_at + (uint32_t)(stage * (Shared::kTensors * Shared::kTile));
+            const uint32_t to = own_at + (uint32_t)(stage * Shared::kStage);
             In::copy(to, x, t0, n, live, lane);
             In::copy(to + Shared::kTile, r, t0, n, live, lane);
             if (has_in)
-                In::copy(to + 2 * Shared::kTile, in, t0, n, live, lane);
+                In::copy(to + Shared::kIn, in, t0, n, live, lane);
             if (has_z)
-                In::copy(to + 3 * Shared::kTile, z, t0, n, live, lane);
+                In::copy(to + Shared::kZ, z, t0, n, live, lane);
         }
         cp_async_commit();
     };
+    for (int w = warps; w < W; ++w)  // of warps that are not there; all that are write the same
+        of_warps[0][w][lane] = {both(1.0f), 0ull};
     ask(first, 0);
     ask(first + step, 1);
     if (ctas > 1)
@@ -380,15 +384,17 @@ __global__ void __launch_bounds__(32 * W, 16 / W) k_gated(const __grid_constant_
     uint32_t parity = 0;  // of the barriers' phases, each of which serves every other tile
     for (int base = 0; base < len; base += step, side ^= 1) {
         const int t0 = base + first, n = len - t0;
-        char *at = own + side * (Shared::kTensors * Shared::kTile);
+        char *at = own + side * Shared::kStage;
         cp_async_wait<kGatedStages - 1>();
         __syncwarp();
         if (n < kFwdT) {  // tokens behind the end: a shut gate, which leaves the state
             const int has = n < 0 ? 0 : n;
             In::fill(at, has, S(0.0f), lane);
             In::fill(at + Shared::kTile, has, S(Lim<float>::lo()), lane);
-            In::fill(at + 2 * Shared::kTile, has, S(0.0f), lane);
-            In::fill(at + 3 * Shared::kTile, has, S(0.0f), lane);
+            if (has_in)
+                In::fill(at + Shared::kIn, has, S(0.0f), lane);
+            if (has_z)
+                In::fill(at + Shared::kZ, has, S(0.0f), lane);
             __syncwarp();
         }
         for (Rows<S, VEC> *rows : {&x, &r, &in, &z})
@@ -402,15 +408,15 @@ __global__ void __launch_bounds__(32 * W, 16 / W) k_gated(const __grid_constant_
             if constexpr (RATE) {
                 f32x2 q;
                 decay_2f(mul2f(rate, sigmoid_2f(rr)), a[k], q);
-                w = has_in ? root_sigmoid_2f(q, In::read(at + 2 * Shared::kTile, in, k, lane)) : mul2f(q, rsqrt_least_2f(q));
+                w = has_in ? root_sigmoid_2f(q, In::read(at + Shared::kIn, in, k, lane)) : mul2f(q, rsqrt_least_2f(q));
             } else {
                 sigmoid_both_2f(rr, w, a[k]);
                 if (has_in)
-                    w = mul2f(w, sigmoid_2f(In::read(at + 2 * Shared::kTile, in, k, lane)));
+                    w = mul2f(w, sigmoid_2f(In::read(at + Shared::kIn, in, k, lane)));
             }
             v[k] = mul2f(w, In::read(at, x, k, lane));
             if (has_z) {
-                const f32x2 zz = In::read(at + 3 * Shared::kTile, z, k, lane);
+                const f32x2 zz = In::read(at + Shared::kZ, z, k, lane);
                 gate[k] = mul2f(zz, sigmoid_2f(zz));
             }
             e.h = fma2f(a[k], e.h, v[k]);
@@ -483,7 +489,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) k_gated(const __grid_constant_
         cluster_arrive();
         cluster_wait();
     }
-    for (int t = len + rank * W + warp; t < total; t += ctas * W)
+    for (int t = len + rank * warps + warp; t < total; t += ctas * warps)
         put_pair<S, VEC>(out.row(t), mine, 0ull, g.pairs);
     if (active && p.state != nullptr && rank == 0 && warp == 0)
         put_state(p.state + slot * p.dim + c, mine, carry);
@@ -497,12 +503,12 @@ __global__ void __launch_bounds__(32 * W, 16 / W) k_gated(const __grid_constant_
 // often, against these, us, all gates, 4096 channels, bf16: 4 x 2048 tokens 140 and 121, 8 x 2048 253 and 237; no output gate 4 x 4096 254 and 198.
 constexpr int kBwdT = 8;
 constexpr int kBwdWarps = 4;
-constexpr int kBwdTensors = 5;
 
 template <class S, bool VEC> struct BwdShared {
     static constexpr int kTile = Tile<S, kBwdT, VEC>::kBytes;
-    static constexpr int kWarp = kGatedStages * kBwdTensors * kTile;
-    static constexpr int kBytes = kBwdWarps * kWarp;
+    static constexpr int kIn = 3 * kTile, kZ = 4 * kTile;  // behind x, r and dout
+    static constexpr int kStage = 5 * kTile;
+    static constexpr int kWarp = kGatedStages * kStage;
 };
 
 template <class S, bool RATE, bool VEC, bool IN, bool Z, bool CLUSTER>
@@ -529,7 +535,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) k_gated_grad(const __grid_c
     }
     pdl_prologue();
     const mt_gated_args &p = g.p;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int warps = blockDim.x / 32, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int rank = ctas > 1 ? (int)cluster_rank() : 0;
     const int64_t unit = blockIdx.x / ctas, b = unit / g.slabs, c0 = (unit - b * g.slabs) * kGatedSlab;
     const int live = (int)(p.dim - c0 < kGatedSlab ? p.dim - c0 : kGatedSlab), mine = live - 2 * lane;
@@ -556,18 +562,20 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) k_gated_grad(const __grid_c
     auto ask = [&](int base, int stage) {
         const int t0 = base + first, n = len - t0;
         if (base >= 0 && n > 0) {
-            const uint32_t to = own_at + (uint32_t)(stage * (kBwdTensors * Shared::kTile));
+            const uint32_t to = own_at + (uint32_t)(stage * Shared::kStage);
             In::copy(to, x, t0, n, live, lane);
             In::copy(to + Shared::kTile, r, t0, n, live, lane);
             if (has_in)
-                In::copy(to + 2 * Shared::kTile, in, t0, n, live, lane);
+                In::copy(to + Shared::kIn, in, t0, n, live, lane);
             if (has_z)
-                In::copy(to + 3 * Shared::kTile, z, t0, n, live, lane);
-            In::copy(to + 4 * Shared::kTile, dout, t0, n, live, lane);
+                In::copy(to + Shared::kZ, z, t0, n, live, lane);
+            In::copy(to + 2 * Shared::kTile, dout, t0, n, live, lane);
         }
         cp_async_commit();
     };
     const int last = len > 0 ? (len - 1) / step * step : -1;  // where the last CTAs' tokens begin
+    for (int w = warps; w < W; ++w)  // of warps that are not there; all that are write the same
+        of_warps[0][w][lane] = back_of_warps[0][w][lane] = {both(1.0f), 0ull};
     ask(last, 0);
     ask(last - step, 1);
     if (ctas > 1)
@@ -577,7 +585,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) k_gated_grad(const __grid_c
     uint32_t parity = 0;  // of the barriers' phases, each of which serves every other tile
     for (int base = last; base >= 0; base -= step, side ^= 1) {
         const int t0 = base + first, n = len - t0;
-        char *at = own + side * (kBwdTensors * Shared::kTile);
+        char *at = own + side * Shared::kStage;
         f32x2 h = 0ull;  // before the first token of the checkpoint's warps
         if (t0 / kGatedTile * kGatedTile < len)
             h = get_state(p.checkpoints + (b * g.ntiles + t0 / kGatedTile) * p.dim + c, mine);
@@ -588,8 +596,10 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) k_gated_grad(const __grid_c
             In::fill(at, has, S(0.0f), lane);
             In::fill(at + Shared::kTile, has, S(Lim<float>::lo()), lane);
             In::fill(at + 2 * Shared::kTile, has, S(0.0f), lane);
-            In::fill(at + 3 * Shared::kTile, has, S(0.0f), lane);
-            In::fill(at + 4 * Shared::kTile, has, S(0.0f), lane);
+            if (has_in)
+                In::fill(at + Shared::kIn, has, S(0.0f), lane);
+            if (has_z)
+                In::fill(at + Shared::kZ, has, S(0.0f), lane);
             __syncwarp();
         }
         for (Rows<S, VEC> *rows : {&x, &r, &in, &z, &dout})
@@ -611,13 +621,13 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) k_gated_grad(const __grid_c
                 a[k] = cs;
                 w = s;
             }
-            const f32x2 xx = In::read(at, x, k, lane), dy = In::read(at + 4 * Shared::kTile, dout, k, lane);
+            const f32x2 xx = In::read(at, x, k, lane), dy = In::read(at + 2 * Shared::kTile, dout, k, lane);
             f32x2 vv = xx;
             to_x[k] = w;
             to_i[k] = 0ull;
             if (has_in) {
                 f32x2 si, ci;
-                sigmoid_both_2f(In::read(at + 2 * Shared::kTile, in, k, lane), si, ci);
+                sigmoid_both_2f(In::read(at + Shared::kIn, in, k, lane), si, ci);
                 vv = mul2f(xx, si);
                 to_x[k] = mul2f(w, si);
                 to_i[k] = mul2f(xx, ci);
@@ -626,7 +636,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) k_gated_grad(const __grid_c
             to_z[k] = 0ull;
             if (has_z) {
                 f32x2 sz, cz;
-                const f32x2 zz = In::read(at + 3 * Shared::kTile, z, k, lane);
+                const f32x2 zz = In::read(at + Shared::kZ, z, k, lane);
                 sigmoid_both_2f(zz, sz, cz);
                 dh[k] = mul2f(dy, mul2f(zz, sz));
                 to_z[k] = mul2f(dy, mul2f(sz, fma2f(zz, cz, both(1.0f))));
@@ -735,7 +745,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) k_gated_grad(const __grid_c
         cluster_arrive();
         cluster_wait();
     }
-    for (int t = len + rank * W + warp; t < total; t += ctas * W) {
+    for (int t = len + rank * warps + warp; t < total; t += ctas * warps) {
         put_pair<S, VEC>(dx.row(t), mine, 0ull, g.pairs);
         put_pair<S, VEC>(dr.row(t), mine, 0ull, g.pairs);
         if (has_in)
@@ -820,24 +830,32 @@ static cudaError_t launch_cluster(void (*kernel)(KArgs...), int64_t grid, unsign
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
+// Warps of a CTA of W: no more than have tokens, so that more short sequences are on an SM. 64 x 16 tokens x 4096 channels, bf16, all
+// gates, us: prompt 11, gradient 25; with all warps 27 and 62.
+static int gated_warps(const GatedArgs &g, int most, int tokens) {
+    const int64_t n = (g.p.len + tokens - 1) / tokens;
+    return g.ctas > 1 || n > most ? most : n < 1 ? 1 : (int)n;
+}
 template <class S, bool RATE, bool VEC, bool IN, bool Z, bool CLUSTER, int W> static cudaError_t gated_forward_of(const GatedArgs &g, const Launch &L) {
     static PerDevice ready;
-    constexpr int smem = FwdShared<S, VEC, W>::kBytes;
-    const cudaError_t e = allow_shared(k_gated<S, RATE, VEC, IN, Z, CLUSTER, W>, smem, ready);
+    constexpr int smem = FwdShared<S, VEC>::kWarp;
+    const cudaError_t e = allow_shared(k_gated<S, RATE, VEC, IN, Z, CLUSTER, W>, W * smem, ready);
     if (e != cudaSuccess)
         return e;
+    const int warps = gated_warps(g, W, kFwdT);
     note_launch();
-    return launch_cluster(k_gated<S, RATE, VEC, IN, Z, CLUSTER, W>, g.p.batch * g.slabs * g.ctas, 32 * W, smem, g.ctas, L.stream, g);
+    return launch_cluster(k_gated<S, RATE, VEC, IN, Z, CLUSTER, W>, g.p.batch * g.slabs * g.ctas, 32 * warps, warps * smem, g.ctas, L.stream, g);
 }
 template <class S, bool RATE, bool VEC, bool IN, bool Z, bool CLUSTER>
 static cudaError_t gated_backward_of(const GatedArgs &g, float *part, const Launch &L) {
     static PerDevice ready;
-    constexpr int smem = BwdShared<S, VEC>::kBytes;
-    const cudaError_t e = allow_shared(k_gated_grad<S, RATE, VEC, IN, Z, CLUSTER>, smem, ready);
+    constexpr int smem = BwdShared<S, VEC>::kWarp;
+    const cudaError_t e = allow_shared(k_gated_grad<S, RATE, VEC, IN, Z, CLUSTER>, kBwdWarps * smem, ready);
     if (e != cudaSuccess)
         return e;
+    const int warps = gated_warps(g, kBwdWarps, kBwdT);
     note_launch();
-    return launch_cluster(k_gated_grad<S, RATE, VEC, IN, Z, CLUSTER>, g.p.batch * g.slabs * g.ctas, 32 * kBwdWarps, smem, g.ctas, L.stream, g, part);
+    return launch_cluster(k_gated_grad<S, RATE, VEC, IN, Z, CLUSTER>, g.p.batch * g.slabs * g.ctas, 32 * warps, warps * smem, g.ctas, L.stream, g, part);
 }
 // The kernel of a call's gates: f(std::bool_constant of the input gate, of the output gate).
 template <class F> static cudaError_t by_gates(const mt_gated_args &p, F f) {

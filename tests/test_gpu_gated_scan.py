@@ -123,6 +123,25 @@ def test_ragged_and_strided(mt, dtype, rate, pad):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("length", [9, 16, 17, 25, 33, 96, 160, 200, 380, 448])
+@pytest.mark.parametrize("d", [64, 65])
+def test_warps_and_ctas_by_length(mt, dtype, length, d):
+    """Lengths from two warps of one CTA to clusters of each size, one sequence ending early."""
+    p = Inputs(dtype, 2, length, d, True, True, length % 2 == 0, lens=torch.tensor([length, length * 2 // 3], dtype=torch.int32))
+    check_forward(mt, p)
+    check_gradient(mt, p)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("length", [3, 16, 40])
+def test_many_short_sequences(mt, dtype, length):
+    lens = torch.tensor([(k * 7) % (length + 1) for k in range(70)], dtype=torch.int32)
+    p = Inputs(dtype, 70, length, 576, length != 16, True, True, lens=lens)
+    check_forward(mt, p)
+    check_gradient(mt, p)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("length", [2048, 4099])
 def test_long_memory(mt, dtype, length):
     """Decays of 0.999 and above: the states sum thousands of tokens."""
