@@ -61,17 +61,11 @@ static bool all_fit(const mt_gated_args &p, int64_t bytes, bool step, bool grad)
            (p.z == nullptr || fits(p.dz, p.dz_batch, p.dz_token, bytes, v));
 }
 
-static GatedArgs gated_args(const mt_gated_args &p, int64_t cta_tokens, bool grad) {
+static GatedArgs gated_args(const mt_gated_args &p, int64_t cta_tokens) {
     GatedArgs g;
     g.p = p;
     g.slabs = (int)((p.dim + kGatedSlab - 1) / kGatedSlab);
     g.ctas = gated_ctas(p.batch, p.len, p.dim, cta_tokens);
-    auto even = [&](const void *q, int64_t batch, int64_t token) {
-        return q == nullptr || ((uintptr_t)q % (p.dtype == MT_F32 ? 8 : 4) == 0 && batch % 2 == 0 && token % 2 == 0);
-    };
-    g.pairs = grad ? even(p.dx, p.dx_batch, p.dx_token) && even(p.dr, p.dr_batch, p.dr_token) && (p.i == nullptr || even(p.di, p.di_batch, p.di_token)) &&
-                         (p.z == nullptr || even(p.dz, p.dz_batch, p.dz_token))
-                   : even(p.out, p.out_batch, p.out_token);
     g.ntiles = (p.len + kGatedTile - 1) / kGatedTile;
     return g;
 }
@@ -84,7 +78,7 @@ static GatedArgs gated_args(const mt_gated_args &p, int64_t cta_tokens, bool gra
     default: return cudaErrorInvalidValue;              \
     }
 cudaError_t gated_launch(const mt_gated_args &p, const Launch &L) {
-    const GatedArgs g = gated_args(p, gated_cluster_warps(p.dtype == MT_F32 ? 4 : 2) * kFwdT, false);
+    const GatedArgs g = gated_args(p, gated_cluster_warps(p.dtype == MT_F32 ? 4 : 2) * kFwdT);
     const bool vec = all_fit(p, 16, false, false);
     if (p.batch * g.slabs * g.ctas > INT32_MAX)
         return cudaErrorInvalidValue;
@@ -93,7 +87,7 @@ cudaError_t gated_launch(const mt_gated_args &p, const Launch &L) {
 cudaError_t gated_step_launch(const mt_gated_args &a, const Launch &L) {
     mt_gated_args p = a;
     p.len = 1;
-    const GatedArgs g = gated_args(p, kFwdT, false);
+    const GatedArgs g = gated_args(p, kFwdT);
     const bool vec = all_fit(p, p.dtype == MT_F32 ? 8 : 4, true, false);
     if (p.batch * ((p.dim + 1) / 2) / 128 >= INT32_MAX)
         return cudaErrorInvalidValue;
@@ -105,7 +99,7 @@ static cudaError_t backward(const GatedArgs &g, float *part, const Launch &L) {
     MT_BY_TYPE(gated_backward, g, part, vec, L)
 }
 cudaError_t gated_grad_launch(const mt_gated_args &p, const Launch &L) {
-    const GatedArgs g = gated_args(p, kBwdWarps * kBwdT, true);
+    const GatedArgs g = gated_args(p, kBwdWarps * kBwdT);
     float *part = p.drate != nullptr ? static_cast<float *>(p.scratch) : nullptr;
     if (p.batch * g.slabs * g.ctas > INT32_MAX)
         return cudaErrorInvalidValue;

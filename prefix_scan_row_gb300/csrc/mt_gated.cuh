@@ -50,7 +50,6 @@ struct GatedArgs {
     mt_gated_args p;
     int slabs;       // of 64 channels
     int ctas;        // of a cluster
-    bool pairs;      // of every output, two neighbouring channels are aligned as one
     int64_t ntiles;  // checkpoints of a sequence
 };
 
@@ -205,9 +204,12 @@ template <class S, bool VEC> struct Rows {
     }
 };
 
+// A lane's two channels: neighbours where rows are vectors, and otherwise half a slab apart, so that a warp's single values are together.
+template <bool VEC> constexpr int kFar = VEC ? 1 : kGatedSlab / 2;
+
 // T tokens of a tensor in a warp's part of shared memory, 64 channels each. VEC: the rows are 16-byte aligned and
 // whole vectors. Otherwise rows are copied as the aligned vectors that they touch (each holds a channel of the row) and read from
-// where they begin in the first, 16-bit ones across words where that is in the middle of one; or, WORDS, f32 value by value.
+// where they begin in the first; or, WORDS, f32 value by value.
 // 4 x 2048 tokens x 4095 channels, all gates, us: bf16 prompt 129 and gradient 286 (as 32-bit words 154 and 332; of 4096
 // channels 73 and 121); f32 prompt by words 189, by vectors 208, gradient 398 and 320.
 template <class S, int T, bool VEC, bool WORDS = false> struct Tile {
@@ -253,14 +255,8 @@ template <class S, int T, bool VEC, bool WORDS = false> struct Tile {
         using P = typename Pair<S>::T;
         if constexpr (VEC)
             return Pair<S>::widen(*reinterpret_cast<const P *>(at + row * kPitch + lane * (int)sizeof(P)));
-        const int shift = WORDS ? 0 : (r.low + row * r.token_low) & 15;
-        if constexpr (sizeof(S) == 4) {
-            const float *f = reinterpret_cast<const float *>(at + row * kPitch + shift) + 2 * lane;
-            return pack2f(f[0], f[1]);
-        } else {
-            const uint32_t *w = reinterpret_cast<const uint32_t *>(at + row * kPitch + (shift & ~3)) + lane;
-            return Pair<S>::widen(__funnelshift_r(w[0], w[1], (shift & 2) * 8));
-        }
+        const S *from = reinterpret_cast<const S *>(at + row * kPitch + (WORDS ? 0 : (r.low + row * r.token_low) & 15)) + lane;
+        return pack2f(Codec<S>::load1(from), Codec<S>::load1(from + kFar<VEC>));
     }
     // Rows from n on hold `v` in every channel.
     static __device__ __forceinline__ void fill(char *at, int n, S v, int lane) {
@@ -270,32 +266,31 @@ template <class S, int T, bool VEC, bool WORDS = false> struct Tile {
     }
 };
 
-// A lane's pair, of which the first `live` channels exist (VEC: none or both). `pairs`: where not VEC, pairs are aligned all
-// the same and leave as one: 4 x 2048 tokens x 4098 channels, bf16, gradient, us: 309, one by one 333.
-template <class S, bool VEC> __device__ __forceinline__ void put_pair(S *to, int live, f32x2 v, bool pairs) {
+// A lane's pair: channels FAR apart, of which those at 0 to `live` - 1 exist (VEC: none or both).
+template <class S, bool VEC, int FAR> __device__ __forceinline__ void put_pair(S *to, int live, f32x2 v) {
     float a, b;
     unpack2f(v, a, b);
-    if (VEC || (pairs && live > 1)) {
+    if constexpr (VEC) {
         if (live > 0)
             *reinterpret_cast<typename Pair<S>::T *>(to) = Pair<S>::narrow(a, b);
     } else {
         if (live > 0)
             Codec<S>::store1(to, a);
-        if (live > 1)
-            Codec<S>::store1(to + 1, b);
+        if (live > FAR)
+            Codec<S>::store1(to + FAR, b);
     }
 }
 // f32 rows of states and parameters, from the lane's first channel on
-__device__ __forceinline__ f32x2 get_state(const float *p, int live) {
-    return pack2f(live > 0 ? p[0] : 0.0f, live > 1 ? p[1] : 0.0f);
+template <int FAR> __device__ __forceinline__ f32x2 get_state(const float *p, int live) {
+    return pack2f(live > 0 ? p[0] : 0.0f, live > FAR ? p[FAR] : 0.0f);
 }
-__device__ __forceinline__ void put_state(float *p, int live, f32x2 v) {
+template <int FAR> __device__ __forceinline__ void put_state(float *p, int live, f32x2 v) {
     float a, b;
     unpack2f(v, a, b);
     if (live > 0)
         p[0] = a;
-    if (live > 1)
-        p[1] = b;
+    if (live > FAR)
+        p[FAR] = b;
 }
 
 struct alignas(16) Element {  // of the scan
@@ -325,6 +320,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) k_gated(const __grid_constant_
     using In = FwdTile<S, VEC>;
     using Shared = FwdShared<S, VEC>;
     constexpr int kCtaTokens = W * kFwdT;
+    constexpr int FAR = kFar<VEC>;
     extern __shared__ __align__(16) char staged[];
     __shared__ Element of_warps[2][W][32];
     __shared__ Element of_ctas[2][8][32];
@@ -343,19 +339,19 @@ __global__ void __launch_bounds__(32 * W, 16 / W) k_gated(const __grid_constant_
     const int warps = blockDim.x / 32, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int rank = ctas > 1 ? (int)cluster_rank() : 0;
     const int64_t unit = blockIdx.x / ctas, b = unit / g.slabs, c0 = (unit - b * g.slabs) * kGatedSlab;
-    const int live = (int)(p.dim - c0 < kGatedSlab ? p.dim - c0 : kGatedSlab), mine = live - 2 * lane;
+    const int live = (int)(p.dim - c0 < kGatedSlab ? p.dim - c0 : kGatedSlab), at0 = VEC ? 2 * lane : lane, mine = live - at0;
     const int64_t slot = gated_slot(p, b);
     const bool active = slot >= 0 || p.state == nullptr;
     const int len = active ? (int)gated_len(p, b) : 0, total = (int)p.len;
     Rows<S, VEC> x = In::lane_rows({p.x, p.x_batch, p.x_token, b, c0}, lane), r = In::lane_rows({p.r, p.r_batch, p.r_token, b, c0}, lane),
                        in = In::lane_rows({p.i, p.i_batch, p.i_token, b, c0}, lane), z = In::lane_rows({p.z, p.z_batch, p.z_token, b, c0}, lane);
-    const Rows<S, VEC> out(p.out, p.out_batch, p.out_token, b, c0 + 2 * lane);
+    const Rows<S, VEC> out(p.out, p.out_batch, p.out_token, b, c0 + at0);
     constexpr bool has_in = IN, has_z = Z;
-    const int64_t c = c0 + 2 * lane;
-    const f32x2 rate = RATE ? get_state(p.rate + c, mine) : 0ull;
+    const int64_t c = c0 + at0;
+    const f32x2 rate = RATE ? get_state<FAR>(p.rate + c, mine) : 0ull;
     f32x2 carry = 0ull;
     if (active && p.state != nullptr && p.carry_in)
-        carry = get_state(p.state + slot * p.dim + c, mine);
+        carry = get_state<FAR>(p.state + slot * p.dim + c, mine);
     char *own = staged + warp * Shared::kWarp;
     const uint32_t own_at = (uint32_t)__cvta_generic_to_shared(own);
     const int step = ctas * kCtaTokens, first = rank * kCtaTokens + warp * kFwdT;
@@ -467,7 +463,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) k_gated(const __grid_constant_
             h = fma2f(before.a, h, before.h);
         }
         if (p.checkpoints != nullptr && warp * kFwdT % kGatedTile == 0 && n > 0)
-            put_state(p.checkpoints + (b * g.ntiles + t0 / kGatedTile) * p.dim + c, mine, h);
+            put_state<FAR>(p.checkpoints + (b * g.ntiles + t0 / kGatedTile) * p.dim + c, mine, h);
         auto finish = [&](bool whole) {
 #pragma unroll
             for (int k = 0; k < kFwdT; ++k) {
@@ -476,7 +472,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) k_gated(const __grid_constant_
                 if (has_z)
                     y = mul2f(h, gate[k]);
                 if (whole || k < n)
-                    put_pair<S, VEC>(out.row(t0 + k), mine, y, g.pairs);
+                    put_pair<S, VEC, FAR>(out.row(t0 + k), mine, y);
             }
         };
         if (n >= kFwdT)
@@ -490,9 +486,9 @@ __global__ void __launch_bounds__(32 * W, 16 / W) k_gated(const __grid_constant_
         cluster_wait();
     }
     for (int t = len + rank * warps + warp; t < total; t += ctas * warps)
-        put_pair<S, VEC>(out.row(t), mine, 0ull, g.pairs);
+        put_pair<S, VEC, FAR>(out.row(t), mine, 0ull);
     if (active && p.state != nullptr && rank == 0 && warp == 0)
-        put_state(p.state + slot * p.dim + c, mine, carry);
+        put_state<FAR>(p.state + slot * p.dim + c, mine, carry);
 }
 
 // ---- gradients ----------------------------------------------------------------------------------------
@@ -519,6 +515,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) k_gated_grad(const __grid_c
     constexpr int kCtaTokens = W * kBwdT;
     constexpr int kMarkWarps = kGatedTile / kBwdT;  // that share a checkpoint
     static_assert(kCtaTokens % kGatedTile == 0 && kGatedTile % kBwdT == 0, "a CTA's tokens begin at a checkpoint");
+    constexpr int FAR = kFar<VEC>;
     extern __shared__ __align__(16) char staged[];
     __shared__ Element of_warps[2][W][32];
     __shared__ Element back_of_warps[2][W][32];  // the adjoint's
@@ -538,17 +535,17 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) k_gated_grad(const __grid_c
     const int warps = blockDim.x / 32, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int rank = ctas > 1 ? (int)cluster_rank() : 0;
     const int64_t unit = blockIdx.x / ctas, b = unit / g.slabs, c0 = (unit - b * g.slabs) * kGatedSlab;
-    const int live = (int)(p.dim - c0 < kGatedSlab ? p.dim - c0 : kGatedSlab), mine = live - 2 * lane;
+    const int live = (int)(p.dim - c0 < kGatedSlab ? p.dim - c0 : kGatedSlab), at0 = VEC ? 2 * lane : lane, mine = live - at0;
     const int len = (int)gated_len(p, b), total = (int)p.len;
     Rows<S, VEC> x = In::lane_rows({p.x, p.x_batch, p.x_token, b, c0}, lane), r = In::lane_rows({p.r, p.r_batch, p.r_token, b, c0}, lane),
                        in = In::lane_rows({p.i, p.i_batch, p.i_token, b, c0}, lane), z = In::lane_rows({p.z, p.z_batch, p.z_token, b, c0}, lane),
                        dout = In::lane_rows({p.dout, p.dout_batch, p.dout_token, b, c0}, lane);
-    const int64_t c = c0 + 2 * lane;
+    const int64_t c = c0 + at0;
     const Rows<S, VEC> dx(p.dx, p.dx_batch, p.dx_token, b, c), dr(p.dr, p.dr_batch, p.dr_token, b, c), di(p.di, p.di_batch, p.di_token, b, c),
         dz(p.dz, p.dz_batch, p.dz_token, b, c);
     constexpr bool has_in = IN, has_z = Z;
-    const f32x2 rate = RATE ? get_state(p.rate + c, mine) : 0ull;
-    f32x2 carry = p.dfinal != nullptr ? get_state(p.dfinal + b * p.dim + c, mine) : 0ull;
+    const f32x2 rate = RATE ? get_state<FAR>(p.rate + c, mine) : 0ull;
+    f32x2 carry = p.dfinal != nullptr ? get_state<FAR>(p.dfinal + b * p.dim + c, mine) : 0ull;
     f32x2 rate_sum = 0ull, least = 0ull;
     if (RATE) {  // without any decay 1 / w counts as 0: 1 / sqrt(inf)
         float r0, r1;
@@ -588,7 +585,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) k_gated_grad(const __grid_c
         char *at = own + side * Shared::kStage;
         f32x2 h = 0ull;  // before the first token of the checkpoint's warps
         if (t0 / kGatedTile * kGatedTile < len)
-            h = get_state(p.checkpoints + (b * g.ntiles + t0 / kGatedTile) * p.dim + c, mine);
+            h = get_state<FAR>(p.checkpoints + (b * g.ntiles + t0 / kGatedTile) * p.dim + c, mine);
         cp_async_wait<kGatedStages - 1>();
         __syncwarp();
         if (n < kBwdT) {  // tokens behind the end: a shut gate, which passes states and gradients by them
@@ -726,12 +723,12 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) k_gated_grad(const __grid_c
                 if (whole || k < n) {
                     if (RATE)
                         rate_sum = add2f(rate_sum, to);
-                    put_pair<S, VEC>(dx.row(t0 + k), mine, gx, g.pairs);
-                    put_pair<S, VEC>(dr.row(t0 + k), mine, mul2f(to, to_r[k]), g.pairs);
+                    put_pair<S, VEC, FAR>(dx.row(t0 + k), mine, gx);
+                    put_pair<S, VEC, FAR>(dr.row(t0 + k), mine, mul2f(to, to_r[k]));
                     if (has_in)
-                        put_pair<S, VEC>(di.row(t0 + k), mine, mul2f(gx, to_i[k]), g.pairs);
+                        put_pair<S, VEC, FAR>(di.row(t0 + k), mine, mul2f(gx, to_i[k]));
                     if (has_z)
-                        put_pair<S, VEC>(dz.row(t0 + k), mine, to_z[k], g.pairs);
+                        put_pair<S, VEC, FAR>(dz.row(t0 + k), mine, to_z[k]);
                 }
             }
         };
@@ -746,15 +743,15 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) k_gated_grad(const __grid_c
         cluster_wait();
     }
     for (int t = len + rank * warps + warp; t < total; t += ctas * warps) {
-        put_pair<S, VEC>(dx.row(t), mine, 0ull, g.pairs);
-        put_pair<S, VEC>(dr.row(t), mine, 0ull, g.pairs);
+        put_pair<S, VEC, FAR>(dx.row(t), mine, 0ull);
+        put_pair<S, VEC, FAR>(dr.row(t), mine, 0ull);
         if (has_in)
-            put_pair<S, VEC>(di.row(t), mine, 0ull, g.pairs);
+            put_pair<S, VEC, FAR>(di.row(t), mine, 0ull);
         if (has_z)
-            put_pair<S, VEC>(dz.row(t), mine, 0ull, g.pairs);
+            put_pair<S, VEC, FAR>(dz.row(t), mine, 0ull);
     }
     if (p.dinit != nullptr && rank == 0 && warp == 0)
-        put_state(p.dinit + b * p.dim + c, mine, carry);
+        put_state<FAR>(p.dinit + b * p.dim + c, mine, carry);
     if (RATE && rate_part != nullptr) {
         __syncthreads();  // the loop's last reads of back_of_warps
         back_of_warps[0][warp][lane].h = rate_sum;
@@ -764,7 +761,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) k_gated_grad(const __grid_c
 #pragma unroll
             for (int w = 0; w < W; ++w)
                 s = add2f(s, back_of_warps[0][w][lane].h);
-            put_state(rate_part + (b * ctas + rank) * p.dim + c, mine, s);
+            put_state<FAR>(rate_part + (b * ctas + rank) * p.dim + c, mine, s);
         }
     }
 }
@@ -782,7 +779,7 @@ template <class S, bool RATE, bool VEC> __global__ void __launch_bounds__(128) k
     const int64_t slot = gated_slot(p, b);
     S *out = static_cast<S *>(p.out) + b * p.out_batch + c;
     if (slot < 0) {
-        put_pair<S, VEC>(out, live, 0ull, false);
+        put_pair<S, VEC, 1>(out, live, 0ull);
         return;
     }
     auto get = [&](const void *q, int64_t batch) {
@@ -794,11 +791,11 @@ template <class S, bool RATE, bool VEC> __global__ void __launch_bounds__(128) k
     };
     float *state = p.state + slot * p.dim + c;
     const f32x2 r = get(p.r, p.r_batch), x = get(p.x, p.x_batch), i = p.i != nullptr ? get(p.i, p.i_batch) : 0ull,
-                z = p.z != nullptr ? get(p.z, p.z_batch) : 0ull, h = get_state(state, live);
+                z = p.z != nullptr ? get(p.z, p.z_batch) : 0ull, h = get_state<1>(state, live);
     f32x2 a, w;
     if constexpr (RATE) {
         f32x2 q;
-        decay_2f(mul2f(get_state(p.rate + c, live), sigmoid_2f(r)), a, q);
+        decay_2f(mul2f(get_state<1>(p.rate + c, live), sigmoid_2f(r)), a, q);
         w = p.i != nullptr ? root_sigmoid_2f(q, i) : mul2f(q, rsqrt_least_2f(q));
     } else {
         sigmoid_both_2f(r, w, a);
@@ -806,8 +803,8 @@ template <class S, bool RATE, bool VEC> __global__ void __launch_bounds__(128) k
             w = mul2f(w, sigmoid_2f(i));
     }
     const f32x2 now = fma2f(a, h, mul2f(w, x));
-    put_state(state, live, now);
-    put_pair<S, VEC>(out, live, p.z != nullptr ? mul2f(now, mul2f(z, sigmoid_2f(z))) : now, false);
+    put_state<1>(state, live, now);
+    put_pair<S, VEC, 1>(out, live, p.z != nullptr ? mul2f(now, mul2f(z, sigmoid_2f(z))) : now);
 }
 
 // ---- launches ---------------------------------------------------------------------------------------
