@@ -24,7 +24,7 @@
 // (88 %), gradient 222 (80 %); 4 x 2048 x 4096 bf16 74 (67 %) and 121 (73 %): 256 CTAs leave some SMs two and others one, and
 // the schedulers, the exponentials' unit and the multiply-adds' are each 25 to 57 % busy (86 instructions for a pair's token in
 // the prompt, 132 in the gradient); 16384 x 2048 bf16 98 (50 %) and 158 (56 %): the same, and clusters' waits; 8 x 2048 x 4096
-// f32 212 (93 %) and 414 (86 %).
+// f32 211 (94 %) and 405 (88 %).
 #pragma once
 
 #include <initializer_list>
@@ -204,14 +204,15 @@ template <class S, bool VEC> struct Rows {
     }
 };
 
-// A lane's two channels: neighbours where rows are vectors, and otherwise half a slab apart, so that a warp's single values are together.
+// A lane's two channels: neighbours where rows are vectors, and otherwise half a slab apart, so that a warp's single values are
+// together: 4 x 2048 tokens x 4095 channels, all gates, gradient, us: bf16 212 for 286 as neighbours, f32 271 for 321.
 template <bool VEC> constexpr int kFar = VEC ? 1 : kGatedSlab / 2;
 
 // T tokens of a tensor in a warp's part of shared memory, 64 channels each. VEC: the rows are 16-byte aligned and
 // whole vectors. Otherwise rows are copied as the aligned vectors that they touch (each holds a channel of the row) and read from
 // where they begin in the first; or, WORDS, f32 value by value.
-// 4 x 2048 tokens x 4095 channels, all gates, us: bf16 prompt 129 and gradient 286 (as 32-bit words 154 and 332; of 4096
-// channels 73 and 121); f32 prompt by words 189, by vectors 208, gradient 398 and 320.
+// 4 x 2048 tokens x 4095 channels, all gates, us: bf16 prompt 117 and gradient 212 (4096 channels 73 and 121); f32 prompt
+// by words 155, by vectors 170, gradient 390 and 271.
 template <class S, int T, bool VEC, bool WORDS = false> struct Tile {
     static constexpr int kPitch = kGatedSlab * (int)sizeof(S) + (VEC ? 0 : 16);
     static constexpr int kBytes = T * kPitch;
