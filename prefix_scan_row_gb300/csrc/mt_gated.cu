@@ -6,10 +6,10 @@ namespace mt {
 // CTAs that share a sequence's tokens: one where sequences and channels give every SM work, and otherwise as many as find
 // place at once, two an SM. A cluster's CTAs wait for one another at every tile, so it pays only then. bf16, all gates, prompt, us, in
 // clusters of 1, 2, 4 and 8 CTAs: 4 x 2048 tokens x 4096 channels (256 CTAs without clusters) 73, 89, 86, 101; 16384 tokens x
-// 2048 (32) 339, 224, 117, 98. Of the sizes with the same number of tiles the smallest.
+// 2048 (32) 339, 224, 117, 98 (with eight warps of 8 tokens a CTA). Of the sizes with the same number of tiles the smallest.
 // The scratch is sized on the host, so the plan counts GB300's 152 SMs, and by the cluster's size the CTAs that were found to run
-// at once: clusters lie within a group of SMs, so not all places can be taken (with 266 CTAs in 38 clusters of 7 a prompt of 2048 tokens takes as
-// long as with 252, its gradient 41 us for 30; 288 in 48 of 6 33 and 51 us for 23 and 32).
+// at once: clusters lie within a group of SMs, so not all places can be taken (a prompt of 2048 tokens
+// and its gradient in 264 CTAs, 44 clusters of 6, 23 and 32 us; in 288, 48 clusters, 33 and 51).
 static int gated_ctas(int64_t batch, int64_t len, int64_t dim, int64_t cta_tokens) {
     constexpr int kPlaces[] = {0, 304, 304, 276, 276, 264, 264, 252, 264};
     const int64_t units = batch * ((dim + kGatedSlab - 1) / kGatedSlab), tiles = (len + cta_tokens - 1) / cta_tokens;
@@ -78,7 +78,7 @@ static GatedArgs gated_args(const mt_gated_args &p, int64_t cta_tokens) {
     default: return cudaErrorInvalidValue;              \
     }
 cudaError_t gated_launch(const mt_gated_args &p, const Launch &L) {
-    const GatedArgs g = gated_args(p, gated_cluster_warps(p.dtype == MT_F32 ? 4 : 2) * kFwdT);
+    const GatedArgs g = gated_args(p, kGatedFewWarps * gated_cluster_tokens(p.dtype == MT_F32 ? 4 : 2));
     const bool vec = all_fit(p, 16, false, false);
     if (p.batch * g.slabs * g.ctas > INT32_MAX)
         return cudaErrorInvalidValue;

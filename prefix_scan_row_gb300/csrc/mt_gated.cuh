@@ -23,7 +23,7 @@
 // Measured, all gates, us (share of the measured copy rate, 6798 GB/s): 16 x 1024 tokens x 4096 channels bf16, prompt 112
 // (88 %), gradient 222 (80 %); 4 x 2048 x 4096 bf16 74 (67 %) and 121 (73 %): 256 CTAs leave some SMs two and others one, and
 // the schedulers, the exponentials' unit and the multiply-adds' are each 25 to 57 % busy (86 instructions for a pair's token in
-// the prompt, 132 in the gradient); 16384 x 2048 bf16 98 (50 %) and 158 (56 %): the same, and clusters' waits; 8 x 2048 x 4096
+// the prompt, 132 in the gradient); 16384 x 2048 bf16 91 (54 %) and 155 (57 %): the same, and clusters' waits; 8 x 2048 x 4096
 // f32 211 (94 %) and 405 (88 %).
 #pragma once
 
@@ -41,9 +41,10 @@ constexpr int kGatedWarps = 8;   // warps of a prompt's CTA
 // 4096 channels, bf16, by sequences x tokens (CTAs): 4 x 2048 (256) 73, 73; 6 x 2048 (384) 110, 125; 8 x 2048 (512)
 // 140, 127; 16 x 1024 (1024) 125, 111. f32: 8 x 2048 211, 246.
 constexpr int kGatedFewWarps = 4;
-// and of a cluster, of values of so many bytes: f32's tiles leave no place for two CTAs of eight warps in an SM, and a cluster's
-// CTAs have to be resident together. f32, us, with four and with eight: 16384 x 2048 135, 221; 4096 x 4096 68, 76; 4 x 333 x 1024 11, 17.
-constexpr int gated_cluster_warps(int bytes) { return bytes == 4 ? kGatedFewWarps : kGatedWarps; }
+// and of a cluster's CTAs, two of which have to be on an SM: of 16-bit values its warps have twice the tokens, f32's tiles leave no
+// place for that. All gates, us, by these and by eight warps of 8 tokens: bf16 16384 x 2048 91, 107 (one warp joining for all: 99); 2 x 2048 x
+// 4096 44, 49; f32 16384 x 2048 127, 221; 4096 x 4096 64, 76.
+constexpr int gated_cluster_tokens(int bytes) { return bytes == 4 ? 8 : 16; }
 constexpr int kGatedStages = 2;  // tiles of a warp on their way or in use
 
 struct GatedArgs {
@@ -211,7 +212,7 @@ template <bool VEC> constexpr int kFar = VEC ? 1 : kGatedSlab / 2;
 // T tokens of a tensor in a warp's part of shared memory, 64 channels each. VEC: the rows are 16-byte aligned and
 // whole vectors. Otherwise rows are copied as the aligned vectors that they touch (each holds a channel of the row) and read from
 // where they begin in the first; or, WORDS, f32 value by value.
-// 4 x 2048 tokens x 4095 channels, all gates, us: bf16 prompt 117 and gradient 212 (4096 channels 73 and 121); f32 prompt
+// 4 x 2048 tokens x 4095 channels, all gates, us: bf16 prompt 110 and gradient 205 (4096 channels 73 and 121); f32 prompt
 // by words 155, by vectors 170, gradient 390 and 271.
 template <class S, int T, bool VEC, bool WORDS = false> struct Tile {
     static constexpr int kPitch = kGatedSlab * (int)sizeof(S) + (VEC ? 0 : 16);
@@ -299,16 +300,16 @@ struct alignas(16) Element {  // of the scan
 };
 
 // ---- prompts ----------------------------------------------------------------------------------------
-// Tokens of a warp. 4 x 2048 x 4096, bf16, all gates, us, eight warps a CTA: 4 tokens 115 (three CTAs an SM), 8 74, 16 77 (one). Four warps
+// Tokens of a warp, but for clusters. 4 x 2048 x 4096, bf16, all gates, us, eight warps a CTA: 4 tokens 115 (three CTAs an SM), 8 74, 16 77 (one). Four warps
 // of 16 take 69 there, but 8 x 2048 134 (of 8: 127), and 4 x 4096 without output gate 147 (114).
 constexpr int kFwdT = 8;
 
-template <class S, bool VEC> using FwdTile = Tile<S, kFwdT, VEC, sizeof(S) == 4>;
+template <class S, bool VEC, int T> using FwdTile = Tile<S, T, VEC, sizeof(S) == 4>;
 
 // With room for all four tensors, used or not: with less a cluster's f32 CTAs go three an SM, and unevenly (2 x 2048 x 4096, no
 // output gate, 72 us for 57).
-template <class S, bool VEC> struct FwdShared {
-    static constexpr int kTile = FwdTile<S, VEC>::kBytes;
+template <class S, bool VEC, int T> struct FwdShared {
+    static constexpr int kTile = FwdTile<S, VEC, T>::kBytes;
     static constexpr int kIn = 2 * kTile, kZ = 3 * kTile;  // behind x and r
     static constexpr int kStage = 4 * kTile;
     static constexpr int kWarp = kGatedStages * kStage;
@@ -316,11 +317,11 @@ template <class S, bool VEC> struct FwdShared {
 
 // IN and Z: the call has an input gate, an output gate; CLUSTER: CTAs share the tokens (or, where not VEC, may).
 // W: warps of the CTA; fewer where these have all tokens.
-template <class S, bool RATE, bool VEC, bool IN, bool Z, bool CLUSTER, int W>
-__global__ void __launch_bounds__(32 * W, 16 / W) k_gated(const __grid_constant__ GatedArgs g) {
-    using In = FwdTile<S, VEC>;
-    using Shared = FwdShared<S, VEC>;
-    constexpr int kCtaTokens = W * kFwdT;
+template <class S, bool RATE, bool VEC, bool IN, bool Z, bool CLUSTER, int W, int T>
+__global__ void __launch_bounds__(32 * W, 128 / W / T) k_gated(const __grid_constant__ GatedArgs g) {
+    using In = FwdTile<S, VEC, T>;
+    using Shared = FwdShared<S, VEC, T>;
+    constexpr int kCtaTokens = W * T;
     constexpr int FAR = kFar<VEC>;
     extern __shared__ __align__(16) char staged[];
     __shared__ Element of_warps[2][W][32];
@@ -355,7 +356,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) k_gated(const __grid_constant_
         carry = get_state<FAR>(p.state + slot * p.dim + c, mine);
     char *own = staged + warp * Shared::kWarp;
     const uint32_t own_at = (uint32_t)__cvta_generic_to_shared(own);
-    const int step = ctas * kCtaTokens, first = rank * kCtaTokens + warp * kFwdT;
+    const int step = ctas * kCtaTokens, first = rank * kCtaTokens + warp * T;
 
     auto ask = [&](int t0, int stage) {
         const int n = len - t0;
@@ -384,7 +385,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) k_gated(const __grid_constant_
         char *at = own + side * Shared::kStage;
         cp_async_wait<kGatedStages - 1>();
         __syncwarp();
-        if (n < kFwdT) {  // tokens behind the end: a shut gate, which leaves the state
+        if (n < T) {  // tokens behind the end: a shut gate, which leaves the state
             const int has = n < 0 ? 0 : n;
             In::fill(at, has, S(0.0f), lane);
             In::fill(at + Shared::kTile, has, S(Lim<float>::lo()), lane);
@@ -396,10 +397,10 @@ __global__ void __launch_bounds__(32 * W, 16 / W) k_gated(const __grid_constant_
         }
         for (Rows<S, VEC> *rows : {&x, &r, &in, &z})
             rows->begin_tile(t0);
-        f32x2 a[kFwdT], v[kFwdT], gate[kFwdT];
+        f32x2 a[T], v[T], gate[T];
         Element e = {both(1.0f), 0ull};
 #pragma unroll
-        for (int k = 0; k < kFwdT; ++k) {
+        for (int k = 0; k < T; ++k) {
             const f32x2 rr = In::read(at + Shared::kTile, r, k, lane);
             f32x2 w;
             if constexpr (RATE) {
@@ -433,22 +434,20 @@ __global__ void __launch_bounds__(32 * W, 16 / W) k_gated(const __grid_constant_
                 carry = fma2f(o.a, carry, o.h);
             }
         } else {
-            // one warp joins the CTA's elements, and tells every CTA of the cluster
-            if (warp == 0) {
-                Element all = {both(1.0f), 0ull};
+            // every warp joins the CTA's elements, and tells its share of the cluster's CTAs
+            Element all = {both(1.0f), 0ull}, before = all;  // of the warps before this one
 #pragma unroll
-                for (int w = 0; w < W; ++w) {
-                    const Element o = of_warps[side][w][lane];
-                    of_warps[side][w][lane] = all;  // of the warps before w
-                    all.h = fma2f(o.a, all.h, o.h);
-                    all.a = mul2f(all.a, o.a);
-                }
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive_expect_tx(&arrived[side], (uint32_t)ctas * 32 * (uint32_t)sizeof(Element));
-                for (int q = 0; q < ctas; ++q)
-                    cluster_send(smem_addr(&of_ctas[side][rank][lane]), smem_addr(&arrived[side]), (unsigned)q, all.a, all.h);
+            for (int w = 0; w < W; ++w) {
+                if (w == warp)
+                    before = all;
+                const Element o = of_warps[side][w][lane];
+                all.h = fma2f(o.a, all.h, o.h);
+                all.a = mul2f(all.a, o.a);
             }
+            if (threadIdx.x == 0)
+                mbar_arrive_expect_tx(&arrived[side], (uint32_t)ctas * 32 * (uint32_t)sizeof(Element));
+            for (int q = warp; q < ctas; q += W)
+                cluster_send(smem_addr(&of_ctas[side][rank][lane]), smem_addr(&arrived[side]), (unsigned)q, all.a, all.h);
             cluster_await(&arrived[side], parity);
             parity ^= (uint32_t)side;
 #pragma unroll
@@ -460,14 +459,13 @@ __global__ void __launch_bounds__(32 * W, 16 / W) k_gated(const __grid_constant_
                     carry = fma2f(o.a, carry, o.h);
                 }
             }
-            const Element before = of_warps[side][warp][lane];
             h = fma2f(before.a, h, before.h);
         }
-        if (p.checkpoints != nullptr && warp * kFwdT % kGatedTile == 0 && n > 0)
+        if (p.checkpoints != nullptr && warp * T % kGatedTile == 0 && n > 0)
             put_state<FAR>(p.checkpoints + (b * g.ntiles + t0 / kGatedTile) * p.dim + c, mine, h);
         auto finish = [&](bool whole) {
 #pragma unroll
-            for (int k = 0; k < kFwdT; ++k) {
+            for (int k = 0; k < T; ++k) {
                 h = fma2f(a[k], h, v[k]);
                 f32x2 y = h;
                 if (has_z)
@@ -476,7 +474,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) k_gated(const __grid_constant_
                     put_pair<S, VEC, FAR>(out.row(t0 + k), mine, y);
             }
         };
-        if (n >= kFwdT)
+        if (n >= T)
             finish(true);
         else
             finish(false);
@@ -675,22 +673,20 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) k_gated_grad(const __grid_c
                 carry = fma2f(o.a, carry, o.h);
             }
         } else {
-            // one warp joins the CTA's elements of the adjoint, and tells every CTA of the cluster
-            if (warp == 0) {
-                Element all = {both(1.0f), 0ull};
+            // every warp joins the CTA's elements of the adjoint, and tells its share of the cluster's CTAs
+            Element all = {both(1.0f), 0ull}, behind = all;  // of the warps behind this one
 #pragma unroll
-                for (int w = W - 1; w >= 0; --w) {
-                    const Element o = back_of_warps[side][w][lane];
-                    back_of_warps[side][w][lane] = all;  // of the warps behind w
-                    all.h = fma2f(o.a, all.h, o.h);
-                    all.a = mul2f(all.a, o.a);
-                }
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive_expect_tx(&arrived[side], (uint32_t)ctas * 32 * (uint32_t)sizeof(Element));
-                for (int q = 0; q < ctas; ++q)
-                    cluster_send(smem_addr(&of_ctas[side][rank][lane]), smem_addr(&arrived[side]), (unsigned)q, all.a, all.h);
+            for (int w = W - 1; w >= 0; --w) {
+                if (w == warp)
+                    behind = all;
+                const Element o = back_of_warps[side][w][lane];
+                all.h = fma2f(o.a, all.h, o.h);
+                all.a = mul2f(all.a, o.a);
             }
+            if (threadIdx.x == 0)
+                mbar_arrive_expect_tx(&arrived[side], (uint32_t)ctas * 32 * (uint32_t)sizeof(Element));
+            for (int q = warp; q < ctas; q += W)
+                cluster_send(smem_addr(&of_ctas[side][rank][lane]), smem_addr(&arrived[side]), (unsigned)q, all.a, all.h);
             cluster_await(&arrived[side], parity);
             parity ^= (uint32_t)side;
 #pragma unroll
@@ -702,7 +698,6 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) k_gated_grad(const __grid_c
                     carry = fma2f(o.a, carry, o.h);
                 }
             }
-            const Element behind = back_of_warps[side][warp][lane];
             gh = fma2f(behind.a, gh, behind.h);
         }
 #pragma unroll
@@ -834,15 +829,16 @@ static int gated_warps(const GatedArgs &g, int most, int tokens) {
     const int64_t n = (g.p.len + tokens - 1) / tokens;
     return g.ctas > 1 || n > most ? most : n < 1 ? 1 : (int)n;
 }
-template <class S, bool RATE, bool VEC, bool IN, bool Z, bool CLUSTER, int W> static cudaError_t gated_forward_of(const GatedArgs &g, const Launch &L) {
+template <class S, bool RATE, bool VEC, bool IN, bool Z, bool CLUSTER, int W, int T>
+static cudaError_t gated_forward_of(const GatedArgs &g, const Launch &L) {
     static PerDevice ready;
-    constexpr int smem = FwdShared<S, VEC>::kWarp;
-    const cudaError_t e = allow_shared(k_gated<S, RATE, VEC, IN, Z, CLUSTER, W>, W * smem, ready);
+    constexpr int smem = FwdShared<S, VEC, T>::kWarp;
+    const cudaError_t e = allow_shared(k_gated<S, RATE, VEC, IN, Z, CLUSTER, W, T>, W * smem, ready);
     if (e != cudaSuccess)
         return e;
-    const int warps = gated_warps(g, W, kFwdT);
+    const int warps = gated_warps(g, W, T);
     note_launch();
-    return launch_cluster(k_gated<S, RATE, VEC, IN, Z, CLUSTER, W>, g.p.batch * g.slabs * g.ctas, 32 * warps, warps * smem, g.ctas, L.stream, g);
+    return launch_cluster(k_gated<S, RATE, VEC, IN, Z, CLUSTER, W, T>, g.p.batch * g.slabs * g.ctas, 32 * warps, warps * smem, g.ctas, L.stream, g);
 }
 template <class S, bool RATE, bool VEC, bool IN, bool Z, bool CLUSTER>
 static cudaError_t gated_backward_of(const GatedArgs &g, float *part, const Launch &L) {
@@ -863,22 +859,19 @@ template <class F> static cudaError_t by_gates(const mt_gated_args &p, F f) {
 }
 template <class S, bool RATE, bool VEC> static cudaError_t gated_forward(const GatedArgs &g, const Launch &L) {
     return by_gates(g.p, [&](auto in, auto z) {
-        if constexpr (!VEC)
-            return gated_forward_of<S, RATE, false, in(), z(), true, gated_cluster_warps(sizeof(S))>(g, L);
-        else if (g.ctas > 1)
-            return gated_forward_of<S, RATE, true, in(), z(), true, gated_cluster_warps(sizeof(S))>(g, L);
-        else if (sizeof(S) == 2 && g.p.batch * g.slabs > 3 * 152)
-            return gated_forward_of<S, RATE, true, in(), z(), false, sizeof(S) == 2 ? kGatedFewWarps : kGatedWarps>(g, L);
-        else
-            return gated_forward_of<S, RATE, true, in(), z(), false, kGatedWarps>(g, L);
+        if (g.ctas > 1)
+            return gated_forward_of<S, RATE, VEC, in(), z(), true, kGatedFewWarps, gated_cluster_tokens(sizeof(S))>(g, L);
+        if constexpr (sizeof(S) == 2)
+            if (g.p.batch * g.slabs > 3 * 152)
+                return gated_forward_of<S, RATE, VEC, in(), z(), false, kGatedFewWarps, kFwdT>(g, L);
+        return gated_forward_of<S, RATE, VEC, in(), z(), false, kGatedWarps, kFwdT>(g, L);
     });
 }
 template <class S, bool RATE, bool VEC> static cudaError_t gated_backward(const GatedArgs &g, float *part, const Launch &L) {
     return by_gates(g.p, [&](auto in, auto z) {
-        if constexpr (VEC)
-            if (g.ctas == 1)
-                return gated_backward_of<S, RATE, true, in(), z(), false>(g, part, L);
-        return gated_backward_of<S, RATE, VEC, in(), z(), true>(g, part, L);
+        if (g.ctas > 1)
+            return gated_backward_of<S, RATE, VEC, in(), z(), true>(g, part, L);
+        return gated_backward_of<S, RATE, VEC, in(), z(), false>(g, part, L);
     });
 }
 template <class S, bool RATE, bool VEC> static cudaError_t gated_single(const GatedArgs &g, const Launch &L) {
