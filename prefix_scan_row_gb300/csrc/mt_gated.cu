@@ -6,7 +6,7 @@ namespace mt {
 // CTAs that share a sequence's tokens: one where sequences and channels give every SM work, and otherwise as many as find
 // place at once, two an SM. A cluster's CTAs wait for one another at every tile, so it pays only then. bf16, all gates, prompt, us, in
 // clusters of 1, 2, 4 and 8 CTAs: 4 x 2048 tokens x 4096 channels (256 CTAs without clusters) 73, 89, 86, 101; 16384 tokens x
-// 2048 (32) 339, 224, 117, 98 (with eight warps of 8 tokens a CTA). Of the sizes with the same number of tiles the smallest.
+// 2048 (32) 339, 224, 117, 98 (eight warps of 8 tokens a CTA). Of the sizes with the same number of tiles the smallest.
 // The scratch is sized on the host, so the plan counts GB300's 152 SMs, and by the cluster's size the CTAs that were found to run
 // at once: clusters lie within a group of SMs, so not all places can be taken (a prompt of 2048 tokens
 // and its gradient in 264 CTAs, 44 clusters of 6, 23 and 32 us; in 288, 48 clusters, 33 and 51).
@@ -78,7 +78,7 @@ static GatedArgs gated_args(const mt_gated_args &p, int64_t cta_tokens) {
     default: return cudaErrorInvalidValue;              \
     }
 cudaError_t gated_launch(const mt_gated_args &p, const Launch &L) {
-    const GatedArgs g = gated_args(p, kGatedFewWarps * gated_cluster_tokens(p.dtype == MT_F32 ? 4 : 2));
+    const GatedArgs g = gated_args(p, kGatedWarps * gated_cluster_tokens(p.dtype == MT_F32 ? 4 : 2));
     const bool vec = all_fit(p, 16, false, false);
     if (p.batch * g.slabs * g.ctas > INT32_MAX)
         return cudaErrorInvalidValue;

@@ -36,15 +36,16 @@
 namespace mt {
 
 constexpr int kGatedSlab = 64;   // channels of a warp
-constexpr int kGatedWarps = 8;   // warps of a prompt's CTA
-// and where 16-bit calls have more CTAs than three an SM, so that a smaller one's end leaves less idle. Both, us, all gates,
-// 4096 channels, bf16, by sequences x tokens (CTAs): 4 x 2048 (256) 73, 73; 6 x 2048 (384) 110, 125; 8 x 2048 (512)
-// 140, 127; 16 x 1024 (1024) 125, 111. f32: 8 x 2048 211, 246.
-constexpr int kGatedFewWarps = 4;
-// and of a cluster's CTAs, two of which have to be on an SM: of 16-bit values its warps have twice the tokens, f32's tiles leave no
-// place for that. All gates, us, by these and by eight warps of 8 tokens: bf16 16384 x 2048 91, 107 (one warp joining for all: 99); 2 x 2048 x
-// 4096 44, 49; f32 16384 x 2048 127, 221; 4096 x 4096 64, 76.
-constexpr int gated_cluster_tokens(int bytes) { return bytes == 4 ? 8 : 16; }
+// A prompt's CTA: its warps and their tokens. us, all gates but where said, 4096 channels, by sequences x tokens (CTAs).
+// 16-bit, four warps of 16 tokens, two CTAs an SM, up to three CTAs an SM in all, and beyond that of 8 tokens, four CTAs an SM, whose ends
+// leave less idle; against eight warps of 8: 4 x 2048 (256) 69, 73; without output gate 4 x 4096 (256) 107, 117; 7 x 2048 (448) 108, 110;
+// 8 x 2048 (512) 128, of 16 tokens 134, eight warps 140; 16 x 1024 (1024) 112, 123, 125. 4 tokens, eight warps, three CTAs an SM, 4 x 2048: 115.
+// f32, eight warps of 8 tokens, one CTA an SM: 8 x 2048 (512) 211, four warps 246.
+// Clusters, two of whose CTAs have to be on an SM: four warps, of 16 and f32 of 8 tokens; against eight of 8: bf16 16384 x 2048 channels 91, 107
+// (one warp joining for all: 99); 2 x 2048 44, 49; f32 16384 x 2048 channels 127, 221; 4096 64, 76.
+constexpr int kGatedWarps = 4, kGatedWholeWarps = 8;
+constexpr int kFwdT = 8, kFwdMoreT = 16;
+constexpr int gated_cluster_tokens(int bytes) { return bytes == 4 ? kFwdT : kFwdMoreT; }
 constexpr int kGatedStages = 2;  // tiles of a warp on their way or in use
 
 struct GatedArgs {
@@ -300,10 +301,6 @@ struct alignas(16) Element {  // of the scan
 };
 
 // ---- prompts ----------------------------------------------------------------------------------------
-// Tokens of a warp, but for clusters. 4 x 2048 x 4096, bf16, all gates, us, eight warps a CTA: 4 tokens 115 (three CTAs an SM), 8 74, 16 77 (one). Four warps
-// of 16 take 69 there, but 8 x 2048 134 (of 8: 127), and 4 x 4096 without output gate 147 (114).
-constexpr int kFwdT = 8;
-
 template <class S, bool VEC, int T> using FwdTile = Tile<S, T, VEC, sizeof(S) == 4>;
 
 // With room for all four tensors, used or not: with less a cluster's f32 CTAs go three an SM, and unevenly (2 x 2048 x 4096, no
@@ -829,16 +826,20 @@ static int gated_warps(const GatedArgs &g, int most, int tokens) {
     const int64_t n = (g.p.len + tokens - 1) / tokens;
     return g.ctas > 1 || n > most ? most : n < 1 ? 1 : (int)n;
 }
+// Shared memory that three CTAs of an SM cannot have: with calls that leave registers for three some SMs would get three and
+// others one (4 x 4096 x 4096, bf16, no output gate, 147 us for 107).
+constexpr int kThird = 80 * 1024;
 template <class S, bool RATE, bool VEC, bool IN, bool Z, bool CLUSTER, int W, int T>
 static cudaError_t gated_forward_of(const GatedArgs &g, const Launch &L) {
     static PerDevice ready;
-    constexpr int smem = FwdShared<S, VEC, T>::kWarp;
-    const cudaError_t e = allow_shared(k_gated<S, RATE, VEC, IN, Z, CLUSTER, W, T>, W * smem, ready);
+    constexpr int smem = FwdShared<S, VEC, T>::kWarp, all = T == kFwdMoreT && W * smem < kThird ? kThird : W * smem;
+    const cudaError_t e = allow_shared(k_gated<S, RATE, VEC, IN, Z, CLUSTER, W, T>, all, ready);
     if (e != cudaSuccess)
         return e;
     const int warps = gated_warps(g, W, T);
     note_launch();
-    return launch_cluster(k_gated<S, RATE, VEC, IN, Z, CLUSTER, W, T>, g.p.batch * g.slabs * g.ctas, 32 * warps, warps * smem, g.ctas, L.stream, g);
+    return launch_cluster(k_gated<S, RATE, VEC, IN, Z, CLUSTER, W, T>, g.p.batch * g.slabs * g.ctas, 32 * warps,
+                          warps == W ? all : warps * smem, g.ctas, L.stream, g);
 }
 template <class S, bool RATE, bool VEC, bool IN, bool Z, bool CLUSTER>
 static cudaError_t gated_backward_of(const GatedArgs &g, float *part, const Launch &L) {
@@ -860,11 +861,13 @@ template <class F> static cudaError_t by_gates(const mt_gated_args &p, F f) {
 template <class S, bool RATE, bool VEC> static cudaError_t gated_forward(const GatedArgs &g, const Launch &L) {
     return by_gates(g.p, [&](auto in, auto z) {
         if (g.ctas > 1)
-            return gated_forward_of<S, RATE, VEC, in(), z(), true, kGatedFewWarps, gated_cluster_tokens(sizeof(S))>(g, L);
-        if constexpr (sizeof(S) == 2)
-            if (g.p.batch * g.slabs > 3 * 152)
-                return gated_forward_of<S, RATE, VEC, in(), z(), false, kGatedFewWarps, kFwdT>(g, L);
-        return gated_forward_of<S, RATE, VEC, in(), z(), false, kGatedWarps, kFwdT>(g, L);
+            return gated_forward_of<S, RATE, VEC, in(), z(), true, kGatedWarps, gated_cluster_tokens(sizeof(S))>(g, L);
+        if constexpr (sizeof(S) == 4)
+            return gated_forward_of<S, RATE, VEC, in(), z(), false, kGatedWholeWarps, kFwdT>(g, L);
+        else if (g.p.batch * g.slabs > 3 * 152)
+            return gated_forward_of<S, RATE, VEC, in(), z(), false, kGatedWarps, kFwdT>(g, L);
+        else
+            return gated_forward_of<S, RATE, VEC, in(), z(), false, kGatedWarps, kFwdMoreT>(g, L);
     });
 }
 template <class S, bool RATE, bool VEC> static cudaError_t gated_backward(const GatedArgs &g, float *part, const Launch &L) {
