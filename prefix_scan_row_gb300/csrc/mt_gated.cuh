@@ -21,8 +21,8 @@
 // computed or read twice. A cluster's CTAs are resident together, so their waits for one another end.
 //
 // Measured, all gates, us (share of the measured copy rate, 6798 GB/s): 16 x 1024 tokens x 4096 channels bf16, prompt 112
-// (88 %), gradient 222 (80 %); 4 x 2048 x 4096 bf16 74 (67 %) and 121 (73 %): 256 CTAs leave some SMs two and others one, and
-// the schedulers, the exponentials' unit and the multiply-adds' are each 25 to 57 % busy (86 instructions for a pair's token in
+// (88 %), gradient 222 (80 %); 4 x 2048 x 4096 bf16 69 (72 %) and 122 (73 %): 256 CTAs leave some SMs two and others one, and
+// the schedulers, the exponentials' unit and the multiply-adds' are each 25 to 57 % busy (some 80 instructions for a pair's token in
 // the prompt, 132 in the gradient); 16384 x 2048 bf16 91 (54 %) and 155 (57 %): the same, and clusters' waits; 8 x 2048 x 4096
 // f32 211 (94 %) and 405 (88 %).
 #pragma once
@@ -213,7 +213,7 @@ template <bool VEC> constexpr int kFar = VEC ? 1 : kGatedSlab / 2;
 // T tokens of a tensor in a warp's part of shared memory, 64 channels each. VEC: the rows are 16-byte aligned and
 // whole vectors. Otherwise rows are copied as the aligned vectors that they touch (each holds a channel of the row) and read from
 // where they begin in the first; or, WORDS, f32 value by value.
-// 4 x 2048 tokens x 4095 channels, all gates, us: bf16 prompt 110 and gradient 205 (4096 channels 73 and 121); f32 prompt
+// 4 x 2048 tokens x 4095 channels, all gates, us: bf16 prompt 107 and gradient 205 (4096 channels 69 and 122); f32 prompt
 // by words 155, by vectors 170, gradient 390 and 271.
 template <class S, int T, bool VEC, bool WORDS = false> struct Tile {
     static constexpr int kPitch = kGatedSlab * (int)sizeof(S) + (VEC ? 0 : 16);
@@ -312,7 +312,7 @@ template <class S, bool VEC, int T> struct FwdShared {
     static constexpr int kWarp = kGatedStages * kStage;
 };
 
-// IN and Z: the call has an input gate, an output gate; CLUSTER: CTAs share the tokens (or, where not VEC, may).
+// IN and Z: the call has an input gate, an output gate; CLUSTER: CTAs share the tokens.
 // W: warps of the CTA; fewer where these have all tokens.
 template <class S, bool RATE, bool VEC, bool IN, bool Z, bool CLUSTER, int W, int T>
 __global__ void __launch_bounds__(32 * W, 128 / W / T) k_gated(const __grid_constant__ GatedArgs g) {
@@ -827,7 +827,7 @@ static int gated_warps(const GatedArgs &g, int most, int tokens) {
     return g.ctas > 1 || n > most ? most : n < 1 ? 1 : (int)n;
 }
 // Shared memory that three CTAs of an SM cannot have: with calls that leave registers for three some SMs would get three and
-// others one (4 x 4096 x 4096, bf16, no output gate, 147 us for 107).
+// others one (4 x 4096 x 4096, bf16: prompt without output gate 147 us for 107, gradient without any but r 157 for 138).
 constexpr int kThird = 80 * 1024;
 template <class S, bool RATE, bool VEC, bool IN, bool Z, bool CLUSTER, int W, int T>
 static cudaError_t gated_forward_of(const GatedArgs &g, const Launch &L) {
@@ -844,13 +844,14 @@ static cudaError_t gated_forward_of(const GatedArgs &g, const Launch &L) {
 template <class S, bool RATE, bool VEC, bool IN, bool Z, bool CLUSTER>
 static cudaError_t gated_backward_of(const GatedArgs &g, float *part, const Launch &L) {
     static PerDevice ready;
-    constexpr int smem = BwdShared<S, VEC>::kWarp;
-    const cudaError_t e = allow_shared(k_gated_grad<S, RATE, VEC, IN, Z, CLUSTER>, kBwdWarps * smem, ready);
+    constexpr int smem = BwdShared<S, VEC>::kWarp, all = kBwdWarps * smem < kThird ? kThird : kBwdWarps * smem;
+    const cudaError_t e = allow_shared(k_gated_grad<S, RATE, VEC, IN, Z, CLUSTER>, all, ready);
     if (e != cudaSuccess)
         return e;
     const int warps = gated_warps(g, kBwdWarps, kBwdT);
     note_launch();
-    return launch_cluster(k_gated_grad<S, RATE, VEC, IN, Z, CLUSTER>, g.p.batch * g.slabs * g.ctas, 32 * warps, warps * smem, g.ctas, L.stream, g, part);
+    return launch_cluster(k_gated_grad<S, RATE, VEC, IN, Z, CLUSTER>, g.p.batch * g.slabs * g.ctas, 32 * warps,
+                          warps == kBwdWarps ? all : warps * smem, g.ctas, L.stream, g, part);
 }
 // The kernel of a call's gates: f(std::bool_constant of the input gate, of the output gate).
 template <class F> static cudaError_t by_gates(const mt_gated_args &p, F f) {
