@@ -22,7 +22,7 @@
 //
 // Measured, all gates, us (share of the measured copy rate, 6798 GB/s): 16 x 1024 tokens x 4096 channels bf16, prompt 112
 // (88 %), gradient 222 (80 %); 4 x 2048 x 4096 bf16 69 (72 %) and 122 (73 %): 256 CTAs leave some SMs two and others one, and
-// the schedulers, the exponentials' unit and the multiply-adds' are each 25 to 57 % busy (some 80 instructions for a pair's token in
+// the schedulers, the exponentials' unit and the multiply-adds' are each 25 to 55 % busy (78 instructions for a pair's token in
 // the prompt, 132 in the gradient); 16384 x 2048 bf16 91 (54 %) and 155 (57 %): the same, and clusters' waits; 8 x 2048 x 4096
 // f32 211 (94 %) and 405 (88 %).
 #pragma once
