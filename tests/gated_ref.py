@@ -11,6 +11,14 @@ kernel groups three factors or terms otherwise, or joins spans of tokens), and t
 * 1 - exp(-u) below u = 1/4 by its series: 4 U of itself (one for the terms left out); above, from exp(-u), good to (2 u + 2) U + 2^-22 of
   itself. An error of u moves exp(-u) by u times its relative error, 1 - exp(-u) by at most that.
 * 1 / sqrt(q): 2^-22, and half of q's error.
+
+The recurrences' sums are made in spans (a warp's tokens, a CTA's, a cluster's), whose sums can be larger than
+the states where terms of both signs meet: one token whose gradient all but cancels the one from behind it has a
+span's sum a dh, rounded to U |a dh|, and only then a g added. So their roundings are counted against the
+recurrence of absolute values, M' = |a| M + |b|, which no span's sum exceeds: for a token at most one for its term in the
+span, one for the span's product of decays, and two where the span is joined to others, 4 U M' (and, for
+the adjoint, one more addition of its own, 2 U (|dh| + M)). The terms' own errors go in as before: every
+grouping is the same function of the computed a and b.
 """
 import torch
 
@@ -51,6 +59,13 @@ def sigmoid(x):
     rel = (2 * x.abs() + 8) * U + 2.0 ** -21
     s, c = torch.sigmoid(x), torch.sigmoid(-x)
     return Ball(s, s * rel), Ball(c, c * rel)
+
+
+def step(a, h, b, m):
+    """a h + b, made in spans; m and its next value are the recurrence of absolute values."""
+    m = a.v.abs() * m + b.v.abs()
+    e = a.v.abs() * h.e + h.v.abs() * a.e + a.e * h.e + b.e
+    return Ball(a.v * h.v + b.v, e + 4 * U * (m + e)), m
 
 
 def stack(balls):
@@ -101,12 +116,13 @@ class GatedCase:
     def forward(self):
         self.gates()
         h, past = Ball(self.h0), []
+        size = self.h0.abs()
         hs = []
         for t in range(self.length):
             past.append(h)
             m = self.mask[:, t]
-            new = self.a.at(t) * h + self.b.at(t)
-            h = Ball(torch.where(m, new.v, h.v), torch.where(m, new.e, h.e))
+            new, grown = step(self.a.at(t), h, self.b.at(t), size)
+            h, size = Ball(torch.where(m, new.v, h.v), torch.where(m, new.e, h.e)), torch.where(m, grown, size)
             hs.append(h)
         self.final = h
         zero = Ball(torch.zeros_like(self.x))
@@ -128,13 +144,16 @@ class GatedCase:
             one = Ball(torch.ones_like(self.z))
             got["dz"] = (dy * self.h * (self.sz * (z * self.cz + one))).where(self.mask)
         carry = Ball(torch.zeros_like(self.h0) if dfinal is None else dfinal.to("cpu", F64))
-        gs = []
+        gs, size = [], carry.v.abs()
+        zero = Ball(torch.zeros_like(self.h0))
         for t in reversed(range(self.length)):
             g = dh.at(t) + carry
+            grown = dh.at(t).v.abs() + size
+            g = Ball(g.v, g.e + 2 * U * grown)
             m = self.mask[:, t]
-            new = g * self.a.at(t)
+            new, grown = step(self.a.at(t), g, zero, grown)
             gs.append(g.where(m))
-            carry = Ball(torch.where(m, new.v, carry.v), torch.where(m, new.e, carry.e))
+            carry, size = Ball(torch.where(m, new.v, carry.v), torch.where(m, new.e, carry.e)), torch.where(m, grown, size)
         got["dinit"] = carry
         g = stack(gs[::-1]) if gs else Ball(torch.zeros_like(self.x))
         dv = g * self.w

@@ -141,6 +141,17 @@ def test_many_short_sequences(mt, dtype, length):
     check_gradient(mt, p)
 
 
+@pytest.mark.parametrize("length", [1, 9, 130])
+def test_terms_that_cancel(mt, length):
+    """First states and last gradients that all but cancel what the first and last tokens add."""
+    p = Inputs(torch.float32, 4, length, 312, False, False, False)
+    s = torch.sigmoid(p.r[:, 0])
+    p.h0 = -s * p.x[:, 0] / (1 - s) * 1.001
+    p.dfinal = p.dout[:, -1] * -1.001
+    check_forward(mt, p)
+    check_gradient(mt, p)
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("length", [2048, 4099])
 def test_long_memory(mt, dtype, length):
