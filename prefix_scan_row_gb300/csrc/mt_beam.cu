@@ -412,7 +412,8 @@ __device__ __forceinline__ void rank_kept(ChooseShared &s, int count, int K) {
 }
 // The K first of get(0) .. get(n - 1), in order, in s.list; returns how many there are (K at most). A threshold that K of them
 // reach at least is the K-th of the first ones of 32 parts of the CTA; few others reach it, and where that is not so (in one
-// part, more than there is place for) they are taken one after the other. A barrier before it; ends with one.
+// part, more than there is place for) they are taken one after the other. A barrier before it, behind the last read of s.count;
+// ends with one.
 template <class F> __device__ __forceinline__ int choose(int64_t n, int K, ChooseShared &s, F get) {
     const int tid = threadIdx.x, lane = tid % 32;
     Choice mine = {0, ~0ull};
@@ -628,6 +629,7 @@ template <class S, bool VEC> __global__ void __launch_bounds__(kJoinThreads) k_b
         __syncthreads();
     } else {
         // Or there are many: of the groups' vectors the first ones, and of their logits.
+        __syncthreads();  // every warp has read the count, which choose() begins anew
         n = choose((int64_t)n * kGroupVectors, K, s, [&](int64_t i) {
             const uint64_t block = blocks[i / kGroupVectors];
             const int k = (int)(block >> 32);
