@@ -81,10 +81,21 @@ __device__ __forceinline__ void cluster_send(uint32_t here, uint32_t bar_here, u
     asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b64 [%0], {%1, %2}, [%3];"
                  :: "r"(there), "l"(a), "l"(b), "r"(bar) : "memory");
 }
+// One poll for phase `parity`. What another CTA sent is acquired at the cluster's scope: a poll's scope is its own CTA unless it says so.
+__device__ __forceinline__ bool cluster_try_wait(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok) : "r"(smem_addr(bar)), "r"(parity) : "memory");
+    return ok != 0;
+}
 // Until all CTAs' elements are here; a wait that gives up is reported as the look-back's are.
 __device__ __forceinline__ void cluster_await(uint64_t *bar, uint32_t parity) {
-    if (!mbar_wait(bar, parity, kCopyWaitLimit))
-        atomicCAS(&g_mt_err, 0, kErrTimeout);
+    for (uint32_t i = 0; i < kCopyWaitLimit; ++i)
+        if (cluster_try_wait(bar, parity))
+            return;
+    atomicCAS(&g_mt_err, 0, kErrTimeout);
 }
 
 // ---- a pair of channels ---------------------------------------------------------------------------
