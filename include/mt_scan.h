@@ -334,6 +334,8 @@ int mt_scan_build_checked(void);
  * polls after which a waiting tile gives up, records
  * MT_ERR_LOOKBACK_TIMEOUT and publishes its own status so that later tiles
  * are not held (0 = the library default, about a second or more of waiting).
+ * In a gated scan whose CTAs share tokens in clusters (a) is a CTA's index,
+ * which stops before its first tile, and (b) the polls of each wait for a cluster's CTAs.
  * Every wait stays bounded. Not for production use.
  */
 int mt_scan_debug_lookback(int64_t skip_publish_tile, uint32_t spin_limit);
@@ -381,7 +383,8 @@ int mt_scan_rows_noalloc(const void *inp, void *out, int64_t rows, int64_t n, in
  * arithmetic with one rounding at each store. Every sum has a fixed order, so a
  * call gives the same bits each time. No call waits between CTAs, but for the
  * gated scan's, whose CTAs of one cluster wait for one another; those waits are
- * bounded, and one that gave up is reported by mt_scan_status.
+ * bounded, and one that gave up is reported by mt_scan_status (the outputs of that
+ * cluster's sequence and channels are then undefined).
  *
  * Activations are [batch, len, dim] with the channels contiguous and any
  * strides (in elements) of the other two axes, so they may be parts of wider

@@ -61,12 +61,14 @@ static bool all_fit(const mt_gated_args &p, int64_t bytes, bool step, bool grad)
            (p.z == nullptr || fits(p.dz, p.dz_batch, p.dz_token, bytes, v));
 }
 
-static GatedArgs gated_args(const mt_gated_args &p, int64_t cta_tokens) {
+static GatedArgs gated_args(const mt_gated_args &p, int64_t cta_tokens, const Launch &L) {
     GatedArgs g;
     g.p = p;
     g.slabs = (int)((p.dim + kGatedSlab - 1) / kGatedSlab);
     g.ctas = gated_ctas(p.batch, p.len, p.dim, cta_tokens);
     g.ntiles = (p.len + kGatedTile - 1) / kGatedTile;
+    g.limit = L.spin_limit != kDefaultSpin ? L.spin_limit : kCopyWaitLimit;  // the test hook's, where it is set
+    g.silent = L.skip_tile;
     return g;
 }
 
@@ -78,7 +80,7 @@ static GatedArgs gated_args(const mt_gated_args &p, int64_t cta_tokens) {
     default: return cudaErrorInvalidValue;              \
     }
 cudaError_t gated_launch(const mt_gated_args &p, const Launch &L) {
-    const GatedArgs g = gated_args(p, kGatedWarps * gated_cluster_tokens(p.dtype == MT_F32 ? 4 : 2));
+    const GatedArgs g = gated_args(p, kGatedWarps * gated_cluster_tokens(p.dtype == MT_F32 ? 4 : 2), L);
     const bool vec = all_fit(p, 16, false, false);
     if (p.batch * g.slabs * g.ctas > INT32_MAX)
         return cudaErrorInvalidValue;
@@ -87,7 +89,7 @@ cudaError_t gated_launch(const mt_gated_args &p, const Launch &L) {
 cudaError_t gated_step_launch(const mt_gated_args &a, const Launch &L) {
     mt_gated_args p = a;
     p.len = 1;
-    const GatedArgs g = gated_args(p, kFwdT);
+    const GatedArgs g = gated_args(p, kFwdT, L);
     const bool vec = all_fit(p, p.dtype == MT_F32 ? 8 : 4, true, false);
     if (p.batch * ((p.dim + 1) / 2) / 128 >= INT32_MAX)
         return cudaErrorInvalidValue;
@@ -99,7 +101,7 @@ static cudaError_t backward(const GatedArgs &g, float *part, const Launch &L) {
     MT_BY_TYPE(gated_backward, g, part, vec, L)
 }
 cudaError_t gated_grad_launch(const mt_gated_args &p, const Launch &L) {
-    const GatedArgs g = gated_args(p, kBwdWarps * kBwdT);
+    const GatedArgs g = gated_args(p, kBwdWarps * kBwdT, L);
     float *part = p.drate != nullptr ? static_cast<float *>(p.scratch) : nullptr;
     if (p.batch * g.slabs * g.ctas > INT32_MAX)
         return cudaErrorInvalidValue;

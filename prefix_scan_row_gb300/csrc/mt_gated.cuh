@@ -53,6 +53,8 @@ struct GatedArgs {
     int slabs;       // of 64 channels
     int ctas;        // of a cluster
     int64_t ntiles;  // checkpoints of a sequence
+    uint32_t limit;  // polls of a wait for a cluster's CTAs
+    int64_t silent;  // test hook: the CTA that tells the others nothing (-1: none)
 };
 
 __device__ __forceinline__ int64_t gated_len(const mt_gated_args &p, int64_t b) {
@@ -63,6 +65,10 @@ __device__ __forceinline__ int64_t gated_slot(const mt_gated_args &p, int64_t b)
     const int64_t s = p.slots != nullptr ? (int64_t)p.slots[b] : b;
     return s >= 0 && s < p.nslots ? s : -1;
 }
+
+struct alignas(16) Element {  // of the scan
+    f32x2 a, h;
+};
 
 // ---- clusters -----------------------------------------------------------------------------------
 __device__ __forceinline__ unsigned cluster_rank() {
@@ -90,12 +96,66 @@ __device__ __forceinline__ bool cluster_try_wait(uint64_t *bar, uint32_t parity)
                  : "=r"(ok) : "r"(smem_addr(bar)), "r"(parity) : "memory");
     return ok != 0;
 }
-// Until all CTAs' elements are here; a wait that gives up is reported as the look-back's are.
-__device__ __forceinline__ void cluster_await(uint64_t *bar, uint32_t parity) {
-    for (uint32_t i = 0; i < kCopyWaitLimit; ++i)
-        if (cluster_try_wait(bar, parity))
+// What the CTAs of a cluster tell one another: the scan's elements of two tiles, and how far a CTA came that stopped early.
+// Waits are bounded. One that gives up is reported as the look-back's are, its CTA stops before the next tile, and the others, which
+// wait for that tile's elements, follow: no call waits longer than the limit twice. A CTA that ends while elements are on their way to it would
+// leave them a place that is no longer its own; so whoever stops says how many tiles' elements it has sent, and each waits for the rest.
+constexpr int kAllSent = INT32_MAX;
+struct ClusterShared {
+    Element element[2][8][32];       // by the tile's side, of each CTA
+    alignas(8) uint64_t arrived[2];  // a side's elements are all here
+    int late[2];                     // a wait of this side gave up
+    int stopped;                     // a CTA of the cluster stopped early
+    int sent[8];                     // and then the tiles whose elements it has sent
+};
+constexpr uint32_t kElementBytes = 32 * sizeof(Element);
+// Before the cluster's first barrier. `silent`: the test hook's CTA, which stops before its first tile.
+__device__ __forceinline__ void cluster_begin(ClusterShared &s, bool silent) {
+    if (threadIdx.x == 0) {
+        mbar_init(&s.arrived[0], 1);
+        mbar_init(&s.arrived[1], 1);
+        fence_mbar_init();
+        s.late[0] = s.stopped = 0;
+        s.late[1] = silent;  // as if of the tile before the first
+        for (int q = 0; q < 8; ++q)
+            s.sent[q] = kAllSent;
+    }
+}
+// Until all CTAs' elements of a tile are here.
+__device__ __forceinline__ void cluster_await(ClusterShared &s, int side, uint32_t parity, uint32_t limit) {
+    for (uint32_t i = 0; i < limit; ++i)
+        if (cluster_try_wait(&s.arrived[side], parity))
             return;
     atomicCAS(&g_mt_err, 0, kErrTimeout);
+    s.late[side] = 1;
+}
+// Behind the loop, of all threads. This CTA has sent its elements of `done` of `tiles` tiles.
+__device__ __forceinline__ void cluster_end(ClusterShared &s, unsigned rank, int ctas, int done, int tiles) {
+    if (done < tiles && threadIdx.x < ctas) {
+        uint32_t sent, stopped;
+        asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(sent) : "r"(smem_addr(&s.sent[rank])), "r"(threadIdx.x));
+        asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(stopped) : "r"(smem_addr(&s.stopped)), "r"(threadIdx.x));
+        asm volatile("st.shared::cluster.s32 [%0], %1;" :: "r"(sent), "r"(done) : "memory");
+        asm volatile("st.shared::cluster.s32 [%0], %1;" :: "r"(stopped), "r"(1) : "memory");
+    }
+    cluster_arrive();  // no CTA ends that another might still send to
+    cluster_wait();
+    if (threadIdx.x != 0 || (s.late[0] | s.late[1] | s.stopped) == 0)
+        return;
+    // The tile before has a wait of this CTA, which may have given up, for everyone's elements: those never sent are counted as here. The next one
+    // has none yet, and those that came further have sent theirs; nobody comes further than that without this CTA's.
+    for (int t = done > 0 ? done - 1 : 0; t <= done && t < tiles; ++t) {
+        uint32_t missing = 0;
+        for (int q = 0; q < ctas; ++q)
+            missing += s.sent[q] <= t ? kElementBytes : 0;
+        if (t == done)
+            mbar_arrive_expect_tx(&s.arrived[t & 1], (uint32_t)ctas * kElementBytes);
+        if (missing != 0)
+            asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cta.b64 [%0], %1;" :: "r"(smem_addr(&s.arrived[t & 1])), "r"(missing) : "memory");
+        for (uint32_t i = 0; i < kCopyWaitLimit; ++i)  // all have been sent
+            if (cluster_try_wait(&s.arrived[t & 1], (uint32_t)(t >> 1 & 1)))
+                break;
+    }
 }
 
 // ---- a pair of channels ---------------------------------------------------------------------------
@@ -307,10 +367,6 @@ template <int FAR> __device__ __forceinline__ void put_state(float *p, int live,
         p[FAR] = b;
 }
 
-struct alignas(16) Element {  // of the scan
-    f32x2 a, h;
-};
-
 // ---- prompts ----------------------------------------------------------------------------------------
 template <class S, bool VEC, int T> using FwdTile = Tile<S, T, VEC, sizeof(S) == 4>;
 
@@ -333,15 +389,10 @@ __global__ void __launch_bounds__(32 * W, 128 / W / T) k_gated(const __grid_cons
     constexpr int FAR = kFar<VEC>;
     extern __shared__ __align__(16) char staged[];
     __shared__ Element of_warps[2][W][32];
-    __shared__ Element of_ctas[2][8][32];
-    __shared__ __align__(8) uint64_t arrived[2];  // of_ctas is complete
+    __shared__ ClusterShared others;
     const int ctas = CLUSTER ? g.ctas : 1;
     if (ctas > 1) {
-        if (threadIdx.x == 0) {
-            mbar_init(&arrived[0], 1);
-            mbar_init(&arrived[1], 1);
-            fence_mbar_init();
-        }
+        cluster_begin(others, blockIdx.x == g.silent);
         cluster_arrive();  // waited for below: no CTA sends to one that has not begun
     }
     pdl_prologue();
@@ -388,7 +439,9 @@ __global__ void __launch_bounds__(32 * W, 128 / W / T) k_gated(const __grid_cons
 
     int side = 0;
     uint32_t parity = 0;  // of the barriers' phases, each of which serves every other tile
-    for (int base = 0; base < len; base += step, side ^= 1) {
+    int base = 0;
+    const int tiles = (len + step - 1) / step;
+    for (; base < len; base += step, side ^= 1) {
         const int t0 = base + first, n = len - t0;
         char *at = own + side * Shared::kStage;
         cp_async_wait<kGatedStages - 1>();
@@ -432,6 +485,8 @@ __global__ void __launch_bounds__(32 * W, 128 / W / T) k_gated(const __grid_cons
         ask(t0 + kGatedStages * step, side);
         of_warps[side][warp][lane] = e;
         __syncthreads();
+        if (ctas > 1 && others.late[side ^ 1])  // a side's mark is not written again before all have passed the next barrier
+            break;
         f32x2 h = carry;  // before the CTA's first token
         if (ctas == 1) {
 #pragma unroll
@@ -453,17 +508,17 @@ __global__ void __launch_bounds__(32 * W, 128 / W / T) k_gated(const __grid_cons
                 all.a = mul2f(all.a, o.a);
             }
             if (threadIdx.x == 0)
-                mbar_arrive_expect_tx(&arrived[side], (uint32_t)ctas * 32 * (uint32_t)sizeof(Element));
+                mbar_arrive_expect_tx(&others.arrived[side], (uint32_t)ctas * kElementBytes);
             for (int q = warp; q < ctas; q += W)
-                cluster_send(smem_addr(&of_ctas[side][rank][lane]), smem_addr(&arrived[side]), (unsigned)q, all.a, all.h);
-            cluster_await(&arrived[side], parity);
+                cluster_send(smem_addr(&others.element[side][rank][lane]), smem_addr(&others.arrived[side]), (unsigned)q, all.a, all.h);
+            cluster_await(others, side, parity, g.limit);
             parity ^= (uint32_t)side;
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
                 if (q == rank)
                     h = carry;
                 if (q < ctas) {
-                    const Element o = of_ctas[side][q][lane];
+                    const Element o = others.element[side][q][lane];
                     carry = fma2f(o.a, carry, o.h);
                 }
             }
@@ -488,10 +543,8 @@ __global__ void __launch_bounds__(32 * W, 128 / W / T) k_gated(const __grid_cons
             finish(false);
     }
     cp_async_wait<0>();
-    if (ctas > 1) {  // no CTA ends that another might still send to
-        cluster_arrive();
-        cluster_wait();
-    }
+    if (ctas > 1)
+        cluster_end(others, (unsigned)rank, ctas, base / step, tiles);
     for (int t = len + rank * warps + warp; t < total; t += ctas * warps)
         put_pair<S, VEC, FAR>(out.row(t), mine, 0ull);
     if (active && p.state != nullptr && rank == 0 && warp == 0)
@@ -526,15 +579,10 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) k_gated_grad(const __grid_c
     extern __shared__ __align__(16) char staged[];
     __shared__ Element of_warps[2][W][32];
     __shared__ Element back_of_warps[2][W][32];  // the adjoint's
-    __shared__ Element of_ctas[2][8][32];
-    __shared__ __align__(8) uint64_t arrived[2];  // of_ctas is complete
+    __shared__ ClusterShared others;
     const int ctas = CLUSTER ? g.ctas : 1;
     if (ctas > 1) {
-        if (threadIdx.x == 0) {
-            mbar_init(&arrived[0], 1);
-            mbar_init(&arrived[1], 1);
-            fence_mbar_init();
-        }
+        cluster_begin(others, blockIdx.x == g.silent);
         cluster_arrive();  // waited for below: no CTA sends to one that has not begun
     }
     pdl_prologue();
@@ -587,7 +635,9 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) k_gated_grad(const __grid_c
 
     int side = 0;
     uint32_t parity = 0;  // of the barriers' phases, each of which serves every other tile
-    for (int base = last; base >= 0; base -= step, side ^= 1) {
+    int base = last;
+    const int tiles = len > 0 ? last / step + 1 : 0;
+    for (; base >= 0; base -= step, side ^= 1) {
         const int t0 = base + first, n = len - t0;
         char *at = own + side * Shared::kStage;
         f32x2 h = 0ull;  // before the first token of the checkpoint's warps
@@ -666,6 +716,8 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) k_gated_grad(const __grid_c
         of_warps[side][warp][lane] = e;
         back_of_warps[side][warp][lane] = {e.a, back};
         __syncthreads();
+        if (ctas > 1 && others.late[side ^ 1])  // a side's mark is not written again before all have passed the next barrier
+            break;
         // the state before this warp's tokens
         for (int w = warp / kMarkWarps * kMarkWarps; w < warp; ++w) {
             const Element o = of_warps[side][w][lane];
@@ -692,17 +744,17 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) k_gated_grad(const __grid_c
                 all.a = mul2f(all.a, o.a);
             }
             if (threadIdx.x == 0)
-                mbar_arrive_expect_tx(&arrived[side], (uint32_t)ctas * 32 * (uint32_t)sizeof(Element));
+                mbar_arrive_expect_tx(&others.arrived[side], (uint32_t)ctas * kElementBytes);
             for (int q = warp; q < ctas; q += W)
-                cluster_send(smem_addr(&of_ctas[side][rank][lane]), smem_addr(&arrived[side]), (unsigned)q, all.a, all.h);
-            cluster_await(&arrived[side], parity);
+                cluster_send(smem_addr(&others.element[side][rank][lane]), smem_addr(&others.arrived[side]), (unsigned)q, all.a, all.h);
+            cluster_await(others, side, parity, g.limit);
             parity ^= (uint32_t)side;
 #pragma unroll
             for (int q = 7; q >= 0; --q) {
                 if (q == rank)
                     gh = carry;
                 if (q < ctas) {
-                    const Element o = of_ctas[side][q][lane];
+                    const Element o = others.element[side][q][lane];
                     carry = fma2f(o.a, carry, o.h);
                 }
             }
@@ -742,10 +794,8 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) k_gated_grad(const __grid_c
             finish(false);
     }
     cp_async_wait<0>();
-    if (ctas > 1) {  // no CTA ends that another might still send to
-        cluster_arrive();
-        cluster_wait();
-    }
+    if (ctas > 1)
+        cluster_end(others, (unsigned)rank, ctas, (last - base) / step, tiles);
     for (int t = len + rank * warps + warp; t < total; t += ctas * warps) {
         put_pair<S, VEC, FAR>(dx.row(t), mine, 0ull);
         put_pair<S, VEC, FAR>(dr.row(t), mine, 0ull);
