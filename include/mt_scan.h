@@ -576,7 +576,7 @@ int64_t mt_selective_scan_checkpoint_slots(int64_t batch, int64_t len, int64_t d
  *   without rate:  a_t = 1 - s_t,              w_t = s_t
  *   h_t = a_t * h_{t-1} + w_t * v_t,   v_t = sigma(i_t) * x_t, or x_t without i
  *   out_t = h_t, or h_t * z_t * sigma(z_t) with z
- * Where w_t is 0 (s_t or rate[d] so small that 1 - a_t^2 is) its derivative counts as 0.
+ * With rate, where 1 - a_t is below 2^-126 (rate[d] * s_t next to 0), w_t and its derivative count as 0.
  */
 typedef struct {
     int64_t dtype;                 /* all activations and their gradients: MT_F32, MT_BF16 or MT_F16 */
@@ -591,7 +591,7 @@ typedef struct {
     int64_t i_batch, i_token;
     const void *z;                 /* [batch, len, dim], optional: the gate of the output */
     int64_t z_batch, z_token;
-    const float *rate;             /* [dim], optional, 0 to 2^100 */
+    const float *rate;             /* [dim], optional, 0 to 2^100 (below 0 counts as 0) */
     float *state;                  /* [nslots, dim] contiguous */
     const int32_t *slots, *lens;   /* optional */
     void *out;                     /* [batch, len, dim] */

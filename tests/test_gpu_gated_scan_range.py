@@ -1,0 +1,85 @@
+"""The gated scan at the ends of f32's range: rates next to 0; infinities. Bounds where there are some: gated_ref.GatedCase."""
+import pytest
+import torch
+
+import gated_ref as G
+import seq_ref as R
+from test_gpu_gated_scan import Inputs
+
+pytestmark = pytest.mark.gpu
+DTYPES = [torch.float32, torch.bfloat16, torch.float16]
+F64 = torch.float64
+SHAPES = [(2, 70, 66), (1, 700, 64)]  # one CTA a sequence and slab and rows that are not aligned; clusters
+
+
+@pytest.fixture(scope="module")
+def mt():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    import prefix_scan_row_gb300 as m
+    return m
+
+
+NEXT_TO_ZERO = [0.0, 1e-45, 1e-40, 5e-39, 1e-37, 1e-36, 1e-30, 1e-20]  # of which the first four let nothing in, with gates near 1/2
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("shape", SHAPES)
+def test_rates_next_to_zero(mt, dtype, shape):
+    """Where 1 - a^2 is below f32's normal numbers, the input's weight is 0, and so is its derivative; elsewhere both are as the definition
+    has them. The sum for a rate of 0 is over the state's part alone: its terms are off by 8 U (products of four factors and their
+    states and gradients, sums of up to the length) of their size."""
+    p = Inputs(dtype, *shape, True, False, False)
+    b, length, d = shape
+    g = torch.Generator().manual_seed(12)
+    p.r = (torch.rand(shape, generator=g) - 0.5).to(dtype)
+    p.rate = torch.tensor(NEXT_TO_ZERO)[torch.arange(d) % 8].clone()
+    dead = p.rate < 1e-38
+    out, state = p.forward(mt)
+    got = p.gradient(mt)
+    assert torch.equal(state.cpu()[:, dead], p.h0[:, dead])
+    assert torch.equal(out.cpu()[..., dead], p.h0[:, None, dead].expand(b, length, -1).to(dtype))
+    assert (got["dx"][..., dead.cuda()] == 0).all() and (got["dr"].float().abs()[..., dead.cuda()] < 1e-30).all()
+    after = p.dout.to(F64).flip(1).cumsum(1).flip(1) + p.dfinal.to(F64)[:, None]
+    size = p.dout.to(F64).abs().flip(1).cumsum(1).flip(1) + p.dfinal.to(F64).abs()[:, None]
+    s, h = torch.sigmoid(p.r.to(F64)), p.h0.to(F64)[:, None]
+    R.assert_within("drate", got["drate"].cpu()[dead], (-after * h * s).sum((0, 1))[dead],
+                    (2 * length + 40) * R.U * (size * h.abs() * s).sum((0, 1))[dead])
+    live = ~dead
+    cut = lambda t: t[..., live].contiguous()  # noqa: E731
+    case = G.GatedCase(cut(p.x), cut(p.r), None, None, p.rate[live], p.h0[:, live])
+    want, final = case.forward()
+    G.check("out", out.cpu()[..., live], want)
+    G.check("state", state.cpu()[:, live], final)
+    want = case.gradient(cut(p.dout), p.dfinal[:, live])
+    for name in want:
+        G.check(name, got[name].cpu()[..., live], want[name])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("where", ["x", "h0"])
+def test_infinities_stay_in_their_channel_and_after_their_token(mt, dtype, shape, where):
+    p = Inputs(dtype, *shape, True, True, False)
+    clean, last = p.forward(mt)
+    at = shape[1] // 3 if where == "x" else 0
+    if where == "x":
+        p.x[0, at, 5] = float("inf")
+    else:
+        p.h0[0, 5] = -float("inf")
+    out, state = p.forward(mt)
+    assert not out[0, at:, 5].isfinite().any() and not state[0, 5].isfinite()
+    out[0, at:, 5], state[0, 5] = clean[0, at:, 5], last[0, 5]
+    assert torch.equal(out, clean) and torch.equal(state, last)
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+def test_rates_below_zero_count_as_zero(mt, shape):
+    p = Inputs(torch.float32, *shape, True, True, True)
+    got = []
+    for below in (0.0, -3.0):
+        p.rate[::2] = below
+        state, out = p.h0.cuda(), torch.empty(shape[0], shape[2], device="cuda")
+        g = p.gates()
+        mt.mt_gated_scan_step(p.x[:, 0].cuda(), p.r[:, 0].cuda(), state, out, i=g["i"][:, 0], z=g["z"][:, 0], rate=g["rate"])
+        got.append((*p.forward(mt), *p.gradient(mt).values(), state, out))
+    assert all(torch.equal(a, b) for a, b in zip(*got))
