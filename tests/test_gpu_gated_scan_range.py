@@ -1,4 +1,5 @@
-"""The gated scan at the ends of f32's range: rates next to 0; infinities. Bounds where there are some: gated_ref.GatedCase."""
+"""The gated scan at the ends of f32's range: gates that are the type's lowest value, with large values beside them; rates next
+to 0; infinities. Bounds where there are some: gated_ref.GatedCase."""
 import pytest
 import torch
 
@@ -17,6 +18,51 @@ def mt():
     assert torch.cuda.is_available(), "GPU tests need a CUDA device"
     import prefix_scan_row_gb300 as m
     return m
+
+
+def lowest(dtype, shape):
+    """Values whose logistic function is below 4e-44, the type's lowest among them."""
+    low = torch.tensor([torch.finfo(dtype).min, -100.0, -1e4, torch.finfo(dtype).min / 3]).to(dtype)
+    return low[torch.arange(shape[0] * shape[1] * shape[2]) % 4].view(shape).contiguous()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("rate", [True, False])
+def test_output_gates_that_are_shut(mt, dtype, shape, rate):
+    """z sigma(z) and its derivative are below 1e-41 in size there, so what is let through, and every gradient, is 0 but for
+    that: values are below 100, a sum has a few thousand terms."""
+    p = Inputs(dtype, *shape, rate, True, True)
+    p.z = lowest(dtype, shape)
+    out, _ = p.forward(mt)
+    assert out.float().abs().max() < 1e-30
+    for name, g in p.gradient(mt, dfinal=False).items():
+        assert g.float().abs().max() < 1e-30, name
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("rate", [0.3, 2.0 ** 100, None])
+def test_shut_gates_pass_nothing_however_large(mt, dtype, shape, rate):
+    """r at the type's lowest value: nothing is let in and nothing forgotten, bit for bit, and no gradient passes but the state's."""
+    p = Inputs(dtype, *shape, rate is not None, False, False)
+    p.r.fill_(torch.finfo(dtype).min)
+    p.r[:, ::3] = -1e4
+    p.x = (torch.finfo(dtype).max / 4 * torch.sign(p.x.float())).to(dtype)
+    if rate is not None:
+        p.rate.fill_(rate)
+    out, state = p.forward(mt)
+    assert torch.equal(state.cpu(), p.h0) and torch.equal(out.cpu(), p.h0[:, None].expand(shape).to(dtype))
+    step = p.h0.cuda()
+    one = torch.empty(shape[0], shape[2], dtype=dtype, device="cuda")
+    mt.mt_gated_scan_step(p.x[:, 0].cuda(), p.r[:, 0].cuda(), step, one, rate=p.gates()["rate"])
+    assert torch.equal(step.cpu(), p.h0) and torch.equal(one, out[:, 0])
+    got = p.gradient(mt)
+    assert (got["dx"] == 0).all() and (got["dr"] == 0).all()
+    if rate is not None:
+        assert (got["drate"] == 0).all()
+    total = p.dout.to(F64)
+    R.assert_within("dinit", got["dinit"], total.sum(1) + p.dfinal.to(F64), (shape[1] + 4) * 2 * R.U * (total.abs().sum(1) + p.dfinal.abs()))
 
 
 NEXT_TO_ZERO = [0.0, 1e-45, 1e-40, 5e-39, 1e-37, 1e-36, 1e-30, 1e-20]  # of which the first four let nothing in, with gates near 1/2
