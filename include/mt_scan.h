@@ -577,6 +577,7 @@ int64_t mt_selective_scan_checkpoint_slots(int64_t batch, int64_t len, int64_t d
  *   h_t = a_t * h_{t-1} + w_t * v_t,   v_t = sigma(i_t) * x_t, or x_t without i
  *   out_t = h_t, or h_t * z_t * sigma(z_t) with z
  * A sigma below 2^-126 (its argument below -87.3) counts as 0, in the gradients too; smaller ones than 2^-102 are good to 2^-126.
+ * In prompts with rate a sigma(i_t) below 2^-63 may count as 0.
  * With rate, where 1 - a_t is below 2^-126 (rate[d] * s_t next to 0), w_t and its derivative count as 0.
  */
 typedef struct {

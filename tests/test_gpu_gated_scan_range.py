@@ -1,11 +1,11 @@
-"""The gated scan at the ends of f32's range: gates that are the type's lowest value, with large values beside them; rates next
-to 0; infinities. Bounds where there are some: gated_ref.GatedCase."""
+"""The gated scan at the ends of f32's range: gates that are the type's lowest value, with large values beside them; input gates far
+below 0 with inputs that make up for it; rates next to 0; infinities. Bounds where there are some: gated_ref.GatedCase."""
 import pytest
 import torch
 
 import gated_ref as G
 import seq_ref as R
-from test_gpu_gated_scan import Inputs
+from test_gpu_gated_scan import Inputs, check_forward, check_gradient
 
 pytestmark = pytest.mark.gpu
 DTYPES = [torch.float32, torch.bfloat16, torch.float16]
@@ -63,6 +63,37 @@ def test_shut_gates_pass_nothing_however_large(mt, dtype, shape, rate):
         assert (got["drate"] == 0).all()
     total = p.dout.to(F64)
     R.assert_within("dinit", got["dinit"], total.sum(1) + p.dfinal.to(F64), (shape[1] + 4) * 2 * R.U * (total.abs().sum(1) + p.dfinal.abs()))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("rate", [True, False])
+def test_input_gates_far_below_zero(mt, monkeypatch, dtype, shape, rate):
+    """Gates of 1e-17 to 1e-35, and inputs of 1e25. As the calls' documentation says, a logistic function below 2^-102 has an error of up to 2^-126
+    beside the relative ones (1 / (1 + e) less 2^-126, rounded once), and an input gate below 2^-63 may count as 0 in a prompt with rate; these
+    go into the bounds as the others do."""
+    plain = G.sigmoid
+
+    def allow(error):
+        def sigmoid(x):
+            s, c = plain(x)
+            return G.Ball(s.v, s.e + error), c
+        monkeypatch.setattr(G, "sigmoid", sigmoid)
+
+    p = Inputs(dtype, *shape, rate, True, False)
+    g = torch.Generator().manual_seed(11)
+    p.i = (-40 - 40 * torch.rand(shape, generator=g)).to(dtype)
+    p.x = (p.x.float() * 1e25).to(dtype)
+    allow(2.0 ** -63 if rate else 2.0 ** -126)
+    check_forward(mt, p)
+    check_gradient(mt, p)
+    allow(2.0 ** -126)
+    want, final = G.GatedCase(p.x[:, :1], p.r[:, :1], p.i[:, :1], None, p.rate, p.h0).forward()
+    state, out = p.h0.cuda(), torch.empty(shape[0], shape[2], dtype=dtype, device="cuda")
+    gates = p.gates()
+    mt.mt_gated_scan_step(p.x[:, 0].cuda(), p.r[:, 0].cuda(), state, out, i=gates["i"][:, 0], rate=gates["rate"])
+    G.check("out", out, G.Ball(want.v[:, 0], want.e[:, 0]))
+    G.check("state", state, final)
 
 
 NEXT_TO_ZERO = [0.0, 1e-45, 1e-40, 5e-39, 1e-37, 1e-36, 1e-30, 1e-20]  # of which the first four let nothing in, with gates near 1/2
