@@ -152,7 +152,7 @@ class SequenceModel:
         tokens, parents, src, dst = (new(torch.int32) for _ in range(4))
         scores, finished = new(torch.float32), new(torch.uint8)
         slots = torch.arange(b * beams, dtype=torch.int32, device="cuda").view(b, beams)
-        scratch = self._slots("beams", max(mt.mt_beam_select_scratch_slots(b, k, beams, vocab) for k in (1, beams)))
+        scratch = self._slots("beams", mt.mt_beam_select_scratch_slots(b, beams, beams, vocab))  # the first step's too, of one beam
         logits = self.prompt(prompts, lens, states, slots=slots[:, 0].contiguous())
         path = []
         for t in range(steps):

@@ -690,7 +690,8 @@ typedef struct {
  */
 int mt_beam_select(const mt_beam_args *args, void *stream);
 
-/* 8-byte scratch slots of mt_beam_select; -1 for a size out of range. */
+/* 8-byte scratch slots of mt_beam_select; -1 for a size out of range. They
+ * serve any call none of whose sizes is larger. */
 int64_t mt_beam_select_scratch_slots(int64_t batch, int64_t beams, int64_t beams_out, int64_t vocab);
 
 /* A pool of state rows: row s of plane l begins at base + l * plane_stride + s * row_stride (bytes). */

@@ -721,13 +721,20 @@ template <class S> cudaError_t launch(const mt_beam_args &a, const Launch &L) {
 
 }  // namespace
 
+// No smaller than what any smaller call takes, although a smaller call may cut its rows into more and shorter spans: spans of
+// fewer groups than the most are chosen only where spans of twice as many are fewer than kEnoughSpans, so there are less than twice
+// that many of them, and no more than these rows have.
 int64_t beam_scratch_slots(int64_t batch, int64_t beams, int64_t, int64_t vocab) {
-    int64_t most = 0;  // of the types
-    for (const int64_t size : {2, 4}) {
-        const BeamPlan plan = beam_plan(batch * beams, vocab, size);
-        const int64_t slots = batch * beams * plan.spans * 2 + (batch * beams * plan.spans * plan.batches + 1) / 2;
-        most = slots > most ? slots : most;
-    }
+    int64_t most = 0;
+    for (const int64_t size : {2, 4})  // of the types
+        for (int batches = kMostBatches; batches >= 1; batches /= 2) {
+            const int64_t bytes = (int64_t)batches * kGroupVectors * 16;
+            int64_t spans = batch * beams * ((vocab * size + bytes - 1) / bytes);
+            if (batches < kMostBatches && spans > 2 * kEnoughSpans)
+                spans = 2 * kEnoughSpans;
+            const int64_t slots = 2 * spans + (spans * batches + 1) / 2;
+            most = slots > most ? slots : most;
+        }
     return most;
 }
 
