@@ -428,7 +428,9 @@ int mt_embed_grad(const void *tokens, int64_t ntokens, int token_dtype, const vo
                   int64_t dim, float scale, void *dtable, int grad_dtype, int accumulate, void *scratch, void *stream);
 
 /* 8-byte scratch slots of mt_embed_grad; -1 for a negative or too large size.
- * Plain host arithmetic, as the other two scratch sizes below. */
+ * Plain host arithmetic, as the other scratch sizes below. A size here is for
+ * the arguments it was asked with: where nothing else is said, a call with
+ * smaller ones may need more. */
 int64_t mt_embed_grad_scratch_slots(int64_t ntokens, int64_t vocab, int64_t dim);
 
 /*
@@ -637,7 +639,8 @@ int mt_gated_scan_step(const mt_gated_args *args, void *stream);
  * checkpoints; slots must be NULL). */
 int mt_gated_scan_grad(const mt_gated_args *args, void *stream);
 
-/* 8-byte slots of mt_gated_scan_grad's scratch and of the checkpoints; -1 for a size out of range. */
+/* 8-byte slots of mt_gated_scan_grad's scratch and of the checkpoints; -1 for a
+ * size out of range. They serve any call none of whose sizes is larger. */
 int64_t mt_gated_scan_scratch_slots(int64_t batch, int64_t len, int64_t dim);
 int64_t mt_gated_scan_checkpoint_slots(int64_t batch, int64_t len, int64_t dim);
 

@@ -10,18 +10,23 @@ namespace mt {
 // The scratch is sized on the host, so the plan counts GB300's 152 SMs, and by the cluster's size the CTAs that were found to run
 // at once: clusters lie within a group of SMs, so not all places can be taken (a prompt of 2048 tokens
 // and its gradient in 264 CTAs, 44 clusters of 6, 23 and 32 us; in 288, 48 clusters, 33 and 51).
+constexpr int kPlaces[] = {0, 304, 304, 276, 276, 264, 264, 252, 264}, kMostCtas = 8;
 static int gated_ctas(int64_t batch, int64_t len, int64_t dim, int64_t cta_tokens) {
-    constexpr int kPlaces[] = {0, 304, 304, 276, 276, 264, 264, 252, 264};
     const int64_t units = batch * ((dim + kGatedSlab - 1) / kGatedSlab), tiles = (len + cta_tokens - 1) / cta_tokens;
-    int64_t n = 8;
+    int64_t n = kMostCtas;
     while (n > 1 && (units * n > kPlaces[n] || n > tiles))
         --n;
     const int64_t rounds = (tiles + n - 1) / n;
     return rounds > 0 ? (int)((tiles + rounds - 1) / rounds) : 1;
 }
 
+// A sum of every CTA and channel, no fewer than any smaller call has, although one may take larger clusters: these have as many CTAs as there are
+// tiles at most, and only where all CTAs, of 64 channels each, are no more than the places for clusters of two.
 int64_t gated_scratch_slots(int64_t batch, int64_t len, int64_t dim) {
-    return (batch * gated_ctas(batch, len, dim, kBwdWarps * kBwdT) * dim + 1) / 2;
+    const int64_t tiles = (len + kBwdWarps * kBwdT - 1) / (kBwdWarps * kBwdT), shared = kPlaces[2] * kGatedSlab;
+    const int64_t sums = batch * dim, more = sums * (tiles < 1 ? 1 : tiles < kMostCtas ? tiles : kMostCtas);
+    const int64_t most = more < shared ? more : shared;
+    return ((sums > most ? sums : most) + 1) / 2;
 }
 
 // Sums of parts [rows, dim] over the rows, in order: a warp's lanes share 32 channels, its CTA's warps the rows.
