@@ -122,8 +122,7 @@ int gated_check(const mt_gated_args &a, bool tokens) {
         return MT_ERR_ARG;
     if ((a.slots != nullptr || a.carry_in) && a.state == nullptr)
         return MT_ERR_ARG;
-    if (!aligned({a.x, a.r, a.i, a.z, a.out, a.dout, a.dx, a.dr, a.di, a.dz}, s) ||
-        !aligned({a.rate, a.state, a.slots, a.lens, a.checkpoints, a.drate, a.dfinal, a.dinit}, 4) || !aligned({a.scratch}, 16))
+    if (!aligned({a.x, a.r, a.i, a.z}, s) || !aligned({a.rate}, 4))  // what all calls read; each looks at its other fields
         return MT_ERR_ALIGN;
     return MT_OK;
 }
@@ -377,6 +376,8 @@ extern "C" int mt_gated_scan(const mt_gated_args *args, void *stream) {
         return bad;
     if ((a.len > 0 && a.out == nullptr) || (a.checkpoints != nullptr && a.slots != nullptr))
         return MT_ERR_ARG;
+    if (!aligned({a.out}, act_size(a.dtype)) || !aligned({a.state, a.slots, a.lens, a.checkpoints}, 4))
+        return MT_ERR_ALIGN;
     for (const void *p : {(const void *)a.out, (const void *)a.state, (const void *)a.checkpoints})
         if (among(p, {a.x, a.r, a.i, a.z, a.rate, a.slots, a.lens}))
             return MT_ERR_ALIAS;
@@ -400,6 +401,8 @@ extern "C" int mt_gated_scan_step(const mt_gated_args *args, void *stream) {
         return bad;
     if (any_null({a.out, a.state}))
         return MT_ERR_ARG;
+    if (!aligned({a.out}, act_size(a.dtype)) || !aligned({a.state, a.slots}, 4))
+        return MT_ERR_ALIGN;
     if (among(a.out, {a.x, a.r, a.i, a.z, a.rate, a.state, a.slots}) || among(a.state, {a.x, a.r, a.i, a.z, a.rate, a.slots}))
         return MT_ERR_ALIAS;
     Launch L;
@@ -428,6 +431,9 @@ extern "C" int mt_gated_scan_grad(const mt_gated_args *args, void *stream) {
         return MT_ERR_ARG;
     const void *outs[] = {a.dx, a.dr, a.i != nullptr ? a.di : nullptr, a.z != nullptr ? a.dz : nullptr, a.drate, a.dinit,
                           a.drate != nullptr ? a.scratch : nullptr};
+    if (!aligned({a.dout, outs[0], outs[1], outs[2], outs[3]}, act_size(a.dtype)) ||
+        !aligned({a.lens, a.checkpoints, a.dfinal, outs[4], outs[5]}, 4) || !aligned({outs[6]}, 16))
+        return MT_ERR_ALIGN;
     for (size_t k = 0; k < sizeof(outs) / sizeof(*outs); ++k) {
         if (among(outs[k], {a.x, a.r, a.i, a.z, a.rate, a.lens, a.dout, a.checkpoints, a.dfinal}))
             return MT_ERR_ALIAS;
