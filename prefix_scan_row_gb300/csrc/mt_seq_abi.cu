@@ -73,8 +73,7 @@ int conv_check(const mt_conv_args &a, bool tokens) {
     if (a.carry_in && a.state == nullptr && a.width > 1)
         return MT_ERR_ARG;
     const int w = a.wdtype == MT_F32 ? 4 : s;
-    if (!aligned({a.x, a.state, a.out, a.dout, a.dx, a.dstate}, s) || !aligned({a.weight, a.bias}, w) ||
-        !aligned({a.slots, a.lens, a.dweight, a.dbias}, 4) || !aligned({a.scratch}, 16))
+    if (!aligned({a.x, a.state}, s) || !aligned({a.weight, a.bias}, w) || !aligned({a.slots}, 4))  // each call looks at its other fields
         return MT_ERR_ALIGN;
     return MT_OK;
 }
@@ -98,9 +97,7 @@ int ssm_check(const mt_ssm_args &a, bool tokens) {
         return MT_ERR_ARG;
     if ((a.slots != nullptr || a.carry_in) && a.state == nullptr)
         return MT_ERR_ARG;
-    if (!aligned({a.u, a.delta, a.z, a.B, a.C, a.out, a.dout, a.du, a.ddelta, a.dz, a.dB, a.dC}, s) ||
-        !aligned({a.A, a.D, a.delta_bias, a.state, a.slots, a.lens, a.checkpoints, a.dA, a.dD, a.ddelta_bias, a.dfinal, a.dinit}, 4) ||
-        !aligned({a.scratch}, 16))
+    if (!aligned({a.u, a.delta, a.z, a.B, a.C}, s) || !aligned({a.A, a.D, a.delta_bias}, 4))  // each call looks at its other fields
         return MT_ERR_ALIGN;
     return MT_OK;
 }
@@ -197,6 +194,8 @@ extern "C" int mt_causal_conv(const mt_conv_args *args, void *stream) {
         return bad;
     if (a.len > 0 && a.out == nullptr)
         return MT_ERR_ARG;
+    if (!aligned({a.out}, act_size(a.dtype)) || !aligned({a.lens}, 4))
+        return MT_ERR_ALIGN;
     if (among(a.out, {a.x, a.weight, a.bias, a.state}) || among(a.state, {a.x, a.weight, a.bias}))
         return MT_ERR_ALIAS;
     Launch L;
@@ -217,6 +216,8 @@ extern "C" int mt_causal_conv_step(const mt_conv_args *args, void *stream) {
         return bad;
     if (a.out == nullptr || (a.state == nullptr && a.width > 1))
         return MT_ERR_ARG;
+    if (!aligned({a.out}, act_size(a.dtype)))
+        return MT_ERR_ALIGN;
     if (among(a.out, {a.x, a.weight, a.bias, a.state}) || among(a.state, {a.x, a.weight, a.bias}))
         return MT_ERR_ALIAS;
     Launch L;
@@ -246,6 +247,9 @@ extern "C" int mt_causal_conv_grad(const mt_conv_args *args, void *stream) {
         return MT_ERR_ARG;
     if (a.batch > 0 && (a.scratch == nullptr || (a.len > 0 && any_null({a.dout, a.dx}))))
         return MT_ERR_ARG;
+    if (!aligned({a.dweight, a.dbias}, 4) || (a.batch > 0 && (!aligned({a.dout, a.dx, a.dstate}, act_size(a.dtype)) || !aligned({a.lens}, 4) ||
+                                                              !aligned({a.scratch}, 16))))
+        return MT_ERR_ALIGN;
     for (const void *p : {(const void *)a.dx, (const void *)a.dweight, (const void *)a.dbias, (const void *)a.dstate, (const void *)a.scratch})
         if (among(p, {a.x, a.weight, a.bias, a.state, a.dout}))
             return MT_ERR_ALIAS;
@@ -290,6 +294,8 @@ extern "C" int mt_selective_scan(const mt_ssm_args *args, void *stream) {
     if ((a.len > 0 && a.out == nullptr) || slots < 0 || (slots > 0 && a.scratch == nullptr) ||
         (a.checkpoints != nullptr && a.slots != nullptr))
         return MT_ERR_ARG;
+    if (!aligned({a.out}, act_size(a.dtype)) || !aligned({a.state, a.slots, a.lens, a.checkpoints}, 4) || !aligned({a.scratch}, 16))
+        return MT_ERR_ALIGN;
     for (const void *p : {(const void *)a.out, (const void *)a.state, (const void *)a.checkpoints, (const void *)a.scratch})
         if (among(p, {a.u, a.delta, a.z, a.B, a.C, a.A, a.D, a.delta_bias}))
             return MT_ERR_ALIAS;
@@ -313,6 +319,8 @@ extern "C" int mt_selective_scan_step(const mt_ssm_args *args, void *stream) {
         return bad;
     if (any_null({a.out, a.state}))
         return MT_ERR_ARG;
+    if (!aligned({a.out}, act_size(a.dtype)) || !aligned({a.state, a.slots}, 4))
+        return MT_ERR_ALIGN;
     if (among(a.out, {a.u, a.delta, a.z, a.B, a.C, a.A, a.D, a.delta_bias, a.state}) ||
         among(a.state, {a.u, a.delta, a.z, a.B, a.C, a.A, a.D, a.delta_bias}))
         return MT_ERR_ALIAS;
@@ -341,6 +349,10 @@ extern "C" int mt_selective_scan_grad(const mt_ssm_args *args, void *stream) {
         return MT_ERR_ARG;
     if (work && (any_null({a.dout, a.checkpoints, a.du, a.ddelta, a.dB, a.dC}) || (a.z != nullptr && a.dz == nullptr)))
         return MT_ERR_ARG;
+    if (!aligned({a.dA, a.dD, a.ddelta_bias}, 4) ||
+        (a.batch > 0 && (!aligned({a.dout, a.du, a.ddelta, a.dz, a.dB, a.dC}, act_size(a.dtype)) ||
+                         !aligned({a.lens, a.checkpoints, a.dfinal, a.dinit}, 4) || !aligned({a.scratch}, 16))))
+        return MT_ERR_ALIGN;
     for (const void *p : {(const void *)a.du, (const void *)a.ddelta, (const void *)a.dz, (const void *)a.dB, (const void *)a.dC, (const void *)a.dA,
                           (const void *)a.dD, (const void *)a.ddelta_bias, (const void *)a.dinit, (const void *)a.scratch})
         if (among(p, {a.u, a.delta, a.z, a.B, a.C, a.A, a.D, a.delta_bias, a.dout, a.checkpoints, a.dfinal}))
@@ -431,8 +443,8 @@ extern "C" int mt_gated_scan_grad(const mt_gated_args *args, void *stream) {
         return MT_ERR_ARG;
     const void *outs[] = {a.dx, a.dr, a.i != nullptr ? a.di : nullptr, a.z != nullptr ? a.dz : nullptr, a.drate, a.dinit,
                           a.drate != nullptr ? a.scratch : nullptr};
-    if (!aligned({a.dout, outs[0], outs[1], outs[2], outs[3]}, act_size(a.dtype)) ||
-        !aligned({a.lens, a.checkpoints, a.dfinal, outs[4], outs[5]}, 4) || !aligned({outs[6]}, 16))
+    if (!aligned({a.drate}, 4) || (a.batch > 0 && (!aligned({a.dout, outs[0], outs[1], outs[2], outs[3]}, act_size(a.dtype)) ||
+                                                   !aligned({a.lens, a.checkpoints, a.dfinal, a.dinit}, 4) || !aligned({outs[6]}, 16))))
         return MT_ERR_ALIGN;
     for (size_t k = 0; k < sizeof(outs) / sizeof(*outs); ++k) {
         if (among(outs[k], {a.x, a.r, a.i, a.z, a.rate, a.lens, a.dout, a.checkpoints, a.dfinal}))
