@@ -881,6 +881,12 @@ template <class S, bool RATE, bool VEC> __global__ void __launch_bounds__(128) k
 }
 
 // ---- launches ---------------------------------------------------------------------------------------
+// Whether this translation unit has launched a cluster: no other of its kernels waits, and its error word is not read for them.
+static std::atomic<bool> g_clusters{false};
+static cudaError_t clusters_take_error(int *code) {
+    *code = 0;
+    return g_clusters.load(std::memory_order_relaxed) ? take_error_word(code) : cudaSuccess;
+}
 template <class... KArgs, class... Args>
 static cudaError_t launch_cluster(void (*kernel)(KArgs...), int64_t grid, unsigned block, int smem, int cluster, cudaStream_t stream,
                                   Args... args) {
@@ -897,6 +903,8 @@ static cudaError_t launch_cluster(void (*kernel)(KArgs...), int64_t grid, unsign
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = cluster > 1 ? 2 : 1;
+    if (cluster > 1)
+        g_clusters.store(true, std::memory_order_relaxed);
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
@@ -971,20 +979,13 @@ template <class S, bool RATE, bool VEC> static cudaError_t gated_single(const Ga
     using S = T;                                                                                                                    \
     cudaError_t gated_forward_##name(const GatedArgs &g, bool vec, const Launch &L) { return MT_GATED_BY(gated_forward, g, L); }    \
     cudaError_t gated_single_##name(const GatedArgs &g, bool vec, const Launch &L) { return MT_GATED_BY(gated_single, g, L); }      \
-    cudaError_t gated_##name##_take_error(int *code) { return gated_take_error_word(code); }
+    cudaError_t gated_##name##_take_error(int *code) { return clusters_take_error(code); }
 #define MT_GATED_GRAD_TYPE(name, T)                                                                                                 \
     using S = T;                                                                                                                    \
     cudaError_t gated_backward_##name(const GatedArgs &g, float *part, bool vec, const Launch &L) {                                 \
         return MT_GATED_BY(gated_backward, g, part, L);                                                                             \
     }                                                                                                                               \
-    cudaError_t gated_grad_##name##_take_error(int *code) { return gated_take_error_word(code); }
-
-// Reads and clears this translation unit's device error word.
-static cudaError_t gated_take_error_word(int *code) {
-    const int zero = 0;
-    const cudaError_t e = cudaMemcpyFromSymbol(code, g_mt_err, sizeof(int));
-    return e != cudaSuccess ? e : cudaMemcpyToSymbol(g_mt_err, &zero, sizeof(int));
-}
+    cudaError_t gated_grad_##name##_take_error(int *code) { return clusters_take_error(code); }
 
 #define MT_GATED_DECL(name)                                                                  \
     cudaError_t gated_forward_##name(const GatedArgs &g, bool vec, const Launch &L);         \
