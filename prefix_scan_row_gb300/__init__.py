@@ -687,6 +687,9 @@ class Library:
             shape, stride, e, row = t.shape, t.stride(), t.element_size(), 1
             if len(shape) <= axis:
                 raise ValueError("a pool has fewer axes than that of its slots")
+            if t.numel() == 0:  # nothing to copy, whatever its strides
+                blocks.append(_POOL.pack(t.data_ptr(), 0, 0, 0, 0, 0))
+                continue
             for d in range(len(shape) - 1, axis, -1):
                 if stride[d] != row and shape[d] > 1:
                     raise ValueError("a pool's rows must be contiguous")
