@@ -2,10 +2,12 @@
 groups' vectors and then among their logits: many sequences side by side, which reach that at different times, and calls one
 after the other. Tokens, parents, marks, slots and copies are the lowest places of the highest value, which needs no sum; scores
 and all else are the same bits in every sequence and call."""
+import math
+
 import pytest
 import torch
 
-from test_gpu_beam_select import check, run
+from test_gpu_beam_select import SLACK, check, run
 
 pytestmark = pytest.mark.gpu
 DTYPES = [torch.float32, torch.bfloat16, torch.float16]
@@ -59,3 +61,19 @@ def test_floods_beside_ordinary_rows_and_finished_beams(mt, dtype):
     ended = (torch.rand(b, k, generator=g) < 0.2).to(torch.uint8)
     slots = torch.randperm(b * k, generator=g).to(torch.int32).view(b, k)
     check(mt, x, k, prior, ended, 5, slots)
+
+
+@pytest.mark.parametrize("at", [0, 5, (1 << 31) - 9])
+def test_the_largest_vocabulary(mt, at):
+    """2^31 - 1 logits, all but three of them equal: a few tokens stand out, at the row's ends or near its last vectors, and the flood's lowest follow.
+    Score: 5 less the logarithm of 2^31 - 4 + 3 exp(5)."""
+    v = (1 << 31) - 1
+    x = torch.zeros(v, dtype=torch.bfloat16, device="cuda")
+    top = sorted({at, 1 << 30, v - 1})
+    x[torch.tensor(top, device="cuda")] = 5.0
+    got = run(mt, x.view(1, 1, v), 5)
+    others = [t for t in range(6) if t not in top]
+    assert got["tokens"][0].tolist() == (top + others)[:5] and got["parents"][0].tolist() == [0] * 5
+    log_sum = math.log(v - 3 + 3 * math.exp(5.0))
+    want = torch.tensor([5.0 - log_sum] * 3 + [-log_sum] * 2)
+    assert (got["scores"][0].cpu() - want).abs().max() <= SLACK + 2.0 ** -24 * 32
