@@ -885,7 +885,11 @@ template <class S, bool RATE, bool VEC> __global__ void __launch_bounds__(128) k
 static std::atomic<bool> g_clusters{false};
 static cudaError_t clusters_take_error(int *code) {
     *code = 0;
-    return g_clusters.load(std::memory_order_relaxed) ? take_error_word(code) : cudaSuccess;
+    if (!g_clusters.load(std::memory_order_relaxed))
+        return cudaSuccess;
+    const int zero = 0;
+    const cudaError_t e = cudaMemcpyFromSymbol(code, g_mt_err, sizeof(int));
+    return e != cudaSuccess || *code == 0 ? e : cudaMemcpyToSymbol(g_mt_err, &zero, sizeof(int));
 }
 template <class... KArgs, class... Args>
 static cudaError_t launch_cluster(void (*kernel)(KArgs...), int64_t grid, unsigned block, int smem, int cluster, cudaStream_t stream,

@@ -153,5 +153,11 @@ extern "C" int mt_scan_rows_noalloc(const void *inp, void *out, int64_t rows, in
 namespace mt {
 // Reads and clears this translation unit's device error word (set only by
 // the bounds-checked build's checks of the clear kernel).
-cudaError_t noalloc_take_error(int *code) { return take_error_word(code); }
+cudaError_t noalloc_take_error(int *code) {
+    const int zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(code, g_mt_err, sizeof(int));
+    if (e != cudaSuccess)
+        return e;
+    return cudaMemcpyToSymbol(g_mt_err, &zero, sizeof(int));
+}
 }  // namespace mt

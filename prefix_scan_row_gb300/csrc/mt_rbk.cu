@@ -534,6 +534,12 @@ cudaError_t rbk_launch(const void *keys, const void *vals, void *keys_out, void 
     return val_float ? launch_rbk<false, true>(a, L) : launch_rbk<false, false>(a, L);
 }
 
-cudaError_t rbk_take_error(int *code) { return take_error_word(code); }
+cudaError_t rbk_take_error(int *code) {
+    const int zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(code, g_mt_err, sizeof(int));
+    if (e != cudaSuccess)
+        return e;
+    return cudaMemcpyToSymbol(g_mt_err, &zero, sizeof(int));
+}
 
 }  // namespace mt

@@ -323,6 +323,12 @@ cudaError_t reduce_launch(const void *arr, void *out, uint64_t *scratch, const i
 
 // Reads and clears this translation unit's device error word (set only by
 // the bounds-checked build's checks).
-cudaError_t reduce_take_error(int *code) { return take_error_word(code); }
+cudaError_t reduce_take_error(int *code) {
+    const int zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(code, g_mt_err, sizeof(int));
+    if (e != cudaSuccess)
+        return e;
+    return cudaMemcpyToSymbol(g_mt_err, &zero, sizeof(int));
+}
 
 }  // namespace mt

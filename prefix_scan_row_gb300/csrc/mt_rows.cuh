@@ -141,4 +141,13 @@ static cudaError_t rows_launch_op(const void *in, void *out, int64_t rows, int64
     return e;
 }
 
+// Reads and clears this translation unit's device error word.
+static cudaError_t take_error_word(int *code) {
+    const int zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(code, g_mt_err, sizeof(int));
+    if (e != cudaSuccess)
+        return e;
+    return cudaMemcpyToSymbol(g_mt_err, &zero, sizeof(int));
+}
+
 }  // namespace mt

@@ -42,6 +42,6 @@ cudaError_t scan1d_launch(const void *arr, void *out, uint64_t *scratch, const i
     }
 }
 
-cudaError_t scan1d_take_error(int *code) { return take_error_word(code); }
+cudaError_t scan1d_take_error(int *code) { return scan1d_take_error_word(code); }
 
 }  // namespace mt

@@ -79,4 +79,13 @@ static SegArgs scan1d_args(const void *arr, void *out, uint64_t *scratch, const 
     return a;
 }
 
+// Reads and clears this translation unit's device error word.
+static cudaError_t scan1d_take_error_word(int *code) {
+    const int zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(code, g_mt_err, sizeof(int));
+    if (e != cudaSuccess)
+        return e;
+    return cudaMemcpyToSymbol(g_mt_err, &zero, sizeof(int));
+}
+
 }  // namespace mt

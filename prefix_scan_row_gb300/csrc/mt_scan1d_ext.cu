@@ -17,6 +17,6 @@ cudaError_t scan1d_launch_ext(const SegArgs &a, int dtype, int op, const Launch 
     }
 }
 
-cudaError_t scan1d_ext_take_error(int *code) { return take_error_word(code); }
+cudaError_t scan1d_ext_take_error(int *code) { return scan1d_take_error_word(code); }
 
 }  // namespace mt

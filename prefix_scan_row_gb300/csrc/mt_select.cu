@@ -795,6 +795,12 @@ cudaError_t select_launch(const void *arr, const uint8_t *flags, void *out, int3
     }
 }
 
-cudaError_t select_take_error(int *code) { return take_error_word(code); }
+cudaError_t select_take_error(int *code) {
+    const int zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(code, g_mt_err, sizeof(int));
+    if (e != cudaSuccess)
+        return e;
+    return cudaMemcpyToSymbol(g_mt_err, &zero, sizeof(int));
+}
 
 }  // namespace mt

@@ -42,14 +42,6 @@ constexpr uint32_t kCopyWaitLimit = 1u << 26;  // mbarrier polls before a copy i
 // Per translation unit device error word; written when a look-back wait gives up.
 static __device__ int g_mt_err;
 
-// Reads this translation unit's word, and clears it where it is set (a copy less for each unit whose word is not, and
-// an error that a kernel records between the two is not lost).
-static inline cudaError_t take_error_word(int *code) {
-    const int zero = 0;
-    const cudaError_t e = cudaMemcpyFromSymbol(code, g_mt_err, sizeof(int));
-    return e != cudaSuccess || *code == 0 ? e : cudaMemcpyToSymbol(g_mt_err, &zero, sizeof(int));
-}
-
 // ---------------------------------------------------------------------------
 // Bounds-checked build. Compiled with MT_CHECKED=1, every global store and
 // every shared-memory access of the kernels is first checked against the
