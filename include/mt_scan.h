@@ -579,6 +579,8 @@ int64_t mt_selective_scan_checkpoint_slots(int64_t batch, int64_t len, int64_t d
  *   h_t = a_t * h_{t-1} + w_t * v_t,   v_t = sigma(i_t) * x_t, or x_t without i
  *   out_t = h_t, or h_t * z_t * sigma(z_t) with z
  * A sigma below 2^-126 (its argument below -87.3) counts as 0, in the gradients too; smaller ones than 2^-102 are good to 2^-126.
+ * An infinite state is infinite or NaN from there on, in its channel alone:
+ * spans of tokens are joined by products of their decays.
  * In prompts with rate a sigma(i_t) below 2^-63 may count as 0.
  * With rate, where 1 - a_t is below 2^-126 (rate[d] * s_t next to 0), w_t and its derivative count as 0.
  */
@@ -673,8 +675,11 @@ typedef struct {
  *   prior[k] + logits[k, v] - log(sum over v' of exp(logits[k, v']))
  * the beams_out best ones, best first; equal scores by the lowest k, then the
  * lowest v. parents[j] = k, tokens[j] = v, scores[j] the score. All arrays but
- * logits are contiguous. Scores are made and compared as pairs of f32 (48 bits),
- * and rounded once, at the store.
+ * logits are contiguous. Scores are compared as pairs of f32 (48 bits) and
+ * rounded once, at the store. A beam's sum, which is in all of its scores, is made of
+ * f32 sums of exponentials and good to some 1e-7 of itself (below 5e-6): the order
+ * within a beam is its logits', but continuations of different beams whose scores
+ * are closer than that may come in either order. Beams of equal logits have equal sums.
  *
  * Logits: NaN counts as -inf (a token that may not come next), +inf as the
  * largest finite value of their type. A beam whose logits are all -inf, or whose prior is -inf or

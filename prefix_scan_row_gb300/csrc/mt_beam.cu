@@ -10,8 +10,8 @@
 //
 // Bound: the first kernel by bytes, f32, and by its instructions, 16-bit (an exponential a logit; issue 63 %, XU 38 %); the second
 // by its chain of loads, barriers and comparisons, 8 to 10 us. Both together, us in a CUDA graph (share of the measured copy rate, 6798 GB/s):
-// 64 x 16 x 131072 logits f32 91 (87 %), bf16 55 (71 %); 64 x 8 x 32768 bf16 16.8 (29 %); 1 x 4 x 32768 f32 7.9. Rows that are not
-// aligned take two loads for a vector: 64 x 16 x 131071 bf16 84 (47 %). All logits equal, 64 x 16 x 131072 bf16: 102.
+// 64 x 16 x 131072 logits f32 91 (87 %), bf16 55 (71 %); 64 x 8 x 32768 bf16 16.8 (29 %); 1 x 4 x 32768 f32 7.8. Rows that are not
+// aligned take two loads for a vector: 64 x 16 x 131071 bf16 84 (47 %). All logits equal, 64 x 16 x 131072 bf16: 106.
 #include <initializer_list>
 
 #include "mt_seq.cuh"
@@ -151,7 +151,8 @@ template <class S, int WORDS> __device__ __forceinline__ uint4 load_logits(const
         return w;
     }
 }
-// A lane's part of a span: its largest value, and the sum of 2^(log2(e) x - k) with k the whole number next to log2(e) times
+// A lane's part of a span: its largest value, and the sum, in f32, of up to 64 terms in each of four places (which is what a beam's sum is
+// good to, some 1e-7; from there on nothing is lost above 2^-30 of a span), of 2^(log2(e) x - k) with k the whole number next to log2(e) times
 // the largest (kept between -+kMostPower). One multiply-add, rounded once, makes an exponent, and a larger k scales the sum by
 // a power of two. (A sum relative to exp of the largest would take a subtraction for each logit.)
 constexpr float kMostPower = 8388608.0f;

@@ -20,11 +20,11 @@
 // knows its first state and finishes its tokens, whose decays and inputs are still in registers. Nothing is
 // computed or read twice. A cluster's CTAs are resident together, so their waits for one another end.
 //
-// Measured, all gates, us (share of the measured copy rate, 6798 GB/s): 16 x 1024 tokens x 4096 channels bf16, prompt 112
-// (88 %), gradient 222 (80 %); 4 x 2048 x 4096 bf16 69 (72 %) and 122 (73 %): 256 CTAs leave some SMs two and others one, and
+// Measured, all gates, us (share of the measured copy rate, 6798 GB/s): 16 x 1024 tokens x 4096 channels bf16, prompt 111
+// (89 %), gradient 221 (81 %); 4 x 2048 x 4096 bf16 68 (73 %) and 121 (73 %): 256 CTAs leave some SMs two and others one, and
 // the schedulers, the exponentials' unit and the multiply-adds' are each 25 to 55 % busy (78 instructions for a pair's token in
-// the prompt, 132 in the gradient); 16384 x 2048 bf16 91 (54 %) and 155 (57 %): the same, and clusters' waits; 8 x 2048 x 4096
-// f32 211 (94 %) and 405 (88 %).
+// the prompt, 136 in the gradient); 16384 x 2048 bf16 86 (58 %) and 147 (60 %): the same, and clusters' waits; 8 x 2048 x 4096
+// f32 211 (94 %) and 410 (87 %).
 #pragma once
 
 #include <initializer_list>
@@ -41,8 +41,8 @@ constexpr int kGatedSlab = 64;   // channels of a warp
 // leave less idle; against eight warps of 8: 4 x 2048 (256) 69, 73; without output gate 4 x 4096 (256) 107, 117; 7 x 2048 (448) 108, 110;
 // 8 x 2048 (512) 128, of 16 tokens 134, eight warps 140; 16 x 1024 (1024) 112, 123, 125. 4 tokens, eight warps, three CTAs an SM, 4 x 2048: 115.
 // f32, eight warps of 8 tokens, one CTA an SM: 8 x 2048 (512) 211, four warps 246.
-// Clusters, two of whose CTAs have to be on an SM: four warps, of 16 and f32 of 8 tokens; against eight of 8: bf16 16384 x 2048 channels 91, 107
-// (one warp joining for all: 99); 2 x 2048 44, 49; f32 16384 x 2048 channels 127, 221; 4096 64, 76.
+// Clusters, two of whose CTAs have to be on an SM: four warps, of 16 and f32 of 8 tokens; against eight of 8, as measured together: bf16 16384 x 2048
+// channels 91, 107 (one warp joining for all: 99), 86 now; 2 x 2048 44, 49; f32 16384 x 2048 channels 127, 221, 115 now; 4096 64, 76.
 constexpr int kGatedWarps = 4, kGatedWholeWarps = 8;
 constexpr int kFwdT = 8, kFwdMoreT = 16;
 constexpr int gated_cluster_tokens(int bytes) { return bytes == 4 ? kFwdT : kFwdMoreT; }
