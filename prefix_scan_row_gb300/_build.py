@@ -7,11 +7,13 @@ library loads without any library path set up. The checked library is the
 same sources compiled with MT_CHECKED=1: every global store and shared-memory
 access of its scan kernels is checked against its buffer first, and a bad one is
 skipped and reported as MT_ERR_BOUNDS by mt_scan_status() (a debugging and
-test build; the ordinary library is the product).
+test build; the ordinary library is the product). Sources without such checks
+(the sequence operators') are compiled once for both.
 """
 from __future__ import annotations
 
 import os
+import re
 import subprocess
 import sys
 from concurrent.futures import ThreadPoolExecutor
@@ -39,6 +41,23 @@ def _headers_mtime():
     hs = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
     hs.append(os.path.join(INCLUDE, "mt_scan.h"))
     return max(os.path.getmtime(h) for h in hs)
+
+
+def _has_checks(src):
+    """Whether a source, or a header that it includes, makes a check: mt_tile.cuh only defines them."""
+    seen, ask = set(), [os.path.basename(src)]
+    while ask:
+        f = ask.pop()
+        path = os.path.join(CSRC, f)
+        if f in seen or f == "mt_tile.cuh" or not os.path.exists(path):
+            continue
+        seen.add(f)
+        with open(path) as text:
+            text = text.read()
+        if "MT_CHECK" in text:
+            return True
+        ask += re.findall(r'#include "([^"]+)"', text)
+    return False
 
 
 def _variant(checked):
@@ -89,12 +108,15 @@ def build_all(force: bool = False, verbose_ptxas: bool = False, variants=(False,
                 os.remove(os.path.join(bdir, f))
     extra = ["-Xptxas", "-v"] if verbose_ptxas else []
     srcs = sources()
-    jobs = [(src, checked) for checked in variants for src in srcs]
+    units = {checked: [(src, checked and _has_checks(src)) for src in srcs] for checked in variants}
+    jobs = sorted(set(sum(units.values(), [])))
+    for checked in {job[1] for job in jobs}:
+        os.makedirs(_variant(checked)[0], exist_ok=True)
     with ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 4)) as ex:
-        objs = list(ex.map(lambda j: _compile(j[0], extra, j[1]), jobs))
+        objs = dict(zip(jobs, ex.map(lambda j: _compile(j[0], extra, j[1]), jobs)))
     libs = []
-    for i, checked in enumerate(variants):
-        libs.append(_link(objs[i * len(srcs):(i + 1) * len(srcs)], checked, force))
+    for checked in variants:
+        libs.append(_link([objs[u] for u in units[checked]], checked, force))
     return libs
 
 
