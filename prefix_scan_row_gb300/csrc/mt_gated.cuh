@@ -301,8 +301,8 @@ template <bool VEC> constexpr int kFar = VEC ? 1 : kGatedSlab / 2;
 // T tokens of a tensor in a warp's part of shared memory, 64 channels each. VEC: the rows are 16-byte aligned and
 // whole vectors. Otherwise rows are copied as the aligned vectors that they touch (each holds a channel of the row) and read from
 // where they begin in the first; or, WORDS, f32 value by value.
-// 4 x 2048 tokens x 4095 channels, all gates, us: bf16 prompt 107 and gradient 205 (4096 channels 69 and 122); f32 prompt
-// by words 155, by vectors 170, gradient 390 and 271.
+// 4 x 2048 tokens x 4095 channels, all gates, us: bf16 prompt 106 and gradient 206 (4096 channels 68 and 121); f32 gradient by words 390, by
+// vectors 260; f32 prompt 182 and 164, but 8 x 1027 x 1001 without input gate 43.0 and 44.7, 3 x 515 x 1001 without output gate 12.4 and 13.4.
 template <class S, int T, bool VEC, bool WORDS = false> struct Tile {
     static constexpr int kPitch = kGatedSlab * (int)sizeof(S) + (VEC ? 0 : 16);
     static constexpr int kBytes = T * kPitch;
